@@ -36,6 +36,14 @@
  *     group of 128 columns one 32-bit word per row holding that row's 4 block scales
  *     in column order (cols % 128 == 0), so that the scales a GEMM stage needs for
  *     consecutive rows are consecutive words.
+ *   - With MOE_FP8 the router and the tokens x stay bf16 too; ring_x, H and the expert
+ *     weights are E4M3 codes with fp32 scales, value = code * scale: a row matrix
+ *     [rows, cols] (tokens, H) has one scale per row and 128 columns, laid out
+ *     [cols/128][rows]; a weight matrix [rows, cols] one per 128 x 128 block, laid out
+ *     [rows/128][cols/128] (an expert stack: [E][rows/128][cols/128]).  d and f are
+ *     multiples of 128.  Scale arguments typed uint8_t* take the address of these floats.
+ *     moe_route, moe_dispatch, moe_expert_ffn and moe_combine take MOE_FP8; so do the
+ *     calls below that say so.
  *   - The caller owns every buffer.  The library allocates nothing, keeps no
  *     pointer after return, and only enqueues work on `stream`: there is no
  *     host synchronisation and no device-to-host copy inside any call.
@@ -69,14 +77,16 @@ enum moe_status {
   MOE_ERR_WORKSPACE = 4,  /* workspace smaller than moe_workspace_bytes() */
   MOE_ERR_HIP = 5,        /* a HIP launch or runtime call failed */
   MOE_ERR_DTYPE = 6,      /* unknown dtype, or a dtype the call does not support */
-  MOE_ERR_SCRATCH = 7     /* shape needs more than the static scratch of moe_decode_noalloc */
+  MOE_ERR_SCRATCH = 7,    /* shape needs more than the static scratch of moe_decode_noalloc */
+  MOE_ERR_ALIGN = 8       /* a tensor is not aligned to 16 bytes (calls that say so) */
 };
 
-enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP8 = 2 };
+enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP8 = 2, MOE_FP8 = 3 };
 
 enum moe_op {
   MOE_OP_ROUTE = 0, MOE_OP_DISPATCH = 1, MOE_OP_EXPERT_FFN = 2,
-  MOE_OP_COMBINE = 3, MOE_OP_DECODE = 4, MOE_OP_BACKWARD = 5, MOE_OP_FORWARD = 6
+  MOE_OP_COMBINE = 3, MOE_OP_DECODE = 4, MOE_OP_BACKWARD = 5, MOE_OP_FORWARD = 6,
+  MOE_OP_NORM_BACKWARD = 7, MOE_OP_ROUTE_BACKWARD = 8
 };
 
 /* Shape of one layer call (host struct). */
@@ -350,6 +360,154 @@ int moe_quantize_mx_t(const void* src_bf16, int64_t batch, int64_t rows, int64_t
 int moe_quantize_mx_both(const void* src_bf16, int64_t batch, int64_t rows, int64_t cols,
                          uint8_t* codes, uint8_t* scales, uint8_t* codes_t, int64_t ld,
                          int64_t col0, uint8_t* scales_t, hipStream_t stream);
+
+/* ------------------------------------------------------------------ residual RMS norm
+ * moe_add_rmsnorm: the norm in front of the layer, per token row:
+ *   h = round(x + residual) (x itself when residual is NULL), rounded to the act type;
+ *   rstd = 1 / sqrt(mean_i h_i^2 + eps);   y = h rstd weight,
+ * everything after h's rounding in fp32.  h is the new residual stream.
+ * In:  x [T,d] act, residual [T,d] act or NULL, weight [d] f32, eps >= 0 (finite).
+ * Out: h [T,d] act or NULL (may be x or residual itself: each element is read before it is
+ *      written); y [T,d] act or NULL; y8 [T,d] E4M3 codes of the unrounded y with y8_scale,
+ *      or both NULL: MOE_FP8: scale = max(amax, 2^-100) / 448 per row and 128 columns, f32
+ *      [d/128][T], code = RNE_E4M3(y / scale); MOE_MXFP8: codes and E8M0 bytes as
+ *      moe_quantize_mx writes them, [d/128][T][4].  A block that holds an infinity or a NaN
+ *      gets the scale NaN (E8M0 byte 255).  y or y8 must be given.  rstd [T] f32 or NULL
+ *      (moe_add_rmsnorm_backward needs it).
+ * Apart from h no output may overlap an input or another output.  y8 needs MOE_MXFP8 or
+ * MOE_FP8 (MOE_ERR_DTYPE).  Tensors are aligned to 16 bytes (MOE_ERR_ALIGN); rstd and
+ * y8_scale to 4.  eps that is negative, NaN or infinite: MOE_ERR_SHAPE.
+ */
+int moe_add_rmsnorm(const moe_shape* shape, const void* x, const void* residual,
+                    const float* weight, float eps, void* h, void* y, uint8_t* y8,
+                    void* y8_scale, float* rstd, hipStream_t stream);
+
+/*
+ * moe_add_rmsnorm_backward: with xh = h rstd and q = weight dy (the 8-bit rounding counts
+ * as the identity):
+ *   dx = dh + rstd (q - xh mean_i(q_i xh_i)),   dweight = sum_t dy xh,
+ * dx being the gradient of x and of residual alike.
+ * In:  dy [T,d] act; dh [T,d] act, the gradient that reaches h from elsewhere, or NULL;
+ *      h, weight, rstd of the forward.
+ * Out: dx [T,d] act (may be dy or dh itself); dweight [d] f32 or NULL.
+ * workspace: moe_workspace_bytes(shape, MOE_OP_NORM_BACKWARD) bytes.  Alignment as above.
+ */
+int moe_add_rmsnorm_backward(const moe_shape* shape, const void* dy, const void* dh,
+                             const void* h, const float* weight, const float* rstd, void* dx,
+                             float* dweight, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
+/* ------------------------------------------------------------------ scored routing */
+enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+/* The rule of moe_route_scored (host struct). */
+typedef struct moe_router {
+  int32_t score;        /* enum moe_score */
+  int32_t groups;       /* G equal groups of consecutive experts (G divides E, G <= 64); 1: none */
+  int32_t top_groups;   /* groups a token may choose from, 1 <= top_groups <= G */
+  int32_t group_top;    /* 1 or 2 (<= E / G): a group's score is the sum of its group_top best c */
+  int32_t renormalise;  /* 0, or 1: the k gates are divided by their sum */
+  float scale;          /* finite: every gate is multiplied by it */
+} moe_router;
+
+/*
+ * moe_route_scored: moe_route with a choice of scores, a balance bias and groups.  In fp32:
+ *   l = x W_r^T (+ b_r);   s = softmax_e(l) or 1 / (1 + exp(-l));   c = s (+ balance);
+ *   the top_groups groups with the largest scores are kept; S = the k largest c among
+ *   their experts (ties, of groups and of experts, to the lower id);
+ *   g_j = scale s_j, or with renormalise scale s_j / sum_S s.
+ * balance decides the choice only: gates and gradients are those of s.  Without balance the
+ * experts of a token are ordered by l (the order of s).  An expert whose logit is -inf has
+ * the score and the gate 0; a row whose scores are all 0 has the gates 0.  A NaN ranks
+ * below every number; a row with a NaN or a +inf logit has valid expert ids, and gates that
+ * may be NaN.
+ * In:  x [T,d] act (bf16 for MOE_MXFP8 and MOE_FP8), w_router [E,d] f32, b_router [E] f32 or
+ *      NULL, balance [E] f32 or NULL.  top_k <= top_groups * E / G.
+ * Out: topk_idx, topk_gate, expert_count as moe_route; logits [T,E] f32 (l, with b_r) or
+ *      NULL (moe_route_scored_backward needs them).
+ * workspace: moe_workspace_bytes(shape, MOE_OP_ROUTE) bytes.  A rule outside the limits
+ * above: MOE_ERR_SHAPE.  x and w_router are aligned to 16 bytes (MOE_ERR_ALIGN).
+ */
+int moe_route_scored(const moe_shape* shape, const moe_router* router, const void* x,
+                     const float* w_router, const float* b_router, const float* balance,
+                     int32_t* topk_idx, float* topk_gate, int32_t* expert_count, float* logits,
+                     void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_route_scored_backward: gradients of the gates, the choice S held fixed.
+ *   renormalised softmax: dl_j = g_j (dg_j - sum_S g_i dg_i / scale), softmax: dl_e =
+ *   s_e (scale dg_e - sum_S scale s_i dg_i) for every e (dg_e = 0 outside S); renormalised
+ *   sigmoid: dl_j = g_j (1 - s_j) (dg_j - sum_S g_i dg_i / scale), sigmoid: dl_j =
+ *   scale dg_j s_j (1 - s_j);   then dl += dlogits,
+ *   dx_t = dx_in_t + dl_t W_r,   dW_r = dl^T x,   db_r = sum_t dl_t.
+ * In:  dgate [T,k] f32; dlogits [T,E] f32, a further gradient of the logits (a balance
+ *      or z loss), or NULL; x, w_router, logits, topk_idx of the forward; dx_in [T,d] act or
+ *      NULL (the experts' part of dx, moe_backward_experts).
+ * Out: dx [T,d] act (may be dx_in itself); dw_router [E,d] f32; db_router [E] f32 or NULL.
+ * An id in topk_idx outside [0, E) is left out of the sums.
+ * workspace: moe_workspace_bytes(shape, MOE_OP_ROUTE_BACKWARD) bytes.  x, w_router, dx_in, dx
+ * and dw_router are aligned to 16 bytes (MOE_ERR_ALIGN).
+ */
+int moe_route_scored_backward(const moe_shape* shape, const moe_router* router,
+                              const float* dgate, const float* dlogits, const void* x,
+                              const float* w_router, const float* logits,
+                              const int32_t* topk_idx, const void* dx_in, void* dx,
+                              float* dw_router, float* db_router, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_backward_experts: moe_backward without its router part, for a layer routed by
+ * moe_route_scored: dgate [T,k] f32 (dg of each copy) is written instead of dw_router, and
+ * dx holds the experts' part alone, rounded to bf16 once (moe_route_scored_backward takes
+ * both and rounds dx a second time).  Arguments, limits and workspace otherwise as
+ * moe_backward.
+ */
+int moe_backward_experts(const moe_shape* shape, const void* dy, const int32_t* topk_idx,
+                         const float* topk_gate, const void* ring_x,
+                         const int32_t* expert_offset, const int32_t* copy_slot,
+                         const int32_t* slot_copy, int64_t ring_head, const void* saved_au,
+                         const void* w_gate, const void* w_up, const void* w_down, void* dx,
+                         void* dw_gate, void* dw_up, void* dw_down, float* dgate,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------ FP8, scales per 128
+ * moe_dispatch_q: moe_dispatch of rows that are 8-bit already (moe_add_rmsnorm's y8): x8 [T,d]
+ * codes and x8_scale [d/128][T] (MOE_FP8: f32; MOE_MXFP8: 4 bytes each) are copied into the
+ * ring; every other argument as moe_dispatch.  MOE_MXFP8 and MOE_FP8 only (MOE_ERR_DTYPE).
+ * x8 and ring_x are aligned to 16 bytes (MOE_ERR_ALIGN).
+ */
+int moe_dispatch_q(const moe_shape* shape, const uint8_t* x8, const uint8_t* x8_scale,
+                   const int32_t* topk_idx, int64_t ring_head, void* ring_x,
+                   uint8_t* ring_x_scale, int32_t* expert_offset, int32_t* copy_slot,
+                   int32_t* slot_copy, void* workspace, size_t workspace_bytes,
+                   hipStream_t stream);
+
+/*
+ * moe_quantize_fp8: a bf16 matrix [rows, cols] (cols % 128 == 0) to E4M3 codes and fp32
+ * scales, scale = max(amax, 2^-100) / 448 per block, code = RNE_E4M3(v / scale) (a block that
+ * holds an infinity or a NaN: scale NaN).  row_block 1: one block per row and 128
+ * columns, scales [cols/128][rows]; row_block 128: one per 128 x 128, the last block of
+ * rows may be short, scales [ceil(rows/128)][cols/128].  src and codes are aligned to 16
+ * bytes (MOE_ERR_ALIGN).
+ */
+int moe_quantize_fp8(const void* src_bf16, int64_t rows, int64_t cols, int row_block,
+                     uint8_t* codes, float* scales, hipStream_t stream);
+
+/*
+ * moe_matmul_fp8: out = A W^T of two E4M3 matrices in nn.Linear layout,
+ *   out[m,n] = sum_b a_scale[b][m] w_scale[n/128][b] sum_{i in block b} a[m,i] w[n,i],
+ * b running over the K/128 blocks of 128; fp32 products and sums, one rounding.
+ * In:  a [M,K], a_scale [K/128][M]; w [N,K], w_scale [ceil(N/128)][K/128] (moe_quantize_fp8
+ *      with row_block 1 and 128).  K % 128 == 0; M K and N K < 2^32, M N < 2^38.
+ * Out: out [M,N]: out_dtype MOE_BF16 or MOE_F32 (MOE_ERR_DTYPE otherwise).
+ * M = 0 or N = 0: nothing is written.
+ * workspace: moe_matmul_fp8_workspace_bytes(M, N, K) bytes (NULL if that is 0).  a and w are
+ * aligned to 16 bytes, out to its element, a_scale, w_scale to 4 (MOE_ERR_ALIGN).
+ */
+int moe_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w,
+                   const float* w_scale, int64_t M, int64_t N, int64_t K, int out_dtype,
+                   void* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t moe_matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 #ifdef __cplusplus
 }

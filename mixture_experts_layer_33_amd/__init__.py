@@ -13,14 +13,17 @@ from typing import Dict, Optional
 
 import torch
 
-from ._lib import (DTYPES, MOE_BF16, MOE_F32, MOE_MXFP8, OP_BACKWARD, OP_COMBINE, OP_DECODE,
-                   OP_DISPATCH, OP_EXPERT_FFN, OP_FORWARD, OP_ROUTE, LIB_PATH, MoeError, MoeShape,
-                   check, lib)
+from ._lib import (DTYPES, MOE_BF16, MOE_F32, MOE_FP8, MOE_MXFP8, OP_BACKWARD, OP_COMBINE,
+                   OP_DECODE, OP_DISPATCH, OP_EXPERT_FFN, OP_FORWARD, OP_NORM_BACKWARD, OP_ROUTE,
+                   OP_ROUTE_BACKWARD, SCORES, LIB_PATH, MoeError, MoeRouter, MoeShape, check, lib)
 
 __all__ = ["make_shape", "check_shape", "workspace_bytes", "moe_route", "moe_dispatch", "moe_expert_ffn",
            "moe_expert_ffn_timed",
            "moe_combine", "moe_forward", "moe_decode", "moe_backward", "moe_backward_mx",
            "moe_quantize_mx", "quantize_mx_t_backward_weights", "Layer",
+           "make_router", "moe_route_scored", "moe_route_scored_backward", "moe_backward_experts",
+           "moe_add_rmsnorm", "moe_add_rmsnorm_backward", "moe_dispatch_q", "quantize_fp8",
+           "moe_matmul_fp8", "matmul_fp8_workspace",
            "MoeError",
            "LIB_PATH"]
 
@@ -71,6 +74,16 @@ def moe_route(shape, x, w_router, b_router, topk_idx, topk_gate, expert_count, w
 
 def moe_dispatch(shape, x, topk_idx, ring_head, ring_x, ring_x_scale, expert_offset, copy_slot,
                  slot_copy, ws, stream=None):
+    if shape.dtype == MOE_FP8:
+        T, d, E, k, C, dev = (shape.tokens, shape.hidden, shape.experts, shape.top_k, shape.capacity, ring_x.device)
+        i32 = torch.int32
+        args = (_a("x", x, torch.bfloat16, (T, d), dev), _a("topk_idx", topk_idx, i32, (T, k), dev),
+                int(ring_head), _a("ring_x", ring_x, torch.uint8, (C, d), dev),
+                _a("ring_x_scale", ring_x_scale, *_scale_spec(shape, C), dev),
+                _a("expert_offset", expert_offset, i32, (E + 1,), dev),
+                _a("copy_slot", copy_slot, i32, (T, k), dev), _a("slot_copy", slot_copy, i32, (C,), dev),
+                *_ws_arg("ws", ws, dev))
+        return _on(dev, stream, "moe_dispatch", lambda s: lib().moe_dispatch(shape, *args, s))
     check("moe_dispatch", lib().moe_dispatch(shape, _p(x), _p(topk_idx), int(ring_head), _p(ring_x),
                                              _p(ring_x_scale), _p(expert_offset), _p(copy_slot),
                                              _p(slot_copy), _p(ws), ws.numel(), _s(stream)))
@@ -78,6 +91,10 @@ def moe_dispatch(shape, x, topk_idx, ring_head, ring_x, ring_x_scale, expert_off
 
 def moe_expert_ffn(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
                    w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws, stream=None):
+    if shape.dtype == MOE_FP8:
+        args = _ffn_fp8_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
+                             w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws)
+        return _on(ring_x.device, stream, "moe_expert_ffn", lambda s: lib().moe_expert_ffn(shape, *args, s))
     check("moe_expert_ffn", lib().moe_expert_ffn(
         shape, _p(ring_x), _p(ring_x_scale), _p(expert_offset), int(ring_head), _p(w_gate),
         _p(w_up), _p(w_down), _p(w_gate_scale), _p(w_up_scale), _p(w_down_scale), _p(ring_y),
@@ -93,6 +110,11 @@ def moe_expert_ffn_timed(shape, ring_x, ring_x_scale, expert_offset, ring_head, 
         if e.cuda_event == 0:
             e.record()
     arr = (ctypes.c_void_p * 3)(*[e.cuda_event for e in events])
+    if shape.dtype == MOE_FP8:
+        args = _ffn_fp8_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
+                             w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws)
+        return _on(ring_x.device, stream, "moe_expert_ffn_timed", lambda s: lib().moe_expert_ffn_timed(
+            shape, *args, ctypes.cast(arr, ctypes.c_void_p), s))
     check("moe_expert_ffn_timed", lib().moe_expert_ffn_timed(
         shape, _p(ring_x), _p(ring_x_scale), _p(expert_offset), int(ring_head), _p(w_gate),
         _p(w_up), _p(w_down), _p(w_gate_scale), _p(w_up_scale), _p(w_down_scale), _p(ring_y),
@@ -201,11 +223,211 @@ def quantize_mx(src: torch.Tensor, stream=None):
     return codes, scales
 
 
+# ------------------------------------------------------------------ scored routing, norm, FP8
+# These calls check every tensor (type, shape, contiguity, one device) and run on that device,
+# on `stream` or its current stream.
+
+def _on(dev: torch.device, stream, fn: str, call):
+    """call(raw stream) with `dev` current; raises MoeError on a status."""
+    if dev.type != "cuda":
+        raise ValueError("libmoe takes device tensors only")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {dev}")
+    if dev.index == torch.cuda.current_device():
+        st = call((stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = call((stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
+    if st:
+        check(fn, st)
+
+
+def _a(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple, dev: torch.device):
+    """The address of an argument after its checks (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: needs a contiguous {dtype} tensor {list(shape)} on {dev}, got "
+                         f"{t.dtype} {list(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+def _act(shape: MoeShape) -> torch.dtype:
+    return torch.float32 if shape.dtype == MOE_F32 else torch.bfloat16
+
+
+def _ws_arg(name: str, ws: Optional[torch.Tensor], dev: torch.device):
+    if ws is None:
+        return None, 0
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"{name}: needs a contiguous tensor on {dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def make_router(score: str = "softmax", groups: int = 1, top_groups: Optional[int] = None, group_top: int = 1,
+                renormalise: bool = True, scale: float = 1.0) -> MoeRouter:
+    """The rule of moe_route_scored: "softmax" or "sigmoid" scores, `groups` groups of experts of
+    which a token keeps `top_groups` (default: all) by the sum of their `group_top` best."""
+    return MoeRouter(score=SCORES[score] if isinstance(score, str) else int(score), groups=groups,
+                     top_groups=groups if top_groups is None else top_groups, group_top=group_top,
+                     renormalise=int(renormalise), scale=scale)
+
+
+def moe_route_scored(shape, router, x, w_router, b_router, balance, topk_idx, topk_gate, expert_count,
+                     logits, ws, stream=None):
+    T, d, E, k, dev = shape.tokens, shape.hidden, shape.experts, shape.top_k, w_router.device
+    f32, i32 = torch.float32, torch.int32
+    args = (_a("x", x, _act(shape), (T, d), dev), _a("w_router", w_router, f32, (E, d), dev),
+            _a("b_router", b_router, f32, (E,), dev), _a("balance", balance, f32, (E,), dev),
+            _a("topk_idx", topk_idx, i32, (T, k), dev), _a("topk_gate", topk_gate, f32, (T, k), dev),
+            _a("expert_count", expert_count, i32, (E,), dev), _a("logits", logits, f32, (T, E), dev),
+            *_ws_arg("ws", ws, dev))
+    _on(dev, stream, "moe_route_scored", lambda s: lib().moe_route_scored(shape, router, *args, s))
+
+
+def moe_route_scored_backward(shape, router, dgate, dlogits, x, w_router, logits, topk_idx, dx_in, dx,
+                              dw_router, db_router, ws, stream=None):
+    T, d, E, k, dev = shape.tokens, shape.hidden, shape.experts, shape.top_k, w_router.device
+    act, f32 = _act(shape), torch.float32
+    args = (_a("dgate", dgate, f32, (T, k), dev), _a("dlogits", dlogits, f32, (T, E), dev),
+            _a("x", x, act, (T, d), dev), _a("w_router", w_router, f32, (E, d), dev),
+            _a("logits", logits, f32, (T, E), dev), _a("topk_idx", topk_idx, torch.int32, (T, k), dev),
+            _a("dx_in", dx_in, act, (T, d), dev), _a("dx", dx, act, (T, d), dev),
+            _a("dw_router", dw_router, f32, (E, d), dev), _a("db_router", db_router, f32, (E,), dev),
+            *_ws_arg("ws", ws, dev))
+    _on(dev, stream, "moe_route_scored_backward",
+        lambda s: lib().moe_route_scored_backward(shape, router, *args, s))
+
+
+def moe_backward_experts(shape, dy, topk_idx, topk_gate, ring_x, expert_offset, copy_slot, slot_copy,
+                         ring_head, saved_au, w_gate, w_up, w_down, dx, dw_gate, dw_up, dw_down, dgate,
+                         ws, stream=None):
+    """moe_backward without the router's part: dx of the experts alone, and the gates' gradient."""
+    T, d, E, k, f, C = (shape.tokens, shape.hidden, shape.experts, shape.top_k, shape.ffn, shape.capacity)
+    dev, bf, f32, i32 = w_gate.device, torch.bfloat16, torch.float32, torch.int32
+    args = (_a("dy", dy, bf, (T, d), dev), _a("topk_idx", topk_idx, i32, (T, k), dev),
+            _a("topk_gate", topk_gate, f32, (T, k), dev), _a("ring_x", ring_x, bf, (C, d), dev),
+            _a("expert_offset", expert_offset, i32, (E + 1,), dev),
+            _a("copy_slot", copy_slot, i32, (T, k), dev), _a("slot_copy", slot_copy, i32, (C,), dev),
+            int(ring_head), _a("saved_au", saved_au, bf, (C, 2 * f), dev),
+            _a("w_gate", w_gate, bf, (E, f, d), dev), _a("w_up", w_up, bf, (E, f, d), dev),
+            _a("w_down", w_down, bf, (E, d, f), dev), _a("dx", dx, bf, (T, d), dev),
+            _a("dw_gate", dw_gate, bf, (E, f, d), dev), _a("dw_up", dw_up, bf, (E, f, d), dev),
+            _a("dw_down", dw_down, bf, (E, d, f), dev), _a("dgate", dgate, f32, (T, k), dev),
+            *_ws_arg("ws", ws, dev))
+    _on(dev, stream, "moe_backward_experts", lambda s: lib().moe_backward_experts(shape, *args, s))
+
+
+def _scale_spec(shape: MoeShape, rows: int):
+    """Type and shape of the scales of 8-bit rows [rows, d]."""
+    if shape.dtype == MOE_FP8:
+        return torch.float32, (shape.hidden // 128, rows)
+    return torch.uint8, (shape.hidden // 128, rows, 4)
+
+
+def _ffn_fp8_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
+                  w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws):
+    d, E, f, C, dev = shape.hidden, shape.experts, shape.ffn, shape.capacity, ring_x.device
+    u8, f32, bf = torch.uint8, torch.float32, torch.bfloat16
+    wide, tall = (E, f // 128, d // 128), (E, d // 128, f // 128)
+    return (_a("ring_x", ring_x, u8, (C, d), dev),
+            _a("ring_x_scale", ring_x_scale, f32, (d // 128, C), dev),
+            _a("expert_offset", expert_offset, torch.int32, (E + 1,), dev), int(ring_head),
+            _a("w_gate", w_gate, u8, (E, f, d), dev), _a("w_up", w_up, u8, (E, f, d), dev),
+            _a("w_down", w_down, u8, (E, d, f), dev), _a("w_gate_scale", w_gate_scale, f32, wide, dev),
+            _a("w_up_scale", w_up_scale, f32, wide, dev), _a("w_down_scale", w_down_scale, f32, tall, dev),
+            _a("ring_y", ring_y, bf, (C, d), dev), _a("saved_au", saved_au, bf, (C, 2 * f), dev),
+            *_ws_arg("ws", ws, dev))
+
+
+def moe_add_rmsnorm(shape, x, residual, weight, eps, h, y, y8, y8_scale, rstd, stream=None):
+    T, d, dev = shape.tokens, shape.hidden, weight.device
+    act, f32 = _act(shape), torch.float32
+    sdt, sshape = _scale_spec(shape, T)
+    args = (_a("x", x, act, (T, d), dev), _a("residual", residual, act, (T, d), dev),
+            _a("weight", weight, f32, (d,), dev), float(eps), _a("h", h, act, (T, d), dev),
+            _a("y", y, act, (T, d), dev), _a("y8", y8, torch.uint8, (T, d), dev),
+            _a("y8_scale", y8_scale, sdt, sshape, dev), _a("rstd", rstd, f32, (T,), dev))
+    _on(dev, stream, "moe_add_rmsnorm", lambda s: lib().moe_add_rmsnorm(shape, *args, s))
+
+
+def moe_add_rmsnorm_backward(shape, dy, dh, h, weight, rstd, dx, dweight, ws, stream=None):
+    T, d, dev = shape.tokens, shape.hidden, weight.device
+    act, f32 = _act(shape), torch.float32
+    args = (_a("dy", dy, act, (T, d), dev), _a("dh", dh, act, (T, d), dev), _a("h", h, act, (T, d), dev),
+            _a("weight", weight, f32, (d,), dev), _a("rstd", rstd, f32, (T,), dev),
+            _a("dx", dx, act, (T, d), dev), _a("dweight", dweight, f32, (d,), dev),
+            *_ws_arg("ws", ws, dev))
+    _on(dev, stream, "moe_add_rmsnorm_backward", lambda s: lib().moe_add_rmsnorm_backward(shape, *args, s))
+
+
+def moe_dispatch_q(shape, x8, x8_scale, topk_idx, ring_head, ring_x, ring_x_scale, expert_offset,
+                   copy_slot, slot_copy, ws, stream=None):
+    """moe_dispatch of 8-bit rows (moe_add_rmsnorm's y8 and its scales)."""
+    T, d, E, k, C, dev = (shape.tokens, shape.hidden, shape.experts, shape.top_k, shape.capacity, ring_x.device)
+    i32, u8 = torch.int32, torch.uint8
+    args = (_a("x8", x8, u8, (T, d), dev), _a("x8_scale", x8_scale, *_scale_spec(shape, T), dev),
+            _a("topk_idx", topk_idx, i32, (T, k), dev), int(ring_head),
+            _a("ring_x", ring_x, u8, (C, d), dev),
+            _a("ring_x_scale", ring_x_scale, *_scale_spec(shape, C), dev),
+            _a("expert_offset", expert_offset, i32, (E + 1,), dev),
+            _a("copy_slot", copy_slot, i32, (T, k), dev), _a("slot_copy", slot_copy, i32, (C,), dev),
+            *_ws_arg("ws", ws, dev))
+    _on(dev, stream, "moe_dispatch_q", lambda s: lib().moe_dispatch_q(shape, *args, s))
+
+
+def quantize_fp8(src: torch.Tensor, row_block: int = 128, stream=None):
+    """(codes uint8, scales f32) of a bf16 tensor [..., cols], E4M3 with one scale per `row_block`
+    (1 or 128) rows and 128 columns: scales [cols/128][rows] for rows, and for 128 x 128
+    blocks [ceil(rows/128)][cols/128] (an expert stack [E, rows, cols]: [E, rows/128, cols/128],
+    its rows a multiple of 128)."""
+    if src.dim() < 2:
+        raise ValueError("quantize_fp8 takes matrices")
+    dev, cols = src.device, src.shape[-1]
+    rows = math.prod(src.shape[:-1])
+    if row_block == 128 and src.dim() > 2 and src.shape[-2] % 128:
+        raise ValueError("the rows of each matrix of a stack must be a multiple of 128")
+    codes = torch.empty(src.shape, dtype=torch.uint8, device=dev)
+    if row_block == 1:
+        shape = (cols // 128, rows)
+    elif src.dim() > 2:
+        shape = (*src.shape[:-2], src.shape[-2] // 128, cols // 128)
+    else:
+        shape = (-(-rows // 128), cols // 128)
+    scales = torch.empty(shape, dtype=torch.float32, device=dev)
+    p = _a("src", src, torch.bfloat16, src.shape, dev)
+    _on(dev, stream, "moe_quantize_fp8",
+        lambda s: lib().moe_quantize_fp8(p, rows, cols, row_block, codes.data_ptr(), scales.data_ptr(), s))
+    return codes, scales
+
+
+def matmul_fp8_workspace(M: int, N: int, K: int, device) -> Optional[torch.Tensor]:
+    """The workspace moe_matmul_fp8 needs for these sizes (None if it needs none)."""
+    n = int(lib().moe_matmul_fp8_workspace_bytes(M, N, K))
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def moe_matmul_fp8(a, a_scale, w, w_scale, out, ws=None, stream=None):
+    """out [M, N] (bf16 or fp32) = A W^T of codes a [M, K], w [N, K] with the scales of
+    quantize_fp8: a_scale [K/128, M] (row_block 1), w_scale [ceil(N/128), K/128]."""
+    if a.dim() != 2 or w.dim() != 2 or out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("moe_matmul_fp8: two matrices of codes, and an output in bfloat16 or float32")
+    dev, (M, K), N = w.device, a.shape, w.shape[0]
+    u8, f32 = torch.uint8, torch.float32
+    args = (_a("a", a, u8, (M, K), dev), _a("a_scale", a_scale, f32, (K // 128, M), dev),
+            _a("w", w, u8, (N, K), dev), _a("w_scale", w_scale, f32, (-(-N // 128), K // 128), dev),
+            M, N, K, MOE_F32 if out.dtype is f32 else MOE_BF16, _a("out", out, out.dtype, (M, N), dev),
+            *_ws_arg("ws", ws, dev))
+    _on(dev, stream, "moe_matmul_fp8", lambda s: lib().moe_matmul_fp8(*args, s))
+
+
 @dataclass
 class Layer:
     """Buffers of one layer shape, and the forward / backward / decode as chained C calls.
 
-    Expert weights are passed per call; for MXFP8 pass their MX codes and scales."""
+    Expert weights are passed per call; for MXFP8 pass their MX codes and scales, for FP8 those of
+    quantize_fp8.  With a `router` (make_router) the layer routes by moe_route_scored."""
     shape: MoeShape
     device: torch.device
     bufs: Dict[str, torch.Tensor] = field(default_factory=dict)
@@ -229,24 +451,62 @@ class Layer:
         n = max(workspace_bytes(self.shape, op), 256)
         return self._buf(f"ws{op}", (n,), torch.uint8)
 
-    def route(self, x, w_router, b_router=None):
+    def route(self, x, w_router, b_router=None, router=None, balance=None):
         s = self.shape
         T, k, E = s.tokens, s.top_k, s.experts
         idx = self._buf("topk_idx", (T, k), torch.int32)
         gate = self._buf("topk_gate", (T, k), torch.float32)
         cnt = self._buf("expert_count", (E,), torch.int32)
+        if router is not None:
+            moe_route_scored(s, router, x, w_router, b_router, balance, idx, gate, cnt,
+                             self._buf("logits", (T, E), torch.float32), self._ws(OP_ROUTE))
+            return idx, gate, cnt
+        if balance is not None:
+            raise ValueError("a balance bias needs a router (make_router)")
         moe_route(s, x, w_router, b_router, idx, gate, cnt, self._ws(OP_ROUTE))
         return idx, gate, cnt
 
-    def dispatch(self, x, topk_idx, head=0):
+    def add_rmsnorm(self, x, residual, weight, eps=1e-6):
+        """h = x + residual and its RMS norm: (h, y, y8, y8_scale); y8 is None in a bf16 or fp32
+        layer.  h and rstd are kept for add_rmsnorm_backward."""
         s = self.shape
-        mx = s.dtype == MOE_MXFP8
+        T, d = s.tokens, s.hidden
+        h, y = self._buf("norm_h", (T, d), self.act_dtype), self._buf("norm_y", (T, d), self.act_dtype)
+        rstd = self._buf("norm_rstd", (T,), torch.float32)
+        y8 = ys = None
+        if s.dtype in (MOE_MXFP8, MOE_FP8):
+            sdt, sshape = _scale_spec(s, T)
+            y8, ys = self._buf("norm_y8", (T, d), torch.uint8), self._buf("norm_y8_scale", sshape, sdt)
+        moe_add_rmsnorm(s, x, residual, weight, eps, h, y, y8, ys, rstd)
+        return h, y, y8, ys
+
+    def add_rmsnorm_backward(self, dy, dh, weight):
+        """(dx, dweight) after add_rmsnorm with the same buffers; dx belongs to x and residual."""
+        s = self.shape
+        dx = self._buf("norm_dx", (s.tokens, s.hidden), self.act_dtype)
+        dw = self._buf("norm_dw", (s.hidden,), torch.float32)
+        moe_add_rmsnorm_backward(s, dy, dh, self.bufs["norm_h"], weight, self.bufs["norm_rstd"], dx, dw,
+                                 self._ws(OP_NORM_BACKWARD))
+        return dx, dw
+
+    def dispatch(self, x, topk_idx, head=0, x_scale=None):
+        """With x_scale: x are 8-bit rows (add_rmsnorm's y8 and y8_scale) in an MXFP8 or FP8 layer."""
+        s = self.shape
+        mx = s.dtype in (MOE_MXFP8, MOE_FP8)
+        if x.dtype is not (self.act_dtype if x_scale is None else torch.uint8):
+            raise ValueError("dispatch takes act rows, or 8-bit rows with their scales")
         ring = self._buf("ring_x", (s.capacity, s.hidden), torch.uint8 if mx else self.act_dtype)
-        rsc = self._buf("ring_x_scale", (s.hidden // 128, s.capacity, 4), torch.uint8) if mx else None
+        rsc = None
+        if mx:
+            sdt, sshape = _scale_spec(s, s.capacity)
+            rsc = self._buf("ring_x_scale", sshape, sdt)
         off = self._buf("expert_offset", (s.experts + 1,), torch.int32)
         cs = self._buf("copy_slot", (s.tokens, s.top_k), torch.int32)
         sc = self._buf("slot_copy", (s.capacity,), torch.int32)
-        moe_dispatch(s, x, topk_idx, head, ring, rsc, off, cs, sc, self._ws(OP_DISPATCH))
+        if x_scale is not None:
+            moe_dispatch_q(s, x, x_scale, topk_idx, head, ring, rsc, off, cs, sc, self._ws(OP_DISPATCH))
+        else:
+            moe_dispatch(s, x, topk_idx, head, ring, rsc, off, cs, sc, self._ws(OP_DISPATCH))
         return ring, rsc, off, cs, sc
 
     def expert_ffn(self, ring_x, ring_x_scale, expert_offset, head, w_gate, w_up, w_down,
@@ -271,9 +531,11 @@ class Layer:
         return y
 
     def forward(self, x, w_router, b_router, w_gate, w_up, w_down, scales=(None, None, None),
-                head=0, save_au=False, events=None):
-        idx, gate, cnt = self.route(x, w_router, b_router)
-        ring, rsc, off, cs, sc = self.dispatch(x, idx, head)
+                head=0, save_au=False, events=None, router=None, balance=None, x8=None, x8_scale=None):
+        """x8 and x8_scale: the 8-bit rows of x for the experts (add_rmsnorm), instead of
+        quantising x in the dispatch."""
+        idx, gate, cnt = self.route(x, w_router, b_router, router, balance)
+        ring, rsc, off, cs, sc = self.dispatch(x if x8 is None else x8, idx, head, x8_scale)
         ring_y, au = self.expert_ffn(ring, rsc, off, head, w_gate, w_up, w_down, scales, save_au,
                                      events)
         y = self.combine(ring_y, cs, gate)
@@ -326,18 +588,41 @@ class Layer:
                         w_down_t, w_down_t_scale, dx, dwg, dwu, dwd, dwr, self._ws(OP_BACKWARD))
         return dx, dwg, dwu, dwd, dwr
 
-    def backward(self, dy, x, w_router, w_gate, w_up, w_down, head=0):
-        """Gradients after a forward(..., save_au=True) with the same buffers."""
+    def backward(self, dy, x, w_router, w_gate, w_up, w_down, head=0, router=None, dlogits=None):
+        """Gradients after a forward(..., save_au=True) with the same buffers (and the same
+        `router`; then dlogits is a further gradient of the logits, and the bias's gradient is
+        left in bufs["db_router"]).  After an FP8 forward the weights are the bf16 ones: the
+        tokens are dispatched again in bf16, and the forward's rounding to 8 bits counts as
+        the identity."""
         s = self.shape
         b = self.bufs
+        ring = b.get("ring_x")
+        if s.dtype == MOE_FP8:
+            s = make_shape(s.tokens, s.hidden, s.experts, s.top_k, s.ffn, s.capacity)
+            check_shape(s)
+            ring = self._buf("ring_x_bf16", (s.capacity, s.hidden), torch.bfloat16)
+            moe_dispatch(s, x, b["topk_idx"], head, ring, None, b["expert_offset"], b["copy_slot"],
+                         b["slot_copy"], self._ws(OP_DISPATCH))
+        ws = self._buf(f"ws{OP_BACKWARD}", (max(workspace_bytes(s, OP_BACKWARD), 256),), torch.uint8)
         dx = self._buf("dx", (s.tokens, s.hidden), torch.bfloat16)
         dwg = self._buf("dw_gate", (s.experts, s.ffn, s.hidden), torch.bfloat16)
         dwu = self._buf("dw_up", (s.experts, s.ffn, s.hidden), torch.bfloat16)
         dwd = self._buf("dw_down", (s.experts, s.hidden, s.ffn), torch.bfloat16)
         dwr = self._buf("dw_router", (s.experts, s.hidden), torch.float32)
-        moe_backward(s, dy, x, w_router, b["topk_idx"], b["topk_gate"], b["ring_x"],
+        if router is not None:
+            dg = self._buf("dgate", (s.tokens, s.top_k), torch.float32)
+            db = self._buf("db_router", (s.experts,), torch.float32)
+            moe_backward_experts(s, dy, b["topk_idx"], b["topk_gate"], ring, b["expert_offset"],
+                                 b["copy_slot"], b["slot_copy"], head, b["saved_au"], w_gate, w_up,
+                                 w_down, dx, dwg, dwu, dwd, dg, ws)
+            moe_route_scored_backward(s, router, dg, dlogits, x, w_router, b["logits"], b["topk_idx"],
+                                      dx, dx, dwr, db, self._ws(OP_ROUTE_BACKWARD))
+            return dx, dwg, dwu, dwd, dwr
+        if dlogits is not None:
+            raise ValueError("a gradient of the logits needs a router (make_router)")
+        moe_backward(s, dy, x, w_router, b["topk_idx"], b["topk_gate"], ring,
                      b["expert_offset"], b["copy_slot"], b["slot_copy"], head, b["saved_au"],
-                     w_gate, w_up, w_down, dx, dwg, dwu, dwd, dwr, self._ws(OP_BACKWARD))
+                     w_gate, w_up, w_down, dx, dwg, dwu, dwd, dwr, ws)
         return dx, dwg, dwu, dwd, dwr
 
 

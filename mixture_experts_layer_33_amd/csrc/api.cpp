@@ -4,6 +4,7 @@
 // crosses the boundary.
 #include "moe.h"
 
+#include <cmath>
 #include <exception>
 
 #include "kernels.h"
@@ -33,10 +34,12 @@ hipError_t zero_words(void* p, size_t words, hipStream_t st) {
   return hipGetLastError();
 }
 
-bool bad_dtype(int dt) { return dt != MOE_F32 && dt != MOE_BF16 && dt != MOE_MXFP8; }
+bool bad_dtype(int dt) { return dt != MOE_F32 && dt != MOE_BF16 && dt != MOE_MXFP8 && dt != MOE_FP8; }
+
+bool unaligned(const void* p, uintptr_t a = 16) { return (uintptr_t)p % a != 0; }
 
 // Shape checks common to the forward calls.  K-dimension multiples follow the
-// kernels' 128-byte K slices: bf16 needs d, f % 64; MX needs d, f % 128.
+// kernels' 128-byte K slices: bf16 needs d, f % 64; MX and FP8 need d, f % 128.
 int check_shape(const moe_shape* s) {
   if (!s) return MOE_ERR_NULL;
   if (bad_dtype(s->dtype)) return MOE_ERR_DTYPE;
@@ -45,7 +48,7 @@ int check_shape(const moe_shape* s) {
   if (s->experts > MAX_E || s->top_k < 1 || s->top_k > s->experts || s->top_k > MAX_K)
     return MOE_ERR_SHAPE;
   if (s->tokens > (int64_t)1 << 30) return MOE_ERR_SHAPE;
-  const int q = s->dtype == MOE_MXFP8 ? 128 : s->dtype == MOE_BF16 ? 64 : 8;
+  const int q = s->dtype == MOE_MXFP8 || s->dtype == MOE_FP8 ? 128 : s->dtype == MOE_BF16 ? 64 : 8;
   if (s->hidden % q || s->ffn % q) return MOE_ERR_SHAPE;
   if (s->capacity < s->tokens * s->top_k) return MOE_ERR_CAPACITY;
   if (s->capacity > ((int64_t)1 << 31) - 1) return MOE_ERR_SHAPE;
@@ -73,6 +76,7 @@ size_t moe_workspace_bytes(const moe_shape* s, int op) {
     case MOE_OP_ROUTE: return align256(moe::route_workspace_bytes(T, s->experts, s->hidden));
     case MOE_OP_DISPATCH: return align256(moe::dispatch_workspace_bytes(T, s->experts));
     case MOE_OP_EXPERT_FFN:
+      if (s->dtype == MOE_FP8) return align256(moe::ffn_fp8_workspace_bytes(n, C, s->experts, s->ffn));
       return align256(moe::ffn_workspace_bytes(n, C, s->hidden, s->experts, s->ffn, s->dtype));
     case MOE_OP_COMBINE: return 0;
     case MOE_OP_DECODE:
@@ -82,7 +86,11 @@ size_t moe_workspace_bytes(const moe_shape* s, int op) {
       return s->dtype == MOE_BF16
                  ? align256(moe::fused_workspace_bytes(T, C, s->hidden, s->experts, s->ffn))
                  : 0;
+    case MOE_OP_NORM_BACKWARD: return align256(moe::norm_bwd_workspace_bytes(T, s->hidden));
+    case MOE_OP_ROUTE_BACKWARD:
+      return align256(moe::route_scored_bwd_workspace_bytes(T, s->experts, s->hidden));
     case MOE_OP_BACKWARD:
+      if (s->dtype == MOE_FP8) return 0;
       if (s->dtype == MOE_MXFP8)
         return align256(moe::backward_mx_workspace_bytes(T, C, s->hidden, s->experts, s->top_k,
                                                          s->ffn));
@@ -105,6 +113,7 @@ const char* moe_status_string(int st) {
     case MOE_ERR_DTYPE: return "unknown or unsupported dtype";
     case MOE_ERR_SCRATCH:
       return "shape needs more scratch than the library's static buffer holds (moe_decode_noalloc)";
+    case MOE_ERR_ALIGN: return "a tensor is not aligned as the call needs";
     default: return "unknown status";
   }
 }
@@ -139,15 +148,16 @@ int moe_dispatch(const moe_shape* s, const void* x, const int32_t* topk_idx, int
     if (missing_tok(x, T) || missing_tok(topk_idx, T) || !ring_x || !expert_offset ||
         missing_tok(copy_slot, T) || !slot_copy || !workspace)
       return MOE_ERR_NULL;
-    if (s->dtype == MOE_MXFP8 && !ring_x_scale) return MOE_ERR_NULL;
+    if ((s->dtype == MOE_MXFP8 || s->dtype == MOE_FP8) && !ring_x_scale) return MOE_ERR_NULL;
     if (ring_head < 0 || ring_head >= s->capacity) return MOE_ERR_SHAPE;
     if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_DISPATCH)) return MOE_ERR_WORKSPACE;
     if (s->tokens == 0)   // no copies: every expert's segment is empty
       return hip_status(zero_words(expert_offset, (size_t)s->experts + 1, stream));
     return hip_status(moe::launch_dispatch(
-        x, s->dtype == MOE_F32 ? 4 : 2, s->dtype == MOE_MXFP8, topk_idx, s->tokens, s->hidden,
-        s->experts, s->top_k, ring_head, s->capacity, ring_x, ring_x_scale, expert_offset,
-        copy_slot, slot_copy, workspace, stream));
+        x, s->dtype == MOE_F32 ? 4 : 2,
+        s->dtype == MOE_MXFP8 ? moe::RowForm::mx : s->dtype == MOE_FP8 ? moe::RowForm::fp8 : moe::RowForm::plain,
+        nullptr, topk_idx, s->tokens, s->hidden, s->experts, s->top_k, ring_head, s->capacity,
+        ring_x, ring_x_scale, expert_offset, copy_slot, slot_copy, workspace, stream));
   } catch (...) {
     return MOE_ERR_HIP;
   }
@@ -164,13 +174,19 @@ int moe_expert_ffn_timed(const moe_shape* s, const void* ring_x, const uint8_t* 
     if (st) return st;
     if (!ring_x || !expert_offset || !w_gate || !w_up || !w_down || !ring_y || !workspace)
       return MOE_ERR_NULL;
-    const bool mx = s->dtype == MOE_MXFP8;
-    if (mx && (!ring_x_scale || !w_gate_scale || !w_up_scale || !w_down_scale))
+    const bool scaled = s->dtype == MOE_MXFP8 || s->dtype == MOE_FP8;
+    if (scaled && (!ring_x_scale || !w_gate_scale || !w_up_scale || !w_down_scale))
       return MOE_ERR_NULL;
     if (saved_au && s->dtype == MOE_F32) return MOE_ERR_DTYPE;
     if (ring_head < 0 || ring_head >= s->capacity) return MOE_ERR_SHAPE;
     if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_EXPERT_FFN)) return MOE_ERR_WORKSPACE;
     if (s->tokens == 0) return MOE_OK;
+    if (s->dtype == MOE_FP8)
+      return hip_status(moe::launch_ffn_fp8(
+          ring_x, (const float*)ring_x_scale, expert_offset, ring_head, s->capacity,
+          s->tokens * s->top_k, s->hidden, s->experts, s->ffn, w_gate, w_up, w_down,
+          (const float*)w_gate_scale, (const float*)w_up_scale, (const float*)w_down_scale, ring_y,
+          saved_au, workspace, events, stream));
     return hip_status(moe::launch_ffn(s->dtype, ring_x, ring_x_scale, expert_offset, ring_head,
                                       s->capacity, s->tokens * s->top_k, s->hidden, s->experts,
                                       s->ffn, w_gate, w_up, w_down, w_gate_scale, w_up_scale,
@@ -329,7 +345,7 @@ int moe_backward(const moe_shape* s, const void* dy, const void* x, const float*
     return hip_status(moe::launch_backward(
         dy, x, w_router, topk_idx, topk_gate, ring_x, expert_offset, copy_slot, slot_copy,
         ring_head, s->capacity, saved_au, w_gate, w_up, w_down, s->tokens, s->hidden, s->experts,
-        s->top_k, s->ffn, dx, dw_gate, dw_up, dw_down, dw_router, workspace, stream));
+        s->top_k, s->ffn, dx, dw_gate, dw_up, dw_down, dw_router, nullptr, workspace, stream));
   } catch (...) {
     return MOE_ERR_HIP;
   }
@@ -410,6 +426,238 @@ int moe_quantize_mx(const void* src_bf16, int64_t rows, int64_t cols, uint8_t* c
     if (!src_bf16 || !codes || !scales) return MOE_ERR_NULL;
     if (rows < 0 || cols <= 0 || cols % 128) return MOE_ERR_SHAPE;   // scale groups of 128 columns
     return hip_status(moe::launch_quantize_mx(src_bf16, rows, cols, codes, scales, stream));
+  } catch (...) {
+    return MOE_ERR_HIP;
+  }
+}
+
+// ------------------------------------------------------------------ residual RMS norm
+int moe_add_rmsnorm(const moe_shape* s, const void* x, const void* residual, const float* weight,
+                    float eps, void* h, void* y, uint8_t* y8, void* y8_scale, float* rstd,
+                    hipStream_t stream) {
+  try {
+    int st = check_shape(s);
+    if (st) return st;
+    const bool coded = s->dtype == MOE_MXFP8 || s->dtype == MOE_FP8;
+    if (!coded && (y8 || y8_scale)) return MOE_ERR_DTYPE;
+    if (!weight || (!y8) != (!y8_scale)) return MOE_ERR_NULL;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return MOE_ERR_SHAPE;
+    if (s->tokens == 0) return MOE_OK;
+    if (!x || (!y && !y8)) return MOE_ERR_NULL;
+    if (unaligned(x) || unaligned(residual) || unaligned(weight) || unaligned(h) || unaligned(y) ||
+        unaligned(y8) || unaligned(y8_scale, 4) || unaligned(rstd, 4))
+      return MOE_ERR_ALIGN;
+    return hip_status(moe::launch_add_rmsnorm(s->dtype == MOE_F32, !y8 ? 0 : s->dtype == MOE_FP8 ? 1 : 2, x,
+                                              residual, weight, eps, s->tokens, s->hidden, h, y, y8,
+                                              y8_scale, rstd, stream));
+  } catch (...) {
+    return MOE_ERR_HIP;
+  }
+}
+
+int moe_add_rmsnorm_backward(const moe_shape* s, const void* dy, const void* dh, const void* h,
+                             const float* weight, const float* rstd, void* dx, float* dweight,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  try {
+    int st = check_shape(s);
+    if (st) return st;
+    const int64_t T = s->tokens;
+    if (missing_tok(dy, T) || missing_tok(h, T) || !weight || missing_tok(rstd, T) ||
+        missing_tok(dx, T) || missing_tok(workspace, T))
+      return MOE_ERR_NULL;
+    if (unaligned(dy) || unaligned(dh) || unaligned(h) || unaligned(weight) || unaligned(dx) ||
+        unaligned(dweight) || unaligned(workspace) || unaligned(rstd, 4))
+      return MOE_ERR_ALIGN;
+    if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_NORM_BACKWARD)) return MOE_ERR_WORKSPACE;
+    if (T == 0) return dweight ? hip_status(zero_words(dweight, (size_t)s->hidden, stream)) : MOE_OK;
+    return hip_status(moe::launch_rmsnorm_bwd(s->dtype == MOE_F32, dy, dh, h, weight, rstd, T,
+                                              s->hidden, dx, dweight, (float*)workspace, stream));
+  } catch (...) {
+    return MOE_ERR_HIP;
+  }
+}
+
+// ------------------------------------------------------------------ scored routing
+namespace {
+int check_router(const moe_shape* s, const moe_router* r, moe::ScoreRule* rule) {
+  if (!r) return MOE_ERR_NULL;
+  if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return MOE_ERR_SHAPE;
+  if (r->groups < 1 || r->groups > 64 || s->experts % r->groups) return MOE_ERR_SHAPE;
+  const int per = s->experts / r->groups;
+  if (r->top_groups < 1 || r->top_groups > r->groups || s->top_k > r->top_groups * per)
+    return MOE_ERR_SHAPE;
+  if (r->group_top < 1 || r->group_top > 2 || r->group_top > per) return MOE_ERR_SHAPE;
+  if (r->renormalise != 0 && r->renormalise != 1) return MOE_ERR_SHAPE;
+  if (!std::isfinite(r->scale)) return MOE_ERR_SHAPE;
+  *rule = {r->score == MOE_SCORE_SIGMOID, r->groups, r->top_groups, r->group_top, r->renormalise, r->scale};
+  return MOE_OK;
+}
+}  // namespace
+
+int moe_route_scored(const moe_shape* s, const moe_router* router, const void* x,
+                     const float* w_router, const float* b_router, const float* balance,
+                     int32_t* topk_idx, float* topk_gate, int32_t* expert_count, float* logits,
+                     void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  try {
+    int st = check_shape(s);
+    if (st) return st;
+    moe::ScoreRule rule;
+    if ((st = check_router(s, router, &rule))) return st;
+    const int64_t T = s->tokens;
+    if (missing_tok(x, T) || !w_router || missing_tok(topk_idx, T) || missing_tok(topk_gate, T) ||
+        !expert_count || missing_tok(workspace, T))
+      return MOE_ERR_NULL;
+    if (unaligned(x) || unaligned(w_router) || unaligned(workspace)) return MOE_ERR_ALIGN;
+    if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_ROUTE)) return MOE_ERR_WORKSPACE;
+    if (T == 0) return hip_status(zero_words(expert_count, (size_t)s->experts, stream));
+    return hip_status(moe::launch_route_scored(x, s->dtype == MOE_F32, w_router, b_router, balance, rule,
+                                               T, s->hidden, s->experts, s->top_k, (float*)workspace,
+                                               topk_idx, topk_gate, expert_count, logits, stream));
+  } catch (...) {
+    return MOE_ERR_HIP;
+  }
+}
+
+int moe_route_scored_backward(const moe_shape* s, const moe_router* router, const float* dgate,
+                              const float* dlogits, const void* x, const float* w_router,
+                              const float* logits, const int32_t* topk_idx, const void* dx_in,
+                              void* dx, float* dw_router, float* db_router, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
+  try {
+    int st = check_shape(s);
+    if (st) return st;
+    moe::ScoreRule rule;
+    if ((st = check_router(s, router, &rule))) return st;
+    const int64_t T = s->tokens;
+    if (missing_tok(dgate, T) || missing_tok(x, T) || !w_router || missing_tok(logits, T) ||
+        missing_tok(topk_idx, T) || missing_tok(dx, T) || !dw_router || missing_tok(workspace, T))
+      return MOE_ERR_NULL;
+    if (unaligned(x) || unaligned(w_router) || unaligned(dx_in) || unaligned(dx) ||
+        unaligned(dw_router) || unaligned(workspace))
+      return MOE_ERR_ALIGN;
+    if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_ROUTE_BACKWARD)) return MOE_ERR_WORKSPACE;
+    if (T == 0) {
+      hipError_t err = zero_words(dw_router, (size_t)s->experts * s->hidden, stream);
+      if (err == hipSuccess && db_router) err = zero_words(db_router, (size_t)s->experts, stream);
+      return hip_status(err);
+    }
+    return hip_status(moe::launch_route_scored_bwd(
+        s->dtype == MOE_F32, rule, dgate, dlogits, x, w_router, logits, topk_idx, dx_in, T,
+        s->hidden, s->experts, s->top_k, dx, dw_router, db_router, workspace, stream));
+  } catch (...) {
+    return MOE_ERR_HIP;
+  }
+}
+
+int moe_backward_experts(const moe_shape* s, const void* dy, const int32_t* topk_idx,
+                         const float* topk_gate, const void* ring_x,
+                         const int32_t* expert_offset, const int32_t* copy_slot,
+                         const int32_t* slot_copy, int64_t ring_head, const void* saved_au,
+                         const void* w_gate, const void* w_up, const void* w_down, void* dx,
+                         void* dw_gate, void* dw_up, void* dw_down, float* dgate,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  try {
+    int st = check_shape(s);
+    if (st) return st;
+    if (s->dtype != MOE_BF16) return MOE_ERR_DTYPE;
+    if (s->hidden % 128 || s->ffn % 128) return MOE_ERR_SHAPE;   // 128 x 128 gradient tiles
+    const int64_t T = s->tokens;
+    if (missing_tok(dy, T) || missing_tok(topk_idx, T) || missing_tok(topk_gate, T) || !ring_x ||
+        !expert_offset || missing_tok(copy_slot, T) || !slot_copy || !saved_au || !w_gate ||
+        !w_up || !w_down || missing_tok(dx, T) || !dw_gate || !dw_up || !dw_down ||
+        missing_tok(dgate, T) || !workspace)
+      return MOE_ERR_NULL;
+    if (ring_head < 0 || ring_head >= s->capacity) return MOE_ERR_SHAPE;
+    if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_BACKWARD)) return MOE_ERR_WORKSPACE;
+    if (T == 0) {
+      const size_t wbytes = (size_t)s->experts * s->ffn * s->hidden * 2;
+      hipError_t err = zero_words(dw_gate, wbytes / 4, stream);
+      if (err == hipSuccess) err = zero_words(dw_up, wbytes / 4, stream);
+      if (err == hipSuccess) err = zero_words(dw_down, wbytes / 4, stream);
+      return hip_status(err);
+    }
+    return hip_status(moe::launch_backward(
+        dy, nullptr, nullptr, topk_idx, topk_gate, ring_x, expert_offset, copy_slot, slot_copy,
+        ring_head, s->capacity, saved_au, w_gate, w_up, w_down, T, s->hidden, s->experts, s->top_k,
+        s->ffn, dx, dw_gate, dw_up, dw_down, nullptr, dgate, workspace, stream));
+  } catch (...) {
+    return MOE_ERR_HIP;
+  }
+}
+
+// ------------------------------------------------------------------ FP8
+int moe_dispatch_q(const moe_shape* s, const uint8_t* x8, const uint8_t* x8_scale,
+                   const int32_t* topk_idx, int64_t ring_head, void* ring_x,
+                   uint8_t* ring_x_scale, int32_t* expert_offset, int32_t* copy_slot,
+                   int32_t* slot_copy, void* workspace, size_t workspace_bytes,
+                   hipStream_t stream) {
+  try {
+    int st = check_shape(s);
+    if (st) return st;
+    if (s->dtype != MOE_MXFP8 && s->dtype != MOE_FP8) return MOE_ERR_DTYPE;
+    const int64_t T = s->tokens;
+    if (missing_tok(x8, T) || missing_tok(x8_scale, T) || missing_tok(topk_idx, T) || !ring_x ||
+        !ring_x_scale || !expert_offset || missing_tok(copy_slot, T) || !slot_copy || !workspace)
+      return MOE_ERR_NULL;
+    if (unaligned(x8) || unaligned(ring_x) || unaligned(x8_scale, 4) || unaligned(ring_x_scale, 4))
+      return MOE_ERR_ALIGN;
+    if (ring_head < 0 || ring_head >= s->capacity) return MOE_ERR_SHAPE;
+    if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_DISPATCH)) return MOE_ERR_WORKSPACE;
+    if (T == 0) return hip_status(zero_words(expert_offset, (size_t)s->experts + 1, stream));
+    return hip_status(moe::launch_dispatch(
+        x8, 1, moe::RowForm::coded, (const uint32_t*)x8_scale, topk_idx, T, s->hidden, s->experts,
+        s->top_k, ring_head, s->capacity, ring_x, ring_x_scale, expert_offset, copy_slot, slot_copy,
+        workspace, stream));
+  } catch (...) {
+    return MOE_ERR_HIP;
+  }
+}
+
+int moe_quantize_fp8(const void* src_bf16, int64_t rows, int64_t cols, int row_block,
+                     uint8_t* codes, float* scales, hipStream_t stream) {
+  try {
+    if (row_block != 1 && row_block != 128) return MOE_ERR_SHAPE;
+    if (rows < 0 || cols <= 0 || cols % 128 || rows > ((int64_t)1 << 40) / cols) return MOE_ERR_SHAPE;
+    if (rows == 0) return MOE_OK;
+    if (!src_bf16 || !codes || !scales) return MOE_ERR_NULL;
+    if (unaligned(src_bf16) || unaligned(codes) || unaligned(scales, 4)) return MOE_ERR_ALIGN;
+    return hip_status(moe::launch_quantize_fp8(src_bf16, rows, cols, row_block, codes, scales, stream));
+  } catch (...) {
+    return MOE_ERR_HIP;
+  }
+}
+
+namespace {
+int check_matmul_fp8(int64_t M, int64_t N, int64_t K) {
+  const int64_t top = ((int64_t)1 << 31) - 1;
+  if (M < 0 || N < 0 || K <= 0 || K % 128 || M > top || N > top || K > top) return MOE_ERR_SHAPE;
+  if (M * K >= ((int64_t)1 << 32) || N * K >= ((int64_t)1 << 32) || M * N >= (int64_t)1 << 38)
+    return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+}  // namespace
+
+size_t moe_matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_matmul_fp8(M, N, K) != MOE_OK || M == 0 || N == 0) return 0;
+  return align256(moe::matmul_fp8_workspace_bytes(M, N, K));
+}
+
+int moe_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale,
+                   int64_t M, int64_t N, int64_t K, int out_dtype, void* out, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream) {
+  try {
+    int st = check_matmul_fp8(M, N, K);
+    if (st) return st;
+    if (out_dtype != MOE_BF16 && out_dtype != MOE_F32) return MOE_ERR_DTYPE;
+    if (M == 0 || N == 0) return MOE_OK;
+    const size_t need = moe_matmul_fp8_workspace_bytes(M, N, K);
+    if (!a || !a_scale || !w || !w_scale || !out || (need && !workspace)) return MOE_ERR_NULL;
+    if (unaligned(a) || unaligned(w) || unaligned(a_scale, 4) || unaligned(w_scale, 4) ||
+        unaligned(out, out_dtype == MOE_F32 ? 4 : 2) || unaligned(workspace))
+      return MOE_ERR_ALIGN;
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    return hip_status(moe::launch_matmul_fp8(a, a_scale, w, w_scale, M, N, K, out_dtype == MOE_F32, out,
+                                             workspace, stream));
   } catch (...) {
     return MOE_ERR_HIP;
   }

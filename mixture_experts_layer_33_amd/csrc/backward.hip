@@ -347,6 +347,9 @@ __global__ __launch_bounds__(DgShape<NWN>::NT, DgShape<NWN>::OCC) void dgrad_ker
 // ----------------------------------------------------------------------------- per token
 // dg of each copy (fixed-order sum of the column-tile partials), dl, and
 // dx[t] = sum_j (dX[copy_slot[t, j]] + dl_j W_r[e_j]) in ascending expert order.
+// EXPERTS: the experts' part alone, dx[t] = sum_j dX[copy_slot[t, j]], and dg itself in
+// dl_slot [T, k].
+template <bool EXPERTS>
 __global__ __launch_bounds__(256) void token_kernel(const int32_t* __restrict__ copy_slot,
                                                     const int32_t* __restrict__ topk_idx,
                                                     const float* __restrict__ gate,
@@ -370,11 +373,15 @@ __global__ __launch_bounds__(256) void token_kernel(const int32_t* __restrict__ 
       slot[tid] = s;
       ex[tid] = topk_idx[t * k + tid];
     }
-    const float S = wave_sum(g * dg);
-    if (tid < k) {
-      const float v = g * (dg - S);
-      dl[tid] = v;
-      dl_slot[s] = v;
+    if constexpr (EXPERTS) {
+      if (tid < k) dl_slot[t * k + tid] = dg;
+    } else {
+      const float S = wave_sum(g * dg);
+      if (tid < k) {
+        const float v = g * (dg - S);
+        dl[tid] = v;
+        dl_slot[s] = v;
+      }
     }
   }
   __syncthreads();
@@ -382,14 +389,15 @@ __global__ __launch_bounds__(256) void token_kernel(const int32_t* __restrict__ 
     float acc[8] = {};
     for (int j = 0; j < k; ++j) {
       const u32x4 w = ((const u32x4*)(dxc + slot[j] * d))[v];
-      const f32x4 r0 = *(const f32x4*)(w_r + (int64_t)ex[j] * d + v * 8);
-      const f32x4 r1 = *(const f32x4*)(w_r + (int64_t)ex[j] * d + v * 8 + 4);
-      const float l = dl[j];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         acc[2 * q] += lo_bf(w[q]);
         acc[2 * q + 1] += hi_bf(w[q]);
       }
+      if constexpr (EXPERTS) continue;
+      const f32x4 r0 = *(const f32x4*)(w_r + (int64_t)ex[j] * d + v * 8);
+      const f32x4 r1 = *(const f32x4*)(w_r + (int64_t)ex[j] * d + v * 8 + 4);
+      const float l = dl[j];
       acc[0] = fmaf(l, r0[0], acc[0]); acc[1] = fmaf(l, r0[1], acc[1]);
       acc[2] = fmaf(l, r0[2], acc[2]); acc[3] = fmaf(l, r0[3], acc[3]);
       acc[4] = fmaf(l, r1[0], acc[4]); acc[5] = fmaf(l, r1[1], acc[5]);
@@ -763,7 +771,7 @@ hipError_t launch_backward(const void* dy, const void* x, const float* w_r,
                            const int32_t* slot_copy, int64_t head, int64_t C, const void* saved_au,
                            const void* w_gate, const void* w_up, const void* w_down, int64_t T,
                            int d, int E, int k, int f, void* dx, void* dw_gate, void* dw_up,
-                           void* dw_down, float* dw_r, void* ws, hipStream_t st) {
+                           void* dw_down, float* dw_r, float* dgate, void* ws, hipStream_t st) {
   (void)x;
   if (d % BT || f % BT) return hipErrorInvalidValue;
   const BwdLayout L = bwd_layout(T, C, d, E, k, f);
@@ -834,14 +842,19 @@ hipError_t launch_backward(const void* dy, const void* x, const float* w_r,
   else
     dgrad_kernel<false, 2><<<(unsigned)(8 * (((int64_t)max_tiles * (d / BT) + 7) / 8)), DgShape<2>::NT,
                              DgShape<2>::LDS, st>>>(b);
-  token_kernel<<<(unsigned)T, 256, 0, st>>>(copy_slot, topk_idx, topk_gate, dgpart, f / dg_cols, dxc,
-                                            w_r, d, k, dl, (bf16_t*)dx);
-  float* rpart = (float*)(w + L.rpart);
-  int32_t* rfirst = (int32_t*)(w + L.rfirst);
-  router_wgrad_part_kernel<<<dim3(max_tiles, (d / 8 + 127) / 128), 128, 0, st>>>(
-      tiles, ntiles, expert_offset, head, C, (const bf16_t*)ring_x, dl, d, rpart, rfirst, nullptr, 1);
-  router_wgrad_sum_kernel<<<dim3(E, (d / 4 + 255) / 256), 256, 0, st>>>(expert_offset, rfirst,
-                                                                        rpart, d, dw_r);
+  if (dgate) {
+    token_kernel<true><<<(unsigned)T, 256, 0, st>>>(copy_slot, topk_idx, topk_gate, dgpart, f / dg_cols,
+                                                    dxc, nullptr, d, k, dgate, (bf16_t*)dx);
+  } else {
+    token_kernel<false><<<(unsigned)T, 256, 0, st>>>(copy_slot, topk_idx, topk_gate, dgpart, f / dg_cols,
+                                                     dxc, w_r, d, k, dl, (bf16_t*)dx);
+    float* rpart = (float*)(w + L.rpart);
+    int32_t* rfirst = (int32_t*)(w + L.rfirst);
+    router_wgrad_part_kernel<<<dim3(max_tiles, (d / 8 + 127) / 128), 128, 0, st>>>(
+        tiles, ntiles, expert_offset, head, C, (const bf16_t*)ring_x, dl, d, rpart, rfirst, nullptr, 1);
+    router_wgrad_sum_kernel<<<dim3(E, (d / 4 + 255) / 256), 256, 0, st>>>(expert_offset, rfirst,
+                                                                          rpart, d, dw_r);
+  }
   WgradArgs wd{};
   wd.A = rdy;
   wd.B = gh;
@@ -1233,7 +1246,7 @@ hipError_t launch_backward_mx(const void* dy, const void* x, const float* w_r,
   g2.out = (uint8_t*)dxc;
   g2.b_rows = (int64_t)E * d;
   if ((err = launch_mx_plain_gemm128(g2, n, E, false, st)) != hipSuccess) return err;
-  token_kernel<<<(unsigned)T, 256, 0, st>>>(copy_slot, topk_idx, topk_gate, dg, 1, dxc, w_r, d,
+  token_kernel<false><<<(unsigned)T, 256, 0, st>>>(copy_slot, topk_idx, topk_gate, dg, 1, dxc, w_r, d,
                                             k, dl, (bf16_t*)dx);
   float* rpart = (float*)(w + L.rpart);
   int32_t* rfirst = (int32_t*)(w + L.rfirst);

@@ -14,6 +14,7 @@
 //      slots (MX: quantised once, codes and scales written k times).
 #include "common.h"
 #include "dispatch_body.h"
+#include "fp8.h"
 #include "kernels.h"
 
 namespace moe {
@@ -120,22 +121,79 @@ __global__ __launch_bounds__(256) void dispatch_mx_kernel(
   }
 }
 
+// FP8: a block of 128 columns is held by 16 consecutive lanes; quantised once per token.
+__global__ __launch_bounds__(256) void dispatch_fp8_kernel(
+    const bf16_t* __restrict__ x, const int32_t* __restrict__ idx,
+    const unsigned long long* __restrict__ masks, const int32_t* __restrict__ base, int k, int E,
+    int64_t head, int64_t C, int d, uint8_t* __restrict__ ring, float* __restrict__ ring_scale,
+    int32_t* __restrict__ copy_slot, int32_t* __restrict__ slot_copy) {
+  __shared__ int64_t slots[64];
+  const int64_t t = blockIdx.x;
+  copy_slots(idx, masks, base, t, k, E, head, C, copy_slot, slot_copy, slots);
+  const int nv = d / 8;
+  for (int v0 = 0; v0 < nv; v0 += 256) {   // uniform trip count: all lanes join the maxima
+    const int v = v0 + threadIdx.x;
+    const bool ok = v < nv;
+    const u32x4 w = ok ? ((const u32x4*)(x + t * d))[v] : u32x4{0, 0, 0, 0};
+    float f[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) { f[2 * q] = lo_bf(w[q]); f[2 * q + 1] = hi_bf(w[q]); }
+    const float s = fp8_scale(block_amax<16>(f));
+    const u32x2 c = fp8_encode8(f, s);
+    if (ok)
+      for (int j = 0; j < k; ++j) {
+        *(u32x2*)(ring + slots[j] * d + (int64_t)v * 8) = c;
+        if ((v & 15) == 0) ring_scale[(int64_t)(v / 16) * C + slots[j]] = s;
+      }
+  }
+}
+
+// 8-bit rows as they are, and their scale words (one per 128 columns: FP8's float, or the four
+// E8M0 bytes of MX), [d / 128][T] to [d / 128][C].
+__global__ __launch_bounds__(256) void dispatch_coded_kernel(
+    const uint8_t* __restrict__ x, const uint32_t* __restrict__ x_scale, int64_t T,
+    const int32_t* __restrict__ idx, const unsigned long long* __restrict__ masks,
+    const int32_t* __restrict__ base, int k, int E, int64_t head, int64_t C, int d,
+    uint8_t* __restrict__ ring, uint32_t* __restrict__ ring_scale, int32_t* __restrict__ copy_slot,
+    int32_t* __restrict__ slot_copy) {
+  __shared__ int64_t slots[64];
+  const int64_t t = blockIdx.x;
+  copy_slots(idx, masks, base, t, k, E, head, C, copy_slot, slot_copy, slots);
+  for (int v = threadIdx.x; v < d / 16; v += 256) {
+    const u32x4 w = ((const u32x4*)(x + t * d))[v];
+    for (int j = 0; j < k; ++j) ((u32x4*)(ring + slots[j] * d))[v] = w;
+  }
+  for (int b = threadIdx.x; b < d / 128; b += 256) {
+    const uint32_t s = x_scale[b * T + t];
+    for (int j = 0; j < k; ++j) ring_scale[b * C + slots[j]] = s;
+  }
+}
+
 size_t dispatch_workspace_bytes(int64_t T, int E) {
   const int64_t nch = (T + DCH - 1) / DCH;
   return (size_t)nch * E * (sizeof(unsigned long long) + sizeof(int32_t));
 }
 
-hipError_t launch_dispatch(const void* x, int elem_bytes, bool mx, const int32_t* topk_idx,
-                           int64_t T, int d, int E, int k, int64_t head, int64_t C, void* ring_x,
-                           uint8_t* ring_scale, int32_t* expert_offset, int32_t* copy_slot,
-                           int32_t* slot_copy, void* ws, hipStream_t st) {
+hipError_t launch_dispatch(const void* x, int elem_bytes, RowForm form, const uint32_t* x_scale,
+                           const int32_t* topk_idx, int64_t T, int d, int E, int k, int64_t head,
+                           int64_t C, void* ring_x, uint8_t* ring_scale, int32_t* expert_offset,
+                           int32_t* copy_slot, int32_t* slot_copy, void* ws, hipStream_t st) {
   const int64_t nch = (T + DCH - 1) / DCH;
   unsigned long long* masks = (unsigned long long*)ws;
   int32_t* base = (int32_t*)(masks + nch * E);
   dispatch_hist_kernel<<<(unsigned)nch, 64, E * sizeof(unsigned long long), st>>>(
       topk_idx, T, k, E, masks, base);
   dispatch_scan_kernel<<<1, 1024, 0, st>>>(base, (int)nch, E, expert_offset);
-  if (mx)
+  if (form == RowForm::fp8)
+    dispatch_fp8_kernel<<<(unsigned)T, 256, 0, st>>>((const bf16_t*)x, topk_idx, masks, base, k, E,
+                                                     head, C, d, (uint8_t*)ring_x,
+                                                     (float*)ring_scale, copy_slot, slot_copy);
+  else if (form == RowForm::coded)
+    dispatch_coded_kernel<<<(unsigned)T, 256, 0, st>>>((const uint8_t*)x, x_scale, T, topk_idx,
+                                                       masks, base, k, E, head, C, d,
+                                                       (uint8_t*)ring_x, (uint32_t*)ring_scale,
+                                                       copy_slot, slot_copy);
+  else if (form == RowForm::mx)
     dispatch_mx_kernel<<<(unsigned)T, 256, 0, st>>>((const bf16_t*)x, topk_idx, masks, base, k, E,
                                                     head, C, d, (uint8_t*)ring_x, ring_scale,
                                                     copy_slot, slot_copy);

@@ -1,0 +1,316 @@
+// FP8 with one scale per block of 128: the quantiser, the dense product and the experts'
+// grouped products.
+//
+//   C[m,n] = sum_b a_scale[b][m] w_scale[n/128][b] sum_{i in block b} a[m,i] w[n,i]
+//
+// A block's 128 products are summed by the matrix cores without a scale; the block's two scales
+// then multiply that partial sum on its way into the fp32 accumulator.  The weight rows are the
+// MFMA's first operand, so that a lane's results all belong to one token row: its row scale
+// is one register, the weight scale is uniform over a wavefront, and one product of the two
+// serves every result of the block.
+//
+// Rounding inside the 8-bit MFMA (probed on gfx950 with single products): the products of eight
+// consecutive bytes of a lane are added on a grid of 2^-13 of the largest one's binade, what lies
+// below is cut off; these sums of eight are added in fp32.  On normal data that is 1.4e-5 of
+// the result, far below a bf16 output's own half step (2e-3) and H's 8 bits, which is why
+// the full fp8 rate is taken there.  An fp32 output asks for more: its codes are widened to
+// bf16 (every E4M3 value is a bf16 value) and multiplied by the bf16 MFMA, whose sums are fp32
+// (error against fp64 5e-7), at half the rate.
+#include <algorithm>
+
+#include "common.h"
+#include "fp8.h"
+#include "gemm_body.h"
+#include "kernels.h"
+
+namespace moe {
+
+// ----------------------------------------------------------------------------- quantiser
+// One block of 128 columns of a row sits in 16 consecutive lanes (8 bf16 each).
+__global__ __launch_bounds__(256) void quantize_fp8_rows_kernel(const bf16_t* __restrict__ src, int64_t rows,
+                                                                int64_t cols, uint8_t* __restrict__ codes,
+                                                                float* __restrict__ scales) {
+  const int64_t vpr = cols / 8, nvec = rows * vpr, stride = (int64_t)gridDim.x * 256;
+  for (int64_t v0 = (int64_t)blockIdx.x * 256; v0 < nvec; v0 += stride) {
+    const int64_t v = v0 + threadIdx.x;
+    const bool ok = v < nvec;   // whole blocks of 16 lanes: nvec is a multiple of 16
+    const u32x4 w = ok ? ((const u32x4*)src)[v] : u32x4{0, 0, 0, 0};
+    float f[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) { f[2 * q] = lo_bf(w[q]); f[2 * q + 1] = hi_bf(w[q]); }
+    const float s = fp8_scale(block_amax<16>(f));
+    const u32x2 c = fp8_encode8(f, s);
+    if (ok) {
+      ((u32x2*)codes)[v] = c;
+      if ((v & 15) == 0) scales[((v % vpr) / 16) * rows + v / vpr] = s;
+    }
+  }
+}
+
+// One workgroup per 128 x 128 block: thread q holds rows
+// q / 16 + 16 i, i < 8, columns 8 (q % 16) .. + 7.
+__global__ __launch_bounds__(256) void quantize_fp8_blocks_kernel(const bf16_t* __restrict__ src, int64_t rows,
+                                                                  int64_t cols, uint8_t* __restrict__ codes,
+                                                                  float* __restrict__ scales) {
+  __shared__ float red[4];
+  const int64_t nb = cols / 128, rb = blockIdx.x / nb, cb = blockIdx.x % nb;
+  const int tid = threadIdx.x;
+  const int64_t r0 = rb * 128 + tid / 16, c0 = cb * 128 + (tid & 15) * 8;
+  u32x4 w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i] = r0 + 16 * i < rows ? *(const u32x4*)(src + (r0 + 16 * i) * cols + c0) : u32x4{0, 0, 0, 0};
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) a = amax2(amax2(a, lo_bf(w[i][q])), hi_bf(w[i][q]));
+  a = lanes_amax<64>(a);
+  if ((tid & 63) == 0) red[tid >> 6] = a;
+  __syncthreads();
+  const float s = fp8_scale(amax2(amax2(red[0], red[1]), amax2(red[2], red[3])));
+  if (tid == 0) scales[rb * nb + cb] = s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (r0 + 16 * i < rows) {
+      const float f[8] = {lo_bf(w[i][0]), hi_bf(w[i][0]), lo_bf(w[i][1]), hi_bf(w[i][1]),
+                          lo_bf(w[i][2]), hi_bf(w[i][2]), lo_bf(w[i][3]), hi_bf(w[i][3])};
+      *(u32x2*)(codes + (r0 + 16 * i) * cols + c0) = fp8_encode8(f, s);
+    }
+}
+
+hipError_t launch_quantize_fp8(const void* src, int64_t rows, int64_t cols, int row_block,
+                               uint8_t* codes, float* scales, hipStream_t st) {
+  if (row_block == 1) {
+    const int64_t wgs = (rows * (cols / 8) + 255) / 256;
+    quantize_fp8_rows_kernel<<<(unsigned)std::min<int64_t>(wgs, 65536), 256, 0, st>>>(
+        (const bf16_t*)src, rows, cols, codes, scales);
+  } else {
+    quantize_fp8_blocks_kernel<<<(unsigned)(((rows + 127) / 128) * (cols / 128)), 256, 0, st>>>(
+        (const bf16_t*)src, rows, cols, codes, scales);
+  }
+  return hipGetLastError();
+}
+
+// ----------------------------------------------------------------------------- products
+struct Fp8Args {
+  const uint8_t* A;        // token rows [C, K] codes
+  const float* As;         // [K/128][a_rows]
+  const uint8_t* W0;       // [E, N, K]
+  const uint8_t* W1;       // SWIGLU: the up weights
+  const float* S0;         // [E][ceil(N/128)][K/128]
+  const float* S1;
+  int64_t a_rows;
+  int K, N;
+  const int32_t* offset;   // ring segments; NULL: one product of all a_rows rows
+  const int32_t* tiles;
+  const int32_t* ntiles;
+  int64_t head, C;
+  void* out;               // SWIGLU: H codes [C, N]; else bf16 or fp32 [C, N]
+  float* out_scale;        // SWIGLU: [N/128][C]
+  bf16_t* saved_au;        // SWIGLU: [C, 2N] or NULL
+};
+
+// Lane l's 32 bytes of row `r`'s block b: bytes 32 (l / 16) .. + 31.  (Which of the block's 128
+// positions a lane's byte is does not matter as long as both operands agree.)
+__device__ __forceinline__ i32x8 fp8_frag(const uint8_t* p) {
+  const u32x4 a = *(const u32x4*)p, b = *(const u32x4*)(p + 16);
+  return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+__device__ __forceinline__ f32x4 fp8_mfma16(i32x8 w, i32x8 a) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// The same sum on the bf16 MFMA: the 32 codes of a lane in four steps of 8.
+__device__ __forceinline__ bf16x8 fp8_widen8(int lo, int hi) {
+  union {
+    __bf16 __attribute__((ext_vector_type(2))) p[4];
+    bf16x8 v;
+  } o;
+  o.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  o.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  o.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  o.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return o.v;
+}
+__device__ __forceinline__ f32x4 fp8_wide16(i32x8 w, i32x8 a) {
+  f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8_widen8(w[2 * q], w[2 * q + 1]),
+                                                fp8_widen8(a[2 * q], a[2 * q + 1]), c, 0, 0, 0);
+  return c;
+}
+
+// 16 token rows per tile; 8 wavefronts of 16 weight rows (SWIGLU: 16 gate and 16 up rows), so a
+// workgroup covers one block of 128 output columns and a SWIGLU tile holds whole H blocks.
+// Result i of lane l: output column n0 + 16 wave + 4 (l / 16) + i of token row l % 16.
+template <bool SWIGLU, bool F32>
+__global__ __launch_bounds__(512) void fp8_rows16_kernel(Fp8Args p) {
+  __shared__ float hmax[8][16];
+  const int nct = (p.N + 127) / 128;
+  const int mt = blockIdx.x / nct, ct = blockIdx.x % nct;
+  int e = 0, row0 = 16 * mt, rows;
+  int64_t seg = 0;
+  if (p.offset) {
+    if (mt >= *p.ntiles) return;
+    e = p.tiles[2 * mt];
+    row0 = p.tiles[2 * mt + 1];
+    seg = p.offset[e];
+    rows = min(16, p.offset[e + 1] - (int)seg - row0);
+  } else {
+    rows = (int)min((int64_t)16, p.a_rows - row0);
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
+  const int KB = p.K / 128;
+  const int64_t slot = ring_slot(p.head, seg, row0 + min(m, rows - 1), p.C);
+  const uint8_t* a = p.A + slot * p.K + g * 32;
+  const float* as = p.As + slot;
+  const int64_t wrow = (int64_t)e * p.N + min(128 * ct + 16 * wave + m, p.N - 1);
+  const uint8_t* w0 = p.W0 + wrow * p.K + g * 32;
+  const uint8_t* w1 = SWIGLU ? p.W1 + wrow * p.K + g * 32 : nullptr;
+  const float* s0 = p.S0 + ((int64_t)e * nct + ct) * KB;
+  const float* s1 = SWIGLU ? p.S1 + ((int64_t)e * nct + ct) * KB : nullptr;
+  f32x4 c0 = {0.f, 0.f, 0.f, 0.f}, c1 = c0;
+#pragma unroll 4
+  for (int b = 0; b < KB; ++b) {
+    const i32x8 av = fp8_frag(a + (int64_t)b * 128);
+    const float sa = as[b * p.a_rows];
+    const i32x8 wv = fp8_frag(w0 + (int64_t)b * 128);
+    const f32x4 q0 = F32 ? fp8_wide16(wv, av) : fp8_mfma16(wv, av);
+    const float t0 = sa * s0[b];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c0[i] = fmaf(q0[i], t0, c0[i]);
+    if constexpr (SWIGLU) {
+      const f32x4 q1 = fp8_mfma16(fp8_frag(w1 + (int64_t)b * 128), av);
+      const float t1 = sa * s1[b];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c1[i] = fmaf(q1[i], t1, c1[i]);
+    }
+  }
+  const int col = 128 * ct + 16 * wave + 4 * g;
+  if constexpr (SWIGLU) {
+    float h[4], am = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = silu(c0[i]) * c1[i];
+      am = amax2(am, h[i]);
+    }
+    am = amax2(am, __shfl_xor(am, 16, 64));
+    am = amax2(am, __shfl_xor(am, 32, 64));
+    if (g == 0) hmax[wave][m] = am;
+    __syncthreads();
+    am = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) am = amax2(am, hmax[w][m]);
+    const float s = fp8_scale(am);
+    if (m < rows) {
+      *(uint32_t*)((uint8_t*)p.out + slot * p.N + col) = fp8_encode4(h[0], h[1], h[2], h[3], s);
+      if (wave == 0 && g == 0) p.out_scale[(int64_t)ct * p.C + slot] = s;
+      if (p.saved_au) {
+        *(u32x2*)(p.saved_au + slot * 2 * p.N + col) = u32x2{pack_bf2(c0[0], c0[1]), pack_bf2(c0[2], c0[3])};
+        *(u32x2*)(p.saved_au + (slot * 2 + 1) * p.N + col) = u32x2{pack_bf2(c1[0], c1[1]), pack_bf2(c1[2], c1[3])};
+      }
+    }
+  } else if (m < rows) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col + i < p.N) {
+        if constexpr (F32) ((float*)p.out)[slot * p.N + col + i] = c0[i];
+        else ((bf16_t*)p.out)[slot * p.N + col + i] = f2bf(c0[i]);
+      }
+  }
+}
+
+// ----------------------------------------------------------------------------- launchers
+size_t matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  (void)M; (void)N; (void)K;
+  return 0;
+}
+
+hipError_t launch_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w,
+                             const float* w_scale, int64_t M, int64_t N, int64_t K, bool f32_out,
+                             void* out, void* ws, hipStream_t st) {
+  (void)ws;
+  Fp8Args p{};
+  p.A = a;
+  p.As = a_scale;
+  p.W0 = w;
+  p.S0 = w_scale;
+  p.a_rows = M;
+  p.C = M;
+  p.K = (int)K;
+  p.N = (int)N;
+  p.out = out;
+  const unsigned grid = (unsigned)(((M + 15) / 16) * ((N + 127) / 128));
+  if (f32_out) fp8_rows16_kernel<false, true><<<grid, 512, 0, st>>>(p);
+  else fp8_rows16_kernel<false, false><<<grid, 512, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+struct FfnFp8Layout {
+  size_t tiles, h, hs, total;
+};
+static FfnFp8Layout ffn_fp8_layout(int64_t n, int64_t C, int E, int f) {
+  auto al = [](size_t b) { return (b + 255) & ~(size_t)255; };
+  FfnFp8Layout L;
+  size_t o = 0;
+  L.tiles = o; o += al((size_t)(2 * max_tiles_for(n, E, 16) + 64) * 4);
+  L.h = o; o += al((size_t)C * f);
+  L.hs = o; o += al((size_t)C * (f / 128) * 4);
+  L.total = o;
+  return L;
+}
+size_t ffn_fp8_workspace_bytes(int64_t n, int64_t C, int E, int f) { return ffn_fp8_layout(n, C, E, f).total; }
+
+hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const int32_t* expert_offset,
+                          int64_t head, int64_t C, int64_t n, int d, int E, int f,
+                          const void* w_gate, const void* w_up, const void* w_down,
+                          const float* sg, const float* su, const float* sd, void* ring_y,
+                          void* saved_au, void* ws, hipEvent_t* events, hipStream_t st) {
+  const FfnFp8Layout L = ffn_fp8_layout(n, C, E, f);
+  uint8_t* w = (uint8_t*)ws;
+  int32_t* ntiles = (int32_t*)(w + L.tiles);
+  int32_t* tiles = ntiles + 64;
+  auto mark = [&](int i) { return events ? hipEventRecord(events[i], st) : hipSuccess; };
+  hipError_t err = launch_build_tiles(expert_offset, E, 16, tiles, ntiles, st);
+  if (err != hipSuccess || (err = mark(0)) != hipSuccess) return err;
+  const int mt = max_tiles_for(n, E, 16);
+  Fp8Args p{};
+  p.A = (const uint8_t*)ring_x;
+  p.As = ring_x_scale;
+  p.W0 = (const uint8_t*)w_gate;
+  p.W1 = (const uint8_t*)w_up;
+  p.S0 = sg;
+  p.S1 = su;
+  p.a_rows = C;
+  p.K = d;
+  p.N = f;
+  p.offset = expert_offset;
+  p.tiles = tiles;
+  p.ntiles = ntiles;
+  p.head = head;
+  p.C = C;
+  p.out = w + L.h;
+  p.out_scale = (float*)(w + L.hs);
+  p.saved_au = (bf16_t*)saved_au;
+  fp8_rows16_kernel<true, false><<<(unsigned)((int64_t)mt * (f / 128)), 512, 0, st>>>(p);
+  if ((err = hipGetLastError()) != hipSuccess || (err = mark(1)) != hipSuccess) return err;
+  Fp8Args q = p;
+  q.A = w + L.h;
+  q.As = p.out_scale;
+  q.W0 = (const uint8_t*)w_down;
+  q.W1 = nullptr;
+  q.S0 = sd;
+  q.S1 = nullptr;
+  q.K = f;
+  q.N = d;
+  q.out = ring_y;
+  q.out_scale = nullptr;
+  q.saved_au = nullptr;
+  fp8_rows16_kernel<false, false><<<(unsigned)((int64_t)mt * (d / 128)), 512, 0, st>>>(q);
+  if ((err = hipGetLastError()) != hipSuccess) return err;
+  return mark(2);
+}
+
+}  // namespace moe

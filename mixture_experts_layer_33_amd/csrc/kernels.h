@@ -12,13 +12,59 @@ size_t route_workspace_bytes(int64_t T, int E, int d);
 hipError_t launch_route(const void* x, bool x_f32, const float* w_r, const float* b_r, int64_t T,
                         int d, int E, int k, float* logits, int32_t* topk_idx, float* topk_gate,
                         int32_t* expert_count, hipStream_t st);
+// the logits alone: *ks partial planes [*ks, T, E] (without the bias)
+hipError_t launch_router_logits(const void* x, bool x_f32, const float* w_r, int64_t T, int d, int E,
+                                float* planes, int* ks, hipStream_t st);
 
-// dispatch (elem_bytes: 4 f32, 2 bf16; mx: quantise bf16 rows to E4M3 + E8M0)
+// scored routing
+struct ScoreRule {
+  int sigmoid, groups, top_groups, group_top, renormalise;
+  float scale;
+};
+hipError_t launch_route_scored(const void* x, bool x_f32, const float* w_r, const float* b_r,
+                               const float* balance, const ScoreRule& rule, int64_t T, int d, int E,
+                               int k, float* planes, int32_t* topk_idx, float* topk_gate,
+                               int32_t* count, float* logits, hipStream_t st);
+size_t route_scored_bwd_workspace_bytes(int64_t T, int E, int d);
+hipError_t launch_route_scored_bwd(bool f32, const ScoreRule& rule, const float* dgate,
+                                   const float* dlogits, const void* x, const float* w_r,
+                                   const float* logits, const int32_t* topk_idx, const void* dx_in,
+                                   int64_t T, int d, int E, int k, void* dx, float* dw, float* db,
+                                   void* ws, hipStream_t st);
+
+// residual RMS norm (q: 8-bit output, 0 none, 1 FP8, 2 MX)
+hipError_t launch_add_rmsnorm(bool f32, int q, const void* x, const void* residual, const float* w,
+                              float eps, int64_t T, int d, void* h, void* y, uint8_t* y8,
+                              void* y8_scale, float* rstd, hipStream_t st);
+size_t norm_bwd_workspace_bytes(int64_t T, int d);
+hipError_t launch_rmsnorm_bwd(bool f32, const void* dy, const void* dh, const void* h, const float* w,
+                              const float* rstd, int64_t T, int d, void* dx, float* dw, float* part,
+                              hipStream_t st);
+// out[c] = sum over g < G of part[g, c], c < d
+hipError_t launch_column_sum(const float* part, int G, int64_t d, float* out, hipStream_t st);
+
+// dispatch.  Rows as they are (elem_bytes 4, 2), bf16 rows quantised to MX or FP8, or 8-bit
+// rows with their scale words x_scale [d/128][T] as they are
+enum class RowForm { plain, mx, fp8, coded };
 size_t dispatch_workspace_bytes(int64_t T, int E);
-hipError_t launch_dispatch(const void* x, int elem_bytes, bool mx, const int32_t* topk_idx,
-                           int64_t T, int d, int E, int k, int64_t head, int64_t C, void* ring_x,
-                           uint8_t* ring_scale, int32_t* expert_offset, int32_t* copy_slot,
-                           int32_t* slot_copy, void* ws, hipStream_t st);
+hipError_t launch_dispatch(const void* x, int elem_bytes, RowForm form, const uint32_t* x_scale,
+                           const int32_t* topk_idx, int64_t T, int d, int E, int k, int64_t head,
+                           int64_t C, void* ring_x, uint8_t* ring_scale, int32_t* expert_offset,
+                           int32_t* copy_slot, int32_t* slot_copy, void* ws, hipStream_t st);
+
+// FP8, one scale per block of 128
+hipError_t launch_quantize_fp8(const void* src, int64_t rows, int64_t cols, int row_block,
+                               uint8_t* codes, float* scales, hipStream_t st);
+size_t matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w,
+                             const float* w_scale, int64_t M, int64_t N, int64_t K, bool f32_out,
+                             void* out, void* ws, hipStream_t st);
+size_t ffn_fp8_workspace_bytes(int64_t n, int64_t C, int E, int f);
+hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const int32_t* expert_offset,
+                          int64_t head, int64_t C, int64_t n, int d, int E, int f,
+                          const void* w_gate, const void* w_up, const void* w_down,
+                          const float* sg, const float* su, const float* sd, void* ring_y,
+                          void* saved_au, void* ws, hipEvent_t* events, hipStream_t st);
 
 // expert FFN (grouped GEMMs)
 // tiles[2i] = expert, tiles[2i+1] = first segment row of row-tile i (height BM); *ntiles = count
@@ -67,7 +113,8 @@ hipError_t launch_backward(const void* dy, const void* x, const float* w_r,
                            const int32_t* slot_copy, int64_t head, int64_t C, const void* saved_au,
                            const void* w_gate, const void* w_up, const void* w_down, int64_t T,
                            int d, int E, int k, int f, void* dx, void* dw_gate, void* dw_up,
-                           void* dw_down, float* dw_r, void* ws, hipStream_t st);
+                           void* dw_down, float* dw_r, float* dgate, void* ws, hipStream_t st);
+// (dgate: NULL, or the gates' gradient [T, k] in place of the router's part: w_r and dw_r unused)
 
 // MX quantisation of a bf16 matrix along its rows
 hipError_t launch_quantize_mx(const void* src, int64_t rows, int64_t cols, uint8_t* codes,

@@ -232,10 +232,10 @@ size_t route_workspace_bytes(int64_t T, int E, int d) {
   return logits_bytes(T, E, d);
 }
 
-hipError_t launch_route(const void* x, bool x_f32, const float* w_r, const float* b_r, int64_t T,
-                        int d, int E, int k, float* logits, int32_t* topk_idx, float* topk_gate,
-                        int32_t* expert_count, hipStream_t st) {
-  int ks = 1;
+hipError_t launch_router_logits(const void* x, bool x_f32, const float* w_r, int64_t T, int d, int E,
+                                float* logits, int* planes, hipStream_t st) {
+  int& ks = *planes;
+  ks = 1;
   if (x_f32) {
     dim3 g1((E + RT_N - 1) / RT_N, (unsigned)((T + RT_M - 1) / RT_M));
     router_logits_kernel<true><<<g1, 256, 0, st>>>(x, w_r, logits, T, d, E);
@@ -253,6 +253,15 @@ hipError_t launch_route(const void* x, bool x_f32, const float* w_r, const float
                                256, 0, st>>>((const bf16_t*)x, w_r, logits, T, d, E);
     }
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_route(const void* x, bool x_f32, const float* w_r, const float* b_r, int64_t T,
+                        int d, int E, int k, float* logits, int32_t* topk_idx, float* topk_gate,
+                        int32_t* expert_count, hipStream_t st) {
+  int ks = 1;
+  hipError_t err = launch_router_logits(x, x_f32, w_r, T, d, E, logits, &ks, st);
+  if (err != hipSuccess) return err;
   const unsigned g2 = (unsigned)((T + 3) / 4);
   const int vpl = (E + 63) / 64;
 #define TOPK(V)                                                                                   \

@@ -1,0 +1,443 @@
+"""GPU: FP8 with one scale per block of 128: quantiser, dense product, the experts' products and the
+layer, against the fp64 oracle.
+
+Tolerances of a product.  E4M3 products are exact in fp32; a block's 128 are summed in fp32 (at most 128
+steps), multiplied by a product of two scales (two steps) and added to the K / 128 blocks before:
+(132 + K / 128) 2^-24 of the sum of the terms' sizes, then the output's own rounding.  A bf16
+output comes from the 8-bit matrix instruction, which adds the products of eight consecutive
+positions on a grid of 2^-13 of the largest one's binade and cuts off what lies below it: each of
+the other seven loses less than 2^-13 of the largest product, 7 * 2^-13 max |a| max |w| for
+every eight positions in all (the maxima taken over the eight)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_33_amd as moe
+import oracle
+from oracle import ops
+from ops_util import DEV, HALF, codes, gen, host, randn, same_bits, within
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+# ----------------------------------------------------------------------------- quantiser
+@pytest.mark.parametrize("rows,cols", [(1, 128), (3, 256), (127, 128), (128, 384), (129, 256), (300, 640)])
+@pytest.mark.parametrize("row_block", [1, 128])
+def test_quantiser(rows, cols, row_block):
+    """The scale is one division of a bf16 maximum (half a step); a code may differ from the
+    oracle's only where the quotient, one step off, crosses a rounding border."""
+    print(f"\n[case] quantize_fp8 {rows}x{cols} {row_block}", flush=True)
+    x = randn(gen(rows), rows, cols, dtype=BF)
+    x[0, :128] = 0
+    x[-1, -128:] *= 2.0 ** 90
+    q, s = moe.quantize_fp8(x, row_block)
+    torch.cuda.synchronize()
+    X = host(x)
+    want_q, want_s = (ops.quantise_rows if row_block == 1 else ops.quantise_blocks)(X)
+    got_s = host(s).T if row_block == 1 else host(s)
+    within(got_s, want_s, HALF[torch.float32] * want_s, "scales")
+    spread = ops.spread_rows if row_block == 1 else ops.spread_blocks
+    one = spread(np.ones_like(X), got_s)
+    within(spread(codes(q), got_s), X, (2.0 ** -4 + 2.0 ** -22) * abs(X) + 2.0 ** -9.9 * one, "values")
+    assert (codes(q) != want_q).mean() < 1e-3
+
+
+@pytest.mark.parametrize("row_block", [1, 128])
+def test_quantiser_of_broken_blocks(row_block):
+    print(f"\n[case] quantize_fp8 NaN {row_block}", flush=True)
+    x = randn(gen(1), 256, 256, dtype=BF)
+    clean, cs = moe.quantize_fp8(x, row_block)
+    y = x.clone()
+    y[5, 3], y[200, 130] = float("nan"), -float("inf")
+    q, s = moe.quantize_fp8(y, row_block)
+    torch.cuda.synchronize()
+    bad = torch.isnan(s)
+    assert int(bad.sum()) == 2 and torch.equal(s[~bad], cs[~bad])
+    assert bool(bad[0, 5] and bad[1, 200]) if row_block == 1 else bool(bad[0, 0] and bad[1, 1])
+
+
+def test_quantiser_of_a_stack_and_of_nothing():
+    print("\n[case] quantize_fp8 stack", flush=True)
+    w = randn(gen(2), 3, 256, 384, dtype=BF)
+    q, s = moe.quantize_fp8(w)
+    assert q.shape == w.shape and s.shape == (3, 2, 3)
+    for e in range(3):
+        qe, se = moe.quantize_fp8(w[e].contiguous())
+        assert torch.equal(q[e], qe) and torch.equal(s[e], se)
+    q, s = moe.quantize_fp8(w[0, :0], 1)
+    assert q.shape == (0, 384)
+
+
+# ----------------------------------------------------------------------------- dense product
+def operands(M, N, K, seed):
+    g = gen(seed)
+    a, sa = moe.quantize_fp8(randn(g, M, K, dtype=BF), 1)
+    w, sw = moe.quantize_fp8(randn(g, N, K, dtype=BF, scale=K ** -0.5), 128)
+    return a, sa, w, sw
+
+
+def matmul(a, sa, w, sw, ty):
+    out = torch.full((a.shape[0], w.shape[0]), 7, dtype=ty, device=DEV)
+    moe.moe_matmul_fp8(a, sa, w, sw, out, moe.matmul_fp8_workspace(a.shape[0], w.shape[0], a.shape[1], DEV))
+    torch.cuda.synchronize()
+    return out
+
+
+def cut(A, W):
+    """What the 8-bit matrix instruction may cut off (see above)."""
+    top = lambda v: abs(v).reshape(v.shape[0], -1, 8).max(2)  # noqa: E731
+    return 7 * 2.0 ** -13 * (top(A) @ top(W).T)
+
+
+def check_product(out, a, sa, w, sw):
+    A, W = ops.spread_rows(codes(a), host(sa).T), ops.spread_blocks(codes(w), host(sw))
+    ref = A @ W.T
+    tol = HALF[out.dtype] * abs(ref) + (132 + A.shape[1] / 128) * 2.0 ** -24 * (abs(A) @ abs(W).T)
+    if out.dtype == BF:
+        tol = tol + cut(A, W)
+        assert np.linalg.norm(host(out) - ref) <= 2.0 ** -8 * np.linalg.norm(ref) + 1e-30
+    within(host(out), ref, tol, "product")
+
+
+SIZES = [(1, 1, 128), (1, 128, 128), (1, 7168, 512), (2, 40, 256), (3, 129, 384), (5, 1000, 2048), (8, 256, 1024), (15, 72, 128), (16, 128, 256),
+         (17, 264, 640), (31, 512, 256), (33, 130, 128), (48, 2048, 1408), (64, 384, 384), (65, 128, 256), (100, 77, 512), (127, 256, 128),
+         (128, 128, 256), (129, 257, 384), (200, 640, 1152), (255, 255, 128), (257, 1032, 256), (512, 512, 512), (700, 4168, 640),
+         (1000, 128, 2048), (1536, 1544, 256)]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("ty", [BF, torch.float32])
+def test_matmul(M, N, K, ty):
+    print(f"\n[case] matmul_fp8 {M}x{N}x{K} {ty}", flush=True)
+    ab = operands(M, N, K, M + N)
+    out = matmul(*ab, ty)
+    check_product(out, *ab)
+    assert same_bits(out, matmul(*ab, ty))
+
+
+@pytest.mark.parametrize("M", [1, 16, 40, 200, 600])
+def test_matmul_keeps_rows_apart(M):
+    """Scales that differ by 2^40 from row to row and from block to block, a row and a block of NaN
+    scale: each row's result is its own."""
+    print(f"\n[case] matmul_fp8 scales {M}", flush=True)
+    N, K = 384, 512
+    a, sa, w, sw = operands(M, N, K, 4)
+    sa = sa * 2.0 ** ((torch.arange(M, device=DEV) % 5) * 10 - 20)[None]
+    sw = sw * 2.0 ** ((torch.arange(3, device=DEV) % 3) * 20 - 20)[:, None]
+    out = matmul(a, sa, w, sw, torch.float32)
+    check_product(out, a, sa, w, sw)
+    sa2 = sa.clone()
+    sa2[1, M // 2] = float("nan")
+    out2 = matmul(a, sa2, w, sw, torch.float32)
+    rest = [m for m in range(M) if m != M // 2]
+    assert torch.isnan(out2[M // 2]).all() and same_bits(out2[rest], out[rest])
+    sw2 = sw.clone()
+    sw2[1, 2] = float("nan")
+    out3 = matmul(a, sa, w, sw2, torch.float32)
+    assert torch.isnan(out3[:, 128:256]).all() and same_bits(out3[:, :128], out[:, :128]) and same_bits(out3[:, 256:], out[:, 256:])
+
+
+@pytest.mark.parametrize("M,N", [(3, 130), (70, 200), (300, 260)])
+def test_matmul_writes_its_own_rows_only(M, N):
+    """Output in the middle of a larger buffer, at an element's alignment: nothing around it is touched."""
+    print(f"\n[case] matmul_fp8 bounds {M}x{N}", flush=True)
+    ab = operands(M, N, 256, 6)
+    for ty in (BF, torch.float32):
+        buf = torch.full((M * N + 2002,), 7, dtype=ty, device=DEV)
+        out = buf[1001:1001 + M * N].view(M, N)
+        moe.moe_matmul_fp8(*ab, out, moe.matmul_fp8_workspace(M, N, 256, DEV))
+        torch.cuda.synchronize()
+        assert (buf[:1001] == 7).all() and (buf[1001 + M * N:] == 7).all()
+        assert same_bits(out.clone(), matmul(*ab, ty))
+
+
+def test_matmul_gradient_by_transposed_products():
+    """dA = dC W by the same product with the weight transposed (a 128 x 128 block keeps its scale)."""
+    print("\n[case] matmul_fp8 transposed", flush=True)
+    M, N, K = 40, 256, 384
+    _, _, w, sw = operands(M, N, K, 8)
+    dc, sdc = moe.quantize_fp8(randn(gen(9), M, N, dtype=BF), 1)
+    wt, swt = w.t().contiguous(), sw.t().contiguous()
+    out = matmul(dc, sdc, wt, swt, BF)
+    check_product(out, dc, sdc, wt, swt)
+
+
+def test_matmul_side_stream_and_graph():
+    print("\n[case] matmul_fp8 graph", flush=True)
+    for M, N, K in ((2, 512, 1024), (40, 512, 1024), (300, 520, 512)):
+        a, sa, w, sw = operands(M, N, K, 10)
+        want = matmul(a, sa, w, sw, BF)
+        ws = moe.matmul_fp8_workspace(M, N, K, DEV)
+        out = torch.zeros_like(want)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        moe.moe_matmul_fp8(a, sa, w, sw, out, ws, stream=side)
+        side.synchronize()
+        assert same_bits(out, want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.moe_matmul_fp8(a, sa, w, sw, out, ws)
+        for j in range(4):
+            sa.mul_(1.5)
+            graph.replay()
+            torch.cuda.synchronize()
+            got = out.clone()
+            assert same_bits(got, matmul(a, sa, w, sw, BF))
+
+
+# ----------------------------------------------------------------------------- experts
+def expert_case(counts, d, f, head, seed, C=None):
+    g = gen(seed)
+    E, n = len(counts), int(sum(counts))
+    C = C or max(n + 3, (5 * n + 3) // 4)
+    s = moe.make_shape(n, d, E, 1, f, C, dtype="fp8")
+    x = randn(g, n, d, dtype=BF)
+    q, qs = moe.quantize_fp8(x, 1)
+    slot = (head + torch.arange(n, device=DEV)) % C
+    ring, rs = torch.full((C, d), 0x7f, dtype=torch.uint8, device=DEV), torch.full((d // 128, C), float("nan"), device=DEV)
+    ring[slot], rs[:, slot] = q, qs
+    off = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).to(DEV)
+    wt = [moe.quantize_fp8(randn(g, E, r, c, dtype=BF, scale=c ** -0.5)) for r, c in ((f, d), (f, d), (d, f))]
+    return s, q, qs, slot, ring, rs, off, wt
+
+
+def experts(s, ring, rs, off, head, wt, save=False, ws=None):
+    y = torch.full((s.capacity, s.hidden), 7, dtype=BF, device=DEV)
+    au = torch.full((s.capacity, 2 * s.ffn), 7, dtype=BF, device=DEV) if save else None
+    ws = moe.workspace(s, moe.OP_EXPERT_FFN, DEV) if ws is None else ws
+    moe.moe_expert_ffn(s, ring, rs, off, head, wt[0][0], wt[1][0], wt[2][0], wt[0][1], wt[1][1], wt[2][1], y, au, ws)
+    torch.cuda.synchronize()
+    return y, au
+
+
+def ffn_within(y, X, W, what, a_got=None, u_got=None):
+    """The experts' outputs against the oracle.  The GPU's a and u are within da, du of the oracle's (the
+    product's tolerance), so its h = silu(a) u is within dh = 1.1 |u| da + (|a| + da) du + 2^-19 |h|
+    (silu's slope is below 1.1 and |silu(a)| <= |a|; sigmoid and products: a few steps), and a
+    block's scale is between those of its largest |h| - dh and |h| + dh.  E4M3 rounding rises with its
+    argument, so the value h is rounded to lies between those of the corners of that range;
+    what that leaves open goes through |W_down|, and the last product has its own tolerance."""
+    c, f = X.shape[0], W[0].shape[0]
+    ref, a, u = ops.expert_ffn(X, *W)
+    steps = (132 + X.shape[1] / 128) * 2.0 ** -24
+    da, du = (cut(X, w) + steps * (abs(X) @ abs(w).T) for w in W[:2])
+    if a_got is not None:
+        within(a_got, a, HALF[BF] * abs(a) + da, what + " a")
+        within(u_got, u, HALF[BF] * abs(u) + du, what + " u")
+    h = a / (1 + np.exp(-a)) * u
+    dh = 1.1 * abs(u) * da + (abs(a) + da) * du + 2.0 ** -19 * abs(h)
+    blocks = lambda v: v.reshape(c, f // 128, 128)  # noqa: E731
+    top = lambda v: np.maximum(blocks(v).max(2), ops.TINY)[:, :, None] / 448 * (1 + 2.0 ** -22)  # noqa: E731
+    s0, s1 = top(np.maximum(abs(h) - dh, 0)) * (1 - 2.0 ** -21), top(abs(h) + dh)
+    m0, m1 = blocks(np.maximum(abs(h) - dh, 0)), blocks(abs(h) + dh)
+    lo, hi = ops.e4m3(m0 / s1) * s0, ops.e4m3(np.minimum(m1 / s0, 448)) * s1
+    v = abs(blocks(ops.spread_rows(*ops.quantise_rows(h))))
+    open_ = np.maximum(hi - v, v - lo).reshape(c, f)
+    flips = blocks(h - dh < 0) & blocks(h + dh > 0)      # the sign itself is open
+    open_ = open_ + np.where(flips, 2 * hi, 0).reshape(c, f)
+    V = v.reshape(c, f) + open_
+    tol = HALF[BF] * abs(ref) + open_ @ abs(W[2]).T + cut(V, W[2]) + (132 + f / 128) * 2.0 ** -24 * (V @ abs(W[2]).T)
+    within(y, ref, tol, what)
+    assert np.linalg.norm(y - ref) <= 2e-2 * np.linalg.norm(ref) + 1e-30
+
+
+def check_experts(y, au, s, q, qs, slot, counts, wt):
+    X = ops.spread_rows(codes(q), host(qs).T)
+    Y, lo, f = host(y[slot]), 0, s.ffn
+    AU = None if au is None else host(au[slot])
+    for e, c in enumerate(counts):
+        if c:
+            W = [ops.spread_blocks(codes(w[e]), host(sw[e])) for w, sw in wt]
+            r = slice(lo, lo + c)
+            ffn_within(Y[r], X[r], W, f"expert {e} ({c} rows)", *(() if au is None else (AU[r, :f], AU[r, f:])))
+        lo += c
+
+
+EXPERTS = [([1], 128, 128, 0), ([1, 0, 0, 1], 256, 128, 3), ([0, 5, 1, 0, 16, 17], 256, 256, 0), ([3, 0, 40, 7], 384, 128, 30),
+           ([64, 60, 70, 66], 256, 384, 100), ([130, 0, 127, 128, 129, 1], 256, 256, 5), ([300, 20], 384, 256, 250),
+           ([257, 512, 255], 256, 128, 900), ([700], 128, 384, 0), ([8] * 16, 512, 256, 17), ([0, 0, 2], 1024, 512, 1)]
+
+
+@pytest.mark.parametrize("counts,d,f,head", EXPERTS, ids=[f"{i}-{sum(c[0])}rows-d{c[1]}f{c[2]}" for i, c in enumerate(EXPERTS)])
+@pytest.mark.parametrize("save", [False, True])
+def test_experts(counts, d, f, head, save):
+    print(f"\n[case] expert_ffn fp8 {counts} d={d} f={f} head={head} save={save}", flush=True)
+    s, q, qs, slot, ring, rs, off, wt = expert_case(counts, d, f, head, d + f)
+    head %= s.capacity
+    y, au = experts(s, ring, rs, off, head, wt, save)
+    check_experts(y, au, s, q, qs, slot, counts, wt)
+    # slots of no copy are left as they were, and the same call gives the same bits
+    other = torch.ones(s.capacity, dtype=torch.bool, device=DEV)
+    other[slot] = False
+    assert (y[other] == 7).all() and (au is None or (au[other] == 7).all())
+    y2, au2 = experts(s, ring, rs, off, head, wt, save)
+    assert same_bits(y, y2) and (au is None or same_bits(au, au2))
+
+
+def test_rows_do_not_depend_on_their_neighbours():
+    """A row whose scale is NaN leaves the other rows of its expert bit for bit as they were."""
+    print("\n[case] expert_ffn fp8 NaN row", flush=True)
+    for counts in ([5, 3], [40, 30], [200, 300]):
+        s, q, qs, slot, ring, rs, off, wt = expert_case(counts, 256, 256, 2, 3)
+        y, _ = experts(s, ring, rs, off, 2, wt)
+        rs2 = rs.clone()
+        rs2[1, slot[2]] = float("nan")
+        y2, _ = experts(s, ring, rs2, off, 2, wt)
+        rest = [int(v) for i, v in enumerate(slot) if i != 2]
+        assert torch.isnan(y2[slot[2]]).all() and same_bits(y2[rest], y[rest])
+
+
+# ----------------------------------------------------------------------------- a run of them
+@pytest.mark.parametrize("dtype", ["fp8", "mxfp8"])
+@pytest.mark.parametrize("T,head", [(1, 0), (9, 4), (130, 300)])
+def test_norm_route_dispatch_experts_combine(dtype, T, head):
+    """The block as a model runs it: norm with 8-bit rows, scored routing, dispatch of those rows,
+    experts, combine, each step from the GPU's own inputs against the oracle."""
+    print(f"\n[case] block {dtype} T={T}", flush=True)
+    d, E, k, f = 256, 16, 4, 128
+    g = gen(T)
+    layer = moe.Layer.create(T, d, E, k, f, dtype=dtype)
+    C = layer.shape.capacity
+    head %= C
+    x, res, nw = randn(g, T, d, dtype=BF), randn(g, T, d, dtype=BF), 1 + randn(g, d, scale=0.1)
+    wr, bal = randn(g, E, d) / 16, randn(g, E, scale=0.05)
+    ws = [randn(g, E, r, c, dtype=BF, scale=c ** -0.5) for r, c in ((f, d), (f, d), (d, f))]
+    qw = [moe.quantize_fp8(w) if dtype == "fp8" else moe.quantize_mx(w) for w in ws]
+    router = moe.make_router("sigmoid", 4, 2, 2, True, 2.5)
+    h, y, y8, ys = layer.add_rmsnorm(x, res, nw)
+    out = layer.forward(y, wr, None, qw[0][0], qw[1][0], qw[2][0], scales=[q[1] for q in qw], head=head,
+                        router=router, balance=bal, x8=y8, x8_scale=ys)
+    torch.cuda.synchronize()
+    b = layer.bufs
+    idx, gate = b["topk_idx"].cpu().numpy(), host(b["topk_gate"])
+    L = host(b["logits"])
+    rule = ops.Rule("sigmoid", 4, 2, 2, True, 2.5)
+    near = ops.margins(L, rule, k, host(bal)) > 1e-6
+    assert near.any() and np.array_equal(idx[near], ops.choose(L, rule, k, host(bal))[near])
+    within(gate, ops.gates(L, idx.astype(np.int64), rule), 2.0 ** -18, "gates")
+    # the ring holds y8's rows and scales at the slots of the counting sort
+    D = oracle.dispatch(idx, E, C, head)
+    slots = b["copy_slot"].cpu().numpy()
+    assert np.array_equal(slots, D.copy_slot)
+    flat = torch.from_numpy(slots.reshape(-1).astype(np.int64)).to(DEV)
+    assert torch.equal(b["ring_x"][flat], y8.repeat_interleave(k, 0))
+    assert torch.equal(b["ring_x_scale"][:, flat], ys.repeat_interleave(k, 1))
+    # experts and combine
+    if dtype == "fp8":
+        V = ops.spread_rows(codes(y8), host(ys).T)
+        W = [lambda e, i=i: ops.spread_blocks(codes(qw[i][0][e]), host(qw[i][1][e])) for i in range(3)]
+        ref, RY = np.zeros((T, d)), host(b["ring_y"])
+        for t in range(T):
+            for j in range(k):
+                e, row = idx[t, j], RY[slots[t, j]]
+                if t < 20:
+                    ffn_within(row[None], V[t:t + 1], [W[i](e) for i in range(3)], f"token {t} expert {e}")
+                ref[t] += gate[t, j] * row
+        # the combine: k fp32 products and sums, one rounding
+        within(host(out), ref, HALF[BF] * abs(ref) + 2.0 ** -20 * 4 * abs(RY).max(), "combine")
+    # the dispatch of the bf16 rows quantises the rounded y: the same block within its rounding
+    out2 = layer.forward(y, wr, None, qw[0][0], qw[1][0], qw[2][0], scales=[q[1] for q in qw], head=head,
+                         router=router, balance=bal).clone()
+    torch.cuda.synchronize()
+    assert oracle.max_abs_rel(host(out2), host(out)) < 6e-2
+
+
+def test_dispatch_quantises_like_the_quantiser():
+    print("\n[case] dispatch fp8", flush=True)
+    T, d, E, k = 37, 640, 8, 3
+    layer = moe.Layer.create(T, d, E, k, 128, dtype="fp8")
+    x, w = randn(gen(1), T, d, dtype=BF), randn(gen(2), E, d)
+    idx, _, _ = layer.route(x, w)
+    ring, rsc, off, cs, sc = layer.dispatch(x, idx, head=20)
+    q, s = moe.quantize_fp8(x, 1)
+    torch.cuda.synchronize()
+    flat = cs.view(-1).long()
+    assert torch.equal(ring[flat], q.repeat_interleave(k, 0)) and torch.equal(rsc[:, flat], s.repeat_interleave(k, 1))
+
+
+def test_training_step_of_an_fp8_layer():
+    """FP8 forward with saved A|U, bf16 backward, scored router: every gradient against the oracle's
+    on the GPU's saved A|U and gates (the forward's rounding to 8 bits is the identity)."""
+    print("\n[case] fp8 training step", flush=True)
+    T, d, E, k, f = 96, 256, 8, 3, 128
+    g = gen(77)
+    layer = moe.Layer.create(T, d, E, k, f, dtype="fp8")
+    x, dy = randn(g, T, d, dtype=BF), randn(g, T, d, dtype=BF)
+    wr = randn(g, E, d) / 16
+    ws = [randn(g, E, r, c, dtype=BF, scale=c ** -0.5) for r, c in ((f, d), (f, d), (d, f))]
+    qw = [moe.quantize_fp8(w) for w in ws]
+    rule = ops.Rule("sigmoid", 2, 1, 2, True, 2.5)
+    router = moe.make_router("sigmoid", 2, 1, 2, True, 2.5)
+    dlog = randn(g, T, E, scale=0.1)
+    layer.forward(x, wr, None, qw[0][0], qw[1][0], qw[2][0], scales=[q[1] for q in qw], save_au=True, router=router)
+    dx, dwg, dwu, dwd, dwr = layer.backward(dy, x, wr, *ws, router=router, dlogits=dlog)
+    torch.cuda.synchronize()
+    b = layer.bufs
+    idx, gate, slots = b["topk_idx"].cpu().numpy().astype(np.int64), host(b["topk_gate"]), b["copy_slot"].cpu().numpy()
+    AU, X, DY, W = host(b["saved_au"]), host(x), host(dy), [host(w) for w in ws]
+    rdx, rg, ru, rd, dg = np.zeros((T, d)), *(np.zeros(w.shape) for w in W), np.zeros((T, k))
+    for t in range(T):
+        for j in range(k):
+            e, au = idx[t, j], AU[slots[t, j]]
+            a, u = au[:f], au[f:]
+            sg = 1 / (1 + np.exp(-a))
+            hh = a * sg * u
+            dh = W[2][e].T @ DY[t]
+            dg[t, j] = dh @ hh
+            da, du = gate[t, j] * dh * u * sg * (1 + a * (1 - sg)), gate[t, j] * dh * a * sg
+            rdx[t] += W[0][e].T @ da + W[1][e].T @ du
+            rg[e] += np.outer(da, X[t])
+            ru[e] += np.outer(du, X[t])
+            rd[e] += gate[t, j] * np.outer(DY[t], hh)
+    dl = ops.gates_backward(dg, host(b["logits"]), idx, rule) + host(dlog)
+    rdx += dl @ host(wr)
+    for name, got, ref in (("dx", dx, rdx), ("dw_gate", dwg, rg), ("dw_up", dwu, ru), ("dw_down", dwd, rd), ("dw_router", dwr, dl.T @ X),
+                           ("db", b["db_router"], dl.sum(0)), ("dgate", b["dgate"], dg)):
+        r = oracle.max_abs_rel(host(got), ref)
+        print(f"  {name} max-abs-rel {r:.2e}", flush=True)
+        assert r <= 2e-2, name
+
+
+def test_backward_experts_is_the_backward_without_its_router():
+    """bf16: the experts' weight gradients are moe_backward's bit for bit; with the softmax rule
+    the two calls together give its dx and dW_r."""
+    print("\n[case] backward_experts", flush=True)
+    T, d, E, k, f = 200, 256, 8, 2, 256
+    g = gen(5)
+    x, dy, wr = randn(g, T, d, dtype=BF), randn(g, T, d, dtype=BF), randn(g, E, d) / 16
+    ws = [randn(g, E, r, c, dtype=BF, scale=c ** -0.5) for r, c in ((f, d), (f, d), (d, f))]
+    a, b = moe.Layer.create(T, d, E, k, f), moe.Layer.create(T, d, E, k, f)
+    router = moe.make_router()
+    a.forward(x, wr, None, *ws, save_au=True)
+    b.forward(x, wr, None, *ws, save_au=True, router=router)
+    ga, gb = a.backward(dy, x, wr, *ws), b.backward(dy, x, wr, *ws, router=router)
+    torch.cuda.synchronize()
+    assert torch.equal(a.bufs["topk_idx"], b.bufs["topk_idx"])
+    for i in (0, 1, 2, 3, 4):
+        assert oracle.max_abs_rel(host(gb[i]), host(ga[i])) < 1e-2
+    # the same gates: bit for bit
+    dx, dg, out = torch.empty_like(x), torch.empty(T, k, device=DEV), [torch.empty_like(w) for w in ws]
+    bb = a.bufs
+    moe.moe_backward_experts(a.shape, dy, bb["topk_idx"], bb["topk_gate"], bb["ring_x"], bb["expert_offset"], bb["copy_slot"],
+                             bb["slot_copy"], 0, bb["saved_au"], *ws, dx, *out, dg, moe.workspace(a.shape, moe.OP_BACKWARD, DEV))
+    torch.cuda.synchronize()
+    assert all(same_bits(o, r) for o, r in zip(out, ga[1:4]))
+
+
+def test_fp8_workload_size_smoke():
+    """The per-GPU share's widths (d 7168, f 2048) on few rows and on more than a tile of them,
+    sampled columns against the oracle."""
+    print("\n[case] expert_ffn fp8 at d=7168 f=2048", flush=True)
+    for counts in ([3, 1], [150, 290]):
+        s, q, qs, slot, ring, rs, off, wt = expert_case(counts, 7168, 2048, 1, 12)
+        y, _ = experts(s, ring, rs, off, 1, wt)
+        rows = [0, 1, counts[0], sum(counts) - 1]
+        X = ops.spread_rows(codes(q[rows]), host(qs[:, rows]).T)
+        for r, m in enumerate(rows):
+            e = 0 if m < counts[0] else 1
+            W = [ops.spread_blocks(codes(w[e]), host(sw[e])) for w, sw in wt]
+            ffn_within(host(y[slot[m]])[None], X[r:r + 1], W, f"row {m}")
+    assert math.isfinite(float(y[slot].float().abs().max()))
