@@ -59,6 +59,8 @@ int check_shape(const moe_shape* s) {
     const int64_t eb = s->dtype == MOE_BF16 ? 2 : 1;
     const int64_t row = (s->hidden > s->ffn ? s->hidden : s->ffn) * eb;
     if (s->capacity * row >= ((int64_t)1 << 32)) return MOE_ERR_SHAPE;
+    // ... and the FP8 products the rows of one expert's matrix likewise
+    if (s->dtype == MOE_FP8 && (int64_t)s->hidden * s->ffn >= ((int64_t)1 << 32)) return MOE_ERR_SHAPE;
   }
   return MOE_OK;
 }

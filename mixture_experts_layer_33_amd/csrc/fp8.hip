@@ -17,10 +17,13 @@
 // bf16 (every E4M3 value is a bf16 value) and multiplied by the bf16 MFMA, whose sums are fp32
 // (error against fp64 5e-7), at half the rate.
 #include <algorithm>
+#ifdef PROBE
+#include <cstdlib>
+#endif
 
 #include "common.h"
 #include "fp8.h"
-#include "gemm_body.h"
+#include "fp8_tile.h"
 #include "kernels.h"
 
 namespace moe {
@@ -93,55 +96,6 @@ hipError_t launch_quantize_fp8(const void* src, int64_t rows, int64_t cols, int 
 }
 
 // ----------------------------------------------------------------------------- products
-struct Fp8Args {
-  const uint8_t* A;        // token rows [C, K] codes
-  const float* As;         // [K/128][a_rows]
-  const uint8_t* W0;       // [E, N, K]
-  const uint8_t* W1;       // SWIGLU: the up weights
-  const float* S0;         // [E][ceil(N/128)][K/128]
-  const float* S1;
-  int64_t a_rows;
-  int K, N;
-  const int32_t* offset;   // ring segments; NULL: one product of all a_rows rows
-  const int32_t* tiles;
-  const int32_t* ntiles;
-  int64_t head, C;
-  void* out;               // SWIGLU: H codes [C, N]; else bf16 or fp32 [C, N]
-  float* out_scale;        // SWIGLU: [N/128][C]
-  bf16_t* saved_au;        // SWIGLU: [C, 2N] or NULL
-};
-
-// Lane l's 32 bytes of row `r`'s block b: bytes 32 (l / 16) .. + 31.  (Which of the block's 128
-// positions a lane's byte is does not matter as long as both operands agree.)
-__device__ __forceinline__ i32x8 fp8_frag(const uint8_t* p) {
-  const u32x4 a = *(const u32x4*)p, b = *(const u32x4*)(p + 16);
-  return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
-}
-__device__ __forceinline__ f32x4 fp8_mfma16(i32x8 w, i32x8 a) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-}
-
-// The same sum on the bf16 MFMA: the 32 codes of a lane in four steps of 8.
-__device__ __forceinline__ bf16x8 fp8_widen8(int lo, int hi) {
-  union {
-    __bf16 __attribute__((ext_vector_type(2))) p[4];
-    bf16x8 v;
-  } o;
-  o.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-  o.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-  o.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-  o.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
-  return o.v;
-}
-__device__ __forceinline__ f32x4 fp8_wide16(i32x8 w, i32x8 a) {
-  f32x4 c = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8_widen8(w[2 * q], w[2 * q + 1]),
-                                                fp8_widen8(a[2 * q], a[2 * q + 1]), c, 0, 0, 0);
-  return c;
-}
-
 // 16 token rows per tile; 8 wavefronts of 16 weight rows (SWIGLU: 16 gate and 16 up rows), so a
 // workgroup covers one block of 128 output columns and a SWIGLU tile holds whole H blocks.
 // Result i of lane l: output column n0 + 16 wave + 4 (l / 16) + i of token row l % 16.
@@ -177,7 +131,7 @@ __global__ __launch_bounds__(512) void fp8_rows16_kernel(Fp8Args p) {
     const i32x8 av = fp8_frag(a + (int64_t)b * 128);
     const float sa = as[b * p.a_rows];
     const i32x8 wv = fp8_frag(w0 + (int64_t)b * 128);
-    const f32x4 q0 = F32 ? fp8_wide16(wv, av) : fp8_mfma16(wv, av);
+    const f32x4 q0 = F32 ? fp8_wide16(fp8_widen(wv), fp8_widen(av)) : fp8_mfma16(wv, av);
     const float t0 = sa * s0[b];
 #pragma unroll
     for (int i = 0; i < 4; ++i) c0[i] = fmaf(q0[i], t0, c0[i]);
@@ -242,6 +196,19 @@ hipError_t launch_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8
   p.K = (int)K;
   p.N = (int)N;
   p.out = out;
+#ifdef PROBE
+  const int fm = getenv("FM") ? atoi(getenv("FM")) : 0;
+#else
+  const int fm = M <= 16 ? 0 : M <= 64 ? 1 : M <= 128 || f32_out ? 2 : 4;
+#endif
+  const int64_t mt = fm ? (M + 64 * fm - 1) / (64 * fm) : 0;
+  p.rotate = M > 256;
+  if (f32_out && fm == 1) return run_fp8_tile<1, FP8_F32, 3, 2>(p, mt, st);
+  if (f32_out && fm) return run_fp8_tile<2, FP8_F32, 3, 2>(p, mt, st);
+  if (fm == 1) return run_fp8_tile<1, FP8_BF16, 3, 2>(p, mt, st);
+  if (fm == 2) return run_fp8_tile<2, FP8_BF16, 3, 2>(p, mt, st);
+  if (fm == 3) return run_fp8_tile<3, FP8_BF16, 2, 2>(p, mt, st);
+  if (fm == 4) return run_fp8_tile<4, FP8_BF16, 2, 2>(p, mt, st);
   const unsigned grid = (unsigned)(((M + 15) / 16) * ((N + 127) / 128));
   if (f32_out) fp8_rows16_kernel<false, true><<<grid, 512, 0, st>>>(p);
   else fp8_rows16_kernel<false, false><<<grid, 512, 0, st>>>(p);
@@ -273,9 +240,16 @@ hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const i
   int32_t* ntiles = (int32_t*)(w + L.tiles);
   int32_t* tiles = ntiles + 64;
   auto mark = [&](int i) { return events ? hipEventRecord(events[i], st) : hipSuccess; };
-  hipError_t err = launch_build_tiles(expert_offset, E, 16, tiles, ntiles, st);
+#ifdef PROBE
+  const int fm = getenv("FM") ? atoi(getenv("FM")) : 0;
+#else
+  const int fm = n <= 16 * (int64_t)E ? 0 : n < 256 * (int64_t)E ? 2 : 4;
+#endif
+  const int BM = fm ? 64 * fm : 16;
+  hipError_t err = launch_build_tiles(expert_offset, E, BM, tiles, ntiles, st);
   if (err != hipSuccess || (err = mark(0)) != hipSuccess) return err;
-  const int mt = max_tiles_for(n, E, 16);
+  const int mt = max_tiles_for(n, E, BM);
+  const bool once = n <= BM * (int64_t)E;   // about one row tile per expert: each weight is read once
   Fp8Args p{};
   p.A = (const uint8_t*)ring_x;
   p.As = ring_x_scale;
@@ -294,8 +268,20 @@ hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const i
   p.out = w + L.h;
   p.out_scale = (float*)(w + L.hs);
   p.saved_au = (bf16_t*)saved_au;
-  fp8_rows16_kernel<true, false><<<(unsigned)((int64_t)mt * (f / 128)), 512, 0, st>>>(p);
-  if ((err = hipGetLastError()) != hipSuccess || (err = mark(1)) != hipSuccess) return err;
+#define RUN(FM, KIND, S, G)                                              \
+  err = once ? run_fp8_tile<FM, KIND, S, 3>(G, mt, st) : run_fp8_tile<FM, KIND, S, 2>(G, mt, st);
+  p.rotate = !once;
+  if (fm == 0) {
+    fp8_rows16_kernel<true, false><<<(unsigned)((int64_t)mt * (f / 128)), 512, 0, st>>>(p);
+    err = hipGetLastError();
+  } else if (fm == 1) {
+    if (saved_au) RUN(1, FP8_SWIGLU_SAVE, 3, p) else RUN(1, FP8_SWIGLU, 3, p)
+  } else if (fm == 2) {
+    if (saved_au) RUN(2, FP8_SWIGLU_SAVE, 3, p) else RUN(2, FP8_SWIGLU, 3, p)
+  } else {
+    if (saved_au) RUN(4, FP8_SWIGLU_SAVE, 2, p) else RUN(4, FP8_SWIGLU, 2, p)
+  }
+  if (err != hipSuccess || (err = mark(1)) != hipSuccess) return err;
   Fp8Args q = p;
   q.A = w + L.h;
   q.As = p.out_scale;
@@ -308,8 +294,15 @@ hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const i
   q.out = ring_y;
   q.out_scale = nullptr;
   q.saved_au = nullptr;
-  fp8_rows16_kernel<false, false><<<(unsigned)((int64_t)mt * (d / 128)), 512, 0, st>>>(q);
-  if ((err = hipGetLastError()) != hipSuccess) return err;
+  q.rotate = !once;
+  if (fm == 0) {
+    fp8_rows16_kernel<false, false><<<(unsigned)((int64_t)mt * (d / 128)), 512, 0, st>>>(q);
+    err = hipGetLastError();
+  } else if (fm == 1) RUN(1, FP8_BF16, 3, q)
+  else if (fm == 2) RUN(2, FP8_BF16, 3, q)
+  else RUN(4, FP8_BF16, 2, q)
+#undef RUN
+  if (err != hipSuccess) return err;
   return mark(2);
 }
 

@@ -1,0 +1,401 @@
+// The FP8 product's tile for many rows: BM = 64 FM token rows x 256 weight rows, eight wavefronts in
+// 4 x 2, K in blocks of 128 through a ring of S LDS stages filled by global -> LDS copies.
+//
+// One 16x16x128 MFMA is exactly one block of 128: its result is the block's partial sum of 16
+// weight rows x 16 token rows, and enters the accumulators with four multiply-adds per lane while
+// the next MFMAs run (the matrix pipe is busy 32 clocks per MFMA, the four multiply-adds take
+// 16).  A wavefront holds token fragments wm, wm + 4, ... of 16 rows (so that the rows of a
+// partly filled tile are spread over all wavefronts) and 128 weight rows, all of one scale block:
+// 64 gate and the matching 64 up rows (SWIGLU), or 128 rows of W.
+#pragma once
+
+#include <type_traits>
+
+#include "fp8.h"
+#include "gemm_body.h"
+
+namespace moe {
+
+struct Fp8Args {
+  const uint8_t* A;        // token rows [C, K] codes
+  const float* As;         // [K/128][a_rows]
+  const uint8_t* W0;       // [E, N, K]
+  const uint8_t* W1;       // SWIGLU: the up weights
+  const float* S0;         // [E][ceil(N/128)][K/128]
+  const float* S1;
+  int64_t a_rows;
+  int K, N;
+  const int32_t* offset;   // ring segments; NULL: one product of all a_rows rows
+  const int32_t* tiles;
+  const int32_t* ntiles;
+  int64_t head, C;
+  void* out;               // SWIGLU: H codes [C, N]; else bf16 or fp32 [C, N]
+  float* out_scale;        // SWIGLU: [N/128][C]
+  bf16_t* saved_au;        // SWIGLU: [C, 2N] or NULL
+  int rotate;              // 1: tile L starts its K loop at block L mod (K / 128)
+};
+
+// Lane l's 32 bytes of a row's block: bytes 32 (l / 16) .. + 31.  (Which of the block's 128
+// positions a lane's byte is does not matter as long as both operands agree.)
+__device__ __forceinline__ i32x8 fp8_join(u32x4 a, u32x4 b) {
+  return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+__device__ __forceinline__ i32x8 fp8_frag(const uint8_t* p) {
+  return fp8_join(*(const u32x4*)p, *(const u32x4*)(p + 16));
+}
+__device__ __forceinline__ f32x4 fp8_mfma16(i32x8 w, i32x8 a) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+// The same sum on the bf16 MFMA: the 32 codes of a lane in four steps of 8.
+struct Wide16 {
+  bf16x8 v[4];
+};
+__device__ __forceinline__ bf16x8 fp8_widen8(int lo, int hi) {
+  union {
+    __bf16 __attribute__((ext_vector_type(2))) p[4];
+    bf16x8 v;
+  } o;
+  o.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  o.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  o.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  o.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return o.v;
+}
+__device__ __forceinline__ Wide16 fp8_widen(i32x8 w) {
+  return Wide16{{fp8_widen8(w[0], w[1]), fp8_widen8(w[2], w[3]), fp8_widen8(w[4], w[5]), fp8_widen8(w[6], w[7])}};
+}
+__device__ __forceinline__ f32x4 fp8_wide16(const Wide16& w, const Wide16& a) {
+  f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[q], a.v[q], c, 0, 0, 0);
+  return c;
+}
+
+enum { FP8_BF16 = 0, FP8_F32 = 1, FP8_SWIGLU = 2, FP8_SWIGLU_SAVE = 3 };
+
+template <int FM>
+struct Fp8Stage {
+  static constexpr int BM = 64 * FM, BN = 256;
+  static constexpr int A = 0, B = BM * 128, SC = B + BN * 128;   // SC: BM row scales, 2 block scales, padding
+  static constexpr int SIZE = SC + 8 * 256;
+  static constexpr int L = FM + 4 + 1;                           // copies per wavefront and stage
+};
+
+template <int FM, int KIND, int S, int POL>
+__global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
+  using SL = Fp8Stage<FM>;
+  constexpr int BM = SL::BM, BN = SL::BN, L = SL::L;
+  constexpr bool SWIGLU = KIND >= FP8_SWIGLU, WIDE = KIND == FP8_F32;
+  static_assert(FM >= 1 && FM <= 4 && S >= 2 && S <= 4, "tile");
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+  constexpr int CB = SWIGLU ? 1 : 2;             // output blocks of 128 columns per tile
+  const int nblk = (p.N + 127) / 128, nct = (nblk + CB - 1) / CB;
+  const int nmt = p.offset ? *p.ntiles : (int)((p.a_rows + BM - 1) / BM);
+  int mt, ct;
+  if (!xcd_tile((int)blockIdx.x, nct, nmt, mt, ct)) return;
+  int e = 0, row0 = mt * BM, rows;
+  int32_t seg = 0;
+  if (p.offset) {
+    e = p.tiles[2 * mt];
+    row0 = p.tiles[2 * mt + 1];
+    seg = p.offset[e];
+    rows = min(BM, p.offset[e + 1] - seg - row0);
+  } else {
+    rows = (int)min((int64_t)BM, p.a_rows - row0);
+  }
+  const int n0 = ct * CB * 128;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1, lr = lane & 15, lg = lane >> 4;
+  const uint32_t K = (uint32_t)p.K;
+  const int KT = p.K / 128;
+
+  // copies: 16-byte chunk j of a tile is slot j % 8 of row j / 8 and holds the chunk of that row whose
+  // swizzled place it is (swz of gemm_body.h)
+  uint32_t a_off[FM], b_off[4], s_off;
+  const uint8_t* b_base[4];
+  const uint8_t* s_base;
+  int64_t s_step;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int j = (8 * i + wave) * 64 + lane, r = j / 8;
+    const int c = (swz<128>(r, j % 8) - r * 128) >> 4;
+    a_off[i] = (uint32_t)ring_slot(p.head, seg, row0 + min(r, rows - 1), p.C) * K + c * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = (8 * i + wave) * 64 + lane, r = j / 8;
+    const int c = (swz<128>(r, j % 8) - r * 128) >> 4;
+    const bool up = SWIGLU && i >= 2;            // rows 128 .. 255
+    b_base[i] = (up ? p.W1 : p.W0) + (int64_t)e * p.N * K;
+    b_off[i] = (uint32_t)min(n0 + (up ? r - 128 : r), p.N - 1) * K + c * 16;
+  }
+  if (wave < FM) {                               // 64 row scales
+    const int r = 64 * wave + lane;
+    s_base = (const uint8_t*)p.As;
+    s_off = (uint32_t)ring_slot(p.head, seg, row0 + min(r, rows - 1), p.C) * 4;
+    s_step = p.a_rows * 4;
+  } else if constexpr (SWIGLU) {                 // a block scale in every lane: wavefront FM gate, FM + 1 up
+    s_base = (const uint8_t*)(((wave - FM) & 1 ? p.S1 : p.S0) + ((int64_t)e * nblk + ct) * KT);
+    s_off = 0;
+    s_step = 4;
+  } else {                                       // the tile's two block scales in turn
+    s_base = (const uint8_t*)(p.S0 + (int64_t)e * nblk * KT);
+    s_off = (uint32_t)min(2 * ct + (lane & 1), nblk - 1) * KT * 4;
+    s_step = 4;
+  }
+  const int s0 = p.rotate ? (int)(((int64_t)mt * nct + ct) % KT) : 0;
+  auto issue_one = [&](int i_, int c) __attribute__((always_inline)) {
+    const uint32_t st = lds0 + (uint32_t)(i_ % S) * SL::SIZE;
+    const int kt = i_ + s0 >= KT ? i_ + s0 - KT : i_ + s0;
+    if (c < FM) {
+      dma16(p.A + (size_t)kt * 128, a_off[c], __builtin_amdgcn_readfirstlane(st + SL::A + (8 * c + wave) * 1024));
+    } else if (c < FM + 4) {
+      const int i = c - FM;
+      const uint32_t to = __builtin_amdgcn_readfirstlane(st + SL::B + (8 * i + wave) * 1024);
+      if (POL & 1) dma16nt(b_base[i] + (size_t)kt * 128, b_off[i], to);
+      else dma16(b_base[i] + (size_t)kt * 128, b_off[i], to);
+    } else {
+      dma4(s_base + (size_t)kt * s_step, s_off, __builtin_amdgcn_readfirstlane(st + SL::SC + wave * 256));
+    }
+  };
+  auto wait_stage = [&](int later) __attribute__((always_inline)) {
+    if (later <= 0) wait_vm<0>();
+    else if (later == 1) wait_vm<L>();
+    else wait_vm<2 * L>();
+  };
+
+  f32x4 acc[FM][8];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // a fragment's two 16-byte chunks of row r = 16 q + lr sit at r * 128 + ((2 lg + h) ^ (r >> 1 & 7)) * 16,
+  // and r >> 1 & 7 is lr >> 1: one per-lane offset and a multiple of 2048
+  const uint32_t l0 = (uint32_t)(lr * 128 + (((2 * lg) ^ ((lr >> 1) & 7)) << 4));
+  auto bfrag = [&](int j) { return SWIGLU ? (j < 4 ? 4 * wn + j : 8 + 4 * wn + j - 4) : 8 * wn + j; };
+
+  // One block of 128: NL live token fragments, and with COPY the copies of stage kt + S - 1 spread
+  // over the MFMAs.  The multiply-adds of an MFMA's result follow LAG MFMAs later, past the matrix
+  // pipe's latency.  Both are compile-time choices: a branch inside the step would let the
+  // compiler sink every multiply-add to the step's end, with all partial sums live.
+  constexpr int LAG = 3;
+  auto step = [&](int kt, auto nl, auto copy) __attribute__((always_inline)) {
+    constexpr int NL = decltype(nl)::value;
+    constexpr bool COPY = decltype(copy)::value;
+    constexpr int NM = 8 * NL;                   // MFMAs per block
+    if constexpr (NL == 0) {
+      if constexpr (COPY) {
+#pragma unroll
+        for (int c = 0; c < L; ++c) issue_one(kt + S - 1, c);
+      }
+    } else {
+      // Four per-lane addresses per stage (both chunks of the token and of the weight fragments); everything
+      // else is a constant offset.  They pass through an empty asm so that the compiler does not
+      // keep one address per fragment and stage live across the loop, which spills.
+      const uint32_t st = (uint32_t)(kt % S) * SL::SIZE;
+      uint32_t pa = st + SL::A + wm * 2048 + l0, pb = st + SL::B + wn * (SWIGLU ? 8192 : 16384) + l0;
+      uint32_t pa1 = st + SL::A + wm * 2048 + (l0 ^ 16), pb1 = st + SL::B + wn * (SWIGLU ? 8192 : 16384) + (l0 ^ 16);
+      uint32_t ps = st + SL::SC + (16 * wm + lr) * 4;
+      asm volatile("" : "+v"(pa), "+v"(pb), "+v"(pa1), "+v"(pb1), "+v"(ps));
+      auto atile = [&](int i) __attribute__((always_inline)) {
+        return fp8_join(*(const u32x4*)(lds + pa + i * 8192), *(const u32x4*)(lds + pa1 + i * 8192));
+      };
+      auto btile = [&](int j) __attribute__((always_inline)) {   // fragment bfrag(j)
+        const int q = SWIGLU && j >= 4 ? j + 4 : j;
+        return fp8_join(*(const u32x4*)(lds + pb + q * 2048), *(const u32x4*)(lds + pb1 + q * 2048));
+      };
+      const float* sc = (const float*)(lds + st + SL::SC);
+      i32x8 af[NL], bq[2];
+      float t[NL][2];
+      bq[0] = btile(0);
+#pragma unroll
+      for (int i = 0; i < NL; ++i) af[i] = atile(i);
+      const float sw0 = SWIGLU ? sc[64 * FM] : sc[64 * FM + wn], sw1 = SWIGLU ? sc[64 * FM + 64] : sw0;
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const float sa = *(const float*)(lds + ps + i * 256);
+        t[i][0] = sa * sw0;
+        t[i][1] = SWIGLU ? sa * sw1 : t[i][0];
+      }
+      f32x4 part[LAG + 1];
+      auto add = [&](int m) __attribute__((always_inline)) {
+        const int j = m / NL, i = m % NL;
+        const float s = t[i][j >> 2];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(part[m % (LAG + 1)][r], s, acc[i][j][r]);
+      };
+      Wide16 aw[WIDE ? NL : 1];
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) aw[i] = fp8_widen(af[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j + 1 < 8) bq[(j + 1) & 1] = btile(j + 1);
+        Wide16 bw;
+        if constexpr (WIDE) bw = fp8_widen(bq[j & 1]);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+          const int m = j * NL + i;
+          if constexpr (WIDE) part[m % (LAG + 1)] = fp8_wide16(bw, aw[i]);
+          else part[m % (LAG + 1)] = fp8_mfma16(bq[j & 1], af[i]);
+          if constexpr (COPY) {
+#pragma unroll
+            for (int c = 0; c < L; ++c)
+              if (c * NM / L == m) issue_one(kt + S - 1, c);
+          }
+          if (m >= LAG) add(m - LAG);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+#pragma unroll
+      for (int m = NM - LAG; m < NM; ++m) add(m);
+    }
+  };
+  auto kloop = [&](auto nl) __attribute__((always_inline)) {
+    const int copied = max(KT - (S - 1), 0);
+    for (int kt = 0; kt < copied; ++kt) {
+      wait_vm<(S - 2) * L>();
+      __syncthreads();
+      step(kt, nl, std::true_type{});
+    }
+    for (int kt = copied; kt < KT; ++kt) {
+      wait_stage(KT - 1 - kt);
+      __syncthreads();
+      step(kt, nl, std::false_type{});
+    }
+  };
+  for (int s = 0; s < S - 1 && s < KT; ++s)
+#pragma unroll
+    for (int c = 0; c < L; ++c) issue_one(s, c);
+  // live token fragments of this wavefront: rows 16 (wm + 4 i) below `rows`
+  const int nlive = rows > 16 * wm ? min(FM, (rows - 16 * wm + 63) / 64) : 0;
+  if (nlive >= FM) kloop(std::integral_constant<int, FM>{});
+  else if (FM > 3 && nlive == 3) kloop(std::integral_constant<int, (FM > 3 ? 3 : 0)>{});
+  else if (FM > 2 && nlive == 2) kloop(std::integral_constant<int, (FM > 2 ? 2 : 0)>{});
+  else if (FM > 1 && nlive == 1) kloop(std::integral_constant<int, (FM > 1 ? 1 : 0)>{});
+  else kloop(std::integral_constant<int, 0>{});
+  __syncthreads();
+
+  // ---------------------------------------------------------------- epilogue
+  // acc[i][j][r]: token row 16 (wm + 4 i) + lr, weight row 16 bfrag(j) + 4 lg + r of the tile.  Output planes
+  // are staged row-major in the idle stage ring (rows padded by 16 bytes) and written as 16-byte pieces.
+  auto slot_of = [&](int m) { return ring_slot(p.head, seg, row0 + m, p.C); };
+  auto flush = [&](uint8_t* dst, int64_t pitch, int col0b, int rowb, int rs) __attribute__((always_inline)) {
+    __syncthreads();
+    const int cpr = (rs - 16) / 16;
+    for (int q = tid; q < BM * cpr; q += 512) {
+      const int m = q / cpr, cb = (q % cpr) * 16;
+      if (m < rows && col0b + cb < rowb)
+        __builtin_nontemporal_store(*(const u32x4*)(lds + m * rs + cb), (u32x4*)(dst + slot_of(m) * pitch + col0b + cb));
+    }
+    __syncthreads();
+  };
+  if constexpr (SWIGLU) {
+    if constexpr (KIND == FP8_SWIGLU_SAVE) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f32x4 v = acc[i][4 * h + j];
+            *(u32x2*)(lds + (16 * (wm + 4 * i) + lr) * 272 + (64 * wn + 16 * j + 4 * lg) * 2) =
+                u32x2{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3])};
+          }
+        flush((uint8_t*)p.saved_au + (int64_t)h * p.N * 2, (int64_t)p.N * 4, n0 * 2, p.N * 2, 272);
+      }
+    }
+    // h = silu(a) u in place of a; the row's maximum over 128 columns: 16 values here, four lanes (lg), two
+    // wavefronts (wn, through LDS)
+    float* hmax = (float*)lds;                   // [2][BM]
+    float am[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      am[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          acc[i][j][r] = silu(acc[i][j][r]) * acc[i][4 + j][r];
+          am[i] = amax2(am[i], acc[i][j][r]);
+        }
+      am[i] = amax2(am[i], __shfl_xor(am[i], 16, 64));
+      am[i] = amax2(am[i], __shfl_xor(am[i], 32, 64));
+      if (lg == 0) hmax[wn * BM + 16 * (wm + 4 * i) + lr] = am[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < FM; ++i) am[i] = amax2(am[i], hmax[(wn ^ 1) * BM + 16 * (wm + 4 * i) + lr]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int m = 16 * (wm + 4 * i) + lr;
+      const float s = fp8_scale(am[i]);
+      if (wn == 0 && lg == 0 && m < rows) p.out_scale[(int64_t)ct * p.C + slot_of(m)] = s;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *(uint32_t*)(lds + m * 144 + 64 * wn + 16 * j + 4 * lg) =
+            fp8_encode4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], s);
+    }
+    flush((uint8_t*)p.out, p.N, n0, p.N, 144);
+  } else if constexpr (KIND == FP8_F32) {
+    const bool whole = (p.N & 3) == 0 && ((uintptr_t)p.out & 15) == 0;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int m = 16 * (wm + 4 * i) + lr;
+      if (m >= rows) continue;
+      float* row = (float*)p.out + slot_of(m) * p.N;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int col = n0 + 16 * bfrag(j) + 4 * lg;
+        if (whole) {
+          if (col < p.N) *(f32x4*)(row + col) = acc[i][j];
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (col + r < p.N) row[col + r] = acc[i][j][r];
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const f32x4 v = acc[i][j];
+        *(u32x2*)(lds + (16 * (wm + 4 * i) + lr) * 528 + (16 * bfrag(j) + 4 * lg) * 2) =
+            u32x2{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3])};
+      }
+    if ((p.N & 7) == 0 && ((uintptr_t)p.out & 15) == 0) {
+      flush((uint8_t*)p.out, (int64_t)p.N * 2, n0 * 2, p.N * 2, 528);
+    } else {                                     // rows that 16-byte pieces do not fit
+      __syncthreads();
+      for (int q = tid; q < BM * 256; q += 512) {
+        const int m = q / 256, c = q % 256;
+        if (m < rows && n0 + c < p.N)
+          ((bf16_t*)p.out)[slot_of(m) * p.N + n0 + c] = *(const bf16_t*)(lds + m * 528 + 2 * c);
+      }
+    }
+  }
+}
+
+template <int FM, int KIND, int S, int POL>
+inline hipError_t run_fp8_tile(const Fp8Args& a, int64_t max_tiles, hipStream_t st) {
+  const int nblk = (a.N + 127) / 128, nct = KIND >= FP8_SWIGLU ? nblk : (nblk + 1) / 2;
+  constexpr int BM = 64 * FM;
+  constexpr int epi = KIND == FP8_BF16 ? BM * 528 : KIND == FP8_SWIGLU_SAVE ? BM * 272 : KIND == FP8_SWIGLU ? BM * 144 : 0;
+  constexpr int ring = S * Fp8Stage<FM>::SIZE, lds = ring > epi ? ring : epi;
+  static_assert(lds <= 160 * 1024, "LDS");
+  auto kern = fp8_tile_kernel<FM, KIND, S, POL>;
+  hipError_t err = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (err != hipSuccess) return err;
+  const int64_t grid = 8 * ((max_tiles * nct + 7) / 8);
+  kern<<<(unsigned)grid, 512, lds, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace moe
