@@ -90,7 +90,7 @@ size_t moe_workspace_bytes(const moe_shape* s, int op) {
                  : 0;
     case MOE_OP_NORM_BACKWARD: return align256(moe::norm_bwd_workspace_bytes(T, s->hidden));
     case MOE_OP_ROUTE_BACKWARD:
-      return align256(moe::route_scored_bwd_workspace_bytes(T, s->experts, s->hidden));
+      return align256(moe::route_scored_bwd_workspace_bytes(s->dtype == MOE_F32, T, s->experts, s->hidden));
     case MOE_OP_BACKWARD:
       if (s->dtype == MOE_FP8) return 0;
       if (s->dtype == MOE_MXFP8)

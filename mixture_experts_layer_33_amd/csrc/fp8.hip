@@ -177,6 +177,34 @@ __global__ __launch_bounds__(512) void fp8_rows16_kernel(Fp8Args p) {
 }
 
 // ----------------------------------------------------------------------------- launchers
+// Row tiles that take a column tile one after another (fp8_tile.h).
+constexpr int FP8_GROUP = 4;
+
+// Tile height (in 64 rows) of a product of M rows with `nct` column tiles of 256: the one with the least
+// time, rounds of 256 workgroups times a stage's time.  Stages of 64 / 128 / 192 / 256 rows took
+// 0.95, 0.98, 1.07 and 1.25 us (M 2,045, N 4,168, K 7,168): low tiles are bound by their
+// weight copies, not by the matrix cores.
+static int tile_height(int64_t M, int64_t nct) {
+  const double us[4] = {0.95, 0.98, 1.07, 1.25};
+  int best = 1;
+  double least = 1e300;
+  for (int fm = 1; fm <= 4; ++fm) {
+    const double t = (double)(((M + 64 * fm - 1) / (64 * fm) * nct + 255) / 256) * us[fm - 1];
+    if (t < least) { least = t; best = fm; }
+  }
+  return best;
+}
+
+hipError_t launch_tile_add(Fp8Args& a, hipStream_t st) {
+  a.group = FP8_GROUP;
+  const int fm = tile_height(a.a_rows, (a.N + 255) / 256);
+  const int64_t mt = (a.a_rows + 64 * fm - 1) / (64 * fm);
+  if (fm == 1) return run_fp8_tile<1, TILE_ADD, 3, 2>(a, mt, st);
+  if (fm == 2) return run_fp8_tile<2, TILE_ADD, 3, 2>(a, mt, st);
+  if (fm == 3) return run_fp8_tile<3, TILE_ADD, 2, 2>(a, mt, st);
+  return run_fp8_tile<4, TILE_ADD, 2, 2>(a, mt, st);
+}
+
 size_t matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   (void)M; (void)N; (void)K;
   return 0;
@@ -199,10 +227,10 @@ hipError_t launch_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8
 #ifdef PROBE
   const int fm = getenv("FM") ? atoi(getenv("FM")) : 0;
 #else
-  const int fm = M <= 16 ? 0 : M <= 64 ? 1 : M <= 128 || f32_out ? 2 : 4;
+  const int fm = M <= 16 ? 0 : f32_out ? (M <= 64 ? 1 : 2) : tile_height(M, (N + 255) / 256);
 #endif
   const int64_t mt = fm ? (M + 64 * fm - 1) / (64 * fm) : 0;
-  p.rotate = M > 256;
+  p.group = FP8_GROUP;
   if (f32_out && fm == 1) return run_fp8_tile<1, FP8_F32, 3, 2>(p, mt, st);
   if (f32_out && fm) return run_fp8_tile<2, FP8_F32, 3, 2>(p, mt, st);
   if (fm == 1) return run_fp8_tile<1, FP8_BF16, 3, 2>(p, mt, st);
@@ -270,7 +298,7 @@ hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const i
   p.saved_au = (bf16_t*)saved_au;
 #define RUN(FM, KIND, S, G)                                              \
   err = once ? run_fp8_tile<FM, KIND, S, 3>(G, mt, st) : run_fp8_tile<FM, KIND, S, 2>(G, mt, st);
-  p.rotate = !once;
+  p.group = FP8_GROUP;
   if (fm == 0) {
     fp8_rows16_kernel<true, false><<<(unsigned)((int64_t)mt * (f / 128)), 512, 0, st>>>(p);
     err = hipGetLastError();
@@ -294,7 +322,6 @@ hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const i
   q.out = ring_y;
   q.out_scale = nullptr;
   q.saved_au = nullptr;
-  q.rotate = !once;
   if (fm == 0) {
     fp8_rows16_kernel<false, false><<<(unsigned)((int64_t)mt * (d / 128)), 512, 0, st>>>(q);
     err = hipGetLastError();

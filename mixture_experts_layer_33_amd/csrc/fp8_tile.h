@@ -32,11 +32,12 @@ struct Fp8Args {
   void* out;               // SWIGLU: H codes [C, N]; else bf16 or fp32 [C, N]
   float* out_scale;        // SWIGLU: [N/128][C]
   bf16_t* saved_au;        // SWIGLU: [C, 2N] or NULL
-  int rotate;              // 1: tile L starts its K loop at block L mod (K / 128)
+  const bf16_t* add;       // TILE_ADD: [C, N] or NULL (may be out)
+  int group;               // row tiles that take the same column tile one after another
 };
 
-// Lane l's 32 bytes of a row's block: bytes 32 (l / 16) .. + 31.  (Which of the block's 128
-// positions a lane's byte is does not matter as long as both operands agree.)
+// Lane l's 32 bytes of a row's block.  (Which of the block's 128 positions a lane's byte is does
+// not matter as long as both operands agree.)
 __device__ __forceinline__ i32x8 fp8_join(u32x4 a, u32x4 b) {
   return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
@@ -71,39 +72,51 @@ __device__ __forceinline__ f32x4 fp8_wide16(const Wide16& w, const Wide16& a) {
   return c;
 }
 
-enum { FP8_BF16 = 0, FP8_F32 = 1, FP8_SWIGLU = 2, FP8_SWIGLU_SAVE = 3 };
+// TILE_ADD: bf16 operands (K: bytes of a row, a stage holds 64 elements) without scales, out = round(add + A W^T).
+enum { FP8_BF16 = 0, FP8_F32 = 1, TILE_ADD = 2, FP8_SWIGLU = 3, FP8_SWIGLU_SAVE = 4 };
 
-template <int FM>
+template <int FM, int KIND>
 struct Fp8Stage {
   static constexpr int BM = 64 * FM, BN = 256;
   static constexpr int A = 0, B = BM * 128, SC = B + BN * 128;   // SC: BM row scales, 2 block scales, padding
-  static constexpr int SIZE = SC + 8 * 256;
-  static constexpr int L = FM + 4 + 1;                           // copies per wavefront and stage
+  static constexpr int SIZE = SC + (KIND == TILE_ADD ? 0 : 8 * 256);
+  static constexpr int L = FM + 4 + (KIND == TILE_ADD ? 0 : 1);  // copies per wavefront and stage
 };
 
 template <int FM, int KIND, int S, int POL>
 __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
-  using SL = Fp8Stage<FM>;
+  using SL = Fp8Stage<FM, KIND>;
   constexpr int BM = SL::BM, BN = SL::BN, L = SL::L;
-  constexpr bool SWIGLU = KIND >= FP8_SWIGLU, WIDE = KIND == FP8_F32;
+  constexpr bool SWIGLU = KIND >= FP8_SWIGLU, WIDE = KIND == FP8_F32, ADD = KIND == TILE_ADD;
   static_assert(FM >= 1 && FM <= 4 && S >= 2 && S <= 4, "tile");
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
   constexpr int CB = SWIGLU ? 1 : 2;             // output blocks of 128 columns per tile
   const int nblk = (p.N + 127) / 128, nct = (nblk + CB - 1) / CB;
   const int nmt = p.offset ? *p.ntiles : (int)((p.a_rows + BM - 1) / BM);
-  int mt, ct;
-  if (!xcd_tile((int)blockIdx.x, nct, nmt, mt, ct)) return;
-  int e = 0, row0 = mt * BM, rows;
+  // Tile order: XCD x (workgroup b runs on XCD b % 8) takes one run of the logical tiles.  An expert's
+  // row tiles form groups of `group`; inside a group the column tile is the slower index, so that
+  // tiles running together on an XCD share both their token rows and their weight rows in its L2
+  // (groups of 4 against 1, 4 experts x 4,096 rows: 749 -> 737 us; starting tiles at different K blocks, as
+  // the bf16 GEMMs do, then loses: 752 us).
+  const int V = nmt * nct, per = (V + 7) / 8, li = (int)(blockIdx.x >> 3);
+  const int T = (int)(blockIdx.x & 7) * per + li;
+  if (li >= per || T >= V) return;
+  int e = 0, t0 = 0, R = nmt, mt = T / nct;      // expert, its first row tile, its row tiles
   int32_t seg = 0;
+  int64_t all = p.a_rows;                        // its rows
   if (p.offset) {
     e = p.tiles[2 * mt];
-    row0 = p.tiles[2 * mt + 1];
+    t0 = mt - p.tiles[2 * mt + 1] / BM;
     seg = p.offset[e];
-    rows = min(BM, p.offset[e + 1] - seg - row0);
-  } else {
-    rows = (int)min((int64_t)BM, p.a_rows - row0);
+    all = p.offset[e + 1] - seg;
+    R = (int)((all + BM - 1) / BM);
   }
+  const int local = T - t0 * nct, grp = local / (p.group * nct), rem = local - grp * p.group * nct;
+  const int rg = min(p.group, R - grp * p.group), ct = rem / rg;
+  const int rt = grp * p.group + rem % rg;       // the row tile inside its expert
+  mt = t0 + rt;
+  const int row0 = rt * BM, rows = (int)min((int64_t)BM, all - row0);
   const int n0 = ct * CB * 128;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -131,7 +144,11 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
     b_base[i] = (up ? p.W1 : p.W0) + (int64_t)e * p.N * K;
     b_off[i] = (uint32_t)min(n0 + (up ? r - 128 : r), p.N - 1) * K + c * 16;
   }
-  if (wave < FM) {                               // 64 row scales
+  if constexpr (ADD) {
+    s_base = nullptr;
+    s_off = 0;
+    s_step = 0;
+  } else if (wave < FM) {                        // 64 row scales
     const int r = 64 * wave + lane;
     s_base = (const uint8_t*)p.As;
     s_off = (uint32_t)ring_slot(p.head, seg, row0 + min(r, rows - 1), p.C) * 4;
@@ -145,10 +162,8 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
     s_off = (uint32_t)min(2 * ct + (lane & 1), nblk - 1) * KT * 4;
     s_step = 4;
   }
-  const int s0 = p.rotate ? (int)(((int64_t)mt * nct + ct) % KT) : 0;
-  auto issue_one = [&](int i_, int c) __attribute__((always_inline)) {
-    const uint32_t st = lds0 + (uint32_t)(i_ % S) * SL::SIZE;
-    const int kt = i_ + s0 >= KT ? i_ + s0 - KT : i_ + s0;
+  auto issue_one = [&](int kt, int c) __attribute__((always_inline)) {
+    const uint32_t st = lds0 + (uint32_t)(kt % S) * SL::SIZE;
     if (c < FM) {
       dma16(p.A + (size_t)kt * 128, a_off[c], __builtin_amdgcn_readfirstlane(st + SL::A + (8 * c + wave) * 1024));
     } else if (c < FM + 4) {
@@ -172,13 +187,17 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // a fragment's two 16-byte chunks of row r = 16 q + lr sit at r * 128 + ((2 lg + h) ^ (r >> 1 & 7)) * 16,
-  // and r >> 1 & 7 is lr >> 1: one per-lane offset and a multiple of 2048
-  const uint32_t l0 = (uint32_t)(lr * 128 + (((2 * lg) ^ ((lr >> 1) & 7)) << 4));
+  // A lane takes the 16-byte chunks lg and lg + 4 of row 16 q + lr, which sit at r * 128 + (chunk ^ (r >> 1 & 7)) * 16,
+  // and r >> 1 & 7 is lr >> 1: one per-lane offset and a multiple of 2048.  A 128-bit read is served in
+  // groups like lanes 0-3, 12-15, 20-27: with chunks that differ by 1 between lg = 0 and 1 (2 and 3) their
+  // 16 places are distinct; with chunks 2 lg, 2 lg + 1 the bank-conflict counter read 47 % of the
+  // LDS cycles (2,045 x 4,168 x 7,168: 80 -> 76 us).
+  const uint32_t l0 = (uint32_t)(lr * 128 + ((lg ^ ((lr >> 1) & 7)) << 4));
   auto bfrag = [&](int j) { return SWIGLU ? (j < 4 ? 4 * wn + j : 8 + 4 * wn + j - 4) : 8 * wn + j; };
 
   // One block of 128: NL live token fragments, and with COPY the copies of stage kt + S - 1 spread
-  // over the MFMAs.  The multiply-adds of an MFMA's result follow LAG MFMAs later, past the matrix
+  // over the MFMAs (with two stages they are issued at once instead, so that they have the
+  // whole step to land: 4 experts x 4,096 rows 762 -> 743 us).  The multiply-adds of an MFMA's result follow LAG MFMAs later, past the matrix
   // pipe's latency.  Both are compile-time choices: a branch inside the step would let the
   // compiler sink every multiply-add to the step's end, with all partial sums live.
   constexpr int LAG = 3;
@@ -197,7 +216,7 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
       // keep one address per fragment and stage live across the loop, which spills.
       const uint32_t st = (uint32_t)(kt % S) * SL::SIZE;
       uint32_t pa = st + SL::A + wm * 2048 + l0, pb = st + SL::B + wn * (SWIGLU ? 8192 : 16384) + l0;
-      uint32_t pa1 = st + SL::A + wm * 2048 + (l0 ^ 16), pb1 = st + SL::B + wn * (SWIGLU ? 8192 : 16384) + (l0 ^ 16);
+      uint32_t pa1 = st + SL::A + wm * 2048 + (l0 ^ 64), pb1 = st + SL::B + wn * (SWIGLU ? 8192 : 16384) + (l0 ^ 64);
       uint32_t ps = st + SL::SC + (16 * wm + lr) * 4;
       asm volatile("" : "+v"(pa), "+v"(pb), "+v"(pa1), "+v"(pb1), "+v"(ps));
       auto atile = [&](int i) __attribute__((always_inline)) {
@@ -207,6 +226,33 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
         const int q = SWIGLU && j >= 4 ? j + 4 : j;
         return fp8_join(*(const u32x4*)(lds + pb + q * 2048), *(const u32x4*)(lds + pb1 + q * 2048));
       };
+      if constexpr (ADD) {
+        i32x8 af[NL], bq[2];
+        bq[0] = btile(0);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) af[i] = atile(i);
+        auto half = [](const i32x8& v, int h) __attribute__((always_inline)) {
+          return __builtin_bit_cast(bf16x8, h ? __builtin_shufflevector(v, v, 4, 5, 6, 7) : __builtin_shufflevector(v, v, 0, 1, 2, 3));
+        };
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j + 1 < 8) bq[(j + 1) & 1] = btile(j + 1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+              const int m = (j * 2 + h) * NL + i;
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(half(bq[j & 1], h), half(af[i], h), acc[i][j], 0, 0, 0);
+              if constexpr (COPY) {
+#pragma unroll
+                for (int c = 0; c < L; ++c)
+                  if ((S == 2 ? (c < 2 * NM ? c : 2 * NM - 1) : c * 2 * NM / L) == m) issue_one(kt + S - 1, c);
+              }
+              __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        return;
+      }
       const float* sc = (const float*)(lds + st + SL::SC);
       i32x8 af[NL], bq[2];
       float t[NL][2];
@@ -245,7 +291,7 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
           if constexpr (COPY) {
 #pragma unroll
             for (int c = 0; c < L; ++c)
-              if (c * NM / L == m) issue_one(kt + S - 1, c);
+              if ((S == 2 ? (c < NM ? c : NM - 1) : c * NM / L) == m) issue_one(kt + S - 1, c);
           }
           if (m >= LAG) add(m - LAG);
           __builtin_amdgcn_sched_barrier(0);
@@ -342,6 +388,33 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
             fp8_encode4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], s);
     }
     flush((uint8_t*)p.out, p.N, n0, p.N, 144);
+  } else if constexpr (ADD) {
+    // fp32 halves of 128 columns through LDS (rows of 512 + 16 bytes), so that the addend is read and the
+    // sum written in whole 16-byte pieces
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (wn == h) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) *(f32x4*)(lds + (16 * (wm + 4 * i) + lr) * 528 + (16 * j + 4 * lg) * 4) = acc[i][j];
+      }
+      __syncthreads();
+#pragma unroll 4
+      for (int q = tid; q < BM * 16; q += 512) {
+        const int m = q / 16, col = n0 + 128 * h + (q % 16) * 8;
+        if (m < rows && col < p.N) {
+          const int64_t at = slot_of(m) * p.N + col;
+          const f32x4 a = *(const f32x4*)(lds + m * 528 + (q % 16) * 32), b = *(const f32x4*)(lds + m * 528 + (q % 16) * 32 + 16);
+          u32x4 w = {0, 0, 0, 0};
+          if (p.add) w = *(const u32x4*)(p.add + at);
+          *(u32x4*)((bf16_t*)p.out + at) =
+              u32x4{pack_bf2(lo_bf(w[0]) + a[0], hi_bf(w[0]) + a[1]), pack_bf2(lo_bf(w[1]) + a[2], hi_bf(w[1]) + a[3]),
+                    pack_bf2(lo_bf(w[2]) + b[0], hi_bf(w[2]) + b[1]), pack_bf2(lo_bf(w[3]) + b[2], hi_bf(w[3]) + b[3])};
+        }
+      }
+      __syncthreads();
+    }
   } else if constexpr (KIND == FP8_F32) {
     const bool whole = (p.N & 3) == 0 && ((uintptr_t)p.out & 15) == 0;
 #pragma unroll
@@ -387,8 +460,8 @@ template <int FM, int KIND, int S, int POL>
 inline hipError_t run_fp8_tile(const Fp8Args& a, int64_t max_tiles, hipStream_t st) {
   const int nblk = (a.N + 127) / 128, nct = KIND >= FP8_SWIGLU ? nblk : (nblk + 1) / 2;
   constexpr int BM = 64 * FM;
-  constexpr int epi = KIND == FP8_BF16 ? BM * 528 : KIND == FP8_SWIGLU_SAVE ? BM * 272 : KIND == FP8_SWIGLU ? BM * 144 : 0;
-  constexpr int ring = S * Fp8Stage<FM>::SIZE, lds = ring > epi ? ring : epi;
+  constexpr int epi = KIND == FP8_BF16 || KIND == TILE_ADD ? BM * 528 : KIND == FP8_SWIGLU_SAVE ? BM * 272 : KIND == FP8_SWIGLU ? BM * 144 : 0;
+  constexpr int ring = S * Fp8Stage<FM, KIND>::SIZE, lds = ring > epi ? ring : epi;
   static_assert(lds <= 160 * 1024, "LDS");
   auto kern = fp8_tile_kernel<FM, KIND, S, POL>;
   hipError_t err = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);

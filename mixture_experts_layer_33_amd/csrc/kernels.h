@@ -25,7 +25,7 @@ hipError_t launch_route_scored(const void* x, bool x_f32, const float* w_r, cons
                                const float* balance, const ScoreRule& rule, int64_t T, int d, int E,
                                int k, float* planes, int32_t* topk_idx, float* topk_gate,
                                int32_t* count, float* logits, hipStream_t st);
-size_t route_scored_bwd_workspace_bytes(int64_t T, int E, int d);
+size_t route_scored_bwd_workspace_bytes(bool f32, int64_t T, int E, int d);
 hipError_t launch_route_scored_bwd(bool f32, const ScoreRule& rule, const float* dgate,
                                    const float* dlogits, const void* x, const float* w_r,
                                    const float* logits, const int32_t* topk_idx, const void* dx_in,
@@ -59,6 +59,9 @@ size_t matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w,
                              const float* w_scale, int64_t M, int64_t N, int64_t K, bool f32_out,
                              void* out, void* ws, hipStream_t st);
+// out = round(add + A W^T) of bf16 rows (the tile of the FP8 products)
+struct Fp8Args;
+hipError_t launch_tile_add(Fp8Args& a, hipStream_t st);
 size_t ffn_fp8_workspace_bytes(int64_t n, int64_t C, int E, int f);
 hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const int32_t* expert_offset,
                           int64_t head, int64_t C, int64_t n, int d, int E, int f,

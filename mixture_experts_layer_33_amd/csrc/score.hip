@@ -9,8 +9,10 @@
 #include <algorithm>
 
 #include "common.h"
+#include "fp8_tile.h"
 #include "kernels.h"
 #include "route_body.h"
+#include "tr_read.h"
 
 namespace moe {
 
@@ -205,98 +207,279 @@ hipError_t launch_route_scored(const void* x, bool x_f32, const float* w_r, cons
 }
 
 // ----------------------------------------------------------------------------- gradient
-// dl [T, E] of the gates, one wavefront per token.  1 - s of a sigmoid is taken as
-// 1 / (1 + exp(l)), which keeps its digits where s is next to 1.
+// dl [T, E] of the gates, one wavefront per token and DL_TW tokens in turn.  1 - s of a sigmoid is
+// taken as 1 / (1 + exp(l)), which keeps its digits where s is next to 1.
+//
+// For bf16 tokens dl leaves as three bf16 parts, hi = bf16(dl), mid = bf16(dl - hi) and lo = bf16(dl - hi - mid),
+// which hold all 24 bits of it, as rows [hi | hi | mid] of 3 Ep values (Ep: E rounded up to 64, the
+// padding 0) and [lo] of Ep.  Against W_r's columns [hi | mid | hi] one product of length 3 Ep is dl W_r
+// to 2^-15 of its terms (mid x mid and the third parts are left out: dx is rounded to bf16, half a
+// step 2^-8); the three parts against the exact bf16 x are dl^T x to fp32, in which dW_r leaves.
+constexpr int DL_TW = 4;
+
 struct DlArgs {
   const float* dgate;
   const float* dlogits;
   const float* logits;
   const int32_t* topk_idx;
-  int64_t T;
-  int E, k;
+  int64_t T, Tp;        // Tp: rows written, those from T on zero
+  int E, Ep, k;
   ScoreRule rule;
-  float* dl;
+  float* dl;            // fp32 tokens: [T, E]
+  bf16_t* planes;       // bf16 tokens: [Tp, 3 Ep]
+  bf16_t* low;          // bf16 tokens: [Tp, Ep]
+  uint32_t* zero;       // bf16 tokens: 256 words set to 0
+  float* db_part;       // [workgroups, E] sums over a workgroup's tokens, or NULL
 };
 
-template <int VPL>
+template <int VPL, bool F32>
 __global__ __launch_bounds__(256) void score_dl_kernel(DlArgs p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= p.T) return;
+  __shared__ float dbs[4][64 * VPL];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int E = p.E, k = p.k;
-  float l[VPL], dl[VPL];
-  float dg = 0.f, lj = -INFINITY;
-  int ej = -1;
-  if (lane < k) {
-    const int e = p.topk_idx[t * k + lane];
-    if (e >= 0 && e < E) {
-      ej = e;
-      dg = p.rule.scale * p.dgate[t * k + lane];
-      lj = p.logits[t * E + e];
+  if (!F32 && blockIdx.x == 0) p.zero[threadIdx.x] = 0u;
+  float db[VPL] = {};
+  for (int w = 0; w < DL_TW; ++w) {
+    const int64_t t = ((int64_t)blockIdx.x * 4 + wave) * DL_TW + w;
+    if (t >= p.Tp) break;
+    const bool ok = t < p.T;
+    float l[VPL], dl[VPL];
+    float dg = 0.f, lj = -INFINITY;
+    int ej = -1;
+    if (ok && lane < k) {
+      const int e = p.topk_idx[t * k + lane];
+      if (e >= 0 && e < E) {
+        ej = e;
+        dg = p.rule.scale * p.dgate[t * k + lane];
+        lj = p.logits[t * E + e];
+      }
     }
-  }
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 64 * i;
-    l[i] = e < E ? p.logits[t * E + e] : -INFINITY;
-    dl[i] = 0.f;
-  }
-  float v = 0.f;   // lane j: dl of the j-th chosen expert (the softmax's own part)
-  if (p.rule.renormalise) {
-    float g;
-    if (p.rule.sigmoid) g = 1.0f / (1.0f + expf(-lj));
-    else {
-      const float m = group_max<64>(lj);
-      g = lj == -INFINITY ? 0.f : expf(lj - m);
-    }
-    g = ej >= 0 ? g : 0.f;
-    const float sum = wave_sum(g);
-    g = sum == 0.f ? 0.f : g / sum;
-    v = g * (dg - wave_sum(g * dg));
-    if (p.rule.sigmoid) v *= 1.0f / (1.0f + expf(lj));
-  } else if (p.rule.sigmoid) {
-    v = dg * (1.0f / (1.0f + expf(-lj))) * (1.0f / (1.0f + expf(lj)));
-  } else {
-    float m = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) m = fmaxf(m, l[i]);
-    m = group_max<64>(m);
+    const bool dense = !p.rule.renormalise && !p.rule.sigmoid;   // every logit moves every softmax score
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      l[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - m);
-      sum += l[i];
+      const int e = lane + 64 * i;
+      l[i] = dense && ok && e < E ? p.logits[t * E + e] : -INFINITY;
+      dl[i] = ok && e < E && p.dlogits ? p.dlogits[t * E + e] : 0.f;
     }
-    sum = wave_sum(sum);
-    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-    v = ej >= 0 && lj != -INFINITY ? expf(lj - m) * inv * dg : 0.f;
-    const float all = wave_sum(v);
+    float v = 0.f;   // lane j: dl of the j-th chosen expert (the softmax's own part)
+    if (p.rule.renormalise) {
+      float g;
+      if (p.rule.sigmoid) g = 1.0f / (1.0f + expf(-lj));
+      else {
+        const float m = group_max<64>(lj);
+        g = lj == -INFINITY ? 0.f : expf(lj - m);
+      }
+      g = ej >= 0 ? g : 0.f;
+      const float sum = wave_sum(g);
+      g = sum == 0.f ? 0.f : g / sum;
+      v = g * (dg - wave_sum(g * dg));
+      if (p.rule.sigmoid) v *= 1.0f / (1.0f + expf(lj));
+    } else if (p.rule.sigmoid) {
+      v = dg * (1.0f / (1.0f + expf(-lj))) * (1.0f / (1.0f + expf(lj)));
+    } else {
+      float m = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) dl[i] = -l[i] * inv * all;
+      for (int i = 0; i < VPL; ++i) m = fmaxf(m, l[i]);
+      m = group_max<64>(m);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        l[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - m);
+        sum += l[i];
+      }
+      sum = wave_sum(sum);
+      const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+      v = ej >= 0 && lj != -INFINITY ? expf(lj - m) * inv * dg : 0.f;
+      const float all = wave_sum(v);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) dl[i] -= l[i] * inv * all;
+    }
+    if (ej < 0 || lj == -INFINITY) v = 0.f;
+    for (int j = 0; j < k; ++j) {
+      const int e = __builtin_amdgcn_readlane(ej, j);
+      const float add = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j));
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (lane + 64 * i == e) dl[i] += add;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane + 64 * i;
+      db[i] += dl[i];
+      if constexpr (F32) {
+        if (e < E) p.dl[t * E + e] = dl[i];
+      } else if (e < p.Ep) {
+        const bf16_t hi = f2bf(dl[i]), mid = f2bf(dl[i] - bf2f(hi));
+        bf16_t* row = p.planes + t * 3 * p.Ep + e;
+        row[0] = hi;
+        row[p.Ep] = hi;
+        row[2 * p.Ep] = mid;
+        p.low[t * p.Ep + e] = f2bf(dl[i] - bf2f(hi) - bf2f(mid));
+      }
+    }
   }
-  if (ej < 0 || lj == -INFINITY) v = 0.f;
-  for (int j = 0; j < k; ++j) {
-    const int e = __builtin_amdgcn_readlane(ej, j);
-    const float add = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j));
+  if (!p.db_part) return;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane + 64 * i == e) dl[i] += add;
+  for (int i = 0; i < VPL; ++i) dbs[wave][lane + 64 * i] = db[i];
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += 256)
+    p.db_part[(int64_t)blockIdx.x * E + e] = (dbs[0][e] + dbs[1][e]) + (dbs[2][e] + dbs[3][e]);
+}
+
+// W_r [E, d] fp32 -> [d, 3 Ep] bf16, rows [hi | mid | hi] of W_r's columns (64 x 64 per workgroup,
+// turned through LDS).
+__global__ __launch_bounds__(256) void score_turn_kernel(const float* __restrict__ w_r, int E, int Ep, int d,
+                                                         bf16_t* __restrict__ out) {
+  __shared__ float tile[64][65];
+  const int c0 = blockIdx.x * 64, e0 = blockIdx.y * 64;
+  for (int q = threadIdx.x; q < 64 * 64; q += 256) {
+    const int e = q / 64, c = q % 64;
+    tile[e][c] = e0 + e < E ? w_r[(int64_t)(e0 + e) * d + c0 + c] : 0.f;   // d is a multiple of 64
   }
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 64 * i;
-    if (e < E) p.dl[t * E + e] = dl[i] + (p.dlogits ? p.dlogits[t * E + e] : 0.f);
+  __syncthreads();
+  for (int q = threadIdx.x; q < 64 * 64; q += 256) {
+    const int c = q / 64, e = q % 64;
+    const float v = tile[e][c];
+    const bf16_t hi = f2bf(v), mid = f2bf(v - bf2f(hi));
+    bf16_t* row = out + (int64_t)(c0 + c) * 3 * Ep + e0 + e;
+    row[0] = hi;
+    row[Ep] = mid;
+    row[2 * Ep] = hi;
   }
 }
 
-// dx [T, d] = dx_in + dl [T, E] W_r [E, d], and partial planes of dW_r [E, d] = dl^T x.
-// 64 x 64 tiles, 256 threads of 4 x 4, the reduction in steps of 16 through LDS, each step's
+// Partial planes of dW_r [E, d] = dl^T x for bf16 tokens.  Both operands are row-major with the
+// reduction index (the token) as the row, so a stage holds 32 token rows of each as they are and the
+// MFMA fragments are read with the transposing LDS reads of the weight gradients
+// (backward.hip).  256 experts x 256 columns per workgroup, eight wavefronts of 64 x 128; the
+// tokens run three times, against the parts of dl in turn, and are split over Z workgroups, each
+// with a plane of its own.  Split z runs on XCD z (Z = 8), so that a token row of x crosses into one
+// L2 only.
+struct DwArgs {
+  const bf16_t* planes;   // [Tp, 3 Ep]: hi | hi | mid
+  const bf16_t* low;      // [Tp, Ep]
+  const bf16_t* x;        // [T, d]
+  const bf16_t* zero;     // 1 KB of zeros: rows past T of x
+  int64_t T, Tp;
+  int E, Ep, d, Z;
+  float* part;            // [Z, E, d]
+};
+constexpr int DW_M = 256, DW_N = 256, DW_K = 32, DW_S = 4, DW_ROW = 512;   // bytes of a staged row
+constexpr int DW_STAGE = DW_K * 2 * DW_ROW, DW_LDS = DW_S * DW_STAGE;
+
+__global__ __launch_bounds__(512) void score_dw_mfma_kernel(DwArgs p) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+  const int z = blockIdx.x % p.Z, tile = blockIdx.x / p.Z;
+  const int mt = (p.E + DW_M - 1) / DW_M;
+  const int m0 = (tile % mt) * DW_M, n0 = (tile / mt) * DW_N;
+  const int64_t steps = p.Tp / DW_K, all = 3 * steps;
+  const int64_t s0 = all * z / p.Z;
+  const int KT = (int)(all * (z + 1) / p.Z - s0);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1, lr = lane & 31, lg = lane >> 5;
+  // copies: kilobyte 8 c + wave of an operand's stage is its rows 2 (8 c + wave) and + 1
+  const int crow = lane / 32;
+  int acol[2], bcol[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int r = 2 * (8 * c + wave) + crow, lc = wsw(r, lane % 32);
+    acol[c] = min(m0 + lc * 8, p.Ep - 8);
+    bcol[c] = min(n0 + lc * 8, p.d - 8);
+  }
+  auto issue = [&](int i) __attribute__((always_inline)) {
+    const uint32_t st = lds0 + (uint32_t)(i % DW_S) * DW_STAGE;
+    const int64_t s = s0 + i;
+    const int part = s < steps ? 0 : s < 2 * steps ? 1 : 2;
+    const int64_t r0 = (s - part * steps) * DW_K;
+    const bf16_t* a = part == 2 ? p.low : p.planes + (part ? 2 * p.Ep : 0);
+    const int lda = part == 2 ? p.Ep : 3 * p.Ep;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int64_t t = r0 + 2 * (8 * c + wave) + crow;
+      dma16_at(a + t * lda + acol[c],
+               __builtin_amdgcn_readfirstlane(st + (8 * c + wave) * 1024));
+      dma16_at(t < p.T ? p.x + t * p.d + bcol[c] : p.zero + (lane & 31) * 8,
+               __builtin_amdgcn_readfirstlane(st + DW_K * DW_ROW + (8 * c + wave) * 1024));
+    }
+  };
+  f32x16 acc[4][2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.f;
+  int foff[6];
+  {
+    const int g = lane >> 4, gi = lane & 15, qq = gi >> 2, ss = gi & 3;
+    const int r0 = 8 * (g >> 1) + qq;
+#pragma unroll
+    for (int q = 0; q < 6; ++q) {
+      const int col = (q < 2 ? wm * 64 + q * 32 : wn * 128 + (q - 2) * 32) + 16 * (g & 1) + 4 * ss;
+      foff[q] = (q < 2 ? 0 : DW_K * DW_ROW) + r0 * DW_ROW + wsw(r0, col >> 3) * 16 + (col & 7) * 2;
+    }
+  }
+  auto frag = [&](const uint8_t* sb, int kk, int q) __attribute__((always_inline)) -> bf16x8 {
+    const uint8_t* a = sb + foff[q] + kk * 16 * DW_ROW;
+    const v4i16_t lo = ds_tr16(a), hi = ds_tr16(a + 4 * DW_ROW);
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  for (int s = 0; s < DW_S - 1 && s < KT; ++s) issue(s);
+  for (int kt = 0; kt < KT; ++kt) {
+    const int later = min(DW_S - 2, KT - 1 - kt);
+    if (later >= 2) bwait_vm<8>();
+    else if (later == 1) bwait_vm<4>();
+    else bwait_vm<0>();
+    __syncthreads();
+    if (kt + DW_S - 1 < KT) issue(kt + DW_S - 1);
+    const uint8_t* sb = lds + (kt % DW_S) * DW_STAGE;
+#pragma unroll
+    for (int kk = 0; kk < DW_K / 16; ++kk) {
+      bf16x8 fa[2], fb[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) fa[i] = frag(sb, kk, i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fb[j] = frag(sb, kk, 2 + j);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[j][i], 0, 0, 0);
+    }
+  }
+  // acc[j][i][r]: expert m0 + 64 wm + 32 i + lr, column n0 + 128 wn + 32 j + 8 (r / 4) + 4 lg + r % 4.  Each half i is
+  // staged in a wavefront's own 16 KB (32 rows of 32 16-byte chunks, XOR-swizzled by the row) and
+  // written as whole rows of 512 bytes.
+  __syncthreads();
+  uint8_t* wl = lds + wave * 16384;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        *(f32x4*)(wl + lr * 512 + (((8 * j + 2 * h + lg) ^ lr) << 4)) =
+            f32x4{acc[j][i][4 * h], acc[j][i][4 * h + 1], acc[j][i][4 * h + 2], acc[j][i][4 * h + 3]};
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 4
+    for (int q = 0; q < 16; ++q) {
+      const int r = 2 * q + (lane >> 5), c = lane & 31;
+      const f32x4 v = *(const f32x4*)(wl + r * 512 + ((c ^ r) << 4));
+      const int e = m0 + wm * 64 + 32 * i + r, n = n0 + wn * 128 + 4 * c;
+      if (e < p.E && n < p.d) *(f32x4*)(p.part + ((int64_t)z * p.E + e) * p.d + n) = v;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// fp32 tokens: dx [T, d] = dx_in + dl [T, E] W_r [E, d], and partial planes of dW_r [E, d] = dl^T x, on the
+// vector units.  64 x 64 tiles, 256 threads of 4 x 4, the reduction in steps of 16 through LDS, each step's
 // sum added to the running one (two levels).
 constexpr int GB = 64, GK = 16;
 
-template <bool F32>
 __global__ __launch_bounds__(256) void score_dx_kernel(const float* __restrict__ dl,
-                                                       const float* __restrict__ w_r, const void* dx_in,
-                                                       int64_t T, int E, int d, void* dx) {
+                                                       const float* __restrict__ w_r, const float* dx_in,
+                                                       int64_t T, int E, int d, float* dx) {
   __shared__ float as[GK][GB + 4], bs[GK][GB + 4];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int64_t t0 = (int64_t)blockIdx.y * GB;
@@ -332,14 +515,12 @@ __global__ __launch_bounds__(256) void score_dx_kernel(const float* __restrict__
       const int c = c0 + tx * 4 + j;
       if (t < T && c < d) {
         const int64_t at = t * d + c;
-        if constexpr (F32) ((float*)dx)[at] = (dx_in ? ((const float*)dx_in)[at] : 0.f) + acc[i][j];
-        else ((bf16_t*)dx)[at] = f2bf((dx_in ? bf2f(((const bf16_t*)dx_in)[at]) : 0.f) + acc[i][j]);
+        dx[at] = (dx_in ? dx_in[at] : 0.f) + acc[i][j];
       }
     }
 }
 
-template <bool F32>
-__global__ __launch_bounds__(256) void score_dw_kernel(const float* __restrict__ dl, const void* __restrict__ x,
+__global__ __launch_bounds__(256) void score_dw_kernel(const float* __restrict__ dl, const float* __restrict__ x,
                                                        int64_t T, int E, int d, float* __restrict__ part) {
   __shared__ float as[GK][GB + 4], bs[GK][GB + 4];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -354,7 +535,7 @@ __global__ __launch_bounds__(256) void score_dw_kernel(const float* __restrict__
       const int64_t t = s * GK + kr;
       as[kr][c] = t < T && e0 + c < E ? dl[t * E + e0 + c] : 0.f;
       float v = 0.f;
-      if (t < T && c0 + c < d) v = F32 ? ((const float*)x)[t * d + c0 + c] : bf2f(((const bf16_t*)x)[t * d + c0 + c]);
+      if (t < T && c0 + c < d) v = x[t * d + c0 + c];
       bs[kr][c] = v;
     }
     __syncthreads();
@@ -390,37 +571,38 @@ __global__ __launch_bounds__(256) void plane_sum_kernel(const float* __restrict_
   *(f32x4*)(out + i) = s;
 }
 
-// db partials: workgroup b adds rows b, b + G, ... of dl.
-constexpr int DB_G = 64;
-__global__ __launch_bounds__(256) void score_db_kernel(const float* __restrict__ dl, int64_t T, int E,
-                                                       float* __restrict__ part) {
-  for (int e = threadIdx.x; e < E; e += 256) {
-    float s = 0.f;
-    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) s += dl[t * E + e];
-    part[(int64_t)blockIdx.x * E + e] = s;
-  }
-}
-
-static int dw_splits(int64_t T, int E, int d) {
-  const int64_t tiles = (int64_t)((E + GB - 1) / GB) * ((d + GB - 1) / GB);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({8, 1024 / tiles, T / 128}));
+static int dw_splits(bool f32, int64_t T, int E, int d) {
+  const int m = f32 ? GB : DW_M, n = f32 ? GB : DW_N;
+  const int64_t tiles = (int64_t)((E + m - 1) / m) * ((d + n - 1) / n);
+  // fp32: about four workgroups a CU; bf16: one, and at least 8 stages of each
+  const int64_t most = f32 ? std::min<int64_t>(1024 / tiles, T / 128) : std::min<int64_t>(256 / tiles, T / 128);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(8, most));
 }
 
 struct ScoreBwdLayout {
-  size_t dl, dw, db, total;
+  size_t dl, low, wt, zero, dw, db, total;
+  int64_t Tp;
+  int Ep, Z, G;
 };
-static ScoreBwdLayout score_bwd_layout(int64_t T, int E, int d) {
+static ScoreBwdLayout score_bwd_layout(bool f32, int64_t T, int E, int d) {
   auto al = [](size_t b) { return (b + 255) & ~(size_t)255; };
   ScoreBwdLayout L;
+  L.Ep = (E + 63) / 64 * 64;
+  L.Tp = f32 ? T : (T + DW_K - 1) / DW_K * DW_K;
+  L.Z = dw_splits(f32, T, E, d);
+  L.G = (int)((L.Tp + 4 * DL_TW - 1) / (4 * DL_TW));
   size_t o = 0;
-  L.dl = o; o += al((size_t)T * E * 4);
-  L.dw = o; o += al((size_t)dw_splits(T, E, d) * E * d * 4);
-  L.db = o; o += al((size_t)DB_G * E * 4);
+  L.dl = o; o += al(f32 ? (size_t)T * E * 4 : (size_t)L.Tp * 3 * L.Ep * 2);
+  L.low = o; o += f32 ? 0 : al((size_t)L.Tp * L.Ep * 2);
+  L.wt = o; o += f32 ? 0 : al((size_t)d * 3 * L.Ep * 2);
+  L.zero = o; o += 1024;
+  L.dw = o; o += al((size_t)L.Z * E * d * 4);
+  L.db = o; o += al((size_t)L.G * E * 4);
   L.total = o;
   return L;
 }
-size_t route_scored_bwd_workspace_bytes(int64_t T, int E, int d) {
-  return T == 0 ? 0 : score_bwd_layout(T, E, d).total;
+size_t route_scored_bwd_workspace_bytes(bool f32, int64_t T, int E, int d) {
+  return T == 0 ? 0 : score_bwd_layout(f32, T, E, d).total;
 }
 
 hipError_t launch_route_scored_bwd(bool f32, const ScoreRule& rule, const float* dgate,
@@ -428,36 +610,58 @@ hipError_t launch_route_scored_bwd(bool f32, const ScoreRule& rule, const float*
                                    const float* logits, const int32_t* topk_idx, const void* dx_in,
                                    int64_t T, int d, int E, int k, void* dx, float* dw, float* db,
                                    void* ws, hipStream_t st) {
-  const ScoreBwdLayout L = score_bwd_layout(T, E, d);
-  float* dl = (float*)((uint8_t*)ws + L.dl);
-  float* part = (float*)((uint8_t*)ws + L.dw);
-  float* dbp = (float*)((uint8_t*)ws + L.db);
-  const DlArgs p{dgate, dlogits, logits, topk_idx, T, E, k, rule, dl};
-  const unsigned g = (unsigned)((T + 3) / 4);
+  const ScoreBwdLayout L = score_bwd_layout(f32, T, E, d);
+  uint8_t* w = (uint8_t*)ws;
+  float* part = L.Z > 1 ? (float*)(w + L.dw) : dw;
+  float* dbp = (float*)(w + L.db);
+  const DlArgs p{dgate, dlogits, logits, topk_idx, T, L.Tp, E, L.Ep, k, rule, (float*)(w + L.dl),
+                 (bf16_t*)(w + L.dl), (bf16_t*)(w + L.low), (uint32_t*)(w + L.zero), db ? dbp : nullptr};
   const int vpl = (E + 63) / 64;
-  if (vpl <= 1) score_dl_kernel<1><<<g, 256, 0, st>>>(p);
-  else if (vpl <= 2) score_dl_kernel<2><<<g, 256, 0, st>>>(p);
-  else if (vpl <= 4) score_dl_kernel<4><<<g, 256, 0, st>>>(p);
-  else if (vpl <= 8) score_dl_kernel<8><<<g, 256, 0, st>>>(p);
-  else score_dl_kernel<16><<<g, 256, 0, st>>>(p);
-  const dim3 gx((d + GB - 1) / GB, (unsigned)((T + GB - 1) / GB));
-  const int Z = dw_splits(T, E, d);
-  const dim3 gw((d + GB - 1) / GB, (E + GB - 1) / GB, Z);
+#define DL(V)                                                                   \
+  {                                                                             \
+    if (f32) score_dl_kernel<V, true><<<(unsigned)L.G, 256, 0, st>>>(p);        \
+    else score_dl_kernel<V, false><<<(unsigned)L.G, 256, 0, st>>>(p);           \
+  }
+  if (vpl <= 1) DL(1)
+  else if (vpl <= 2) DL(2)
+  else if (vpl <= 4) DL(4)
+  else if (vpl <= 8) DL(8)
+  else DL(16)
+#undef DL
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
   if (f32) {
-    score_dx_kernel<true><<<gx, 256, 0, st>>>(dl, w_r, dx_in, T, E, d, dx);
-    score_dw_kernel<true><<<gw, 256, 0, st>>>(dl, x, T, E, d, part);
+    score_dx_kernel<<<dim3((d + GB - 1) / GB, (unsigned)((T + GB - 1) / GB)), 256, 0, st>>>(
+        p.dl, w_r, (const float*)dx_in, T, E, d, (float*)dx);
+    score_dw_kernel<<<dim3((d + GB - 1) / GB, (E + GB - 1) / GB, L.Z), 256, 0, st>>>(p.dl, (const float*)x, T, E,
+                                                                                    d, part);
   } else {
-    score_dx_kernel<false><<<gx, 256, 0, st>>>(dl, w_r, dx_in, T, E, d, dx);
-    score_dw_kernel<false><<<gw, 256, 0, st>>>(dl, x, T, E, d, part);
+    bf16_t* wt = (bf16_t*)(w + L.wt);
+    score_turn_kernel<<<dim3(d / 64, L.Ep / 64), 256, 0, st>>>(w_r, E, L.Ep, d, wt);
+    // dx: at most 2^18 rows a launch (32-bit offsets inside the operands)
+    for (int64_t t0 = 0; t0 < T; t0 += (int64_t)1 << 18) {
+      Fp8Args a{};
+      a.A = (const uint8_t*)(p.planes + t0 * 3 * L.Ep);
+      a.W0 = (const uint8_t*)wt;
+      a.a_rows = std::min<int64_t>(T - t0, (int64_t)1 << 18);
+      a.C = a.a_rows;
+      a.K = 6 * L.Ep;
+      a.N = d;
+      a.out = (bf16_t*)dx + t0 * d;
+      a.add = dx_in ? (const bf16_t*)dx_in + t0 * d : nullptr;
+      if ((err = launch_tile_add(a, st)) != hipSuccess) return err;
+    }
+    const DwArgs a{p.planes, p.low, (const bf16_t*)x, (const bf16_t*)p.zero, T, L.Tp, E, L.Ep, d, L.Z, part};
+    if ((err = hipFuncSetAttribute((const void*)score_dw_mfma_kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                   DW_LDS)) != hipSuccess)
+      return err;
+    const int64_t tiles = (int64_t)((E + DW_M - 1) / DW_M) * ((d + DW_N - 1) / DW_N);
+    score_dw_mfma_kernel<<<(unsigned)(tiles * L.Z), 512, DW_LDS, st>>>(a);
   }
+  if ((err = hipGetLastError()) != hipSuccess) return err;
   const int64_t n = (int64_t)E * d;
-  plane_sum_kernel<<<(unsigned)((n / 4 + 255) / 256), 256, 0, st>>>(part, Z, n, dw);
-  if (db) {
-    const int G = (int)std::min<int64_t>(T, DB_G);
-    score_db_kernel<<<G, 256, 0, st>>>(dl, T, E, dbp);
-    hipError_t err = launch_column_sum(dbp, G, E, db, st);
-    if (err != hipSuccess) return err;
-  }
+  if (L.Z > 1) plane_sum_kernel<<<(unsigned)((n / 4 + 255) / 256), 256, 0, st>>>(part, L.Z, n, dw);
+  if (db && (err = launch_column_sum(dbp, L.G, E, db, st)) != hipSuccess) return err;
   return hipGetLastError();
 }
 
