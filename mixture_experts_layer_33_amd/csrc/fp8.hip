@@ -96,84 +96,253 @@ hipError_t launch_quantize_fp8(const void* src, int64_t rows, int64_t cols, int 
 }
 
 // ----------------------------------------------------------------------------- products
-// 16 token rows per tile; 8 wavefronts of 16 weight rows (SWIGLU: 16 gate and 16 up rows), so a
-// workgroup covers one block of 128 output columns and a SWIGLU tile holds whole H blocks.
-// Result i of lane l: output column n0 + 16 wave + 4 (l / 16) + i of token row l % 16.
-template <bool SWIGLU, bool F32>
-__global__ __launch_bounds__(512) void fp8_rows16_kernel(Fp8Args p) {
+// Wait until at most n stages of L copies are outstanding.
+template <int L, int MOST>
+__device__ __forceinline__ void wait_stages(int n) {
+  if constexpr (MOST == 0) wait_vm<0>();
+  else if (n >= MOST) wait_vm<MOST * L>();
+  else wait_stages<L, MOST - 1>(n);
+}
+
+// Row tile mt of 16 rows in expert-major order, found by every wavefront for itself from the segment offsets
+// (lane l counts the tiles of experts l V .. l V + V - 1): a separate launch for a tile list costs more
+// than a few tokens' products can spare (4.7 of 75 us).  False past the last tile.
+__device__ __forceinline__ bool thin_tile(const int32_t* offset, int E, int mt, int& e, int& row0, int32_t& seg,
+                                          int& rows) {
+  const int lane = threadIdx.x & 63, V = (E + 63) / 64, e0 = lane * V;
+  auto at = [&](int i) { return offset[min(e0 + i, E)]; };
+  int n = 0;
+  int32_t lo = at(0);
+  for (int i = 1; i <= V; ++i) {
+    const int32_t hi = at(i);
+    n += (hi - lo + 15) / 16;
+    lo = hi;
+  }
+  int incl = n;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += v;
+  }
+  const unsigned long long past = __ballot(incl > mt);
+  if (past == 0) return false;
+  const int owner = __builtin_ctzll(past);
+  int left = mt - (__builtin_amdgcn_readlane(incl, owner) - __builtin_amdgcn_readlane(n, owner));
+  for (int i = owner * V;; ++i) {   // ends: the owner's experts hold tile `left`
+    const int32_t a = offset[i], b = offset[i + 1];
+    const int t = (b - a + 15) / 16;
+    if (left < t) {
+      e = i;
+      row0 = 16 * left;
+      seg = a;
+      rows = min(16, b - a - row0);
+      return true;
+    }
+    left -= t;
+  }
+}
+
+// Few token rows: a weight stream.  16 token rows x 32 W weight rows, W wavefronts, each with 32 weight rows
+// (SWIGLU: 16 gate and the matching 16 up rows; W = 8: a workgroup's 128 columns are a whole block of H, which
+// it quantises; W = 4: twice the workgroups where 128 columns each would leave half of the chip
+// idle, h in fp32 for quantise_h_kernel).  The work is one pass over the weights, so what counts is bytes in flight: S stages
+// of whole 128-byte lines are copied global -> LDS, S - 1 of them ahead.  The same stream read straight
+// into registers in the MFMA's layout asks for each line in halves by 16 rows and ran at 3.7 TB/s where
+// this one runs at 5 to 6 (one token, 8 of 64 experts, d 7168, f 2048).
+//
+// Per stage a wavefront issues four 1 KB copies of weights and EX small ones: the token rows' two
+// kilobytes, the row scales and the block scales, dealt to the wavefronts in turn and padded with
+// repeats so that all issue the same number (the stage waits count them).
+template <int W, int S>
+struct ThinStage {
+  static constexpr int EX = (5 + W - 1) / W, L = 4 + EX;
+  static constexpr int B = 0, A = W * 4096, SC = A + 2048;       // SC: row scales, S0's, S1's, padding
+  static constexpr int SIZE = SC + 4 * 256;
+};
+
+template <int KIND, int W, int S>
+__global__ __launch_bounds__(64 * W) void fp8_thin_kernel(Fp8Args p) {
+  using SL = ThinStage<W, S>;
+  constexpr bool SWIGLU = KIND >= FP8_SWIGLU, WIDE = KIND == FP8_F32;
+  constexpr int L = SL::L, COLS = SWIGLU ? 16 * W : 32 * W;
+  static_assert(!SWIGLU || W == 8 || W == 4, "a SWIGLU tile holds a block of H or half of one");
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   __shared__ float hmax[8][16];
-  const int nct = (p.N + 127) / 128;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lr = lane & 15, lg = lane >> 4;
+  const int nct = (p.N + COLS - 1) / COLS, nblk = (p.N + 127) / 128;
   const int mt = blockIdx.x / nct, ct = blockIdx.x % nct;
-  int e = 0, row0 = 16 * mt, rows;
-  int64_t seg = 0;
+  int e = 0, row0 = 16 * mt, rows = 16;
+  int32_t seg = 0;
   if (p.offset) {
-    if (mt >= *p.ntiles) return;
-    e = p.tiles[2 * mt];
-    row0 = p.tiles[2 * mt + 1];
-    seg = p.offset[e];
-    rows = min(16, p.offset[e + 1] - (int)seg - row0);
+    if (!thin_tile(p.offset, p.E, mt, e, row0, seg, rows)) return;
+    auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    e = uni(e); row0 = uni(row0); seg = uni(seg); rows = uni(rows);
   } else {
     rows = (int)min((int64_t)16, p.a_rows - row0);
   }
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
-  const int KB = p.K / 128;
-  const int64_t slot = ring_slot(p.head, seg, row0 + min(m, rows - 1), p.C);
-  const uint8_t* a = p.A + slot * p.K + g * 32;
-  const float* as = p.As + slot;
-  const int64_t wrow = (int64_t)e * p.N + min(128 * ct + 16 * wave + m, p.N - 1);
-  const uint8_t* w0 = p.W0 + wrow * p.K + g * 32;
-  const uint8_t* w1 = SWIGLU ? p.W1 + wrow * p.K + g * 32 : nullptr;
-  const float* s0 = p.S0 + ((int64_t)e * nct + ct) * KB;
-  const float* s1 = SWIGLU ? p.S1 + ((int64_t)e * nct + ct) * KB : nullptr;
-  f32x4 c0 = {0.f, 0.f, 0.f, 0.f}, c1 = c0;
-#pragma unroll 4
-  for (int b = 0; b < KB; ++b) {
-    const i32x8 av = fp8_frag(a + (int64_t)b * 128);
-    const float sa = as[b * p.a_rows];
-    const i32x8 wv = fp8_frag(w0 + (int64_t)b * 128);
-    const f32x4 q0 = F32 ? fp8_wide16(fp8_widen(wv), fp8_widen(av)) : fp8_mfma16(wv, av);
-    const float t0 = sa * s0[b];
+  const uint32_t K = (uint32_t)p.K;
+  const int KT = p.K / 128, n0 = COLS * ct;
+  auto slot_of = [&](int m) { return ring_slot(p.head, seg, row0 + m, p.C); };
+
+  // weights: copy i is kilobyte W i + wave of the tile, rows 8 (W i + wave) .. + 7
+  const uint8_t* b_base[4];
+  uint32_t b_off[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c0[i] = fmaf(q0[i], t0, c0[i]);
-    if constexpr (SWIGLU) {
-      const f32x4 q1 = fp8_mfma16(fp8_frag(w1 + (int64_t)b * 128), av);
-      const float t1 = sa * s1[b];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c1[i] = fmaf(q1[i], t1, c1[i]);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * (W * i + wave) + lane / 8, c = (swz<128>(r, lane % 8) - r * 128) >> 4;
+    const bool up = SWIGLU && i >= 2;
+    b_base[i] = (up ? p.W1 : p.W0) + (int64_t)e * p.N * K;
+    b_off[i] = (uint32_t)min(n0 + (up ? r - 16 * W : r), p.N - 1) * K + c * 16;
   }
-  const int col = 128 * ct + 16 * wave + 4 * g;
+  // small copy x of a stage (wavefront x % W): 0, 1 token rows, 2 row scales, 3 S0's, 4 S1's block scale, then repeats
+  auto small = [&](int x, int kt, uint32_t st) __attribute__((always_inline)) {
+    if (x < 2) {
+      const int r = 8 * x + lane / 8, c = (swz<128>(r, lane % 8) - r * 128) >> 4;
+      dma16(p.A + (size_t)kt * 128, (uint32_t)slot_of(min(r, rows - 1)) * K + c * 16,
+            __builtin_amdgcn_readfirstlane(st + SL::A + x * 1024));
+    } else if (x == 2) {
+      dma4((const uint8_t*)(p.As + (size_t)kt * p.a_rows), (uint32_t)slot_of(min(lr, rows - 1)) * 4,
+           __builtin_amdgcn_readfirstlane(st + SL::SC));
+    } else {
+      const float* s = SWIGLU && x == 4 ? p.S1 : p.S0;
+      // the block of this lane's column: lane l < W of the plain product holds wavefront l's
+      const int blk = SWIGLU ? n0 / 128 : min((n0 + 32 * (lane % W)) / 128, nblk - 1);
+      dma4((const uint8_t*)(s + (int64_t)e * nblk * KT + kt), (uint32_t)blk * KT * 4,
+           __builtin_amdgcn_readfirstlane(st + SL::SC + (x == 3 ? 256 : x == 4 ? 512 : 768)));
+    }
+  };
+  auto issue = [&](int kt) __attribute__((always_inline)) {
+    const uint32_t st = lds0 + (uint32_t)(kt % S) * SL::SIZE;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      dma16nt(b_base[i] + (size_t)kt * 128, b_off[i], __builtin_amdgcn_readfirstlane(st + SL::B + (W * i + wave) * 1024));
+#pragma unroll
+    for (int x = 0; x < SL::EX; ++x) small(W * x + wave, kt, st);
+  };
+  f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  const uint32_t l0 = (uint32_t)(lr * 128 + ((lg ^ ((lr >> 1) & 7)) << 4));   // as in fp8_tile.h
+  const int f0 = SWIGLU ? wave : 2 * wave, f1 = SWIGLU ? wave + W : f0 + 1;   // weight fragments
+  auto multiply = [&](int kt) __attribute__((always_inline)) {
+    const uint8_t* st = lds + (kt % S) * SL::SIZE;
+    auto frag = [&](uint32_t at) { return fp8_join(*(const u32x4*)(st + at + l0), *(const u32x4*)(st + at + (l0 ^ 64))); };
+    const i32x8 a = frag(SL::A), w0 = frag(SL::B + f0 * 2048), w1 = frag(SL::B + f1 * 2048);
+    const float* sc = (const float*)(st + SL::SC);
+    const float sa = sc[lr], t0 = sa * sc[64 + (SWIGLU ? 0 : wave)], t1 = SWIGLU ? sa * sc[128] : t0;
+    f32x4 q0, q1;
+    if constexpr (WIDE) {
+      const Wide16 aw = fp8_widen(a);
+      q0 = fp8_wide16(fp8_widen(w0), aw);
+      q1 = fp8_wide16(fp8_widen(w1), aw);
+    } else {
+      q0 = fp8_mfma16(w0, a);
+      q1 = fp8_mfma16(w1, a);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      acc[0][r] = fmaf(q0[r], t0, acc[0][r]);
+      acc[1][r] = fmaf(q1[r], t1, acc[1][r]);
+    }
+  };
+  for (int s = 0; s < S - 1 && s < KT; ++s) issue(s);
+  int kt = 0;
+  for (; kt < KT - (S - 1); ++kt) {
+    wait_vm<(S - 2) * L>();
+    __syncthreads();
+    issue(kt + S - 1);
+    multiply(kt);
+  }
+  for (; kt < KT; ++kt) {
+    wait_stages<L, S - 2>(KT - 1 - kt);
+    __syncthreads();
+    multiply(kt);
+  }
+  // acc[c][r]: token row lr, weight row 16 f_c + 4 lg + r
+  const int64_t slot = slot_of(min(lr, rows - 1));
   if constexpr (SWIGLU) {
     float h[4], am = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[i] = silu(c0[i]) * c1[i];
-      am = amax2(am, h[i]);
+    for (int r = 0; r < 4; ++r) {
+      h[r] = silu(acc[0][r]) * acc[1][r];
+      am = amax2(am, h[r]);
     }
-    am = amax2(am, __shfl_xor(am, 16, 64));
-    am = amax2(am, __shfl_xor(am, 32, 64));
-    if (g == 0) hmax[wave][m] = am;
-    __syncthreads();
-    am = 0.f;
+    const int col = n0 + 16 * wave + 4 * lg;
+    if constexpr (W == 4) {
+      if (lr >= rows) return;
+      *(f32x4*)(p.h32 + ((int64_t)seg + row0 + lr) * p.N + col) = f32x4{h[0], h[1], h[2], h[3]};
+    } else {
+      am = amax2(am, __shfl_xor(am, 16, 64));
+      am = amax2(am, __shfl_xor(am, 32, 64));
+      if (lg == 0) hmax[wave][lr] = am;
+      __syncthreads();
+      am = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) am = amax2(am, hmax[w][m]);
-    const float s = fp8_scale(am);
-    if (m < rows) {
-      *(uint32_t*)((uint8_t*)p.out + slot * p.N + col) = fp8_encode4(h[0], h[1], h[2], h[3], s);
-      if (wave == 0 && g == 0) p.out_scale[(int64_t)ct * p.C + slot] = s;
-      if (p.saved_au) {
-        *(u32x2*)(p.saved_au + slot * 2 * p.N + col) = u32x2{pack_bf2(c0[0], c0[1]), pack_bf2(c0[2], c0[3])};
-        *(u32x2*)(p.saved_au + (slot * 2 + 1) * p.N + col) = u32x2{pack_bf2(c1[0], c1[1]), pack_bf2(c1[2], c1[3])};
+      for (int w = 0; w < 8; ++w) am = amax2(am, hmax[w][lr]);
+      const float s = fp8_scale(am);
+      if (lr >= rows) return;
+      *(uint32_t*)((uint8_t*)p.out + slot * p.N + col) = h_encode4(h[0], h[1], h[2], h[3], s);
+      if (wave == 0 && lg == 0) p.out_scale[(int64_t)ct * p.C + slot] = s;
+    }
+    if constexpr (KIND == FP8_SWIGLU_SAVE) {
+      *(u32x2*)(p.saved_au + slot * 2 * p.N + col) = u32x2{pack_bf2(acc[0][0], acc[0][1]), pack_bf2(acc[0][2], acc[0][3])};
+      *(u32x2*)(p.saved_au + (slot * 2 + 1) * p.N + col) = u32x2{pack_bf2(acc[1][0], acc[1][1]), pack_bf2(acc[1][2], acc[1][3])};
+    }
+  } else {
+    if (lr >= rows) return;
+    constexpr int EB = WIDE ? 4 : 2;
+    const bool whole = (p.N & 3) == 0 && ((uintptr_t)p.out & (4 * EB - 1)) == 0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int col = n0 + 16 * (f0 + c) + 4 * lg;
+      const f32x4 v = acc[c];
+      if (whole) {
+        if (col >= p.N) continue;
+        if constexpr (WIDE) *(f32x4*)((float*)p.out + slot * p.N + col) = v;
+        else *(u32x2*)((bf16_t*)p.out + slot * p.N + col) = u32x2{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3])};
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (col + r < p.N) {
+            if constexpr (WIDE) ((float*)p.out)[slot * p.N + col + r] = v[r];
+            else ((bf16_t*)p.out)[slot * p.N + col + r] = f2bf(v[r]);
+          }
       }
     }
-  } else if (m < rows) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (col + i < p.N) {
-        if constexpr (F32) ((float*)p.out)[slot * p.N + col + i] = c0[i];
-        else ((bf16_t*)p.out)[slot * p.N + col + i] = f2bf(c0[i]);
-      }
   }
+}
+
+// h [n, f] fp32, in segment order, to H's codes and scales at the rows' slots: a block of 128 columns sits in 16 lanes.
+__global__ __launch_bounds__(256) void quantise_h_kernel(const float* __restrict__ h, int64_t n, int f, int64_t head,
+                                                         int64_t C, uint8_t* __restrict__ codes,
+                                                         float* __restrict__ scales) {
+  const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x, r = v / (f / 8);
+  if (r >= n) return;   // whole blocks: f / 8 is a multiple of 16
+  const int c = (int)(v % (f / 8));
+  const f32x4 a = *(const f32x4*)(h + r * f + c * 8), b = *(const f32x4*)(h + r * f + c * 8 + 4);
+  const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  const float s = fp8_scale(block_amax<16>(x));
+  const int64_t slot = ring_slot(head, 0, r, C);
+  *(u32x2*)(codes + slot * f + c * 8) = u32x2{h_encode4(x[0], x[1], x[2], x[3], s), h_encode4(x[4], x[5], x[6], x[7], s)};
+  if ((c & 15) == 0) scales[(int64_t)(c / 16) * C + slot] = s;
+}
+
+template <int KIND, int W, int S>
+static hipError_t run_fp8_thin(const Fp8Args& a, int64_t tiles, hipStream_t st) {
+  constexpr int cols = KIND >= FP8_SWIGLU ? 16 * W : 32 * W, lds = S * ThinStage<W, S>::SIZE;
+  static_assert(lds + 512 <= 160 * 1024, "LDS");
+  auto kern = fp8_thin_kernel<KIND, W, S>;
+  hipError_t err = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (err != hipSuccess) return err;
+  kern<<<(unsigned)(tiles * ((a.N + cols - 1) / cols)), 64 * W, lds, st>>>(a);
+  return hipGetLastError();
+}
+// Columns per workgroup: as many as leave about 200 workgroups.
+template <int KIND>
+static hipError_t run_fp8_thin_plain(const Fp8Args& a, int64_t tiles, hipStream_t st) {
+  if (tiles * ((a.N + 255) / 256) >= 200) return run_fp8_thin<KIND, 8, 4>(a, tiles, st);
+  if (tiles * ((a.N + 127) / 128) >= 200) return run_fp8_thin<KIND, 4, 7>(a, tiles, st);
+  return run_fp8_thin<KIND, 2, 8>(a, tiles, st);
 }
 
 // ----------------------------------------------------------------------------- launchers
@@ -227,7 +396,7 @@ hipError_t launch_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8
 #ifdef PROBE
   const int fm = getenv("FM") ? atoi(getenv("FM")) : 0;
 #else
-  const int fm = M <= 16 ? 0 : f32_out ? (M <= 64 ? 1 : 2) : tile_height(M, (N + 255) / 256);
+  const int fm = M <= 64 ? 0 : f32_out ? (M <= 64 ? 1 : 2) : tile_height(M, (N + 255) / 256);
 #endif
   const int64_t mt = fm ? (M + 64 * fm - 1) / (64 * fm) : 0;
   p.group = FP8_GROUP;
@@ -237,22 +406,37 @@ hipError_t launch_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8
   if (fm == 2) return run_fp8_tile<2, FP8_BF16, 3, 2>(p, mt, st);
   if (fm == 3) return run_fp8_tile<3, FP8_BF16, 2, 2>(p, mt, st);
   if (fm == 4) return run_fp8_tile<4, FP8_BF16, 2, 2>(p, mt, st);
-  const unsigned grid = (unsigned)(((M + 15) / 16) * ((N + 127) / 128));
-  if (f32_out) fp8_rows16_kernel<false, true><<<grid, 512, 0, st>>>(p);
-  else fp8_rows16_kernel<false, false><<<grid, 512, 0, st>>>(p);
-  return hipGetLastError();
+  return f32_out ? run_fp8_thin_plain<FP8_F32>(p, (M + 15) / 16, st) : run_fp8_thin_plain<FP8_BF16>(p, (M + 15) / 16, st);
 }
 
+// The experts' path by the mean rows of an expert (host-known): the thin kernel up to 16, tiles of 128 rows
+// below 256 (one tile holds an expert's rows, each weight is read once), else of 256.
+static int ffn_fm(int64_t n, int E) {
+#ifdef PROBE
+  if (getenv("FM")) return atoi(getenv("FM"));
+#endif
+  return n <= 16 * (int64_t)E ? 0 : n < 256 * (int64_t)E ? 2 : 4;
+}
+// Workgroups of the thin gate/up kernel below which it takes half blocks of H.
+constexpr int64_t THIN_FEW = 200;
+
 struct FfnFp8Layout {
-  size_t tiles, h, hs, total;
+  size_t tiles, h, hs, h32, total;
+  int fm;
+  int64_t mt;   // bound on the row tiles: every tile holds a row
+  bool few;
 };
 static FfnFp8Layout ffn_fp8_layout(int64_t n, int64_t C, int E, int f) {
   auto al = [](size_t b) { return (b + 255) & ~(size_t)255; };
   FfnFp8Layout L;
+  L.fm = ffn_fm(n, E);
+  L.mt = std::min<int64_t>(max_tiles_for(n, E, L.fm ? 64 * L.fm : 16), n);
+  L.few = L.fm == 0 && L.mt * (f / 128) < THIN_FEW;
   size_t o = 0;
-  L.tiles = o; o += al((size_t)(2 * max_tiles_for(n, E, 16) + 64) * 4);
+  L.tiles = o; o += al((size_t)(2 * L.mt + 64) * 4);
   L.h = o; o += al((size_t)C * f);
   L.hs = o; o += al((size_t)C * (f / 128) * 4);
+  L.h32 = o; o += L.few ? al((size_t)n * f * 4) : 0;
   L.total = o;
   return L;
 }
@@ -268,16 +452,11 @@ hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const i
   int32_t* ntiles = (int32_t*)(w + L.tiles);
   int32_t* tiles = ntiles + 64;
   auto mark = [&](int i) { return events ? hipEventRecord(events[i], st) : hipSuccess; };
-#ifdef PROBE
-  const int fm = getenv("FM") ? atoi(getenv("FM")) : 0;
-#else
-  const int fm = n <= 16 * (int64_t)E ? 0 : n < 256 * (int64_t)E ? 2 : 4;
-#endif
-  const int BM = fm ? 64 * fm : 16;
-  hipError_t err = launch_build_tiles(expert_offset, E, BM, tiles, ntiles, st);
+  const int fm = L.fm;
+  const int64_t mt = L.mt;
+  hipError_t err = fm ? launch_build_tiles(expert_offset, E, 64 * fm, tiles, ntiles, st) : hipSuccess;
   if (err != hipSuccess || (err = mark(0)) != hipSuccess) return err;
-  const int mt = max_tiles_for(n, E, BM);
-  const bool once = n <= BM * (int64_t)E;   // about one row tile per expert: each weight is read once
+  const bool once = n <= 64 * fm * (int64_t)E;   // about one row tile per expert: each weight is read once
   Fp8Args p{};
   p.A = (const uint8_t*)ring_x;
   p.As = ring_x_scale;
@@ -296,12 +475,20 @@ hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const i
   p.out = w + L.h;
   p.out_scale = (float*)(w + L.hs);
   p.saved_au = (bf16_t*)saved_au;
+  p.E = E;
+  p.h32 = (float*)(w + L.h32);
+  p.group = FP8_GROUP;
 #define RUN(FM, KIND, S, G)                                              \
   err = once ? run_fp8_tile<FM, KIND, S, 3>(G, mt, st) : run_fp8_tile<FM, KIND, S, 2>(G, mt, st);
-  p.group = FP8_GROUP;
   if (fm == 0) {
-    fp8_rows16_kernel<true, false><<<(unsigned)((int64_t)mt * (f / 128)), 512, 0, st>>>(p);
-    err = hipGetLastError();
+    if (L.few) {
+      err = saved_au ? run_fp8_thin<FP8_SWIGLU_SAVE, 4, 7>(p, mt, st) : run_fp8_thin<FP8_SWIGLU, 4, 7>(p, mt, st);
+      if (err != hipSuccess) return err;
+      quantise_h_kernel<<<(unsigned)((n * (f / 8) + 255) / 256), 256, 0, st>>>(p.h32, n, f, head, C, w + L.h, p.out_scale);
+      err = hipGetLastError();
+    } else {
+      err = saved_au ? run_fp8_thin<FP8_SWIGLU_SAVE, 8, 4>(p, mt, st) : run_fp8_thin<FP8_SWIGLU, 8, 4>(p, mt, st);
+    }
   } else if (fm == 1) {
     if (saved_au) RUN(1, FP8_SWIGLU_SAVE, 3, p) else RUN(1, FP8_SWIGLU, 3, p)
   } else if (fm == 2) {
@@ -323,8 +510,7 @@ hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const i
   q.out_scale = nullptr;
   q.saved_au = nullptr;
   if (fm == 0) {
-    fp8_rows16_kernel<false, false><<<(unsigned)((int64_t)mt * (d / 128)), 512, 0, st>>>(q);
-    err = hipGetLastError();
+    err = run_fp8_thin_plain<FP8_BF16>(q, mt, st);
   } else if (fm == 1) RUN(1, FP8_BF16, 3, q)
   else if (fm == 2) RUN(2, FP8_BF16, 3, q)
   else RUN(4, FP8_BF16, 2, q)

@@ -33,6 +33,8 @@ struct Fp8Args {
   float* out_scale;        // SWIGLU: [N/128][C]
   bf16_t* saved_au;        // SWIGLU: [C, 2N] or NULL
   const bf16_t* add;       // TILE_ADD: [C, N] or NULL (may be out)
+  int E;                   // experts (the thin kernel)
+  float* h32;              // the thin kernel's h in fp32 [n, N], segment order
   int group;               // row tiles that take the same column tile one after another
 };
 
@@ -385,7 +387,7 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         *(uint32_t*)(lds + m * 144 + 64 * wn + 16 * j + 4 * lg) =
-            fp8_encode4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], s);
+            h_encode4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], s);
     }
     flush((uint8_t*)p.out, p.N, n0, p.N, 144);
   } else if constexpr (ADD) {
