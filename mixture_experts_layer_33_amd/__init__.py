@@ -83,7 +83,7 @@ def moe_dispatch(shape, x, topk_idx, ring_head, ring_x, ring_x_scale, expert_off
                 _a("expert_offset", expert_offset, i32, (E + 1,), dev),
                 _a("copy_slot", copy_slot, i32, (T, k), dev), _a("slot_copy", slot_copy, i32, (C,), dev),
                 *_ws_arg("ws", ws, dev))
-        return _on(dev, stream, "moe_dispatch", lambda s: lib().moe_dispatch(shape, *args, s))
+        return _on(dev, stream, "moe_dispatch", lib().moe_dispatch, shape, *args)
     check("moe_dispatch", lib().moe_dispatch(shape, _p(x), _p(topk_idx), int(ring_head), _p(ring_x),
                                              _p(ring_x_scale), _p(expert_offset), _p(copy_slot),
                                              _p(slot_copy), _p(ws), ws.numel(), _s(stream)))
@@ -94,7 +94,7 @@ def moe_expert_ffn(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate
     if shape.dtype == MOE_FP8:
         args = _ffn_fp8_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
                              w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws)
-        return _on(ring_x.device, stream, "moe_expert_ffn", lambda s: lib().moe_expert_ffn(shape, *args, s))
+        return _on(ring_x.device, stream, "moe_expert_ffn", lib().moe_expert_ffn, shape, *args)
     check("moe_expert_ffn", lib().moe_expert_ffn(
         shape, _p(ring_x), _p(ring_x_scale), _p(expert_offset), int(ring_head), _p(w_gate),
         _p(w_up), _p(w_down), _p(w_gate_scale), _p(w_up_scale), _p(w_down_scale), _p(ring_y),
@@ -113,8 +113,8 @@ def moe_expert_ffn_timed(shape, ring_x, ring_x_scale, expert_offset, ring_head, 
     if shape.dtype == MOE_FP8:
         args = _ffn_fp8_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
                              w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws)
-        return _on(ring_x.device, stream, "moe_expert_ffn_timed", lambda s: lib().moe_expert_ffn_timed(
-            shape, *args, ctypes.cast(arr, ctypes.c_void_p), s))
+        return _on(ring_x.device, stream, "moe_expert_ffn_timed", lib().moe_expert_ffn_timed,
+                   shape, *args, ctypes.cast(arr, ctypes.c_void_p))
     check("moe_expert_ffn_timed", lib().moe_expert_ffn_timed(
         shape, _p(ring_x), _p(ring_x_scale), _p(expert_offset), int(ring_head), _p(w_gate),
         _p(w_up), _p(w_down), _p(w_gate_scale), _p(w_up_scale), _p(w_down_scale), _p(ring_y),
@@ -227,17 +227,26 @@ def quantize_mx(src: torch.Tensor, stream=None):
 # These calls check every tensor (type, shape, contiguity, one device) and run on that device,
 # on `stream` or its current stream.
 
-def _on(dev: torch.device, stream, fn: str, call):
-    """call(raw stream) with `dev` current; raises MoeError on a status."""
+try:   # the raw handle of a device's current stream, without building a Stream object (2 us a call)
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    def _raw_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
+
+
+def _on(dev: torch.device, stream, fn: str, c_fn, *args):
+    """c_fn(*args, raw stream) with `dev` current; raises MoeError on a status."""
     if dev.type != "cuda":
         raise ValueError("libmoe takes device tensors only")
     if stream is not None and stream.device != dev:
         raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {dev}")
-    if dev.index == torch.cuda.current_device():
-        st = call((stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
+    index = dev.index
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        st = c_fn(*args, raw)
     else:
-        with torch.cuda.device(dev):
-            st = call((stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
+        with torch.cuda.device(index):
+            st = c_fn(*args, raw)
     if st:
         check(fn, st)
 
@@ -246,11 +255,10 @@ def _a(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple, d
     """The address of an argument after its checks (None for None)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: needs a contiguous {dtype} tensor {list(shape)} on {dev}, got "
-                         f"{t.dtype} {list(t.shape)} on {t.device}"
-                         f"{'' if t.is_contiguous() else ', not contiguous'}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev:
+        return t.data_ptr()
+    raise ValueError(f"{name}: needs a contiguous {dtype} tensor {list(shape)} on {dev}, got {t.dtype} {list(t.shape)} on "
+                     f"{t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
 def _act(shape: MoeShape) -> torch.dtype:
@@ -283,7 +291,7 @@ def moe_route_scored(shape, router, x, w_router, b_router, balance, topk_idx, to
             _a("topk_idx", topk_idx, i32, (T, k), dev), _a("topk_gate", topk_gate, f32, (T, k), dev),
             _a("expert_count", expert_count, i32, (E,), dev), _a("logits", logits, f32, (T, E), dev),
             *_ws_arg("ws", ws, dev))
-    _on(dev, stream, "moe_route_scored", lambda s: lib().moe_route_scored(shape, router, *args, s))
+    _on(dev, stream, "moe_route_scored", lib().moe_route_scored, shape, router, *args)
 
 
 def moe_route_scored_backward(shape, router, dgate, dlogits, x, w_router, logits, topk_idx, dx_in, dx,
@@ -296,8 +304,7 @@ def moe_route_scored_backward(shape, router, dgate, dlogits, x, w_router, logits
             _a("dx_in", dx_in, act, (T, d), dev), _a("dx", dx, act, (T, d), dev),
             _a("dw_router", dw_router, f32, (E, d), dev), _a("db_router", db_router, f32, (E,), dev),
             *_ws_arg("ws", ws, dev))
-    _on(dev, stream, "moe_route_scored_backward",
-        lambda s: lib().moe_route_scored_backward(shape, router, *args, s))
+    _on(dev, stream, "moe_route_scored_backward", lib().moe_route_scored_backward, shape, router, *args)
 
 
 def moe_backward_experts(shape, dy, topk_idx, topk_gate, ring_x, expert_offset, copy_slot, slot_copy,
@@ -316,7 +323,7 @@ def moe_backward_experts(shape, dy, topk_idx, topk_gate, ring_x, expert_offset, 
             _a("dw_gate", dw_gate, bf, (E, f, d), dev), _a("dw_up", dw_up, bf, (E, f, d), dev),
             _a("dw_down", dw_down, bf, (E, d, f), dev), _a("dgate", dgate, f32, (T, k), dev),
             *_ws_arg("ws", ws, dev))
-    _on(dev, stream, "moe_backward_experts", lambda s: lib().moe_backward_experts(shape, *args, s))
+    _on(dev, stream, "moe_backward_experts", lib().moe_backward_experts, shape, *args)
 
 
 def _scale_spec(shape: MoeShape, rows: int):
@@ -349,7 +356,7 @@ def moe_add_rmsnorm(shape, x, residual, weight, eps, h, y, y8, y8_scale, rstd, s
             _a("weight", weight, f32, (d,), dev), float(eps), _a("h", h, act, (T, d), dev),
             _a("y", y, act, (T, d), dev), _a("y8", y8, torch.uint8, (T, d), dev),
             _a("y8_scale", y8_scale, sdt, sshape, dev), _a("rstd", rstd, f32, (T,), dev))
-    _on(dev, stream, "moe_add_rmsnorm", lambda s: lib().moe_add_rmsnorm(shape, *args, s))
+    _on(dev, stream, "moe_add_rmsnorm", lib().moe_add_rmsnorm, shape, *args)
 
 
 def moe_add_rmsnorm_backward(shape, dy, dh, h, weight, rstd, dx, dweight, ws, stream=None):
@@ -359,7 +366,7 @@ def moe_add_rmsnorm_backward(shape, dy, dh, h, weight, rstd, dx, dweight, ws, st
             _a("weight", weight, f32, (d,), dev), _a("rstd", rstd, f32, (T,), dev),
             _a("dx", dx, act, (T, d), dev), _a("dweight", dweight, f32, (d,), dev),
             *_ws_arg("ws", ws, dev))
-    _on(dev, stream, "moe_add_rmsnorm_backward", lambda s: lib().moe_add_rmsnorm_backward(shape, *args, s))
+    _on(dev, stream, "moe_add_rmsnorm_backward", lib().moe_add_rmsnorm_backward, shape, *args)
 
 
 def moe_dispatch_q(shape, x8, x8_scale, topk_idx, ring_head, ring_x, ring_x_scale, expert_offset,
@@ -374,7 +381,7 @@ def moe_dispatch_q(shape, x8, x8_scale, topk_idx, ring_head, ring_x, ring_x_scal
             _a("expert_offset", expert_offset, i32, (E + 1,), dev),
             _a("copy_slot", copy_slot, i32, (T, k), dev), _a("slot_copy", slot_copy, i32, (C,), dev),
             *_ws_arg("ws", ws, dev))
-    _on(dev, stream, "moe_dispatch_q", lambda s: lib().moe_dispatch_q(shape, *args, s))
+    _on(dev, stream, "moe_dispatch_q", lib().moe_dispatch_q, shape, *args)
 
 
 def quantize_fp8(src: torch.Tensor, row_block: int = 128, stream=None):
@@ -397,8 +404,7 @@ def quantize_fp8(src: torch.Tensor, row_block: int = 128, stream=None):
         shape = (-(-rows // 128), cols // 128)
     scales = torch.empty(shape, dtype=torch.float32, device=dev)
     p = _a("src", src, torch.bfloat16, src.shape, dev)
-    _on(dev, stream, "moe_quantize_fp8",
-        lambda s: lib().moe_quantize_fp8(p, rows, cols, row_block, codes.data_ptr(), scales.data_ptr(), s))
+    _on(dev, stream, "moe_quantize_fp8", lib().moe_quantize_fp8, p, rows, cols, row_block, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -419,7 +425,7 @@ def moe_matmul_fp8(a, a_scale, w, w_scale, out, ws=None, stream=None):
             _a("w", w, u8, (N, K), dev), _a("w_scale", w_scale, f32, (-(-N // 128), K // 128), dev),
             M, N, K, MOE_F32 if out.dtype is f32 else MOE_BF16, _a("out", out, out.dtype, (M, N), dev),
             *_ws_arg("ws", ws, dev))
-    _on(dev, stream, "moe_matmul_fp8", lambda s: lib().moe_matmul_fp8(*args, s))
+    _on(dev, stream, "moe_matmul_fp8", lib().moe_matmul_fp8, *args)
 
 
 @dataclass

@@ -58,133 +58,246 @@ struct SelectArgs {
   float* logits;
 };
 
-// One wavefront per token; lane l owns experts l + 64 i.
+// Row `at` of a [., E] array, this lane's experts lane VPL .. + VPL - 1 (0 past E), in 16-byte pieces where the
+// rows allow it.
 template <int VPL>
-__global__ __launch_bounds__(256) void score_select_kernel(SelectArgs p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= p.T) return;
-  const int E = p.E, k = p.k;
-  float l[VPL], s[VPL];
-  uint32_t key[VPL];
+__device__ __forceinline__ void lane_row(const float* __restrict__ at, int E, float (&v)[VPL]) {
+  const int e0 = (threadIdx.x & 63) * VPL;
+  if (VPL % 4 == 0 && E % 4 == 0) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 64 * i;
-    if (e < E) {
-      float v = p.planes[t * E + e];
-      for (int z = 1; z < p.KS; ++z) v += p.planes[((int64_t)z * p.T + t) * E + e];
-      l[i] = v + (p.b_r ? p.b_r[e] : 0.f);
-      if (p.logits) p.logits[t * E + e] = l[i];
-    } else {
-      l[i] = -INFINITY;
+    for (int c = 0; c < VPL / 4; ++c) {
+      const f32x4 w = e0 + 4 * c < E ? *(const f32x4*)(at + e0 + 4 * c) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[4 * c + q] = w[q];
     }
-  }
-  if (p.rule.sigmoid) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) s[i] = 1.0f / (1.0f + expf(-l[i]));
   } else {
-    float m = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) m = fmaxf(m, l[i]);
-    m = group_max<64>(m);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      s[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - m);   // also where every logit is -inf
-      sum += s[i];
-    }
-    sum = wave_sum(sum);
-    const bool none = sum == 0.f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) s[i] = none ? 0.f : s[i] / sum;
-  }
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 64 * i;
-    key[i] = e < E ? order_key(p.balance ? s[i] + p.balance[e] : p.rule.groups > 1 && p.rule.top_groups < p.rule.groups ? s[i] : l[i]) : 0u;
-  }
-  if (p.rule.top_groups < p.rule.groups) {
-    const int per = E / p.rule.groups;
-    uint32_t mine = 0;   // lane g: the key of group g's score
-    for (int g = 0; g < p.rule.groups; ++g) {
-      uint32_t best = 0;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 64 * i;
-        if (e >= g * per && e < (g + 1) * per && key[i] > best) best = key[i];
-      }
-      const uint32_t top = group_max_u<64>(best);
-      float score = top > 1u ? key_value(top) : -INFINITY;
-      if (p.rule.group_top == 2) {
-        // the second largest: the largest below `top`, or `top` again if two experts hold it
-        int holders = 0;
-        uint32_t next = 0;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const int e = lane + 64 * i;
-          if (e >= g * per && e < (g + 1) * per) {
-            if (key[i] == top) ++holders;
-            else if (key[i] > next) next = key[i];
-          }
-        }
-        const unsigned long long once = __ballot(holders > 0), twice = __ballot(holders > 1);
-        const uint32_t second = (__popcll(once) > 1 || twice) ? top : group_max_u<64>(next);
-        score += second > 1u ? key_value(second) : -INFINITY;
-      }
-      if (lane == g) mine = order_key(score);
-    }
-    int before = 0;
-    for (int g = 0; g < p.rule.groups; ++g) {
-      const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)mine, g);
-      before += (o > mine || (o == mine && g < lane)) ? 1 : 0;
-    }
-    const unsigned long long keep = __ballot(lane < p.rule.groups && before < p.rule.top_groups);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 64 * i;
-      if (e < E) {
-        if (!((keep >> (e / per)) & 1ull)) key[i] = 0u;
-        else if (!p.balance) key[i] = order_key(l[i]);
-      }
-    }
-  }
-  int choice = 0;
-  float my_s = 0.f, my_l = -INFINITY;
-  for (int r = 0; r < k; ++r) {
-    uint32_t bk = 0;
-    int bi = 0x7fffffff;
-    float bs = 0.f, bl = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (key[i] > bk) { bk = key[i]; bi = lane + 64 * i; bs = s[i]; bl = l[i]; }
-    const uint32_t mk = group_max_u<64>(bk);
-    const int e = group_min_i<64>(bk == mk ? bi : 0x7fffffff);
-    const float se = __int_as_float(__builtin_amdgcn_ds_bpermute((e & 63) * 4, __float_as_int(bs)));
-    const float le = __int_as_float(__builtin_amdgcn_ds_bpermute((e & 63) * 4, __float_as_int(bl)));
-    if (lane == r) { choice = e; my_s = se; my_l = le; }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane + 64 * i == e) key[i] = 0u;
-  }
-  float g = my_s;
-  if (p.rule.renormalise) {
-    if (!p.rule.sigmoid) {   // over S alone: exact also where every s of S is tiny
-      const float m = group_max<64>(lane < k ? my_l : -INFINITY);
-      g = lane < k && my_l != -INFINITY ? expf(my_l - m) : 0.f;
-    }
-    const float sum = wave_sum(lane < k ? g : 0.f);
-    g = sum == 0.f ? 0.f : g / sum;
-  }
-  int rank = 0;
-  for (int i = 0; i < k; ++i) rank += (__builtin_amdgcn_readlane(choice, i) < choice) ? 1 : 0;
-  if (lane < k) {
-    p.topk_idx[t * k + rank] = choice;
-    p.topk_gate[t * k + rank] = p.rule.scale * g;
-    atomicAdd(&p.count[choice], 1);   // integers: the same counts in any order
+    for (int i = 0; i < VPL; ++i) v[i] = e0 + i < E ? at[e0 + i] : 0.f;
   }
 }
 
-__global__ __launch_bounds__(1024) void zero_count_kernel(int32_t* __restrict__ count, int E) {
-  for (int e = threadIdx.x; e < E; e += 1024) count[e] = 0;
+// One wavefront per token; lane l owns the consecutive experts l VPL .. l VPL + VPL - 1, so that the lowest lane
+// of a tie holds the lowest id, and a group of experts is a run of lanes where its size allows it
+// (`run` lanes, a power of two; 0: the general form).  What bounds it is the latency of one token's
+// chain (loads, then k rounds of a 64-lane maximum): all planes' loads are issued first, a round
+// is a maximum in VALU moves, one ballot and two lane reads (8 of 256 experts in 8 groups, 2,048
+// tokens: 30 us with strided ownership, plane after plane, and two butterflies a round).
+template <int VPL>
+__global__ __launch_bounds__(256) void score_select_kernel(SelectArgs p, int run) {
+  __shared__ int chosen[4 * 32];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+  const int E = p.E, k = p.k, e0 = lane * VPL;
+  const bool alone = gridDim.x == 1;   // one workgroup counts its own choices
+  if (!alone && blockIdx.x == 0)
+    for (int e = threadIdx.x; e < E; e += 256) p.count[e] = 0;
+  if (t < p.T) {
+    float l[VPL], s[VPL], bias[VPL], bal[VPL];
+    uint32_t key[VPL];
+    constexpr int PB = VPL <= 4 ? RT_MAX_KS : 2;   // planes in flight
+    lane_row<VPL>(p.planes + t * E, E, l);
+    for (int z0 = 1; z0 < p.KS; z0 += PB) {
+      float v[PB][VPL];
+#pragma unroll
+      for (int z = 0; z < PB; ++z)
+        if (z0 + z < p.KS) lane_row<VPL>(p.planes + ((int64_t)(z0 + z) * p.T + t) * E, E, v[z]);
+#pragma unroll
+      for (int z = 0; z < PB; ++z)
+        if (z0 + z < p.KS)
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) l[i] += v[z][i];
+    }
+    if (p.b_r) {
+      lane_row<VPL>(p.b_r, E, bias);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) l[i] += bias[i];
+    }
+    if (p.balance) lane_row<VPL>(p.balance, E, bal);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if (e0 + i >= E) l[i] = -INFINITY;
+      else if (p.logits) p.logits[t * E + e0 + i] = l[i];
+    }
+    if (p.rule.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) s[i] = 1.0f / (1.0f + expf(-l[i]));
+    } else {
+      float m = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) m = fmaxf(m, l[i]);
+      m = group_max<64>(m);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        s[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - m);   // also where every logit is -inf
+        sum += s[i];
+      }
+      sum = wave_sum(sum);
+      const bool none = sum == 0.f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) s[i] = none ? 0.f : s[i] / sum;
+    }
+    const bool grouped = p.rule.top_groups < p.rule.groups;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      key[i] = e0 + i < E ? order_key(p.balance ? s[i] + bal[i] : grouped ? s[i] : l[i]) : 0u;
+    if (grouped) {
+      auto score_key = [&](uint32_t top, uint32_t second) {
+        float v = top > 1u ? key_value(top) : -INFINITY;
+        if (p.rule.group_top == 2) v += second > 1u ? key_value(second) : -INFINITY;
+        return order_key(v);
+      };
+      auto drop = [&](int i, bool kept) {
+        if (e0 + i < E) {
+          if (!kept) key[i] = 0u;
+          else if (!p.balance) key[i] = order_key(l[i]);
+        }
+      };
+      if (run) {
+        // the two largest keys of a run of lanes, merged pairwise
+        uint32_t a = 0, b = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          b = max(b, min(a, key[i]));
+          a = max(a, key[i]);
+        }
+        for (int o = 1; o < run; o <<= 1) {
+          const uint32_t c = __shfl_xor(a, o, 64), d = __shfl_xor(b, o, 64);
+          b = max(min(a, c), max(b, d));
+          a = max(a, c);
+        }
+        const uint32_t mine = score_key(a, b);
+        const int g = lane / run;
+        int before = 0;
+        for (int o = 0; o < p.rule.groups; ++o) {
+          const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)mine, o * run);
+          before += (other > mine || (other == mine && o < g)) ? 1 : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) drop(i, before < p.rule.top_groups);
+      } else {
+        const int per = E / p.rule.groups;
+        uint32_t mine = 0;   // lane g: the key of group g's score
+        for (int g = 0; g < p.rule.groups; ++g) {
+          uint32_t a = 0, b = 0;
+#pragma unroll
+          for (int i = 0; i < VPL; ++i)
+            if (e0 + i >= g * per && e0 + i < (g + 1) * per) {
+              b = max(b, min(a, key[i]));
+              a = max(a, key[i]);
+            }
+          const uint32_t top = group_max_u<64>(a);
+          const unsigned long long holders = __ballot(a == top);
+          const uint32_t second = __popcll(holders) > 1 ? top : group_max_u<64>(a == top ? b : a);
+          const uint32_t score = score_key(top, second);
+          if (lane == g) mine = score;
+        }
+        int before = 0;
+        for (int g = 0; g < p.rule.groups; ++g) {
+          const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)mine, g);
+          before += (o > mine || (o == mine && g < lane)) ? 1 : 0;
+        }
+        const unsigned long long keep = __ballot(lane < p.rule.groups && before < p.rule.top_groups);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) drop(i, e0 + i < E && ((keep >> ((e0 + i) / per)) & 1ull));
+      }
+    }
+    int choice = 0;
+    float my_s = 0.f, my_l = -INFINITY;
+    for (int r = 0; r < k; ++r) {
+      uint32_t bk = 0;
+      int bi = 0;
+      float bs = 0.f, bl = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (key[i] > bk) { bk = key[i]; bi = i; bs = s[i]; bl = l[i]; }
+      const uint32_t mk = group_max_u<64>(bk);
+      const int owner = __builtin_ctzll(__ballot(bk == mk));
+      const int i_ = __builtin_amdgcn_readlane(bi, owner);
+      const float s_ = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bs), owner));
+      const float l_ = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bl), owner));
+      if (lane == r) { choice = owner * VPL + i_; my_s = s_; my_l = l_; }
+      if (lane == owner)
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (i == i_) key[i] = 0u;
+    }
+    float g = my_s;
+    if (p.rule.renormalise) {
+      if (!p.rule.sigmoid) {   // over S alone: exact also where every s of S is tiny
+        const float m = group_max<64>(lane < k ? my_l : -INFINITY);
+        g = lane < k && my_l != -INFINITY ? expf(my_l - m) : 0.f;
+      }
+      const float sum = wave_sum(lane < k ? g : 0.f);
+      g = sum == 0.f ? 0.f : g / sum;
+    }
+    int rank = 0;
+    for (int i = 0; i < k; ++i) rank += (__builtin_amdgcn_readlane(choice, i) < choice) ? 1 : 0;
+    if (lane < k) {
+      p.topk_idx[t * k + rank] = choice;
+      p.topk_gate[t * k + rank] = p.rule.scale * g;
+      chosen[wave * 32 + lane] = choice;
+    }
+  }
+  if (!alone) return;
+  __syncthreads();
+  const int T = (int)p.T;
+  for (int e = threadIdx.x; e < E; e += 256) {
+    int n = 0;
+    for (int w = 0; w < T; ++w)
+      for (int j = 0; j < k; ++j) n += chosen[w * 32 + j] == e ? 1 : 0;
+    p.count[e] = n;
+  }
+}
+
+// count[e] += the copies of e among 8,192 ids per workgroup: an LDS histogram, then one integer addition per
+// workgroup and expert (the same counts in any order).  One addition per copy would put a hot
+// expert's thousands on one address.
+__global__ __launch_bounds__(1024) void score_count_kernel(const int32_t* __restrict__ idx, int64_t n, int E,
+                                                           int32_t* __restrict__ count) {
+  extern __shared__ int32_t hist[];
+  for (int e = threadIdx.x; e < E; e += 1024) hist[e] = 0;
+  __syncthreads();
+  const int64_t c0 = (int64_t)blockIdx.x * 8192 + threadIdx.x;
+  int32_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = c0 + 1024 * i < n ? idx[c0 + 1024 * i] : -1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (v[i] >= 0) atomicAdd(&hist[v[i]], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += 1024)
+    if (hist[e]) atomicAdd(&count[e], hist[e]);
+}
+
+// Logits of a few tokens (T <= SMALL_T, bf16): a weight stream.  One wavefront per expert row and K split (the
+// splits of the MFMA router, whose tiles of 128 tokens would be empty here and its workgroups few: one
+// token, 256 experts, d 7168: 24 -> 6 us), W_r in fp32 and x widened: plain fp32 sums.
+constexpr int SMALL_T = 8;
+template <int NT>
+__global__ __launch_bounds__(256) void router_small_kernel(const bf16_t* __restrict__ x, const float* __restrict__ w_r,
+                                                           float* __restrict__ planes, int T, int d, int E, int KS) {
+  const int lane = threadIdx.x & 63, item = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (item >= E * KS) return;
+  const int e = item / KS, z = item % KS, KA = d / 64;
+  const int i0 = (int)((int64_t)KA * z / KS) * 64, i1 = (int)((int64_t)KA * (z + 1) / KS) * 64;
+  float acc[NT] = {};
+#pragma unroll 4
+  for (int i = i0 + lane * 4; i < i1; i += 256) {
+    const f32x4 w = __builtin_nontemporal_load((const f32x4*)(w_r + (int64_t)e * d + i));
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const u32x2 v = *(const u32x2*)(x + (int64_t)min(t, T - 1) * d + i);
+      acc[t] = fmaf(w[0], lo_bf(v[0]), acc[t]);
+      acc[t] = fmaf(w[1], hi_bf(v[0]), acc[t]);
+      acc[t] = fmaf(w[2], lo_bf(v[1]), acc[t]);
+      acc[t] = fmaf(w[3], hi_bf(v[1]), acc[t]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const float sum = wave_sum(acc[t]);
+    if (lane == 0 && t < T) planes[((int64_t)z * T + t) * E + e] = sum;
+  }
 }
 
 hipError_t launch_route_scored(const void* x, bool x_f32, const float* w_r, const float* b_r,
@@ -192,17 +305,34 @@ hipError_t launch_route_scored(const void* x, bool x_f32, const float* w_r, cons
                                int k, float* planes, int32_t* topk_idx, float* topk_gate,
                                int32_t* count, float* logits, hipStream_t st) {
   int ks = 1;
-  zero_count_kernel<<<1, 1024, 0, st>>>(count, E);
-  hipError_t err = launch_router_logits(x, x_f32, w_r, T, d, E, planes, &ks, st);
+  hipError_t err = hipSuccess;
+  if (!x_f32 && T <= SMALL_T) {
+    ks = router_ksplit(T, E, d);
+    const unsigned g = (unsigned)((E * ks + 3) / 4);
+    if (T == 1) router_small_kernel<1><<<g, 256, 0, st>>>((const bf16_t*)x, w_r, planes, (int)T, d, E, ks);
+    else if (T <= 4) router_small_kernel<4><<<g, 256, 0, st>>>((const bf16_t*)x, w_r, planes, (int)T, d, E, ks);
+    else router_small_kernel<8><<<g, 256, 0, st>>>((const bf16_t*)x, w_r, planes, (int)T, d, E, ks);
+    err = hipGetLastError();
+  } else {
+    err = launch_router_logits(x, x_f32, w_r, T, d, E, planes, &ks, st);
+  }
   if (err != hipSuccess) return err;
   const SelectArgs p{planes, ks, b_r, balance, T, E, k, rule, topk_idx, topk_gate, count, logits};
   const unsigned g = (unsigned)((T + 3) / 4);
-  const int vpl = (E + 63) / 64;
-  if (vpl <= 1) score_select_kernel<1><<<g, 256, 0, st>>>(p);
-  else if (vpl <= 2) score_select_kernel<2><<<g, 256, 0, st>>>(p);
-  else if (vpl <= 4) score_select_kernel<4><<<g, 256, 0, st>>>(p);
-  else if (vpl <= 8) score_select_kernel<8><<<g, 256, 0, st>>>(p);
-  else score_select_kernel<16><<<g, 256, 0, st>>>(p);
+  const int vpl = (E + 63) / 64, per = E / rule.groups;
+#define SELECT(V)                                                                             \
+  {                                                                                           \
+    const int q = per % V == 0 ? per / V : 0;                                                 \
+    score_select_kernel<V><<<g, 256, 0, st>>>(p, q > 0 && (q & (q - 1)) == 0 ? q : 0);        \
+  }
+  if (vpl <= 1) SELECT(1)
+  else if (vpl <= 2) SELECT(2)
+  else if (vpl <= 4) SELECT(4)
+  else if (vpl <= 8) SELECT(8)
+  else SELECT(16)
+#undef SELECT
+  if (g > 1)
+    score_count_kernel<<<(unsigned)((T * k + 8191) / 8192), 1024, E * sizeof(int32_t), st>>>(topk_idx, T * k, E, count);
   return hipGetLastError();
 }
 
