@@ -172,7 +172,7 @@ __global__ __launch_bounds__(64 * W) void fp8_thin_kernel(Fp8Args p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lr = lane & 15, lg = lane >> 4;
   const int nct = (p.N + COLS - 1) / COLS, nblk = (p.N + 127) / 128;
-  const int mt = blockIdx.x / nct, ct = blockIdx.x % nct;
+  const int z = blockIdx.x % p.Z, item = blockIdx.x / p.Z, mt = item / nct, ct = item % nct;
   int e = 0, row0 = 16 * mt, rows = 16;
   int32_t seg = 0;
   if (p.offset) {
@@ -183,7 +183,8 @@ __global__ __launch_bounds__(64 * W) void fp8_thin_kernel(Fp8Args p) {
     rows = (int)min((int64_t)16, p.a_rows - row0);
   }
   const uint32_t K = (uint32_t)p.K;
-  const int KT = p.K / 128, n0 = COLS * ct;
+  const int KA = p.K / 128, kb = (int)((int64_t)KA * z / p.Z), KT = (int)((int64_t)KA * (z + 1) / p.Z) - kb;
+  const int n0 = COLS * ct;
   auto slot_of = [&](int m) { return ring_slot(p.head, seg, row0 + m, p.C); };
 
   // weights: copy i is kilobyte W i + wave of the tile, rows 8 (W i + wave) .. + 7
@@ -209,12 +210,13 @@ __global__ __launch_bounds__(64 * W) void fp8_thin_kernel(Fp8Args p) {
       const float* s = SWIGLU && x == 4 ? p.S1 : p.S0;
       // the block of this lane's column: lane l < W of the plain product holds wavefront l's
       const int blk = SWIGLU ? n0 / 128 : min((n0 + 32 * (lane % W)) / 128, nblk - 1);
-      dma4((const uint8_t*)(s + (int64_t)e * nblk * KT + kt), (uint32_t)blk * KT * 4,
+      dma4((const uint8_t*)(s + (int64_t)e * nblk * KA + kt), (uint32_t)blk * KA * 4,
            __builtin_amdgcn_readfirstlane(st + SL::SC + (x == 3 ? 256 : x == 4 ? 512 : 768)));
     }
   };
-  auto issue = [&](int kt) __attribute__((always_inline)) {
-    const uint32_t st = lds0 + (uint32_t)(kt % S) * SL::SIZE;
+  auto issue = [&](int i_) __attribute__((always_inline)) {   // step i_: block kb + i_
+    const uint32_t st = lds0 + (uint32_t)(i_ % S) * SL::SIZE;
+    const int kt = kb + i_;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       dma16nt(b_base[i] + (size_t)kt * 128, b_off[i], __builtin_amdgcn_readfirstlane(st + SL::B + (W * i + wave) * 1024));
@@ -290,22 +292,24 @@ __global__ __launch_bounds__(64 * W) void fp8_thin_kernel(Fp8Args p) {
     }
   } else {
     if (lr >= rows) return;
-    constexpr int EB = WIDE ? 4 : 2;
+    constexpr bool FLOATS = KIND != FP8_BF16;
+    constexpr int EB = FLOATS ? 4 : 2;
     const bool whole = (p.N & 3) == 0 && ((uintptr_t)p.out & (4 * EB - 1)) == 0;
+    const int64_t row = (z * p.C + slot) * p.N;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int col = n0 + 16 * (f0 + c) + 4 * lg;
       const f32x4 v = acc[c];
       if (whole) {
         if (col >= p.N) continue;
-        if constexpr (WIDE) *(f32x4*)((float*)p.out + slot * p.N + col) = v;
-        else *(u32x2*)((bf16_t*)p.out + slot * p.N + col) = u32x2{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3])};
+        if constexpr (FLOATS) *(f32x4*)((float*)p.out + row + col) = v;
+        else *(u32x2*)((bf16_t*)p.out + row + col) = u32x2{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3])};
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           if (col + r < p.N) {
-            if constexpr (WIDE) ((float*)p.out)[slot * p.N + col + r] = v[r];
-            else ((bf16_t*)p.out)[slot * p.N + col + r] = f2bf(v[r]);
+            if constexpr (FLOATS) ((float*)p.out)[row + col + r] = v[r];
+            else ((bf16_t*)p.out)[row + col + r] = f2bf(v[r]);
           }
       }
     }
@@ -334,55 +338,125 @@ static hipError_t run_fp8_thin(const Fp8Args& a, int64_t tiles, hipStream_t st) 
   auto kern = fp8_thin_kernel<KIND, W, S>;
   hipError_t err = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (err != hipSuccess) return err;
-  kern<<<(unsigned)(tiles * ((a.N + cols - 1) / cols)), 64 * W, lds, st>>>(a);
+  kern<<<(unsigned)(tiles * ((a.N + cols - 1) / cols) * a.Z), 64 * W, lds, st>>>(a);
   return hipGetLastError();
 }
-// Columns per workgroup: as many as leave about 200 workgroups.
+// Wavefronts of a plain thin workgroup: the fewest columns that still run at once (two workgroups of two
+// wavefronts share a CU's LDS, one of four or eight fills it).
+static int thin_waves(int64_t tiles, int64_t N) {
+  return tiles * ((N + 63) / 64) <= 512 ? 2 : tiles * ((N + 127) / 128) <= 256 ? 4 : 8;
+}
 template <int KIND>
-static hipError_t run_fp8_thin_plain(const Fp8Args& a, int64_t tiles, hipStream_t st) {
-  if (tiles * ((a.N + 255) / 256) >= 200) return run_fp8_thin<KIND, 8, 4>(a, tiles, st);
-  if (tiles * ((a.N + 127) / 128) >= 200) return run_fp8_thin<KIND, 4, 7>(a, tiles, st);
-  return run_fp8_thin<KIND, 2, 8>(a, tiles, st);
+static hipError_t run_fp8_thin_plain(const Fp8Args& a, int64_t tiles, int W, hipStream_t st) {
+  if (W == 8) return run_fp8_thin<KIND, 8, 4>(a, tiles, st);
+  if (W == 4) return run_fp8_thin<KIND, 4, 7>(a, tiles, st);
+  return run_fp8_thin<KIND, 2, 7>(a, tiles, st);
 }
 
-// ----------------------------------------------------------------------------- launchers
 // Row tiles that take a column tile one after another (fp8_tile.h).
 constexpr int FP8_GROUP = 4;
 
-// Tile height (in 64 rows) of a product of M rows with `nct` column tiles of 256: the one with the least
-// time, rounds of 256 workgroups times a stage's time.  Stages of 64 / 128 / 192 / 256 rows took
-// 0.95, 0.98, 1.07 and 1.25 us (M 2,045, N 4,168, K 7,168): low tiles are bound by their
-// weight copies, not by the matrix cores.
-static int tile_height(int64_t M, int64_t nct) {
-  const double us[4] = {0.95, 0.98, 1.07, 1.25};
-  int best = 1;
+// How a dense product runs: fm = 0 the thin kernel (16 token rows a tile, W wavefronts), else tiles of 64 fm rows;
+// Z: K splits.  The least estimated time of all: rounds of 256 workgroups times the blocks of one,
+// where a block of a tile of 64 / 128 / 192 / 256 rows took 0.95, 0.98, 1.07 and 1.25 us (M 2,045, N 4,168,
+// K 7,168: low tiles are bound by their weight copies, not by the matrix cores; the fp32 output's
+// bf16 MFMAs 1.1 and 2.0 us at 64 and 128 rows), and a block of a thin workgroup its share of a
+// copy's latency (0.67, 0.33, 0.29 us with 8, 4, 2 wavefronts), or the weights at 6 TB/s.  A split fills
+// idle CUs, but its planes are written and read once more, and the second launch costs 6 us.
+struct DensePlan {
+  int fm, W, Z;
+};
+static DensePlan dense_plan(int64_t M, int64_t N, int64_t K, bool f32, bool split) {
+  const double us[4] = {0.95, f32 ? 2.0 : 0.98, 1.07, 1.25};
+  const int64_t KT = K / 128;
+  DensePlan best{};
   double least = 1e300;
-  for (int fm = 1; fm <= 4; ++fm) {
-    const double t = (double)(((M + 64 * fm - 1) / (64 * fm) * nct + 255) / 256) * us[fm - 1];
-    if (t < least) { least = t; best = fm; }
+  auto offer = [&](DensePlan p, int64_t wgs, double block, double floor_us) {
+    const int64_t most = split ? std::min<int64_t>({256 / wgs, KT / 4, 16}) : 1;
+    for (p.Z = 1; p.Z == 1 || p.Z <= most; p.Z *= 2) {
+      const double rounds = (double)((wgs * p.Z + 255) / 256), blocks = (double)((KT + p.Z - 1) / p.Z);
+      const double t = std::max(rounds * (blocks * block + 3.0), floor_us) +
+                       (p.Z > 1 ? 6.0 + (double)p.Z * M * N * 8 / 4e6 : 0.0);
+      if (t < least) { least = t; best = p; }
+    }
+  };
+  for (int fm = 1; fm <= (f32 ? 2 : 4); ++fm) {
+    if (f32 && fm == 1) offer({fm, 0, 1}, (M + 63) / 64 * ((N + 255) / 256), 1.1, 0.0);
+    else offer({fm, 0, 1}, (M + 64 * fm - 1) / (64 * fm) * ((N + 255) / 256), us[fm - 1], 0.0);
+  }
+  if (M <= 256) {
+    const int64_t tiles = (M + 15) / 16;
+    const int W = thin_waves(tiles, N);
+    const int64_t wgs = tiles * ((N + 32 * W - 1) / (32 * W));
+    offer({0, W, 1}, W == 2 ? (wgs + 1) / 2 : wgs, W == 8 ? 0.67 : W == 4 ? 0.33 : 0.29, (double)tiles * N * K / 6e6);
   }
   return best;
 }
 
 hipError_t launch_tile_add(Fp8Args& a, hipStream_t st) {
   a.group = FP8_GROUP;
-  const int fm = tile_height(a.a_rows, (a.N + 255) / 256);
-  const int64_t mt = (a.a_rows + 64 * fm - 1) / (64 * fm);
-  if (fm == 1) return run_fp8_tile<1, TILE_ADD, 3, 2>(a, mt, st);
+  a.Z = 1;
+  const int fm = dense_plan(a.a_rows, a.N, a.K, false, false).fm;
+  const int64_t mt = fm ? (a.a_rows + 64 * fm - 1) / (64 * fm) : 0;
+  if (fm <= 1) return run_fp8_tile<1, TILE_ADD, 3, 2>(a, (a.a_rows + 63) / 64, st);
   if (fm == 2) return run_fp8_tile<2, TILE_ADD, 3, 2>(a, mt, st);
   if (fm == 3) return run_fp8_tile<3, TILE_ADD, 2, 2>(a, mt, st);
   return run_fp8_tile<4, TILE_ADD, 2, 2>(a, mt, st);
 }
 
 size_t matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  (void)M; (void)N; (void)K;
-  return 0;
+  size_t b = 0;
+  for (bool f32 : {false, true}) {
+    const DensePlan d = dense_plan(M, N, K, f32, true);
+    if (d.Z > 1) b = std::max(b, (size_t)d.Z * M * N * 4);
+  }
+  return b;
+}
+
+// out[i] = the sum of the Z planes in order, rounded once.
+template <bool F32>
+__global__ __launch_bounds__(256) void plane_join_kernel(const float* __restrict__ part, int Z, int64_t n, void* out) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const int live = (int)min((int64_t)4, n - i);
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (live == 4 && (n & 3) == 0) {   // every plane starts on 16 bytes
+    f32x4 v = *(const f32x4*)(part + i);
+    for (int z = 1; z < Z; ++z) v += *(const f32x4*)(part + z * n + i);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[r] = v[r];
+  } else {
+    for (int r = 0; r < live; ++r)
+      for (int z = 0; z < Z; ++z) s[r] += part[z * n + i + r];
+  }
+  const int EB = F32 ? 4 : 2;
+  if (live == 4 && ((uintptr_t)out & (4 * EB - 1)) == 0) {
+    if constexpr (F32) *(f32x4*)((float*)out + i) = f32x4{s[0], s[1], s[2], s[3]};
+    else *(u32x2*)((bf16_t*)out + i) = u32x2{pack_bf2(s[0], s[1]), pack_bf2(s[2], s[3])};
+  } else {
+    for (int r = 0; r < live; ++r) {
+      if constexpr (F32) ((float*)out)[i + r] = s[r];
+      else ((bf16_t*)out)[i + r] = f2bf(s[r]);
+    }
+  }
+}
+
+template <int KIND>
+static hipError_t run_dense(const Fp8Args& p, const DensePlan& d, hipStream_t st) {
+  const int64_t M = p.a_rows, mt = d.fm ? (M + 64 * d.fm - 1) / (64 * d.fm) : (M + 15) / 16;
+  if (d.fm == 0) return run_fp8_thin_plain<KIND>(p, mt, d.W, st);
+  if (d.fm == 1) return run_fp8_tile<1, KIND, 3, 2>(p, mt, st);
+  if constexpr (KIND != FP8_F32) {
+    if (d.fm == 3) return run_fp8_tile<3, KIND, 2, 2>(p, mt, st);
+    if (d.fm == 4) return run_fp8_tile<4, KIND, 2, 2>(p, mt, st);
+  }
+  return run_fp8_tile<2, KIND, 3, 2>(p, mt, st);
 }
 
 hipError_t launch_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w,
                              const float* w_scale, int64_t M, int64_t N, int64_t K, bool f32_out,
                              void* out, void* ws, hipStream_t st) {
-  (void)ws;
+  const DensePlan d = dense_plan(M, N, K, f32_out, true);
   Fp8Args p{};
   p.A = a;
   p.As = a_scale;
@@ -392,21 +466,15 @@ hipError_t launch_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8
   p.C = M;
   p.K = (int)K;
   p.N = (int)N;
-  p.out = out;
-#ifdef PROBE
-  const int fm = getenv("FM") ? atoi(getenv("FM")) : 0;
-#else
-  const int fm = M <= 64 ? 0 : f32_out ? (M <= 64 ? 1 : 2) : tile_height(M, (N + 255) / 256);
-#endif
-  const int64_t mt = fm ? (M + 64 * fm - 1) / (64 * fm) : 0;
+  p.Z = d.Z;
   p.group = FP8_GROUP;
-  if (f32_out && fm == 1) return run_fp8_tile<1, FP8_F32, 3, 2>(p, mt, st);
-  if (f32_out && fm) return run_fp8_tile<2, FP8_F32, 3, 2>(p, mt, st);
-  if (fm == 1) return run_fp8_tile<1, FP8_BF16, 3, 2>(p, mt, st);
-  if (fm == 2) return run_fp8_tile<2, FP8_BF16, 3, 2>(p, mt, st);
-  if (fm == 3) return run_fp8_tile<3, FP8_BF16, 2, 2>(p, mt, st);
-  if (fm == 4) return run_fp8_tile<4, FP8_BF16, 2, 2>(p, mt, st);
-  return f32_out ? run_fp8_thin_plain<FP8_F32>(p, (M + 15) / 16, st) : run_fp8_thin_plain<FP8_BF16>(p, (M + 15) / 16, st);
+  p.out = d.Z > 1 ? ws : out;
+  hipError_t err = f32_out ? run_dense<FP8_F32>(p, d, st) : d.Z > 1 ? run_dense<FP8_PART>(p, d, st) : run_dense<FP8_BF16>(p, d, st);
+  if (err != hipSuccess || d.Z == 1) return err;
+  const unsigned g = (unsigned)((M * N + 1023) / 1024);
+  if (f32_out) plane_join_kernel<true><<<g, 256, 0, st>>>((const float*)ws, d.Z, M * N, out);
+  else plane_join_kernel<false><<<g, 256, 0, st>>>((const float*)ws, d.Z, M * N, out);
+  return hipGetLastError();
 }
 
 // The experts' path by the mean rows of an expert (host-known): the thin kernel up to 16, tiles of 128 rows
@@ -476,6 +544,7 @@ hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const i
   p.out_scale = (float*)(w + L.hs);
   p.saved_au = (bf16_t*)saved_au;
   p.E = E;
+  p.Z = 1;
   p.h32 = (float*)(w + L.h32);
   p.group = FP8_GROUP;
 #define RUN(FM, KIND, S, G)                                              \
@@ -510,7 +579,7 @@ hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const i
   q.out_scale = nullptr;
   q.saved_au = nullptr;
   if (fm == 0) {
-    err = run_fp8_thin_plain<FP8_BF16>(q, mt, st);
+    err = run_fp8_thin_plain<FP8_BF16>(q, mt, thin_waves(mt, d), st);
   } else if (fm == 1) RUN(1, FP8_BF16, 3, q)
   else if (fm == 2) RUN(2, FP8_BF16, 3, q)
   else RUN(4, FP8_BF16, 2, q)

@@ -33,6 +33,7 @@ struct Fp8Args {
   float* out_scale;        // SWIGLU: [N/128][C]
   bf16_t* saved_au;        // SWIGLU: [C, 2N] or NULL
   const bf16_t* add;       // TILE_ADD: [C, N] or NULL (may be out)
+  int Z;                   // K splits of a dense product (1 elsewhere)
   int E;                   // experts (the thin kernel)
   float* h32;              // the thin kernel's h in fp32 [n, N], segment order
   int group;               // row tiles that take the same column tile one after another
@@ -74,8 +75,9 @@ __device__ __forceinline__ f32x4 fp8_wide16(const Wide16& w, const Wide16& a) {
   return c;
 }
 
+// FP8_PART: K split over Z workgroups, each with an fp32 plane of its own [Z, C, N] (FP8_F32 with Z > 1 likewise).
 // TILE_ADD: bf16 operands (K: bytes of a row, a stage holds 64 elements) without scales, out = round(add + A W^T).
-enum { FP8_BF16 = 0, FP8_F32 = 1, TILE_ADD = 2, FP8_SWIGLU = 3, FP8_SWIGLU_SAVE = 4 };
+enum { FP8_BF16 = 0, FP8_F32 = 1, FP8_PART = 2, TILE_ADD = 3, FP8_SWIGLU = 4, FP8_SWIGLU_SAVE = 5 };
 
 template <int FM, int KIND>
 struct Fp8Stage {
@@ -101,9 +103,10 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
   // tiles running together on an XCD share both their token rows and their weight rows in its L2
   // (groups of 4 against 1, 4 experts x 4,096 rows: 749 -> 737 us; starting tiles at different K blocks, as
   // the bf16 GEMMs do, then loses: 752 us).
-  const int V = nmt * nct, per = (V + 7) / 8, li = (int)(blockIdx.x >> 3);
-  const int T = (int)(blockIdx.x & 7) * per + li;
-  if (li >= per || T >= V) return;
+  const int V = nmt * nct, per = (V * p.Z + 7) / 8, li = (int)(blockIdx.x >> 3);
+  const int TZ = (int)(blockIdx.x & 7) * per + li;
+  if (li >= per || TZ >= V * p.Z) return;
+  const int z = TZ / V, T = TZ - z * V;          // the K split, the tile
   int e = 0, t0 = 0, R = nmt, mt = T / nct;      // expert, its first row tile, its row tiles
   int32_t seg = 0;
   int64_t all = p.a_rows;                        // its rows
@@ -124,7 +127,7 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1, lr = lane & 15, lg = lane >> 4;
   const uint32_t K = (uint32_t)p.K;
-  const int KT = p.K / 128;
+  const int KA = p.K / 128, kb = (int)((int64_t)KA * z / p.Z), KT = (int)((int64_t)KA * (z + 1) / p.Z) - kb;
 
   // copies: 16-byte chunk j of a tile is slot j % 8 of row j / 8 and holds the chunk of that row whose
   // swizzled place it is (swz of gemm_body.h)
@@ -156,16 +159,17 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
     s_off = (uint32_t)ring_slot(p.head, seg, row0 + min(r, rows - 1), p.C) * 4;
     s_step = p.a_rows * 4;
   } else if constexpr (SWIGLU) {                 // a block scale in every lane: wavefront FM gate, FM + 1 up
-    s_base = (const uint8_t*)(((wave - FM) & 1 ? p.S1 : p.S0) + ((int64_t)e * nblk + ct) * KT);
+    s_base = (const uint8_t*)(((wave - FM) & 1 ? p.S1 : p.S0) + ((int64_t)e * nblk + ct) * KA);
     s_off = 0;
     s_step = 4;
   } else {                                       // the tile's two block scales in turn
-    s_base = (const uint8_t*)(p.S0 + (int64_t)e * nblk * KT);
-    s_off = (uint32_t)min(2 * ct + (lane & 1), nblk - 1) * KT * 4;
+    s_base = (const uint8_t*)(p.S0 + (int64_t)e * nblk * KA);
+    s_off = (uint32_t)min(2 * ct + (lane & 1), nblk - 1) * KA * 4;
     s_step = 4;
   }
-  auto issue_one = [&](int kt, int c) __attribute__((always_inline)) {
-    const uint32_t st = lds0 + (uint32_t)(kt % S) * SL::SIZE;
+  auto issue_one = [&](int i_, int c) __attribute__((always_inline)) {   // step i_: block kb + i_
+    const uint32_t st = lds0 + (uint32_t)(i_ % S) * SL::SIZE;
+    const int kt = kb + i_;
     if (c < FM) {
       dma16(p.A + (size_t)kt * 128, a_off[c], __builtin_amdgcn_readfirstlane(st + SL::A + (8 * c + wave) * 1024));
     } else if (c < FM + 4) {
@@ -417,13 +421,13 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
       }
       __syncthreads();
     }
-  } else if constexpr (KIND == FP8_F32) {
+  } else if constexpr (KIND == FP8_F32 || KIND == FP8_PART) {
     const bool whole = (p.N & 3) == 0 && ((uintptr_t)p.out & 15) == 0;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int m = 16 * (wm + 4 * i) + lr;
       if (m >= rows) continue;
-      float* row = (float*)p.out + slot_of(m) * p.N;
+      float* row = (float*)p.out + (z * p.C + slot_of(m)) * p.N;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int col = n0 + 16 * bfrag(j) + 4 * lg;
@@ -468,7 +472,7 @@ inline hipError_t run_fp8_tile(const Fp8Args& a, int64_t max_tiles, hipStream_t 
   auto kern = fp8_tile_kernel<FM, KIND, S, POL>;
   hipError_t err = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (err != hipSuccess) return err;
-  const int64_t grid = 8 * ((max_tiles * nct + 7) / 8);
+  const int64_t grid = 8 * ((max_tiles * nct * a.Z + 7) / 8);
   kern<<<(unsigned)grid, 512, lds, st>>>(a);
   return hipGetLastError();
 }
