@@ -396,7 +396,23 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
     flush((uint8_t*)p.out, p.N, n0, p.N, 144);
   } else if constexpr (ADD) {
     // fp32 halves of 128 columns through LDS (rows of 512 + 16 bytes), so that the addend is read and the
-    // sum written in whole 16-byte pieces
+    // sum written in whole 16-byte pieces; a half's addend is requested before its sums are staged
+    constexpr int PC = BM * 16 / 512;            // pieces per thread and half
+    u32x4 w[2][PC];
+    auto place = [&](int h, int q, int& m, int& col) __attribute__((always_inline)) {
+      m = (tid + 512 * q) / 16;
+      col = n0 + 128 * h + (tid % 16) * 8;
+      return m < rows && col < p.N;
+    };
+    auto request = [&](int h) __attribute__((always_inline)) {
+#pragma unroll
+      for (int q = 0; q < PC; ++q) {
+        int m, col;
+        w[h][q] = u32x4{0, 0, 0, 0};
+        if (place(h, q, m, col) && p.add) w[h][q] = *(const u32x4*)(p.add + slot_of(m) * p.N + col);
+      }
+    };
+    request(0);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (wn == h) {
@@ -405,19 +421,18 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) *(f32x4*)(lds + (16 * (wm + 4 * i) + lr) * 528 + (16 * j + 4 * lg) * 4) = acc[i][j];
       }
+      if (h == 0) request(1);
       __syncthreads();
-#pragma unroll 4
-      for (int q = tid; q < BM * 16; q += 512) {
-        const int m = q / 16, col = n0 + 128 * h + (q % 16) * 8;
-        if (m < rows && col < p.N) {
-          const int64_t at = slot_of(m) * p.N + col;
-          const f32x4 a = *(const f32x4*)(lds + m * 528 + (q % 16) * 32), b = *(const f32x4*)(lds + m * 528 + (q % 16) * 32 + 16);
-          u32x4 w = {0, 0, 0, 0};
-          if (p.add) w = *(const u32x4*)(p.add + at);
-          *(u32x4*)((bf16_t*)p.out + at) =
-              u32x4{pack_bf2(lo_bf(w[0]) + a[0], hi_bf(w[0]) + a[1]), pack_bf2(lo_bf(w[1]) + a[2], hi_bf(w[1]) + a[3]),
-                    pack_bf2(lo_bf(w[2]) + b[0], hi_bf(w[2]) + b[1]), pack_bf2(lo_bf(w[3]) + b[2], hi_bf(w[3]) + b[3])};
-        }
+#pragma unroll
+      for (int q = 0; q < PC; ++q) {
+        int m, col;
+        if (!place(h, q, m, col)) continue;
+        const f32x4 a = *(const f32x4*)(lds + m * 528 + (tid % 16) * 32), b = *(const f32x4*)(lds + m * 528 + (tid % 16) * 32 + 16);
+        const u32x4 v = w[h][q];
+        __builtin_nontemporal_store(
+            u32x4{pack_bf2(lo_bf(v[0]) + a[0], hi_bf(v[0]) + a[1]), pack_bf2(lo_bf(v[1]) + a[2], hi_bf(v[1]) + a[3]),
+                  pack_bf2(lo_bf(v[2]) + b[0], hi_bf(v[2]) + b[1]), pack_bf2(lo_bf(v[3]) + b[2], hi_bf(v[3]) + b[3])},
+            (u32x4*)((bf16_t*)p.out + slot_of(m) * p.N + col));
       }
       __syncthreads();
     }

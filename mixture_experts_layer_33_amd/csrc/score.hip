@@ -345,7 +345,7 @@ hipError_t launch_route_scored(const void* x, bool x_f32, const float* w_r, cons
 // padding 0) and [lo] of Ep.  Against W_r's columns [hi | mid | hi] one product of length 3 Ep is dl W_r
 // to 2^-15 of its terms (mid x mid and the third parts are left out: dx is rounded to bf16, half a
 // step 2^-8); the three parts against the exact bf16 x are dl^T x to fp32, in which dW_r leaves.
-constexpr int DL_TW = 4;
+constexpr int DL_TW = 2;
 
 struct DlArgs {
   const float* dgate;
@@ -359,12 +359,37 @@ struct DlArgs {
   bf16_t* planes;       // bf16 tokens: [Tp, 3 Ep]
   bf16_t* low;          // bf16 tokens: [Tp, Ep]
   uint32_t* zero;       // bf16 tokens: 256 words set to 0
+  const float* w_r;     // bf16 tokens: W_r [E, d] to be turned by the workgroups from G on
+  bf16_t* wt;           // [d, 3 Ep]
+  int d, G;
   float* db_part;       // [workgroups, E] sums over a workgroup's tokens, or NULL
 };
+
+// W_r [E, d] fp32 -> [d, 3 Ep] bf16, rows [hi | mid | hi] of W_r's columns: 64 x 64 of them, turned through LDS.
+__device__ __forceinline__ void score_turn(const DlArgs& p, int at, float (*tile)[65]) {
+  const int c0 = at % (p.d / 64) * 64, e0 = at / (p.d / 64) * 64;   // d is a multiple of 64
+  for (int q = threadIdx.x; q < 64 * 64; q += 256) {
+    const int e = q / 64, c = q % 64;
+    tile[e][c] = e0 + e < p.E ? p.w_r[(int64_t)(e0 + e) * p.d + c0 + c] : 0.f;
+  }
+  __syncthreads();
+  for (int q = threadIdx.x; q < 64 * 64; q += 256) {
+    const int c = q / 64, e = q % 64;
+    const float v = tile[e][c];
+    const bf16_t hi = f2bf(v), mid = f2bf(v - bf2f(hi));
+    bf16_t* row = p.wt + (int64_t)(c0 + c) * 3 * p.Ep + e0 + e;
+    row[0] = hi;
+    row[p.Ep] = mid;
+    row[2 * p.Ep] = hi;
+  }
+}
 
 template <int VPL, bool F32>
 __global__ __launch_bounds__(256) void score_dl_kernel(DlArgs p) {
   __shared__ float dbs[4][64 * VPL];
+  __shared__ float tile[F32 ? 1 : 64][65];
+  if constexpr (!F32)
+    if ((int)blockIdx.x >= p.G) return score_turn(p, (int)blockIdx.x - p.G, tile);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int E = p.E, k = p.k;
   if (!F32 && blockIdx.x == 0) p.zero[threadIdx.x] = 0u;
@@ -455,35 +480,14 @@ __global__ __launch_bounds__(256) void score_dl_kernel(DlArgs p) {
     p.db_part[(int64_t)blockIdx.x * E + e] = (dbs[0][e] + dbs[1][e]) + (dbs[2][e] + dbs[3][e]);
 }
 
-// W_r [E, d] fp32 -> [d, 3 Ep] bf16, rows [hi | mid | hi] of W_r's columns (64 x 64 per workgroup,
-// turned through LDS).
-__global__ __launch_bounds__(256) void score_turn_kernel(const float* __restrict__ w_r, int E, int Ep, int d,
-                                                         bf16_t* __restrict__ out) {
-  __shared__ float tile[64][65];
-  const int c0 = blockIdx.x * 64, e0 = blockIdx.y * 64;
-  for (int q = threadIdx.x; q < 64 * 64; q += 256) {
-    const int e = q / 64, c = q % 64;
-    tile[e][c] = e0 + e < E ? w_r[(int64_t)(e0 + e) * d + c0 + c] : 0.f;   // d is a multiple of 64
-  }
-  __syncthreads();
-  for (int q = threadIdx.x; q < 64 * 64; q += 256) {
-    const int c = q / 64, e = q % 64;
-    const float v = tile[e][c];
-    const bf16_t hi = f2bf(v), mid = f2bf(v - bf2f(hi));
-    bf16_t* row = out + (int64_t)(c0 + c) * 3 * Ep + e0 + e;
-    row[0] = hi;
-    row[Ep] = mid;
-    row[2 * Ep] = hi;
-  }
-}
-
 // Partial planes of dW_r [E, d] = dl^T x for bf16 tokens.  Both operands are row-major with the
-// reduction index (the token) as the row, so a stage holds 32 token rows of each as they are and the
-// MFMA fragments are read with the transposing LDS reads of the weight gradients
-// (backward.hip).  256 experts x 256 columns per workgroup, eight wavefronts of 64 x 128; the
-// tokens run three times, against the parts of dl in turn, and are split over Z workgroups, each
-// with a plane of its own.  Split z runs on XCD z (Z = 8), so that a token row of x crosses into one
-// L2 only.
+// reduction index (the token) as the row, so a stage holds 32 token rows as they are, of x once and of the
+// three parts of dl, and the MFMA fragments are read with the transposing LDS reads of the weight
+// gradients (backward.hip).  256 experts x 256 columns per workgroup, eight wavefronts of 64 x 128: a
+// fragment of x meets all three parts (with a stage per part instead, x staged and read three times:
+// 122 us where this takes 100, 8,192 tokens, d 4,096, 512 experts).  The tokens are split over Z
+// workgroups, each with a plane of its own; split z runs on XCD z (Z = 8), so that a token row of
+// x crosses into one L2 only.
 struct DwArgs {
   const bf16_t* planes;   // [Tp, 3 Ep]: hi | hi | mid
   const bf16_t* low;      // [Tp, Ep]
@@ -493,8 +497,8 @@ struct DwArgs {
   int E, Ep, d, Z;
   float* part;            // [Z, E, d]
 };
-constexpr int DW_M = 256, DW_N = 256, DW_K = 32, DW_S = 4, DW_ROW = 512;   // bytes of a staged row
-constexpr int DW_STAGE = DW_K * 2 * DW_ROW, DW_LDS = DW_S * DW_STAGE;
+constexpr int DW_M = 256, DW_N = 256, DW_K = 32, DW_S = 2, DW_ROW = 512;   // bytes of a staged row
+constexpr int DW_TILE = DW_K * DW_ROW, DW_STAGE = 4 * DW_TILE, DW_LDS = DW_S * DW_STAGE;
 
 __global__ __launch_bounds__(512) void score_dw_mfma_kernel(DwArgs p) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
@@ -502,13 +506,12 @@ __global__ __launch_bounds__(512) void score_dw_mfma_kernel(DwArgs p) {
   const int z = blockIdx.x % p.Z, tile = blockIdx.x / p.Z;
   const int mt = (p.E + DW_M - 1) / DW_M;
   const int m0 = (tile % mt) * DW_M, n0 = (tile / mt) * DW_N;
-  const int64_t steps = p.Tp / DW_K, all = 3 * steps;
-  const int64_t s0 = all * z / p.Z;
-  const int KT = (int)(all * (z + 1) / p.Z - s0);
+  const int64_t steps = p.Tp / DW_K, s0 = steps * z / p.Z;
+  const int KT = (int)(steps * (z + 1) / p.Z - s0);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1, lr = lane & 31, lg = lane >> 5;
-  // copies: kilobyte 8 c + wave of an operand's stage is its rows 2 (8 c + wave) and + 1
+  // copies: kilobyte 8 c + wave of a tile (x, hi, mid, lo) is its rows 2 (8 c + wave) and + 1
   const int crow = lane / 32;
   int acol[2], bcol[2];
 #pragma unroll
@@ -519,18 +522,16 @@ __global__ __launch_bounds__(512) void score_dw_mfma_kernel(DwArgs p) {
   }
   auto issue = [&](int i) __attribute__((always_inline)) {
     const uint32_t st = lds0 + (uint32_t)(i % DW_S) * DW_STAGE;
-    const int64_t s = s0 + i;
-    const int part = s < steps ? 0 : s < 2 * steps ? 1 : 2;
-    const int64_t r0 = (s - part * steps) * DW_K;
-    const bf16_t* a = part == 2 ? p.low : p.planes + (part ? 2 * p.Ep : 0);
-    const int lda = part == 2 ? p.Ep : 3 * p.Ep;
+    const int64_t r0 = (s0 + i) * DW_K;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int64_t t = r0 + 2 * (8 * c + wave) + crow;
-      dma16_at(a + t * lda + acol[c],
-               __builtin_amdgcn_readfirstlane(st + (8 * c + wave) * 1024));
-      dma16_at(t < p.T ? p.x + t * p.d + bcol[c] : p.zero + (lane & 31) * 8,
-               __builtin_amdgcn_readfirstlane(st + DW_K * DW_ROW + (8 * c + wave) * 1024));
+      const uint32_t to = __builtin_amdgcn_readfirstlane(st + (8 * c + wave) * 1024);
+      const bf16_t* row = p.planes + t * 3 * p.Ep + acol[c];
+      dma16_at(t < p.T ? p.x + t * p.d + bcol[c] : p.zero + (lane & 31) * 8, to);
+      dma16_at(row, to + DW_TILE);
+      dma16_at(row + 2 * p.Ep, to + 2 * DW_TILE);
+      dma16_at(p.low + t * p.Ep + acol[c], to + 3 * DW_TILE);
     }
   };
   f32x16 acc[4][2];
@@ -540,41 +541,42 @@ __global__ __launch_bounds__(512) void score_dw_mfma_kernel(DwArgs p) {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.f;
-  int foff[6];
+  int foff[6];   // offsets in a stage: 2 fragments of dl's first part, 4 of x
   {
     const int g = lane >> 4, gi = lane & 15, qq = gi >> 2, ss = gi & 3;
     const int r0 = 8 * (g >> 1) + qq;
 #pragma unroll
     for (int q = 0; q < 6; ++q) {
       const int col = (q < 2 ? wm * 64 + q * 32 : wn * 128 + (q - 2) * 32) + 16 * (g & 1) + 4 * ss;
-      foff[q] = (q < 2 ? 0 : DW_K * DW_ROW) + r0 * DW_ROW + wsw(r0, col >> 3) * 16 + (col & 7) * 2;
+      foff[q] = (q < 2 ? DW_TILE : 0) + r0 * DW_ROW + wsw(r0, col >> 3) * 16 + (col & 7) * 2;
     }
   }
-  auto frag = [&](const uint8_t* sb, int kk, int q) __attribute__((always_inline)) -> bf16x8 {
-    const uint8_t* a = sb + foff[q] + kk * 16 * DW_ROW;
-    const v4i16_t lo = ds_tr16(a), hi = ds_tr16(a + 4 * DW_ROW);
+  auto frag = [&](const uint8_t* sb, int at) __attribute__((always_inline)) -> bf16x8 {
+    const v4i16_t lo = ds_tr16(sb + at), hi = ds_tr16(sb + at + 4 * DW_ROW);
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  for (int s = 0; s < DW_S - 1 && s < KT; ++s) issue(s);
+  if (KT > 0) issue(0);
   for (int kt = 0; kt < KT; ++kt) {
-    const int later = min(DW_S - 2, KT - 1 - kt);
-    if (later >= 2) bwait_vm<8>();
-    else if (later == 1) bwait_vm<4>();
-    else bwait_vm<0>();
+    bwait_vm<0>();
     __syncthreads();
-    if (kt + DW_S - 1 < KT) issue(kt + DW_S - 1);
+    if (kt + 1 < KT) issue(kt + 1);
     const uint8_t* sb = lds + (kt % DW_S) * DW_STAGE;
 #pragma unroll
     for (int kk = 0; kk < DW_K / 16; ++kk) {
-      bf16x8 fa[2], fb[4];
+      const int o = kk * 16 * DW_ROW;
+      bf16x8 fa[3][2], fb[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) fa[i] = frag(sb, kk, i);
+      for (int j = 0; j < 4; ++j) fb[j] = frag(sb, foff[2 + j] + o);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) fb[j] = frag(sb, kk, 2 + j);
+      for (int q = 0; q < 3; ++q)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < 2; ++i) fa[q][i] = frag(sb, foff[i] + q * DW_TILE + o);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[j][i], 0, 0, 0);
+      for (int q = 0; q < 3; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[q][i], acc[j][i], 0, 0, 0);
     }
   }
   // acc[j][i][r]: expert m0 + 64 wm + 32 i + lr, column n0 + 128 wn + 32 j + 8 (r / 4) + 4 lg + r % 4.  Each half i is
@@ -691,14 +693,34 @@ __global__ __launch_bounds__(256) void score_dw_kernel(const float* __restrict__
     }
 }
 
-// out[i] = sum over z of part[z, i], z ascending.
-__global__ __launch_bounds__(256) void plane_sum_kernel(const float* __restrict__ part, int Z, int64_t n,
-                                                        float* __restrict__ out) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= n) return;
-  f32x4 s = *(const f32x4*)(part + i);
-  for (int z = 1; z < Z; ++z) s += *(const f32x4*)(part + z * n + i);
-  *(f32x4*)(out + i) = s;
+// The last sums: dw[i] = sum over z of part[z, i], z ascending (workgroups below `planes`), and
+// db[e] = sum over g of db_part[g, e], eight interleaved sums per expert (the rest).
+__global__ __launch_bounds__(256) void score_sum_kernel(const float* __restrict__ part, int Z, int64_t n, float* __restrict__ dw,
+                                                        int planes, const float* __restrict__ db_part, int G, int E,
+                                                        float* __restrict__ db) {
+  __shared__ float red[8][32];
+  if ((int)blockIdx.x < planes) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    f32x4 s = *(const f32x4*)(part + i);
+    for (int z = 1; z < Z; ++z) s += *(const f32x4*)(part + z * n + i);
+    *(f32x4*)(dw + i) = s;
+    return;
+  }
+  const int cl = threadIdx.x & 31, r = threadIdx.x >> 5, e = ((int)blockIdx.x - planes) * 32 + cl;
+  float s = 0.f;
+  if (e < E) {
+#pragma unroll 8
+    for (int g = r; g < G; g += 8) s += db_part[(int64_t)g * E + e];
+  }
+  red[r][cl] = s;
+  __syncthreads();
+  if (r == 0 && e < E) {
+    s = red[0][cl];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += red[i][cl];
+    db[e] = s;
+  }
 }
 
 static int dw_splits(bool f32, int64_t T, int E, int d) {
@@ -745,12 +767,13 @@ hipError_t launch_route_scored_bwd(bool f32, const ScoreRule& rule, const float*
   float* part = L.Z > 1 ? (float*)(w + L.dw) : dw;
   float* dbp = (float*)(w + L.db);
   const DlArgs p{dgate, dlogits, logits, topk_idx, T, L.Tp, E, L.Ep, k, rule, (float*)(w + L.dl),
-                 (bf16_t*)(w + L.dl), (bf16_t*)(w + L.low), (uint32_t*)(w + L.zero), db ? dbp : nullptr};
+                 (bf16_t*)(w + L.dl), (bf16_t*)(w + L.low), (uint32_t*)(w + L.zero),
+                 w_r, (bf16_t*)(w + L.wt), d, L.G, db ? dbp : nullptr};
   const int vpl = (E + 63) / 64;
 #define DL(V)                                                                   \
   {                                                                             \
     if (f32) score_dl_kernel<V, true><<<(unsigned)L.G, 256, 0, st>>>(p);        \
-    else score_dl_kernel<V, false><<<(unsigned)L.G, 256, 0, st>>>(p);           \
+    else score_dl_kernel<V, false><<<(unsigned)(L.G + d / 64 * (L.Ep / 64)), 256, 0, st>>>(p); \
   }
   if (vpl <= 1) DL(1)
   else if (vpl <= 2) DL(2)
@@ -766,13 +789,11 @@ hipError_t launch_route_scored_bwd(bool f32, const ScoreRule& rule, const float*
     score_dw_kernel<<<dim3((d + GB - 1) / GB, (E + GB - 1) / GB, L.Z), 256, 0, st>>>(p.dl, (const float*)x, T, E,
                                                                                     d, part);
   } else {
-    bf16_t* wt = (bf16_t*)(w + L.wt);
-    score_turn_kernel<<<dim3(d / 64, L.Ep / 64), 256, 0, st>>>(w_r, E, L.Ep, d, wt);
     // dx: at most 2^18 rows a launch (32-bit offsets inside the operands)
     for (int64_t t0 = 0; t0 < T; t0 += (int64_t)1 << 18) {
       Fp8Args a{};
       a.A = (const uint8_t*)(p.planes + t0 * 3 * L.Ep);
-      a.W0 = (const uint8_t*)wt;
+      a.W0 = (const uint8_t*)p.wt;
       a.a_rows = std::min<int64_t>(T - t0, (int64_t)1 << 18);
       a.C = a.a_rows;
       a.K = 6 * L.Ep;
@@ -789,9 +810,10 @@ hipError_t launch_route_scored_bwd(bool f32, const ScoreRule& rule, const float*
     score_dw_mfma_kernel<<<(unsigned)(tiles * L.Z), 512, DW_LDS, st>>>(a);
   }
   if ((err = hipGetLastError()) != hipSuccess) return err;
-  const int64_t n = (int64_t)E * d;
-  if (L.Z > 1) plane_sum_kernel<<<(unsigned)((n / 4 + 255) / 256), 256, 0, st>>>(part, L.Z, n, dw);
-  if (db && (err = launch_column_sum(dbp, L.G, E, db, st)) != hipSuccess) return err;
+  const int64_t n = (int64_t)E * d;   // d is a multiple of 8
+  const int planes = L.Z > 1 ? (int)((n / 4 + 255) / 256) : 0, sums = db ? (E + 31) / 32 : 0;
+  if (planes + sums)
+    score_sum_kernel<<<(unsigned)(planes + sums), 256, 0, st>>>(part, L.Z, n, dw, planes, dbp, L.G, E, db);
   return hipGetLastError();
 }
 
