@@ -123,10 +123,11 @@ int moe_route(const moe_shape* shape, const void* x, const float* w_router,
  *   slot = (ring_head + rank(c)) mod C,
  * where rank orders copies by (expert, token): segments are expert-contiguous
  * and hold their tokens in ascending order.
- * In:  x [T,d] act (bf16 for MOE_MXFP8), topk_idx [T,k], ring_head in [0, C).
- * Out: ring_x [C,d] act (MOE_MXFP8: E4M3 codes, each row MX-quantised along d)
+ * In:  x [T,d] act (bf16 for MOE_MXFP8 and MOE_FP8), topk_idx [T,k], ring_head in [0, C).
+ * Out: ring_x [C,d] act (MOE_MXFP8, MOE_FP8: E4M3 codes, each row quantised along d)
  *        — only the T*k used slots are written;
- *      ring_x_scale [d/128][C][4] E8M0 bytes (MOE_MXFP8 only, else NULL);
+ *      ring_x_scale [d/128][C][4] E8M0 bytes (MOE_MXFP8), [d/128][C] f32 (MOE_FP8: codes and
+ *      scales of moe_quantize_fp8 with row_block 1), else NULL;
  *      expert_offset [E+1] int32, segment starts relative to the head (offset[E] = T*k);
  *      copy_slot [T,k] int32 absolute slot of each copy;
  *      slot_copy [C] int32 copy id t*k+j held by each used slot (other slots untouched).
@@ -142,15 +143,16 @@ int moe_dispatch(const moe_shape* shape, const void* x, const int32_t* topk_idx,
  * grouped GEMMs (the expert-centric scheme the warp-decode page contrasts with;
  * MXFP8 expert kernels per the @rohanpaul_ai tweet on the khabar-ai page):
  *   [A|U] = X_e [W_gate[e]; W_up[e]]^T,  H = silu(A) * U,  Y_e = H W_down[e]^T.
- * H is bf16 (fp32 for MOE_F32; MX along f for MOE_MXFP8) and lives in the workspace.
+ * H is bf16 (fp32 for MOE_F32; 8-bit along f for MOE_MXFP8 and MOE_FP8) and lives in the workspace.
  * In:  ring_x (+ ring_x_scale), expert_offset, ring_head; w_gate, w_up [E,f,d] and
  *      w_down [E,d,f] act, or E4M3 codes with w_gate_scale/w_up_scale [d/128][E*f][4]
- *      and w_down_scale [f/128][E*d][4] for MOE_MXFP8 (NULL otherwise), as
- *      moe_quantize_mx writes them for the [E*f, d] and [E*d, f] matrices.
+ *      and w_down_scale [f/128][E*d][4] for MOE_MXFP8, as moe_quantize_mx writes them for
+ *      the [E*f, d] and [E*d, f] matrices, or one fp32 scale per 128 x 128 for MOE_FP8 (above),
+ *      as moe_quantize_fp8 writes them for the same matrices (NULL otherwise).
  * Out: ring_y [C,d] (bf16; fp32 for MOE_F32) at the segment slots;
  *      saved_au [C,2f] bf16 (A then U per slot) when not NULL — the backward's input
- *      (MOE_BF16 and MOE_MXFP8: the gate/up fp32 accumulations rounded to bf16; NULL for
- *      MOE_F32).
+ *      (MOE_BF16, MOE_MXFP8 and MOE_FP8: the gate/up fp32 accumulations rounded to bf16; NULL
+ *      for MOE_F32).
  * workspace: moe_workspace_bytes(shape, MOE_OP_EXPERT_FFN) bytes.
  */
 int moe_expert_ffn(const moe_shape* shape, const void* ring_x, const uint8_t* ring_x_scale,

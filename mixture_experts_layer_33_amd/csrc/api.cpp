@@ -78,7 +78,7 @@ size_t moe_workspace_bytes(const moe_shape* s, int op) {
     case MOE_OP_ROUTE: return align256(moe::route_workspace_bytes(T, s->experts, s->hidden));
     case MOE_OP_DISPATCH: return align256(moe::dispatch_workspace_bytes(T, s->experts));
     case MOE_OP_EXPERT_FFN:
-      if (s->dtype == MOE_FP8) return align256(moe::ffn_fp8_workspace_bytes(n, C, s->experts, s->ffn));
+      if (s->dtype == MOE_FP8) return align256(moe::ffn_fp8_workspace_bytes(n, C, s->hidden, s->experts, s->ffn));
       return align256(moe::ffn_workspace_bytes(n, C, s->hidden, s->experts, s->ffn, s->dtype));
     case MOE_OP_COMBINE: return 0;
     case MOE_OP_DECODE:

@@ -17,6 +17,7 @@
 // bf16 (every E4M3 value is a bf16 value) and multiplied by the bf16 MFMA, whose sums are fp32
 // (error against fp64 5e-7), at half the rate.
 #include <algorithm>
+#include <cmath>
 #ifdef PROBE
 #include <cstdlib>
 #endif
@@ -143,9 +144,9 @@ __device__ __forceinline__ bool thin_tile(const int32_t* offset, int E, int mt, 
 }
 
 // Few token rows: a weight stream.  16 token rows x 32 W weight rows, W wavefronts, each with 32 weight rows
-// (SWIGLU: 16 gate and the matching 16 up rows; W = 8: a workgroup's 128 columns are a whole block of H, which
-// it quantises; W = 4: twice the workgroups where 128 columns each would leave half of the chip
-// idle, h in fp32 for quantise_h_kernel).  The work is one pass over the weights, so what counts is bytes in flight: S stages
+// (SWIGLU: 16 gate and the matching 16 up rows, W = 4: 64 columns a workgroup, half a block of H, so that twice
+// the workgroups fill the chip; h leaves in fp32 for quantise_h_kernel: 46 -> 36 us for the gate and up
+// products of one token, 8 of 64 experts, d 7168, f 2048).  The work is one pass over the weights, so what counts is bytes in flight: S stages
 // of whole 128-byte lines are copied global -> LDS, S - 1 of them ahead.  The same stream read straight
 // into registers in the MFMA's layout asks for each line in halves by 16 rows and ran at 3.7 TB/s where
 // this one runs at 5 to 6 (one token, 8 of 64 experts, d 7168, f 2048).
@@ -165,9 +166,8 @@ __global__ __launch_bounds__(64 * W) void fp8_thin_kernel(Fp8Args p) {
   using SL = ThinStage<W, S>;
   constexpr bool SWIGLU = KIND >= FP8_SWIGLU, WIDE = KIND == FP8_F32;
   constexpr int L = SL::L, COLS = SWIGLU ? 16 * W : 32 * W;
-  static_assert(!SWIGLU || W == 8 || W == 4, "a SWIGLU tile holds a block of H or half of one");
+  static_assert(!SWIGLU || W == 4, "half a block of H");
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  __shared__ float hmax[8][16];
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lr = lane & 15, lg = lane >> 4;
@@ -263,29 +263,10 @@ __global__ __launch_bounds__(64 * W) void fp8_thin_kernel(Fp8Args p) {
   // acc[c][r]: token row lr, weight row 16 f_c + 4 lg + r
   const int64_t slot = slot_of(min(lr, rows - 1));
   if constexpr (SWIGLU) {
-    float h[4], am = 0.f;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      h[r] = silu(acc[0][r]) * acc[1][r];
-      am = amax2(am, h[r]);
-    }
+    if (lr >= rows) return;
     const int col = n0 + 16 * wave + 4 * lg;
-    if constexpr (W == 4) {
-      if (lr >= rows) return;
-      *(f32x4*)(p.h32 + ((int64_t)seg + row0 + lr) * p.N + col) = f32x4{h[0], h[1], h[2], h[3]};
-    } else {
-      am = amax2(am, __shfl_xor(am, 16, 64));
-      am = amax2(am, __shfl_xor(am, 32, 64));
-      if (lg == 0) hmax[wave][lr] = am;
-      __syncthreads();
-      am = 0.f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) am = amax2(am, hmax[w][lr]);
-      const float s = fp8_scale(am);
-      if (lr >= rows) return;
-      *(uint32_t*)((uint8_t*)p.out + slot * p.N + col) = h_encode4(h[0], h[1], h[2], h[3], s);
-      if (wave == 0 && lg == 0) p.out_scale[(int64_t)ct * p.C + slot] = s;
-    }
+    *(f32x4*)(p.h32 + ((int64_t)seg + row0 + lr) * p.N + col) =
+        f32x4{silu(acc[0][0]) * acc[1][0], silu(acc[0][1]) * acc[1][1], silu(acc[0][2]) * acc[1][2], silu(acc[0][3]) * acc[1][3]};
     if constexpr (KIND == FP8_SWIGLU_SAVE) {
       *(u32x2*)(p.saved_au + slot * 2 * p.N + col) = u32x2{pack_bf2(acc[0][0], acc[0][1]), pack_bf2(acc[0][2], acc[0][3])};
       *(u32x2*)(p.saved_au + (slot * 2 + 1) * p.N + col) = u32x2{pack_bf2(acc[1][0], acc[1][1]), pack_bf2(acc[1][2], acc[1][3])};
@@ -334,7 +315,7 @@ __global__ __launch_bounds__(256) void quantise_h_kernel(const float* __restrict
 template <int KIND, int W, int S>
 static hipError_t run_fp8_thin(const Fp8Args& a, int64_t tiles, hipStream_t st) {
   constexpr int cols = KIND >= FP8_SWIGLU ? 16 * W : 32 * W, lds = S * ThinStage<W, S>::SIZE;
-  static_assert(lds + 512 <= 160 * 1024, "LDS");
+  static_assert(lds <= 160 * 1024, "LDS");
   auto kern = fp8_thin_kernel<KIND, W, S>;
   hipError_t err = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (err != hipSuccess) return err;
@@ -477,16 +458,34 @@ hipError_t launch_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8
   return hipGetLastError();
 }
 
-// The experts' path by the mean rows of an expert (host-known): the thin kernel up to 16, tiles of 128 rows
-// below 256 (one tile holds an expert's rows, each weight is read once), else of 256.
-static int ffn_fm(int64_t n, int E) {
-#ifdef PROBE
-  if (getenv("FM")) return atoi(getenv("FM"));
-#endif
-  return n <= 16 * (int64_t)E ? 0 : n < 256 * (int64_t)E ? 2 : 4;
-}
-// Workgroups of the thin gate/up kernel below which it takes half blocks of H.
+// How the experts' products run.  The host knows the mean rows of an expert, not their spread.
+//   * `few`: fewer than THIN_FEW workgroups of 128 columns over all 16-row tiles: the thin kernel (4 experts x
+//     16 rows, d 7168, f 2048: 47 us against 65 with tiles of 64 rows; 64 experts x 8 rows: 309 us
+//     either way, and a batch that falls on one expert would read its weights once per 16 rows).
+//   * else tiles of 64 fm rows, the least estimated time of both products: rounds of 256 workgroups times the
+//     blocks of one (dense_plan's times), or the weights at the rate that height streams them at
+//     (5.3, 5.1, 4.6, 4.5 TB/s: the lower tiles keep three stages).  A tile list is shared by both products.
+//     Measured at 64 experts, d 4096, f 2048, us for fm = 1 | 2 | 3 | 4: 32 rows 310 | 313 | 363 | 371, 64 rows 344 |
+//     325 | 370 | 377, 128 rows 470 | 404 | 390 | 394, 200 rows 621 | 477 | 562 | 434, 300 rows 872 | 667 | 652 | 713.
 constexpr int64_t THIN_FEW = 200;
+
+static int ffn_tile(int64_t n, int d, int E, int f) {
+#ifdef PROBE
+  if (getenv("FM")) return std::max(1, atoi(getenv("FM")));
+#endif
+  const double us[4] = {0.95, 0.98, 1.07, 1.25}, tbs[4] = {5.3, 5.1, 4.6, 4.5};
+  const double r = (double)n / E, typical = r + 0.5 * std::sqrt(r);
+  int best = 1;
+  double least = 1e300;
+  for (int fm = 1; fm <= 4; ++fm) {
+    const double tiles = E * std::ceil(typical / (64 * fm));
+    auto rounds = [&](double cols) { return std::ceil(tiles * cols / 256); };
+    const double busy = (rounds(f / 128) * (d / 128) + rounds((d + 255) / 256) * (f / 128)) * us[fm - 1];
+    const double t = std::max(busy, 3.0 * E * d * f / tbs[fm - 1] * 1e-6);
+    if (t < least) { least = t; best = fm; }
+  }
+  return best;
+}
 
 struct FfnFp8Layout {
   size_t tiles, h, hs, h32, total;
@@ -494,12 +493,12 @@ struct FfnFp8Layout {
   int64_t mt;   // bound on the row tiles: every tile holds a row
   bool few;
 };
-static FfnFp8Layout ffn_fp8_layout(int64_t n, int64_t C, int E, int f) {
+static FfnFp8Layout ffn_fp8_layout(int64_t n, int64_t C, int d, int E, int f) {
   auto al = [](size_t b) { return (b + 255) & ~(size_t)255; };
   FfnFp8Layout L;
-  L.fm = ffn_fm(n, E);
-  L.mt = std::min<int64_t>(max_tiles_for(n, E, L.fm ? 64 * L.fm : 16), n);
-  L.few = L.fm == 0 && L.mt * (f / 128) < THIN_FEW;
+  L.few = std::min<int64_t>(max_tiles_for(n, E, 16), n) * (f / 128) < THIN_FEW;
+  L.fm = L.few ? 0 : ffn_tile(n, d, E, f);
+  L.mt = std::min<int64_t>(max_tiles_for(n, E, L.few ? 16 : 64 * L.fm), n);
   size_t o = 0;
   L.tiles = o; o += al((size_t)(2 * L.mt + 64) * 4);
   L.h = o; o += al((size_t)C * f);
@@ -508,14 +507,16 @@ static FfnFp8Layout ffn_fp8_layout(int64_t n, int64_t C, int E, int f) {
   L.total = o;
   return L;
 }
-size_t ffn_fp8_workspace_bytes(int64_t n, int64_t C, int E, int f) { return ffn_fp8_layout(n, C, E, f).total; }
+size_t ffn_fp8_workspace_bytes(int64_t n, int64_t C, int d, int E, int f) {
+  return ffn_fp8_layout(n, C, d, E, f).total;
+}
 
 hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const int32_t* expert_offset,
                           int64_t head, int64_t C, int64_t n, int d, int E, int f,
                           const void* w_gate, const void* w_up, const void* w_down,
                           const float* sg, const float* su, const float* sd, void* ring_y,
                           void* saved_au, void* ws, hipEvent_t* events, hipStream_t st) {
-  const FfnFp8Layout L = ffn_fp8_layout(n, C, E, f);
+  const FfnFp8Layout L = ffn_fp8_layout(n, C, d, E, f);
   uint8_t* w = (uint8_t*)ws;
   int32_t* ntiles = (int32_t*)(w + L.tiles);
   int32_t* tiles = ntiles + 64;
@@ -550,18 +551,16 @@ hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const i
 #define RUN(FM, KIND, S, G)                                              \
   err = once ? run_fp8_tile<FM, KIND, S, 3>(G, mt, st) : run_fp8_tile<FM, KIND, S, 2>(G, mt, st);
   if (fm == 0) {
-    if (L.few) {
-      err = saved_au ? run_fp8_thin<FP8_SWIGLU_SAVE, 4, 7>(p, mt, st) : run_fp8_thin<FP8_SWIGLU, 4, 7>(p, mt, st);
-      if (err != hipSuccess) return err;
-      quantise_h_kernel<<<(unsigned)((n * (f / 8) + 255) / 256), 256, 0, st>>>(p.h32, n, f, head, C, w + L.h, p.out_scale);
-      err = hipGetLastError();
-    } else {
-      err = saved_au ? run_fp8_thin<FP8_SWIGLU_SAVE, 8, 4>(p, mt, st) : run_fp8_thin<FP8_SWIGLU, 8, 4>(p, mt, st);
-    }
+    err = saved_au ? run_fp8_thin<FP8_SWIGLU_SAVE, 4, 7>(p, mt, st) : run_fp8_thin<FP8_SWIGLU, 4, 7>(p, mt, st);
+    if (err != hipSuccess) return err;
+    quantise_h_kernel<<<(unsigned)((n * (f / 8) + 255) / 256), 256, 0, st>>>(p.h32, n, f, head, C, w + L.h, p.out_scale);
+    err = hipGetLastError();
   } else if (fm == 1) {
     if (saved_au) RUN(1, FP8_SWIGLU_SAVE, 3, p) else RUN(1, FP8_SWIGLU, 3, p)
   } else if (fm == 2) {
     if (saved_au) RUN(2, FP8_SWIGLU_SAVE, 3, p) else RUN(2, FP8_SWIGLU, 3, p)
+  } else if (fm == 3) {
+    if (saved_au) RUN(3, FP8_SWIGLU_SAVE, 2, p) else RUN(3, FP8_SWIGLU, 2, p)
   } else {
     if (saved_au) RUN(4, FP8_SWIGLU_SAVE, 2, p) else RUN(4, FP8_SWIGLU, 2, p)
   }
@@ -582,6 +581,7 @@ hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const i
     err = run_fp8_thin_plain<FP8_BF16>(q, mt, thin_waves(mt, d), st);
   } else if (fm == 1) RUN(1, FP8_BF16, 3, q)
   else if (fm == 2) RUN(2, FP8_BF16, 3, q)
+  else if (fm == 3) RUN(3, FP8_BF16, 2, q)
   else RUN(4, FP8_BF16, 2, q)
 #undef RUN
   if (err != hipSuccess) return err;

@@ -62,7 +62,7 @@ hipError_t launch_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8
 // out = round(add + A W^T) of bf16 rows (the tile of the FP8 products)
 struct Fp8Args;
 hipError_t launch_tile_add(Fp8Args& a, hipStream_t st);
-size_t ffn_fp8_workspace_bytes(int64_t n, int64_t C, int E, int f);
+size_t ffn_fp8_workspace_bytes(int64_t n, int64_t C, int d, int E, int f);
 hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const int32_t* expert_offset,
                           int64_t head, int64_t C, int64_t n, int d, int E, int f,
                           const void* w_gate, const void* w_up, const void* w_down,
