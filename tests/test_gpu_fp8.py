@@ -118,6 +118,38 @@ def test_matmul(M, N, K, ty):
     assert same_bits(out, matmul(*ab, ty))
 
 
+# sizes at which taller tiles, or K splits with their planes, take the least time
+LARGE = [(2000, 2056, 128), (1000, 4168, 256), (2000, 4168, 128), (2045, 4168, 384), (2900, 4168, 256), (4093, 4090, 128),
+         (129, 130, 4096), (301, 303, 8192), (77, 511, 16384), (3, 7169, 16384), (1, 33, 16384)]
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+@pytest.mark.parametrize("ty", [BF, torch.float32])
+def test_matmul_of_many_rows_or_a_long_k(M, N, K, ty):
+    print(f"\n[case] matmul_fp8 {M}x{N}x{K} {ty}", flush=True)
+    ab = operands(M, N, K, M + N)
+    out = matmul(*ab, ty)
+    check_product(out, *ab)
+    assert same_bits(out, matmul(*ab, ty))
+
+
+def test_matmul_twice_at_once():
+    """Two products on two streams, each with its own workspace."""
+    print("\n[case] matmul_fp8 two streams", flush=True)
+    sizes = [(129, 130, 4096), (700, 1032, 512)]
+    ab = [operands(*m, 30 + i) for i, m in enumerate(sizes)]
+    want = [matmul(*o, BF) for o in ab]
+    out = [torch.zeros_like(w) for w in want]
+    ws = [moe.matmul_fp8_workspace(*m, DEV) for m in sizes]
+    streams = [torch.cuda.Stream() for _ in sizes]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            moe.moe_matmul_fp8(*ab[i], out[i], ws[i], stream=st)
+    torch.cuda.synchronize()
+    assert all(same_bits(o, w) for o, w in zip(out, want))
+
+
 @pytest.mark.parametrize("M", [1, 16, 40, 200, 600])
 def test_matmul_keeps_rows_apart(M):
     """Scales that differ by 2^40 from row to row and from block to block, a row and a block of NaN
@@ -244,7 +276,8 @@ def ffn_within(y, X, W, what, a_got=None, u_got=None):
     assert np.linalg.norm(y - ref) <= 2e-2 * np.linalg.norm(ref) + 1e-30
 
 
-def check_experts(y, au, s, q, qs, slot, counts, wt):
+def check_experts(y, au, s, q, qs, slot, counts, wt, some=False):
+    """some: of an expert with many rows only those at its ends, at the borders of 64 rows, and a few more."""
     X = ops.spread_rows(codes(q), host(qs).T)
     Y, lo, f = host(y[slot]), 0, s.ffn
     AU = None if au is None else host(au[slot])
@@ -252,6 +285,9 @@ def check_experts(y, au, s, q, qs, slot, counts, wt):
         if c:
             W = [ops.spread_blocks(codes(w[e]), host(sw[e])) for w, sw in wt]
             r = slice(lo, lo + c)
+            if some and c > 24:
+                near = [m for m in range(c) if m < 2 or m >= c - 2 or m % 64 in (0, 63)]
+                r = lo + np.unique(near + list(np.random.default_rng(e).integers(0, c, 16)))
             ffn_within(Y[r], X[r], W, f"expert {e} ({c} rows)", *(() if au is None else (AU[r, :f], AU[r, f:])))
         lo += c
 
@@ -275,6 +311,56 @@ def test_experts(counts, d, f, head, save):
     assert (y[other] == 7).all() and (au is None or (au[other] == 7).all())
     y2, au2 = experts(s, ring, rs, off, head, wt, save)
     assert same_bits(y, y2) and (au is None or same_bits(au, au2))
+
+
+# tiles of 64, 128, 192 and 256 rows take the least time here, in this order: full, ragged and empty tiles
+TILES = [([5, 0, 1, 17, 40, 2, 3, 0, 7, 1, 4, 0, 0, 9, 7, 1], 128, 1280, 3), ([64, 65, 63, 0, 128, 129, 1, 200, 0, 31, 97, 60, 45, 12, 100, 28], 128, 1280, 1000),
+         ([2000, 1, 0, 1333, 666], 128, 1024, 4444), ([4096, 0, 257, 4883], 256, 640, 11000)]
+
+
+@pytest.mark.parametrize("counts,d,f,head", TILES, ids=[f"{sum(c[0])}rows-d{c[1]}f{c[2]}" for c in TILES])
+@pytest.mark.parametrize("save", [False, True])
+def test_experts_in_tiles(counts, d, f, head, save):
+    print(f"\n[case] expert_ffn fp8 {counts} d={d} f={f} head={head} save={save}", flush=True)
+    s, q, qs, slot, ring, rs, off, wt = expert_case(counts, d, f, head, d + f)
+    head %= s.capacity
+    y, au = experts(s, ring, rs, off, head, wt, save)
+    check_experts(y, au, s, q, qs, slot, counts, wt, some=True)
+    other = torch.ones(s.capacity, dtype=torch.bool, device=DEV)
+    other[slot] = False
+    assert (y[other] == 7).all() and (au is None or (au[other] == 7).all())
+    y2, au2 = experts(s, ring, rs, off, head, wt, save)
+    assert same_bits(y, y2) and (au is None or same_bits(au, au2))
+    # a row whose scale is NaN leaves the others bit for bit as they were
+    bad = slot[sum(counts) // 2]
+    rs[0, bad] = float("nan")
+    y3, _ = experts(s, ring, rs, off, head, wt, save)
+    assert torch.isnan(y3[bad]).all()
+    y3[bad] = y[bad]
+    assert same_bits(y3, y)
+
+
+def test_experts_in_graphs_that_share_a_workspace():
+    """Two captured products over one workspace, replayed in turn with eager calls between."""
+    print("\n[case] expert_ffn fp8 graphs", flush=True)
+    cases = [expert_case(c, 256, 256, 3, 40 + i) for i, c in enumerate(([3, 9], [300, 410]))]
+    ws = max((moe.workspace(c[0], moe.OP_EXPERT_FFN, DEV) for c in cases), key=lambda w: w.numel())
+    outs, graphs = [], []
+    for s, q, qs, slot, ring, rs, off, wt in cases:
+        y = torch.zeros(s.capacity, s.hidden, dtype=BF, device=DEV)
+        experts(s, ring, rs, off, 3, wt, ws=ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.moe_expert_ffn(s, ring, rs, off, 3, wt[0][0], wt[1][0], wt[2][0], wt[0][1], wt[1][1], wt[2][1], y, None, ws)
+        outs.append(y)
+        graphs.append(graph)
+    for j in range(4):
+        for c, y, graph in zip(cases, outs, graphs):
+            c[5].mul_(1.5)
+            graph.replay()
+            torch.cuda.synchronize()
+            want, _ = experts(c[0], c[4], c[5], c[6], 3, c[7], ws=ws)
+            assert same_bits(y[c[3]], want[c[3]])
 
 
 def test_rows_do_not_depend_on_their_neighbours():

@@ -217,6 +217,66 @@ def test_backward(case, more):
         assert same_bits(dx, dx2) and same_bits(dw, dw2)
 
 
+# sizes at which dx is built from taller tiles
+MANY = [("bf16", 4100, 1024, 64, 6, R("sigmoid")), ("bf16", 5000, 1600, 40, 4, R()), ("bf16", 6001, 2112, 64, 4, R(renormalise=False))]
+
+
+@pytest.mark.parametrize("case", MANY, ids=[f"{c[1]}x{c[2]}" for c in MANY])
+def test_backward_of_many_tokens(case):
+    test_backward(case, True)
+
+
+def test_vectors_at_an_element_s_alignment():
+    """Biases, counts, gates and ids may start at any element."""
+    print("\n[case] route_scored alignment", flush=True)
+    rule = R("sigmoid", 4, 2, 2, True, 2.5)
+    for T in (3, 70):
+        d, E, k = 128, 160, 3
+        x, w, b, bal, _ = draw("bf16", T, d, E, k, rule, 6, True, biased=True)
+        s, idx, gate, cnt, logits = run("bf16", x, w, b, bal, k, rule)
+        dg, dlog = randn(gen(1), T, k), randn(gen(2), T, E)
+        want = backward("bf16", s, rule, dg, dlog, x, w, logits, idx, None)
+
+        def shift(t):
+            buf = torch.full((t.numel() + 8,), 7, dtype=t.dtype, device=DEV)
+            o = buf[1:1 + t.numel()].view(t.shape)
+            o.copy_(t)
+            return o, buf
+        (b1, _), (bal1, _), (dg1, _) = shift(b), shift(bal), shift(dg)
+        out = [shift(torch.zeros_like(t)) for t in (idx, gate, cnt)]
+        moe.moe_route_scored(s, make(rule), x, w, b1, bal1, *(o for o, _ in out), None, moe.workspace(s, moe.OP_ROUTE, DEV))
+        torch.cuda.synchronize()
+        for (o, buf), ref in zip(out, (idx, gate, cnt)):
+            assert torch.equal(o, ref) and buf[0] == 7 and (buf[1 + o.numel():] == 7).all()
+        db, buf = shift(torch.zeros(E, device=DEV))
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        moe.moe_route_scored_backward(s, make(rule), dg1, dlog, x, w, logits, out[0][0], None, dx, dw, db, moe.workspace(s, moe.OP_ROUTE_BACKWARD, DEV))
+        torch.cuda.synchronize()
+        assert same_bits(dx, want[0]) and same_bits(dw, want[1]) and same_bits(db, want[2]) and buf[0] == 7 and (buf[1 + E:] == 7).all()
+
+
+def test_two_routers_at_once():
+    """Two calls on two streams, each with its own workspace, forward and backward."""
+    print("\n[case] route_scored two streams", flush=True)
+    rule = R("sigmoid", 8, 4, 2, True, 2.5)
+    work = []
+    for T in (5, 300):
+        x, w, _, bal, _ = draw("bf16", T, 256, 64, 6, rule, T, True)
+        s, idx, gate, cnt, logits = run("bf16", x, w, None, bal, 6, rule)
+        dg = randn(gen(T), T, 6)
+        want = (idx, gate, cnt, logits, *backward("bf16", s, rule, dg, None, x, w, logits, idx, x)[:3])
+        work.append((s, x, w, bal, dg, want, [torch.zeros_like(t) for t in want], moe.workspace(s, moe.OP_ROUTE, DEV),
+                     moe.workspace(s, moe.OP_ROUTE_BACKWARD, DEV), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, x, w, bal, dg, _, o, ws, wb, st in work:
+            moe.moe_route_scored(s, make(rule), x, w, None, bal, *o[:4], ws, stream=st)
+            moe.moe_route_scored_backward(s, make(rule), dg, None, x, w, o[3], o[0], x, *o[4:], wb, stream=st)
+    torch.cuda.synchronize()
+    for v in work:
+        assert all(same_bits(a, c) for a, c in zip(v[5], v[6]))
+
+
 @pytest.mark.parametrize("rule", [R(), R(renormalise=False), R("sigmoid"), R("sigmoid", renormalise=False, scale=2.5)], ids=str)
 def test_gradient_against_differences(rule):
     """fp32 layer: x, W_r and b_r along random directions against central differences of the oracle's gates."""
