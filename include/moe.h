@@ -131,7 +131,8 @@ int moe_route(const moe_shape* shape, const void* x, const float* w_router,
  *      expert_offset [E+1] int32, segment starts relative to the head (offset[E] = T*k);
  *      copy_slot [T,k] int32 absolute slot of each copy;
  *      slot_copy [C] int32 copy id t*k+j held by each used slot (other slots untouched).
- * workspace: moe_workspace_bytes(shape, MOE_OP_DISPATCH) bytes.
+ * workspace: moe_workspace_bytes(shape, MOE_OP_DISPATCH) bytes.  MOE_FP8: x and ring_x are aligned to
+ * 16 bytes, ring_x_scale to 4 (MOE_ERR_ALIGN).
  */
 int moe_dispatch(const moe_shape* shape, const void* x, const int32_t* topk_idx,
                  int64_t ring_head, void* ring_x, uint8_t* ring_x_scale,
@@ -153,7 +154,8 @@ int moe_dispatch(const moe_shape* shape, const void* x, const int32_t* topk_idx,
  *      saved_au [C,2f] bf16 (A then U per slot) when not NULL — the backward's input
  *      (MOE_BF16, MOE_MXFP8 and MOE_FP8: the gate/up fp32 accumulations rounded to bf16; NULL
  *      for MOE_F32).
- * workspace: moe_workspace_bytes(shape, MOE_OP_EXPERT_FFN) bytes.
+ * workspace: moe_workspace_bytes(shape, MOE_OP_EXPERT_FFN) bytes.  MOE_FP8: tensors and workspace
+ * are aligned to 16 bytes, scales and offsets to 4 (MOE_ERR_ALIGN).
  */
 int moe_expert_ffn(const moe_shape* shape, const void* ring_x, const uint8_t* ring_x_scale,
                    const int32_t* expert_offset, int64_t ring_head,
@@ -378,7 +380,9 @@ int moe_quantize_mx_both(const void* src_bf16, int64_t batch, int64_t rows, int6
  *      (moe_add_rmsnorm_backward needs it).
  * Apart from h no output may overlap an input or another output.  y8 needs MOE_MXFP8 or
  * MOE_FP8 (MOE_ERR_DTYPE).  Tensors are aligned to 16 bytes (MOE_ERR_ALIGN); rstd and
- * y8_scale to 4.  eps that is negative, NaN or infinite: MOE_ERR_SHAPE.
+ * y8_scale to 4.  eps that is negative, NaN or infinite, or more than 2^23 tokens: MOE_ERR_SHAPE.
+ * A row whose sum of squares is above fp32's range has rstd 0; a row of zeros with eps 0 has
+ * rstd infinite and y NaN.
  */
 int moe_add_rmsnorm(const moe_shape* shape, const void* x, const void* residual,
                     const float* weight, float eps, void* h, void* y, uint8_t* y8,
@@ -392,6 +396,7 @@ int moe_add_rmsnorm(const moe_shape* shape, const void* x, const void* residual,
  * In:  dy [T,d] act; dh [T,d] act, the gradient that reaches h from elsewhere, or NULL;
  *      h, weight, rstd of the forward.
  * Out: dx [T,d] act (may be dy or dh itself); dweight [d] f32 or NULL.
+ * Apart from dx no output may overlap an input or another output.
  * workspace: moe_workspace_bytes(shape, MOE_OP_NORM_BACKWARD) bytes.  Alignment as above.
  */
 int moe_add_rmsnorm_backward(const moe_shape* shape, const void* dy, const void* dh,
@@ -427,8 +432,9 @@ typedef struct moe_router {
  *      NULL, balance [E] f32 or NULL.  top_k <= top_groups * E / G.
  * Out: topk_idx, topk_gate, expert_count as moe_route; logits [T,E] f32 (l, with b_r) or
  *      NULL (moe_route_scored_backward needs them).
+ * No output may overlap an input or another output.
  * workspace: moe_workspace_bytes(shape, MOE_OP_ROUTE) bytes.  A rule outside the limits
- * above: MOE_ERR_SHAPE.  x and w_router are aligned to 16 bytes (MOE_ERR_ALIGN).
+ * above, or MOE_F32 with more than 2^21 tokens: MOE_ERR_SHAPE.  x and w_router are aligned to 16 bytes (MOE_ERR_ALIGN).
  */
 int moe_route_scored(const moe_shape* shape, const moe_router* router, const void* x,
                      const float* w_router, const float* b_router, const float* balance,
@@ -446,7 +452,9 @@ int moe_route_scored(const moe_shape* shape, const moe_router* router, const voi
  *      or z loss), or NULL; x, w_router, logits, topk_idx of the forward; dx_in [T,d] act or
  *      NULL (the experts' part of dx, moe_backward_experts).
  * Out: dx [T,d] act (may be dx_in itself); dw_router [E,d] f32; db_router [E] f32 or NULL.
- * An id in topk_idx outside [0, E) is left out of the sums.
+ * Apart from dx no output may overlap an input or another output.
+ * An id in topk_idx outside [0, E) is left out of the sums.  bf16 tokens: d times 6 E (E rounded up to
+ * 64) below 2^32; MOE_F32: at most 2^21 tokens (MOE_ERR_SHAPE).
  * workspace: moe_workspace_bytes(shape, MOE_OP_ROUTE_BACKWARD) bytes.  x, w_router, dx_in, dx
  * and dw_router are aligned to 16 bytes (MOE_ERR_ALIGN).
  */
@@ -489,7 +497,7 @@ int moe_dispatch_q(const moe_shape* shape, const uint8_t* x8, const uint8_t* x8_
  * scales, scale = max(amax, 2^-100) / 448 per block, code = RNE_E4M3(v / scale) (a block that
  * holds an infinity or a NaN: scale NaN).  row_block 1: one block per row and 128
  * columns, scales [cols/128][rows]; row_block 128: one per 128 x 128, the last block of
- * rows may be short, scales [ceil(rows/128)][cols/128].  src and codes are aligned to 16
+ * rows may be short, scales [ceil(rows/128)][cols/128].  At most 2^37 elements.  src and codes are aligned to 16
  * bytes (MOE_ERR_ALIGN).
  */
 int moe_quantize_fp8(const void* src_bf16, int64_t rows, int64_t cols, int row_block,
@@ -498,7 +506,9 @@ int moe_quantize_fp8(const void* src_bf16, int64_t rows, int64_t cols, int row_b
 /*
  * moe_matmul_fp8: out = A W^T of two E4M3 matrices in nn.Linear layout,
  *   out[m,n] = sum_b a_scale[b][m] w_scale[n/128][b] sum_{i in block b} a[m,i] w[n,i],
- * b running over the K/128 blocks of 128; fp32 products and sums, one rounding.
+ * b running over the K/128 blocks of 128; fp32 products and sums, one rounding (a_scale w_scale is
+ * formed first; a bf16 out takes a block's sum from the 8-bit matrix instruction, to 2^-13 of
+ * the largest of every eight products).  out may not overlap an input.
  * In:  a [M,K], a_scale [K/128][M]; w [N,K], w_scale [ceil(N/128)][K/128] (moe_quantize_fp8
  *      with row_block 1 and 128).  K % 128 == 0; M K and N K < 2^32, M N < 2^38.
  * Out: out [M,N]: out_dtype MOE_BF16 or MOE_F32 (MOE_ERR_DTYPE otherwise).

@@ -151,6 +151,8 @@ int moe_dispatch(const moe_shape* s, const void* x, const int32_t* topk_idx, int
         missing_tok(copy_slot, T) || !slot_copy || !workspace)
       return MOE_ERR_NULL;
     if ((s->dtype == MOE_MXFP8 || s->dtype == MOE_FP8) && !ring_x_scale) return MOE_ERR_NULL;
+    if (s->dtype == MOE_FP8 && (unaligned(x) || unaligned(ring_x) || unaligned(ring_x_scale, 4)))
+      return MOE_ERR_ALIGN;
     if (ring_head < 0 || ring_head >= s->capacity) return MOE_ERR_SHAPE;
     if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_DISPATCH)) return MOE_ERR_WORKSPACE;
     if (s->tokens == 0)   // no copies: every expert's segment is empty
@@ -180,6 +182,12 @@ int moe_expert_ffn_timed(const moe_shape* s, const void* ring_x, const uint8_t* 
     if (scaled && (!ring_x_scale || !w_gate_scale || !w_up_scale || !w_down_scale))
       return MOE_ERR_NULL;
     if (saved_au && s->dtype == MOE_F32) return MOE_ERR_DTYPE;
+    if (s->dtype == MOE_FP8 &&
+        (unaligned(ring_x) || unaligned(w_gate) || unaligned(w_up) || unaligned(w_down) ||
+         unaligned(ring_y) || unaligned(saved_au) || unaligned(workspace) ||
+         unaligned(ring_x_scale, 4) || unaligned(w_gate_scale, 4) || unaligned(w_up_scale, 4) ||
+         unaligned(w_down_scale, 4)))
+      return MOE_ERR_ALIGN;
     if (ring_head < 0 || ring_head >= s->capacity) return MOE_ERR_SHAPE;
     if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_EXPERT_FFN)) return MOE_ERR_WORKSPACE;
     if (s->tokens == 0) return MOE_OK;
@@ -434,6 +442,11 @@ int moe_quantize_mx(const void* src_bf16, int64_t rows, int64_t cols, uint8_t* c
 }
 
 // ------------------------------------------------------------------ residual RMS norm
+namespace {
+// One workgroup of 256 threads per row, and a grid of fewer than 2^32 threads.
+constexpr int64_t NORM_ROWS = (int64_t)1 << 23;
+}  // namespace
+
 int moe_add_rmsnorm(const moe_shape* s, const void* x, const void* residual, const float* weight,
                     float eps, void* h, void* y, uint8_t* y8, void* y8_scale, float* rstd,
                     hipStream_t stream) {
@@ -443,7 +456,7 @@ int moe_add_rmsnorm(const moe_shape* s, const void* x, const void* residual, con
     const bool coded = s->dtype == MOE_MXFP8 || s->dtype == MOE_FP8;
     if (!coded && (y8 || y8_scale)) return MOE_ERR_DTYPE;
     if (!weight || (!y8) != (!y8_scale)) return MOE_ERR_NULL;
-    if (!(eps >= 0.f) || !std::isfinite(eps)) return MOE_ERR_SHAPE;
+    if (!(eps >= 0.f) || !std::isfinite(eps) || s->tokens > NORM_ROWS) return MOE_ERR_SHAPE;
     if (s->tokens == 0) return MOE_OK;
     if (!x || (!y && !y8)) return MOE_ERR_NULL;
     if (unaligned(x) || unaligned(residual) || unaligned(weight) || unaligned(h) || unaligned(y) ||
@@ -481,6 +494,9 @@ int moe_add_rmsnorm_backward(const moe_shape* s, const void* dy, const void* dh,
 
 // ------------------------------------------------------------------ scored routing
 namespace {
+// fp32 tokens: one grid dimension holds tiles of 64 of them (65,535 at most).
+constexpr int64_t SCORED_F32_ROWS = (int64_t)1 << 21;
+
 int check_router(const moe_shape* s, const moe_router* r, moe::ScoreRule* rule) {
   if (!r) return MOE_ERR_NULL;
   if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return MOE_ERR_SHAPE;
@@ -491,6 +507,7 @@ int check_router(const moe_shape* s, const moe_router* r, moe::ScoreRule* rule) 
   if (r->group_top < 1 || r->group_top > 2 || r->group_top > per) return MOE_ERR_SHAPE;
   if (r->renormalise != 0 && r->renormalise != 1) return MOE_ERR_SHAPE;
   if (!std::isfinite(r->scale)) return MOE_ERR_SHAPE;
+  if (s->dtype == MOE_F32 && s->tokens > SCORED_F32_ROWS) return MOE_ERR_SHAPE;
   *rule = {r->score == MOE_SCORE_SIGMOID, r->groups, r->top_groups, r->group_top, r->renormalise, r->scale};
   return MOE_OK;
 }
@@ -537,6 +554,9 @@ int moe_route_scored_backward(const moe_shape* s, const moe_router* router, cons
     if (unaligned(x) || unaligned(w_router) || unaligned(dx_in) || unaligned(dx) ||
         unaligned(dw_router) || unaligned(workspace))
       return MOE_ERR_ALIGN;
+    // dx's second operand, [d, 3 E'] bf16 (E': E rounded up to 64), is addressed with 32-bit offsets
+    if (s->dtype != MOE_F32 && (int64_t)s->hidden * 6 * ((s->experts + 63) / 64 * 64) >= (int64_t)1 << 32)
+      return MOE_ERR_SHAPE;
     if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_ROUTE_BACKWARD)) return MOE_ERR_WORKSPACE;
     if (T == 0) {
       hipError_t err = zero_words(dw_router, (size_t)s->experts * s->hidden, stream);
@@ -619,7 +639,7 @@ int moe_quantize_fp8(const void* src_bf16, int64_t rows, int64_t cols, int row_b
                      uint8_t* codes, float* scales, hipStream_t stream) {
   try {
     if (row_block != 1 && row_block != 128) return MOE_ERR_SHAPE;
-    if (rows < 0 || cols <= 0 || cols % 128 || rows > ((int64_t)1 << 40) / cols) return MOE_ERR_SHAPE;
+    if (rows < 0 || cols <= 0 || cols % 128 || rows > ((int64_t)1 << 37) / cols) return MOE_ERR_SHAPE;
     if (rows == 0) return MOE_OK;
     if (!src_bf16 || !codes || !scales) return MOE_ERR_NULL;
     if (unaligned(src_bf16) || unaligned(codes) || unaligned(scales, 4)) return MOE_ERR_ALIGN;

@@ -59,8 +59,8 @@ __device__ __forceinline__ u32x2 fp8_encode8(const float (&v)[8], float s) {
 }
 
 // H's codes: times the scale's reciprocal, which may take a value that lies within the last bit of a
-// rounding border to its other side.  H stays inside the experts' products and its division
-// was a tenth of a gate/up tile's arithmetic.
+// rounding border to its other side.  H stays inside the experts' products, and a division per
+// value would cost a gate/up tile's epilogue some ten instructions where one will do.
 __device__ __forceinline__ uint32_t h_encode4(float a, float b, float c, float d, float s) {
   const float r = 1.0f / s;
   auto q = [r](float v) { return __builtin_amdgcn_fmed3f(v * r, -FP8_MAX, FP8_MAX); };

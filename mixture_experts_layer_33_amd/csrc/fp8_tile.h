@@ -87,7 +87,8 @@ struct Fp8Stage {
   static constexpr int L = FM + 4 + (KIND == TILE_ADD ? 0 : 1);  // copies per wavefront and stage
 };
 
-template <int FM, int KIND, int S, int POL>
+// NT: the weights are read past the caches' retention (each is read about once).
+template <int FM, int KIND, int S, bool NT>
 __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
   using SL = Fp8Stage<FM, KIND>;
   constexpr int BM = SL::BM, BN = SL::BN, L = SL::L;
@@ -175,7 +176,7 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
     } else if (c < FM + 4) {
       const int i = c - FM;
       const uint32_t to = __builtin_amdgcn_readfirstlane(st + SL::B + (8 * i + wave) * 1024);
-      if (POL & 1) dma16nt(b_base[i] + (size_t)kt * 128, b_off[i], to);
+      if (NT) dma16nt(b_base[i] + (size_t)kt * 128, b_off[i], to);
       else dma16(b_base[i] + (size_t)kt * 128, b_off[i], to);
     } else {
       dma4(s_base + (size_t)kt * s_step, s_off, __builtin_amdgcn_readfirstlane(st + SL::SC + wave * 256));
@@ -477,14 +478,14 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
   }
 }
 
-template <int FM, int KIND, int S, int POL>
+template <int FM, int KIND, int S, bool NT>
 inline hipError_t run_fp8_tile(const Fp8Args& a, int64_t max_tiles, hipStream_t st) {
   const int nblk = (a.N + 127) / 128, nct = KIND >= FP8_SWIGLU ? nblk : (nblk + 1) / 2;
   constexpr int BM = 64 * FM;
   constexpr int epi = KIND == FP8_BF16 || KIND == TILE_ADD ? BM * 528 : KIND == FP8_SWIGLU_SAVE ? BM * 272 : KIND == FP8_SWIGLU ? BM * 144 : 0;
   constexpr int ring = S * Fp8Stage<FM, KIND>::SIZE, lds = ring > epi ? ring : epi;
   static_assert(lds <= 160 * 1024, "LDS");
-  auto kern = fp8_tile_kernel<FM, KIND, S, POL>;
+  auto kern = fp8_tile_kernel<FM, KIND, S, NT>;
   hipError_t err = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (err != hipSuccess) return err;
   const int64_t grid = 8 * ((max_tiles * nct * a.Z + 7) / 8);

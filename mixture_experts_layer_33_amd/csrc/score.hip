@@ -54,9 +54,11 @@ struct SelectArgs {
   ScoreRule rule;
   int32_t* topk_idx;
   float* topk_gate;
-  int32_t* count;        // [E], zeroed before
+  int32_t* count;        // [E]; with several workgroups block 0 clears it for score_count_kernel
   float* logits;
 };
+
+typedef float __attribute__((ext_vector_type(4), aligned(4))) f32x4_any;   // 16 bytes at a float's alignment
 
 // Row `at` of a [., E] array, this lane's experts lane VPL .. + VPL - 1 (0 past E), in 16-byte pieces where the
 // rows allow it.
@@ -66,7 +68,7 @@ __device__ __forceinline__ void lane_row(const float* __restrict__ at, int E, fl
   if (VPL % 4 == 0 && E % 4 == 0) {
 #pragma unroll
     for (int c = 0; c < VPL / 4; ++c) {
-      const f32x4 w = e0 + 4 * c < E ? *(const f32x4*)(at + e0 + 4 * c) : f32x4{0.f, 0.f, 0.f, 0.f};
+      const f32x4 w = e0 + 4 * c < E ? *(const f32x4_any*)(at + e0 + 4 * c) : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[4 * c + q] = w[q];
     }
@@ -81,7 +83,7 @@ __device__ __forceinline__ void lane_row(const float* __restrict__ at, int E, fl
 // (`run` lanes, a power of two; 0: the general form).  What bounds it is the latency of one token's
 // chain (loads, then k rounds of a 64-lane maximum): all planes' loads are issued first, a round
 // is a maximum in VALU moves, one ballot and two lane reads (8 of 256 experts in 8 groups, 2,048
-// tokens: 30 us with strided ownership, plane after plane, and two butterflies a round).
+// tokens: 9 us; 30 with strided ownership, plane after plane, and two butterflies a round).
 template <int VPL>
 __global__ __launch_bounds__(256) void score_select_kernel(SelectArgs p, int run) {
   __shared__ int chosen[4 * 32];
@@ -271,7 +273,7 @@ __global__ __launch_bounds__(1024) void score_count_kernel(const int32_t* __rest
 
 // Logits of a few tokens (T <= SMALL_T, bf16): a weight stream.  One wavefront per expert row and K split (the
 // splits of the MFMA router, whose tiles of 128 tokens would be empty here and its workgroups few: one
-// token, 256 experts, d 7168: 24 -> 6 us), W_r in fp32 and x widened: plain fp32 sums.
+// token, 256 experts, d 7168: 24 -> 4 us), W_r in fp32 and x widened: plain fp32 sums.
 constexpr int SMALL_T = 8;
 template <int NT>
 __global__ __launch_bounds__(256) void router_small_kernel(const bf16_t* __restrict__ x, const float* __restrict__ w_r,
@@ -282,7 +284,7 @@ __global__ __launch_bounds__(256) void router_small_kernel(const bf16_t* __restr
   const int i0 = (int)((int64_t)KA * z / KS) * 64, i1 = (int)((int64_t)KA * (z + 1) / KS) * 64;
   float acc[NT] = {};
 #pragma unroll 4
-  for (int i = i0 + lane * 4; i < i1; i += 256) {
+  for (uint32_t i = i0 + lane * 4; i < (uint32_t)i1; i += 256) {
     const f32x4 w = __builtin_nontemporal_load((const f32x4*)(w_r + (int64_t)e * d + i));
 #pragma unroll
     for (int t = 0; t < NT; ++t) {

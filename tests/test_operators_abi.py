@@ -38,6 +38,7 @@ def test_norm_refusals():
         assert norm(shape(ty), y8=FAKE) == _lib.MOE_ERR_NULL
         assert norm(shape(ty), ys=FAKE) == _lib.MOE_ERR_NULL
         assert norm(shape(ty), y8=ODD, ys=FAKE) == _lib.MOE_ERR_ALIGN
+    assert norm(shape("f32", T=(1 << 23) + 1, d=8, f=8)) == _lib.MOE_ERR_SHAPE
     assert norm(shape(d=100)) == _lib.MOE_ERR_SHAPE and norm(None) == _lib.MOE_ERR_NULL
     assert norm(shape(T=0), x=None, r=None, h=None, y=None, rstd=None) == _lib.MOE_OK
 
@@ -91,6 +92,11 @@ def test_route_scored_refusals():
     for bad in (dict(x=ODD), dict(w=ODD), dict(dxi=ODD), dict(dx=ODD), dict(dw=ODD), dict(ws=ODD)):
         assert route_bwd(s, r, **bad) == _lib.MOE_ERR_ALIGN, bad
     assert route_bwd(s, r, n=moe.workspace_bytes(s, moe.OP_ROUTE_BACKWARD) - 1) == _lib.MOE_ERR_WORKSPACE
+    many = shape("f32", T=(1 << 21) + 1, d=8, f=8)
+    assert route(many, r) == _lib.MOE_ERR_SHAPE and route_bwd(many, r) == _lib.MOE_ERR_SHAPE
+    wide = shape(T=1, d=64 * 10923, E=1024, f=64)      # d * 6 E is past 2^32
+    assert route_bwd(wide, r) == _lib.MOE_ERR_SHAPE
+    assert route_bwd(shape(T=1, d=64 * 10922, E=1024, f=64), r, n=0) == _lib.MOE_ERR_WORKSPACE
     with pytest.raises(KeyError):
         moe.make_router(score="tanh")
 
@@ -117,6 +123,16 @@ def test_fp8_layer_refusals():
         a[i] = None
         assert L().moe_expert_ffn(*a, 1 << 30, None) == _lib.MOE_ERR_NULL
     assert L().moe_expert_ffn(*ffn, moe.workspace_bytes(s, moe.OP_EXPERT_FFN) - 1, None) == _lib.MOE_ERR_WORKSPACE
+    for i in (1, 5, 6, 7, 11, 12, 13):
+        a = list(ffn)
+        a[i] = ODD
+        assert L().moe_expert_ffn(*a, 1 << 30, None) == _lib.MOE_ERR_ALIGN, i
+    for i in (2, 8, 9, 10):
+        a = list(ffn)
+        a[i] = FAKE + 2
+        assert L().moe_expert_ffn(*a, 1 << 30, None) == _lib.MOE_ERR_ALIGN, i
+    for x, ring, scale in ((ODD, FAKE, FAKE), (FAKE, ODD, FAKE), (FAKE, FAKE, FAKE + 2)):
+        assert L().moe_dispatch(s, x, FAKE, 0, ring, scale, FAKE, FAKE, FAKE, FAKE, 1 << 30, None) == _lib.MOE_ERR_ALIGN
     # what has no FP8 form says so
     assert L().moe_forward(s, *([FAKE] * 6), 0, *([FAKE] * 10), 0, FAKE, 1 << 40, None) == _lib.MOE_ERR_DTYPE
     assert L().moe_backward_mx(s, *([FAKE] * 8), 0, *([FAKE] * 11), 1 << 40, None) == _lib.MOE_ERR_DTYPE
@@ -144,6 +160,7 @@ def test_quantise_and_matmul_refusals():
     assert q(FAKE, -1, 128, 1, FAKE, FAKE, None) == _lib.MOE_ERR_SHAPE
     assert q(None, 4, 128, 1, FAKE, FAKE, None) == _lib.MOE_ERR_NULL
     assert q(ODD, 4, 128, 128, FAKE, FAKE, None) == _lib.MOE_ERR_ALIGN
+    assert q(FAKE, 1 << 31, 128, 1, FAKE, FAKE, None) == _lib.MOE_ERR_SHAPE
     assert q(None, 0, 128, 1, None, None, None) == _lib.MOE_OK
 
     def mm(M=16, N=256, K=256, ty=_lib.MOE_BF16, a=FAKE, sa=FAKE, w=FAKE, sw=FAKE, out=FAKE, ws=FAKE, n=1 << 30):
