@@ -4,6 +4,7 @@
 // crosses the boundary.
 #include "moe.h"
 
+#include <algorithm>
 #include <cmath>
 #include <exception>
 
@@ -75,7 +76,9 @@ size_t moe_workspace_bytes(const moe_shape* s, int op) {
   if (!s || check_shape(s) != MOE_OK) return 0;
   const int64_t T = s->tokens, n = s->tokens * s->top_k, C = s->capacity;
   switch (op) {
-    case MOE_OP_ROUTE: return align256(moe::route_workspace_bytes(T, s->experts, s->hidden));
+    case MOE_OP_ROUTE:   // of moe_route and moe_route_scored
+      return align256(std::max(moe::route_workspace_bytes(T, s->experts, s->hidden),
+                               s->dtype == MOE_F32 ? 0 : moe::route_scored_workspace_bytes(T, s->experts, s->hidden)));
     case MOE_OP_DISPATCH: return align256(moe::dispatch_workspace_bytes(T, s->experts));
     case MOE_OP_EXPERT_FFN:
       if (s->dtype == MOE_FP8) return align256(moe::ffn_fp8_workspace_bytes(n, C, s->hidden, s->experts, s->ffn));

@@ -21,6 +21,10 @@ struct ScoreRule {
   int sigmoid, groups, top_groups, group_top, renormalise;
   float scale;
 };
+// bf16 tokens: partial logit planes [ks, T, E] by 64 x 64 tiles with ks K splits.
+hipError_t launch_router_logits_64(const void* x, const float* w_r, int64_t T, int d, int E, int ks, float* planes,
+                                   hipStream_t st);
+size_t route_scored_workspace_bytes(int64_t T, int E, int d);
 hipError_t launch_route_scored(const void* x, bool x_f32, const float* w_r, const float* b_r,
                                const float* balance, const ScoreRule& rule, int64_t T, int d, int E,
                                int k, float* planes, int32_t* topk_idx, float* topk_gate,

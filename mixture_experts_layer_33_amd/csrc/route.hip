@@ -256,6 +256,13 @@ hipError_t launch_router_logits(const void* x, bool x_f32, const float* w_r, int
   return hipGetLastError();
 }
 
+hipError_t launch_router_logits_64(const void* x, const float* w_r, int64_t T, int d, int E, int ks, float* planes,
+                                   hipStream_t st) {
+  router_mfma_kernel<64><<<dim3((unsigned)((E + 63) / 64), (unsigned)((T + 63) / 64), (unsigned)ks), 256, 0, st>>>(
+      (const bf16_t*)x, w_r, planes, T, d, E);
+  return hipGetLastError();
+}
+
 hipError_t launch_route(const void* x, bool x_f32, const float* w_r, const float* b_r, int64_t T,
                         int d, int E, int k, float* logits, int32_t* topk_idx, float* topk_gate,
                         int32_t* expert_count, hipStream_t st) {

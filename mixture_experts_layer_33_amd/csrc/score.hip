@@ -44,6 +44,61 @@ __device__ __forceinline__ uint32_t group_max_u(uint32_t u) {
   return u;
 }
 
+// Sum over the wavefront in VALU cross-lane moves (as group_max), the same bits in every lane.
+template <int FROM>
+__device__ __forceinline__ float lanes_sum(float v) {   // over lanes that differ in bits FROM .. 32
+  auto dpp = [](float u, auto ctl) __attribute__((always_inline)) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(u), decltype(ctl)::value, 0xf, 0xf, false));
+  };
+  if constexpr (FROM <= 1) v += dpp(v, std::integral_constant<int, 0xB1>{});    // quad_perm [1,0,3,2]
+  if constexpr (FROM <= 2) v += dpp(v, std::integral_constant<int, 0x4E>{});    // [2,3,0,1]
+  if constexpr (FROM <= 4) v += dpp(v, std::integral_constant<int, 0x141>{});   // row_half_mirror
+  v += dpp(v, std::integral_constant<int, 0x128>{});                            // row_ror:8
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_int(v), __float_as_int(v), false, false);
+  v = __int_as_float(a[0]) + __int_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_int(v), __float_as_int(v), false, false);
+  return __int_as_float(b[0]) + __int_as_float(b[1]);
+}
+
+// The value of the lane `O` apart (O = 4: some lane of the other quad, 8 lanes holding one value per quad).
+template <int O>
+__device__ __forceinline__ uint32_t partner(uint32_t u) {
+  if constexpr (O == 1) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0xB1, 0xf, 0xf, false);
+  else if constexpr (O == 2) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x4E, 0xf, 0xf, false);
+  else if constexpr (O == 4) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x141, 0xf, 0xf, false);
+  else if constexpr (O == 8) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x128, 0xf, 0xf, false);
+  else if constexpr (O == 16) {
+    const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return s[0] == u ? s[1] : s[0];
+  } else {
+    const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return s[0] == u ? s[1] : s[0];
+  }
+}
+
+// A lane's keys, largest first, equal ones by their place (an odd-even merge network).
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[N], int (&at)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i) {
+          const int a = i + j, b = i + j + k;
+          if (b >= N || a / (2 * p) != b / (2 * p)) continue;
+          const bool swap = key[b] > key[a] || (key[b] == key[a] && at[b] < at[a]);
+          const uint32_t ka = key[a];
+          const int ia = at[a];
+          key[a] = swap ? key[b] : ka;
+          at[a] = swap ? at[b] : ia;
+          key[b] = swap ? ka : key[b];
+          at[b] = swap ? ia : at[b];
+        }
+}
+
 struct SelectArgs {
   const float* planes;   // KS partial planes of the logits [KS, T, E]
   int KS;
@@ -60,33 +115,36 @@ struct SelectArgs {
 
 typedef float __attribute__((ext_vector_type(4), aligned(4))) f32x4_any;   // 16 bytes at a float's alignment
 
-// Row `at` of a [., E] array, this lane's experts lane VPL .. + VPL - 1 (0 past E), in 16-byte pieces where the
-// rows allow it.
-template <int VPL>
+// Row `at` of a [., E] array, this lane's experts lane VPL .. + VPL - 1 (past E: some other's), in 16-byte pieces
+// (VEC: E a multiple of 4).  Without a branch: a branch around a load makes the next one wait for it.
+template <bool VEC, int VPL>
 __device__ __forceinline__ void lane_row(const float* __restrict__ at, int E, float (&v)[VPL]) {
   const int e0 = (threadIdx.x & 63) * VPL;
-  if (VPL % 4 == 0 && E % 4 == 0) {
+  if constexpr (VEC && VPL % 4 == 0) {
 #pragma unroll
     for (int c = 0; c < VPL / 4; ++c) {
-      const f32x4 w = e0 + 4 * c < E ? *(const f32x4_any*)(at + e0 + 4 * c) : f32x4{0.f, 0.f, 0.f, 0.f};
+      const f32x4 w = *(const f32x4_any*)(at + min(e0 + 4 * c, E - 4));
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[4 * c + q] = w[q];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) v[i] = e0 + i < E ? at[e0 + i] : 0.f;
+    for (int i = 0; i < VPL; ++i) v[i] = at[min(e0 + i, E - 1)];
   }
 }
 
 // One wavefront per token; lane l owns the consecutive experts l VPL .. l VPL + VPL - 1, so that the lowest lane
 // of a tie holds the lowest id, and a group of experts is a run of lanes where its size allows it
 // (`run` lanes, a power of two; 0: the general form).  What bounds it is the latency of one token's
-// chain (loads, then k rounds of a 64-lane maximum): all planes' loads are issued first, a round
-// is a maximum in VALU moves, one ballot and two lane reads (8 of 256 experts in 8 groups, 2,048
-// tokens: 9 us; 30 with strided ownership, plane after plane, and two butterflies a round).
-template <int VPL>
+// chain (loads, then k rounds of a 64-lane maximum): all planes' loads are issued first, a lane sorts
+// its own keys once, and a round is a maximum of the lanes' first keys in VALU moves, one ballot and
+// one lane read (8 of 256 experts in 8 groups, 2,048 tokens: 8 us; 30 with strided ownership, plane
+// after plane, and two butterflies a round).  Past four keys a lane the sort costs more than looking
+// through them each round (512 experts, 8,192 tokens: 26 us sorted, 18 not).
+template <int VPL, int PB>   // PB: planes in flight after the first
 __global__ __launch_bounds__(256) void score_select_kernel(SelectArgs p, int run) {
   __shared__ int chosen[4 * 32];
+  __shared__ __attribute__((aligned(16))) float rows[4][64 * VPL];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * 4 + wave;
   const int E = p.E, k = p.k, e0 = lane * VPL;
@@ -96,49 +154,52 @@ __global__ __launch_bounds__(256) void score_select_kernel(SelectArgs p, int run
   if (t < p.T) {
     float l[VPL], s[VPL], bias[VPL], bal[VPL];
     uint32_t key[VPL];
-    constexpr int PB = VPL <= 4 ? RT_MAX_KS : 2;   // planes in flight
-    lane_row<VPL>(p.planes + t * E, E, l);
-    for (int z0 = 1; z0 < p.KS; z0 += PB) {
-      float v[PB][VPL];
+    auto read = [&](auto vec) __attribute__((always_inline)) {
+      constexpr bool VEC = decltype(vec)::value;
+      lane_row<VEC>(p.b_r ? p.b_r : p.planes, E, bias);
+      lane_row<VEC>(p.balance ? p.balance : p.planes, E, bal);
+      lane_row<VEC>(p.planes + t * E, E, l);
+      for (int z0 = 1; z0 < p.KS; z0 += PB) {
+        float v[PB][VPL];
 #pragma unroll
-      for (int z = 0; z < PB; ++z)
-        if (z0 + z < p.KS) lane_row<VPL>(p.planes + ((int64_t)(z0 + z) * p.T + t) * E, E, v[z]);
+        for (int z = 0; z < PB; ++z)   // past the last plane: the last again, not added
+          lane_row<VEC>(p.planes + ((int64_t)min(z0 + z, p.KS - 1) * p.T + t) * E, E, v[z]);
 #pragma unroll
-      for (int z = 0; z < PB; ++z)
-        if (z0 + z < p.KS)
+        for (int z = 0; z < PB; ++z)
 #pragma unroll
-          for (int i = 0; i < VPL; ++i) l[i] += v[z][i];
-    }
+          for (int i = 0; i < VPL; ++i) l[i] += z0 + z < p.KS ? v[z][i] : 0.f;
+      }
+    };
+    if (E % 4 == 0) read(std::true_type{});
+    else read(std::false_type{});
     if (p.b_r) {
-      lane_row<VPL>(p.b_r, E, bias);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) l[i] += bias[i];
     }
-    if (p.balance) lane_row<VPL>(p.balance, E, bal);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       if (e0 + i >= E) l[i] = -INFINITY;
       else if (p.logits) p.logits[t * E + e0 + i] = l[i];
     }
-    if (p.rule.sigmoid) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) s[i] = 1.0f / (1.0f + expf(-l[i]));
-    } else {
-      float m = -INFINITY, sum = 0.f;
+    for (int i = 0; i < VPL; ++i) rows[wave][e0 + i] = l[i];
+    const bool grouped = p.rule.top_groups < p.rule.groups, by_score = grouped || p.balance;
+    float m = -INFINITY, sum = 0.f;   // softmax over all experts, where something asks for it
+    auto sigmoid = [](float v) { return 1.0f / (1.0f + expf(-v)); };
+    auto term = [&](float v) { return v == -INFINITY ? 0.f : expf(v - m); };   // also where every logit is -inf
+    if (!p.rule.sigmoid && (by_score || !p.rule.renormalise)) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) m = fmaxf(m, l[i]);
       m = group_max<64>(m);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        s[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - m);   // also where every logit is -inf
-        sum += s[i];
-      }
-      sum = wave_sum(sum);
-      const bool none = sum == 0.f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) s[i] = none ? 0.f : s[i] / sum;
+      for (int i = 0; i < VPL; ++i) sum += s[i] = term(l[i]);
+      sum = lanes_sum<1>(sum);
     }
-    const bool grouped = p.rule.top_groups < p.rule.groups;
+    const bool none = sum == 0.f;
+    if (by_score) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) s[i] = p.rule.sigmoid ? sigmoid(l[i]) : none ? 0.f : s[i] / sum;
+    }
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       key[i] = e0 + i < E ? order_key(p.balance ? s[i] + bal[i] : grouped ? s[i] : l[i]) : 0u;
@@ -162,11 +223,18 @@ __global__ __launch_bounds__(256) void score_select_kernel(SelectArgs p, int run
           b = max(b, min(a, key[i]));
           a = max(a, key[i]);
         }
-        for (int o = 1; o < run; o <<= 1) {
-          const uint32_t c = __shfl_xor(a, o, 64), d = __shfl_xor(b, o, 64);
+        auto merge = [&](auto o) __attribute__((always_inline)) {
+          if (run <= decltype(o)::value) return;
+          const uint32_t c = partner<decltype(o)::value>(a), d = partner<decltype(o)::value>(b);
           b = max(min(a, c), max(b, d));
           a = max(a, c);
-        }
+        };
+        merge(std::integral_constant<int, 1>{});
+        merge(std::integral_constant<int, 2>{});
+        merge(std::integral_constant<int, 4>{});
+        merge(std::integral_constant<int, 8>{});
+        merge(std::integral_constant<int, 16>{});
+        merge(std::integral_constant<int, 32>{});
         const uint32_t mine = score_key(a, b);
         const int g = lane / run;
         int before = 0;
@@ -203,33 +271,42 @@ __global__ __launch_bounds__(256) void score_select_kernel(SelectArgs p, int run
         for (int i = 0; i < VPL; ++i) drop(i, e0 + i < E && ((keep >> ((e0 + i) / per)) & 1ull));
       }
     }
-    int choice = 0;
-    float my_s = 0.f, my_l = -INFINITY;
+    int at[VPL], choice = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) at[i] = i;
+    constexpr bool SORTED = VPL <= 4;   // else a lane looks through its keys in every round
+    if constexpr (SORTED) sort_keys<VPL>(key, at);
     for (int r = 0; r < k; ++r) {
-      uint32_t bk = 0;
-      int bi = 0;
-      float bs = 0.f, bl = 0.f;
+      uint32_t first = key[0];
+      int place = at[0];
+      if constexpr (!SORTED) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (key[i] > bk) { bk = key[i]; bi = i; bs = s[i]; bl = l[i]; }
-      const uint32_t mk = group_max_u<64>(bk);
-      const int owner = __builtin_ctzll(__ballot(bk == mk));
-      const int i_ = __builtin_amdgcn_readlane(bi, owner);
-      const float s_ = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bs), owner));
-      const float l_ = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bl), owner));
-      if (lane == r) { choice = owner * VPL + i_; my_s = s_; my_l = l_; }
-      if (lane == owner)
+        for (int i = 1; i < VPL; ++i)
+          if (key[i] > first) { first = key[i]; place = i; }
+      }
+      const int owner = __builtin_ctzll(__ballot(first == group_max_u<64>(first)));
+      place = __builtin_amdgcn_readlane(place, owner);
+      if (lane == r) choice = owner * VPL + place;
+      const bool pop = lane == owner;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (i == i_) key[i] = 0u;
+      for (int i = 0; i < VPL; ++i) {
+        if constexpr (SORTED) {
+          key[i] = !pop ? key[i] : i + 1 < VPL ? key[min(i + 1, VPL - 1)] : 0u;
+          at[i] = pop ? at[min(i + 1, VPL - 1)] : at[i];
+        } else {
+          key[i] = pop && i == place ? 0u : key[i];
+        }
+      }
     }
-    float g = my_s;
+    __builtin_amdgcn_wave_barrier();
+    const float my_l = lane < k ? rows[wave][choice] : -INFINITY;
+    float g = p.rule.sigmoid ? sigmoid(my_l) : none ? 0.f : term(my_l) / sum;
     if (p.rule.renormalise) {
       if (!p.rule.sigmoid) {   // over S alone: exact also where every s of S is tiny
-        const float m = group_max<64>(lane < k ? my_l : -INFINITY);
-        g = lane < k && my_l != -INFINITY ? expf(my_l - m) : 0.f;
+        m = group_max<64>(my_l);
+        g = term(my_l);
       }
-      const float sum = wave_sum(lane < k ? g : 0.f);
+      const float sum = lanes_sum<1>(lane < k ? g : 0.f);
       g = sum == 0.f ? 0.f : g / sum;
     }
     int rank = 0;
@@ -274,7 +351,7 @@ __global__ __launch_bounds__(1024) void score_count_kernel(const int32_t* __rest
 // Logits of a few tokens (T <= SMALL_T, bf16): a weight stream.  One wavefront per expert row and K split (the
 // splits of the MFMA router, whose tiles of 128 tokens would be empty here and its workgroups few: one
 // token, 256 experts, d 7168: 24 -> 4 us), W_r in fp32 and x widened: plain fp32 sums.
-constexpr int SMALL_T = 8;
+constexpr int SMALL_T = 8, SCORE_KS = 32;
 template <int NT>
 __global__ __launch_bounds__(256) void router_small_kernel(const bf16_t* __restrict__ x, const float* __restrict__ w_r,
                                                            float* __restrict__ planes, int T, int d, int E, int KS) {
@@ -297,9 +374,22 @@ __global__ __launch_bounds__(256) void router_small_kernel(const bf16_t* __restr
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const float sum = wave_sum(acc[t]);
+    const float sum = lanes_sum<1>(acc[t]);
     if (lane == 0 && t < T) planes[((int64_t)z * T + t) * E + e] = sum;
   }
+}
+
+// K splits of 64 x 64 logit tiles where the 128 x 128 tiles (or the plain router's fewer splits) would leave
+// half of the CUs idle, at least four slices of 64 each; 0: the plain router's choice.  (256 experts, d 7168, the
+// whole call: 9 tokens 33 -> 16 us, 400 tokens 35 -> 24; 128 experts, d 4096, 200 tokens 23 -> 15.)
+static int fine_splits(int64_t T, int E, int d) {
+  if (T <= SMALL_T) return 0;
+  const int64_t big = ((T + 127) / 128) * ((E + 127) / 128), tiles = ((T + 63) / 64) * ((E + 63) / 64);
+  if ((router_big(E) ? big : (tiles + 1) / 2) * router_ksplit(T, E, d) >= 128) return 0;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({SCORE_KS, 512 / tiles, d / 256}));
+}
+size_t route_scored_workspace_bytes(int64_t T, int E, int d) {
+  return ((size_t)fine_splits(T, E, d) * T * E * sizeof(float) + 255) & ~(size_t)255;
 }
 
 hipError_t launch_route_scored(const void* x, bool x_f32, const float* w_r, const float* b_r,
@@ -315,6 +405,9 @@ hipError_t launch_route_scored(const void* x, bool x_f32, const float* w_r, cons
     else if (T <= 4) router_small_kernel<4><<<g, 256, 0, st>>>((const bf16_t*)x, w_r, planes, (int)T, d, E, ks);
     else router_small_kernel<8><<<g, 256, 0, st>>>((const bf16_t*)x, w_r, planes, (int)T, d, E, ks);
     err = hipGetLastError();
+  } else if (const int fine = x_f32 ? 0 : fine_splits(T, E, d)) {
+    ks = fine;
+    err = launch_router_logits_64(x, w_r, T, d, E, ks, planes, st);
   } else {
     err = launch_router_logits(x, x_f32, w_r, T, d, E, planes, &ks, st);
   }
@@ -325,7 +418,10 @@ hipError_t launch_route_scored(const void* x, bool x_f32, const float* w_r, cons
 #define SELECT(V)                                                                             \
   {                                                                                           \
     const int q = per % V == 0 ? per / V : 0;                                                 \
-    score_select_kernel<V><<<g, 256, 0, st>>>(p, q > 0 && (q & (q - 1)) == 0 ? q : 0);        \
+    const int run = q > 0 && (q & (q - 1)) == 0 ? q : 0;                                      \
+    if (ks <= 2) score_select_kernel<V, 1><<<g, 256, 0, st>>>(p, run);                        \
+    else if (ks <= 8 || V >= 8) score_select_kernel<V, V <= 8 ? 7 : 4><<<g, 256, 0, st>>>(p, run); \
+    else score_select_kernel<V, V <= 4 ? 16 : V <= 8 ? 7 : 4><<<g, 256, 0, st>>>(p, run);                  \
   }
   if (vpl <= 1) SELECT(1)
   else if (vpl <= 2) SELECT(2)
@@ -367,22 +463,97 @@ struct DlArgs {
   float* db_part;       // [workgroups, E] sums over a workgroup's tokens, or NULL
 };
 
-// W_r [E, d] fp32 -> [d, 3 Ep] bf16, rows [hi | mid | hi] of W_r's columns: 64 x 64 of them, turned through LDS.
+// W_r [E, d] fp32 -> [d, 3 Ep] bf16, rows [hi | mid | hi] of W_r's columns: 64 x 64 of them, turned through LDS,
+// read and written in 16-byte pieces.
 __device__ __forceinline__ void score_turn(const DlArgs& p, int at, float (*tile)[65]) {
   const int c0 = at % (p.d / 64) * 64, e0 = at / (p.d / 64) * 64;   // d is a multiple of 64
-  for (int q = threadIdx.x; q < 64 * 64; q += 256) {
-    const int e = q / 64, c = q % 64;
-    tile[e][c] = e0 + e < p.E ? p.w_r[(int64_t)(e0 + e) * p.d + c0 + c] : 0.f;
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = tid / 16 + 16 * i, c = tid % 16 * 4;
+    const f32x4 w = e0 + e < p.E ? *(const f32x4*)(p.w_r + (int64_t)(e0 + e) * p.d + c0 + c) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) tile[e][c + q] = w[q];
   }
   __syncthreads();
-  for (int q = threadIdx.x; q < 64 * 64; q += 256) {
-    const int c = q / 64, e = q % 64;
-    const float v = tile[e][c];
-    const bf16_t hi = f2bf(v), mid = f2bf(v - bf2f(hi));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = tid / 8 + 32 * i, e = tid % 8 * 8;
+    u32x4 hi, mid;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float u = tile[e + 2 * q][c], v = tile[e + 2 * q + 1][c];
+      hi[q] = pack_bf2(u, v);
+      mid[q] = pack_bf2(u - lo_bf(hi[q]), v - hi_bf(hi[q]));
+    }
     bf16_t* row = p.wt + (int64_t)(c0 + c) * 3 * p.Ep + e0 + e;
-    row[0] = hi;
-    row[p.Ep] = mid;
-    row[2 * p.Ep] = hi;
+    *(u32x4*)row = hi;
+    *(u32x4*)(row + p.Ep) = mid;
+    *(u32x4*)(row + 2 * p.Ep) = hi;
+  }
+}
+
+// dl of token t by one wavefront: lane l holds experts l, l + 64, ... (zeros where ok is false).
+template <int VPL>
+__device__ __forceinline__ void token_dl(const DlArgs& p, int64_t t, bool ok, float (&dl)[VPL]) {
+  const int lane = threadIdx.x & 63, E = p.E, k = p.k;
+  float l[VPL];
+  float dg = 0.f, lj = -INFINITY;
+  int ej = -1;
+  if (ok && lane < k) {
+    const int e = p.topk_idx[t * k + lane];
+    if (e >= 0 && e < E) {
+      ej = e;
+      dg = p.rule.scale * p.dgate[t * k + lane];
+      lj = p.logits[t * E + e];
+    }
+  }
+  const bool dense = !p.rule.renormalise && !p.rule.sigmoid;   // every logit moves every softmax score
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 64 * i;
+    l[i] = dense && ok && e < E ? p.logits[t * E + e] : -INFINITY;
+    dl[i] = ok && e < E && p.dlogits ? p.dlogits[t * E + e] : 0.f;
+  }
+  float v = 0.f;   // lane j: dl of the j-th chosen expert (the softmax's own part)
+  if (p.rule.renormalise) {
+    float g;
+    if (p.rule.sigmoid) g = 1.0f / (1.0f + expf(-lj));
+    else {
+      const float m = group_max<64>(lj);
+      g = lj == -INFINITY ? 0.f : expf(lj - m);
+    }
+    g = ej >= 0 ? g : 0.f;
+    const float sum = lanes_sum<1>(g);
+    g = sum == 0.f ? 0.f : g / sum;
+    v = g * (dg - lanes_sum<1>(g * dg));
+    if (p.rule.sigmoid) v *= 1.0f / (1.0f + expf(lj));
+  } else if (p.rule.sigmoid) {
+    v = dg * (1.0f / (1.0f + expf(-lj))) * (1.0f / (1.0f + expf(lj)));
+  } else {
+    float m = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) m = fmaxf(m, l[i]);
+    m = group_max<64>(m);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      l[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - m);
+      sum += l[i];
+    }
+    sum = lanes_sum<1>(sum);
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    v = ej >= 0 && lj != -INFINITY ? expf(lj - m) * inv * dg : 0.f;
+    const float all = lanes_sum<1>(v);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) dl[i] -= l[i] * inv * all;
+  }
+  if (ej < 0 || lj == -INFINITY) v = 0.f;
+  for (int j = 0; j < k; ++j) {
+    const int e = __builtin_amdgcn_readlane(ej, j);
+    const float add = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j));
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (lane + 64 * i == e) dl[i] += add;
   }
 }
 
@@ -393,71 +564,15 @@ __global__ __launch_bounds__(256) void score_dl_kernel(DlArgs p) {
   if constexpr (!F32)
     if ((int)blockIdx.x >= p.G) return score_turn(p, (int)blockIdx.x - p.G, tile);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int E = p.E, k = p.k;
+  const int E = p.E;
   if (!F32 && blockIdx.x == 0) p.zero[threadIdx.x] = 0u;
   float db[VPL] = {};
   for (int w = 0; w < DL_TW; ++w) {
     const int64_t t = ((int64_t)blockIdx.x * 4 + wave) * DL_TW + w;
     if (t >= p.Tp) break;
     const bool ok = t < p.T;
-    float l[VPL], dl[VPL];
-    float dg = 0.f, lj = -INFINITY;
-    int ej = -1;
-    if (ok && lane < k) {
-      const int e = p.topk_idx[t * k + lane];
-      if (e >= 0 && e < E) {
-        ej = e;
-        dg = p.rule.scale * p.dgate[t * k + lane];
-        lj = p.logits[t * E + e];
-      }
-    }
-    const bool dense = !p.rule.renormalise && !p.rule.sigmoid;   // every logit moves every softmax score
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 64 * i;
-      l[i] = dense && ok && e < E ? p.logits[t * E + e] : -INFINITY;
-      dl[i] = ok && e < E && p.dlogits ? p.dlogits[t * E + e] : 0.f;
-    }
-    float v = 0.f;   // lane j: dl of the j-th chosen expert (the softmax's own part)
-    if (p.rule.renormalise) {
-      float g;
-      if (p.rule.sigmoid) g = 1.0f / (1.0f + expf(-lj));
-      else {
-        const float m = group_max<64>(lj);
-        g = lj == -INFINITY ? 0.f : expf(lj - m);
-      }
-      g = ej >= 0 ? g : 0.f;
-      const float sum = wave_sum(g);
-      g = sum == 0.f ? 0.f : g / sum;
-      v = g * (dg - wave_sum(g * dg));
-      if (p.rule.sigmoid) v *= 1.0f / (1.0f + expf(lj));
-    } else if (p.rule.sigmoid) {
-      v = dg * (1.0f / (1.0f + expf(-lj))) * (1.0f / (1.0f + expf(lj)));
-    } else {
-      float m = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) m = fmaxf(m, l[i]);
-      m = group_max<64>(m);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        l[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - m);
-        sum += l[i];
-      }
-      sum = wave_sum(sum);
-      const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-      v = ej >= 0 && lj != -INFINITY ? expf(lj - m) * inv * dg : 0.f;
-      const float all = wave_sum(v);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) dl[i] -= l[i] * inv * all;
-    }
-    if (ej < 0 || lj == -INFINITY) v = 0.f;
-    for (int j = 0; j < k; ++j) {
-      const int e = __builtin_amdgcn_readlane(ej, j);
-      const float add = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j));
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (lane + 64 * i == e) dl[i] += add;
-    }
+    float dl[VPL];
+    token_dl<VPL>(p, t, ok, dl);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = lane + 64 * i;
@@ -480,6 +595,73 @@ __global__ __launch_bounds__(256) void score_dl_kernel(DlArgs p) {
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += 256)
     p.db_part[(int64_t)blockIdx.x * E + e] = (dbs[0][e] + dbs[1][e]) + (dbs[2][e] + dbs[3][e]);
+}
+
+// The whole gradient of a few bf16 tokens (T <= NT) in one launch, in fp32: one pass over W_r (dx) and dW_r. A
+// workgroup owns 32 columns, a thread four of them and every 64th expert; each workgroup makes
+// dl for itself (T rows of logits from the L2), which costs less than another launch.  dx is
+// joined over the lanes, then over the wavefronts in order.  (One token, d 4096, 512 experts: 34 us with the four
+// launches below, 9 here, of which 8 in the kernel; 16 tokens, 64 experts: 20 -> 9.)
+template <int VPL, int NT>
+__global__ __launch_bounds__(512) void score_bwd_few_kernel(DlArgs p, const bf16_t* __restrict__ x, const bf16_t* dx_in,
+                                                            bf16_t* dx, float* __restrict__ dw, float* __restrict__ db) {
+  constexpr int PITCH = NT + 4;            // floats per expert of dl
+  __shared__ __attribute__((aligned(16))) float red[8][NT][32];
+  extern __shared__ __attribute__((aligned(16))) float dls[];   // [E][PITCH]
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int T = (int)p.T, E = p.E, c0 = blockIdx.x * 32 + (tid & 7) * 4;
+  for (int t = wave; t < NT; t += 8) {
+    float dl[VPL];
+    token_dl<VPL>(p, t, t < T, dl);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (lane + 64 * i < E) dls[(lane + 64 * i) * PITCH + t] = dl[i];
+  }
+  float xf[NT][4], acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const u32x2 v = *(const u32x2*)(x + (int64_t)min(t, T - 1) * p.d + c0);   // rows past T meet zeros of dl
+    xf[t][0] = lo_bf(v[0]); xf[t][1] = hi_bf(v[0]); xf[t][2] = lo_bf(v[1]); xf[t][3] = hi_bf(v[1]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[t][q] = 0.f;
+  }
+  __syncthreads();
+  if (db && blockIdx.x == 0)
+    for (int e = tid; e < E; e += 512) {
+      float s = 0.f;
+      for (int t = 0; t < T; ++t) s += dls[e * PITCH + t];
+      db[e] = s;
+    }
+#pragma unroll 2
+  for (int e = tid >> 3; e < E; e += 64) {
+    const f32x4 w = __builtin_nontemporal_load((const f32x4*)(p.w_r + (int64_t)e * p.d + c0));
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float s = dls[e * PITCH + t];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        o[q] = fmaf(s, xf[t][q], o[q]);
+        acc[t][q] = fmaf(s, w[q], acc[t][q]);
+      }
+    }
+    *(f32x4*)(dw + (int64_t)e * p.d + c0) = o;
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[t][q] = lanes_sum<8>(acc[t][q]);
+    if (lane < 8) *(f32x4*)&red[wave][t][lane * 4] = f32x4{acc[t][0], acc[t][1], acc[t][2], acc[t][3]};
+  }
+  __syncthreads();
+  for (int i = tid; i < T * 32; i += 512) {
+    const int t = i / 32, c = i % 32;
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += red[w][t][c];
+    const int64_t at = (int64_t)t * p.d + blockIdx.x * 32 + c;
+    dx[at] = f2bf((dx_in ? bf2f(dx_in[at]) : 0.f) + s);
+  }
 }
 
 // Partial planes of dW_r [E, d] = dl^T x for bf16 tokens.  Both operands are row-major with the
@@ -557,11 +739,13 @@ __global__ __launch_bounds__(512) void score_dw_mfma_kernel(DwArgs p) {
     const v4i16_t lo = ds_tr16(sb + at), hi = ds_tr16(sb + at + 4 * DW_ROW);
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
+  const bool live = m0 + wm * 64 < p.E && n0 + wn * 128 < p.d;   // else none of this wavefront's results exists
   if (KT > 0) issue(0);
   for (int kt = 0; kt < KT; ++kt) {
     bwait_vm<0>();
     __syncthreads();
     if (kt + 1 < KT) issue(kt + 1);
+    if (!live) continue;
     const uint8_t* sb = lds + (kt % DW_S) * DW_STAGE;
 #pragma unroll
     for (int kk = 0; kk < DW_K / 16; ++kk) {
@@ -772,6 +956,25 @@ hipError_t launch_route_scored_bwd(bool f32, const ScoreRule& rule, const float*
                  (bf16_t*)(w + L.dl), (bf16_t*)(w + L.low), (uint32_t*)(w + L.zero),
                  w_r, (bf16_t*)(w + L.wt), d, L.G, db ? dbp : nullptr};
   const int vpl = (E + 63) / 64;
+  if (!f32 && T <= 16) {
+#define FEW(V, N)                                                                                                \
+  {                                                                                                             \
+    hipError_t e_ = hipFuncSetAttribute((const void*)score_bwd_few_kernel<V, N>,                                 \
+                                        hipFuncAttributeMaxDynamicSharedMemorySize, 64 * V * (N + 4) * 4);       \
+    if (e_ != hipSuccess) return e_;                                                                             \
+    score_bwd_few_kernel<V, N><<<(unsigned)(d / 32), 512, E * (N + 4) * 4, st>>>(                               \
+        p, (const bf16_t*)x, (const bf16_t*)dx_in, (bf16_t*)dx, dw, db);                                         \
+  }
+#define FEW_V(V) if (T <= 4) FEW(V, 4) else FEW(V, 16)
+    if (vpl <= 1) FEW_V(1)
+    else if (vpl <= 2) FEW_V(2)
+    else if (vpl <= 4) FEW_V(4)
+    else if (vpl <= 8) FEW_V(8)
+    else FEW_V(16)
+#undef FEW_V
+#undef FEW
+    return hipGetLastError();
+  }
 #define DL(V)                                                                   \
   {                                                                             \
     if (f32) score_dl_kernel<V, true><<<(unsigned)L.G, 256, 0, st>>>(p);        \
