@@ -453,7 +453,7 @@ int moe_route_scored(const moe_shape* shape, const moe_router* router, const voi
  *      NULL (the experts' part of dx, moe_backward_experts).
  * Out: dx [T,d] act (may be dx_in itself); dw_router [E,d] f32; db_router [E] f32 or NULL.
  * Apart from dx no output may overlap an input or another output.
- * An id in topk_idx outside [0, E) is left out of the sums.  bf16 tokens: d times 6 E (E rounded up to
+ * An id in topk_idx outside [0, E) is left out of the sums.  bf16 tokens: d times 4 E (E rounded up to
  * 64) below 2^32; MOE_F32: at most 2^21 tokens (MOE_ERR_SHAPE).
  * workspace: moe_workspace_bytes(shape, MOE_OP_ROUTE_BACKWARD) bytes.  x, w_router, dx_in, dx
  * and dw_router are aligned to 16 bytes (MOE_ERR_ALIGN).

@@ -557,8 +557,8 @@ int moe_route_scored_backward(const moe_shape* s, const moe_router* router, cons
     if (unaligned(x) || unaligned(w_router) || unaligned(dx_in) || unaligned(dx) ||
         unaligned(dw_router) || unaligned(workspace))
       return MOE_ERR_ALIGN;
-    // dx's second operand, [d, 3 E'] bf16 (E': E rounded up to 64), is addressed with 32-bit offsets
-    if (s->dtype != MOE_F32 && (int64_t)s->hidden * 6 * ((s->experts + 63) / 64 * 64) >= (int64_t)1 << 32)
+    // dx's second operand, [d, 2 E'] bf16 (E': E rounded up to 64), is addressed with 32-bit offsets
+    if (s->dtype != MOE_F32 && (int64_t)s->hidden * 4 * ((s->experts + 63) / 64 * 64) >= (int64_t)1 << 32)
       return MOE_ERR_SHAPE;
     if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_ROUTE_BACKWARD)) return MOE_ERR_WORKSPACE;
     if (T == 0) {

@@ -331,9 +331,6 @@ static hipError_t run_fp8_thin_plain(const Fp8Args& a, int64_t tiles, int W, hip
   return run_fp8_thin<KIND, 2, 7>(a, tiles, st);
 }
 
-// Row tiles that take a column tile one after another (fp8_tile.h).
-constexpr int FP8_GROUP = 4;
-
 // How a dense product runs: fm = 0 the thin kernel (16 token rows a tile, W wavefronts), else tiles of 64 fm rows;
 // Z: K splits.  The least estimated time of all: rounds of 256 workgroups times the blocks of one,
 // where a block of a tile of 64 / 128 / 192 / 256 rows took 0.95, 0.98, 1.07 and 1.25 us (M 2,045, N 4,168,
@@ -371,16 +368,7 @@ static DensePlan dense_plan(int64_t M, int64_t N, int64_t K, bool f32, bool spli
   return best;
 }
 
-hipError_t launch_tile_add(Fp8Args& a, hipStream_t st) {
-  a.group = FP8_GROUP;
-  a.Z = 1;
-  const int fm = dense_plan(a.a_rows, a.N, a.K, false, false).fm;
-  const int64_t mt = fm ? (a.a_rows + 64 * fm - 1) / (64 * fm) : 0;
-  if (fm <= 1) return run_fp8_tile<1, TILE_ADD, 3, false>(a, (a.a_rows + 63) / 64, st);
-  if (fm == 2) return run_fp8_tile<2, TILE_ADD, 3, false>(a, mt, st);
-  if (fm == 3) return run_fp8_tile<3, TILE_ADD, 2, false>(a, mt, st);
-  return run_fp8_tile<4, TILE_ADD, 2, false>(a, mt, st);
-}
+int tile_add_height(int64_t M, int64_t N, int64_t K) { return std::max(1, dense_plan(M, N, K, false, false).fm); }
 
 size_t matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   size_t b = 0;

@@ -39,6 +39,8 @@ struct Fp8Args {
   int group;               // row tiles that take the same column tile one after another
 };
 
+constexpr int FP8_GROUP = 4;   // row tiles that take a column tile one after another
+
 // Lane l's 32 bytes of a row's block.  (Which of the block's 128 positions a lane's byte is does
 // not matter as long as both operands agree.)
 __device__ __forceinline__ i32x8 fp8_join(u32x4 a, u32x4 b) {
@@ -76,7 +78,8 @@ __device__ __forceinline__ f32x4 fp8_wide16(const Wide16& w, const Wide16& a) {
 }
 
 // FP8_PART: K split over Z workgroups, each with an fp32 plane of its own [Z, C, N] (FP8_F32 with Z > 1 likewise).
-// TILE_ADD: bf16 operands (K: bytes of a row, a stage holds 64 elements) without scales, out = round(add + A W^T).
+// TILE_ADD: two bf16 parts [hi | mid] of each operand's rows (K: bytes of such a row, a stage holds 64 elements),
+// without scales: out = round(add + hi hi^T + hi mid^T + mid hi^T).
 enum { FP8_BF16 = 0, FP8_F32 = 1, FP8_PART = 2, TILE_ADD = 3, FP8_SWIGLU = 4, FP8_SWIGLU_SAVE = 5 };
 
 template <int FM, int KIND>
@@ -89,7 +92,7 @@ struct Fp8Stage {
 
 // NT: the weights are read past the caches' retention (each is read about once).
 template <int FM, int KIND, int S, bool NT>
-__global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
+__device__ __forceinline__ void fp8_tile_body(const Fp8Args& p, const int block) {
   using SL = Fp8Stage<FM, KIND>;
   constexpr int BM = SL::BM, BN = SL::BN, L = SL::L;
   constexpr bool SWIGLU = KIND >= FP8_SWIGLU, WIDE = KIND == FP8_F32, ADD = KIND == TILE_ADD;
@@ -104,8 +107,8 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
   // tiles running together on an XCD share both their token rows and their weight rows in its L2
   // (groups of 4 against 1, 4 experts x 4,096 rows: 749 -> 737 us; starting tiles at different K blocks, as
   // the bf16 GEMMs do, then loses: 752 us).
-  const int V = nmt * nct, per = (V * p.Z + 7) / 8, li = (int)(blockIdx.x >> 3);
-  const int TZ = (int)(blockIdx.x & 7) * per + li;
+  const int V = nmt * nct, per = (V * p.Z + 7) / 8, li = block >> 3;
+  const int TZ = (block & 7) * per + li;
   if (li >= per || TZ >= V * p.Z) return;
   const int z = TZ / V, T = TZ - z * V;          // the K split, the tile
   int e = 0, t0 = 0, R = nmt, mt = T / nct;      // expert, its first row tile, its row tiles
@@ -128,7 +131,8 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1, lr = lane & 15, lg = lane >> 4;
   const uint32_t K = (uint32_t)p.K;
-  const int KA = p.K / 128, kb = (int)((int64_t)KA * z / p.Z), KT = (int)((int64_t)KA * (z + 1) / p.Z) - kb;
+  const int part = p.K / 256;                    // ADD: blocks of one part of a row
+  const int KA = ADD ? 3 * part : p.K / 128, kb = (int)((int64_t)KA * z / p.Z), KT = (int)((int64_t)KA * (z + 1) / p.Z) - kb;
 
   // copies: 16-byte chunk j of a tile is slot j % 8 of row j / 8 and holds the chunk of that row whose
   // swizzled place it is (swz of gemm_body.h)
@@ -172,12 +176,14 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
     const uint32_t st = lds0 + (uint32_t)(i_ % S) * SL::SIZE;
     const int kt = kb + i_;
     if (c < FM) {
-      dma16(p.A + (size_t)kt * 128, a_off[c], __builtin_amdgcn_readfirstlane(st + SL::A + (8 * c + wave) * 1024));
+      const int ka = ADD && kt >= part ? kt - part : kt;
+      dma16(p.A + (size_t)ka * 128, a_off[c], __builtin_amdgcn_readfirstlane(st + SL::A + (8 * c + wave) * 1024));
     } else if (c < FM + 4) {
       const int i = c - FM;
       const uint32_t to = __builtin_amdgcn_readfirstlane(st + SL::B + (8 * i + wave) * 1024);
-      if (NT) dma16nt(b_base[i] + (size_t)kt * 128, b_off[i], to);
-      else dma16(b_base[i] + (size_t)kt * 128, b_off[i], to);
+      const int kw = ADD && kt >= 2 * part ? kt - 2 * part : kt;
+      if (NT) dma16nt(b_base[i] + (size_t)kw * 128, b_off[i], to);
+      else dma16(b_base[i] + (size_t)kw * 128, b_off[i], to);
     } else {
       dma4(s_base + (size_t)kt * s_step, s_off, __builtin_amdgcn_readfirstlane(st + SL::SC + wave * 256));
     }
@@ -479,11 +485,22 @@ __global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
 }
 
 template <int FM, int KIND, int S, bool NT>
-inline hipError_t run_fp8_tile(const Fp8Args& a, int64_t max_tiles, hipStream_t st) {
-  const int nblk = (a.N + 127) / 128, nct = KIND >= FP8_SWIGLU ? nblk : (nblk + 1) / 2;
+__global__ __launch_bounds__(512) void fp8_tile_kernel(Fp8Args p) {
+  fp8_tile_body<FM, KIND, S, NT>(p, (int)blockIdx.x);
+}
+
+template <int FM, int KIND, int S>
+constexpr int fp8_tile_lds() {
   constexpr int BM = 64 * FM;
   constexpr int epi = KIND == FP8_BF16 || KIND == TILE_ADD ? BM * 528 : KIND == FP8_SWIGLU_SAVE ? BM * 272 : KIND == FP8_SWIGLU ? BM * 144 : 0;
-  constexpr int ring = S * Fp8Stage<FM, KIND>::SIZE, lds = ring > epi ? ring : epi;
+  constexpr int ring = S * Fp8Stage<FM, KIND>::SIZE;
+  return ring > epi ? ring : epi;
+}
+
+template <int FM, int KIND, int S, bool NT>
+inline hipError_t run_fp8_tile(const Fp8Args& a, int64_t max_tiles, hipStream_t st) {
+  const int nblk = (a.N + 127) / 128, nct = KIND >= FP8_SWIGLU ? nblk : (nblk + 1) / 2;
+  constexpr int lds = fp8_tile_lds<FM, KIND, S>();
   static_assert(lds <= 160 * 1024, "LDS");
   auto kern = fp8_tile_kernel<FM, KIND, S, NT>;
   hipError_t err = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);

@@ -65,7 +65,7 @@ hipError_t launch_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8
                              void* out, void* ws, hipStream_t st);
 // out = round(add + A W^T) of bf16 rows (the tile of the FP8 products)
 struct Fp8Args;
-hipError_t launch_tile_add(Fp8Args& a, hipStream_t st);
+int tile_add_height(int64_t M, int64_t N, int64_t K);   // in 64 rows
 size_t ffn_fp8_workspace_bytes(int64_t n, int64_t C, int d, int E, int f);
 hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const int32_t* expert_offset,
                           int64_t head, int64_t C, int64_t n, int d, int E, int f,

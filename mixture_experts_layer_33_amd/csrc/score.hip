@@ -439,8 +439,8 @@ hipError_t launch_route_scored(const void* x, bool x_f32, const float* w_r, cons
 // taken as 1 / (1 + exp(l)), which keeps its digits where s is next to 1.
 //
 // For bf16 tokens dl leaves as three bf16 parts, hi = bf16(dl), mid = bf16(dl - hi) and lo = bf16(dl - hi - mid),
-// which hold all 24 bits of it, as rows [hi | hi | mid] of 3 Ep values (Ep: E rounded up to 64, the
-// padding 0) and [lo] of Ep.  Against W_r's columns [hi | mid | hi] one product of length 3 Ep is dl W_r
+// which hold all 24 bits of it, as rows [hi | mid] of 2 Ep values (Ep: E rounded up to 64, the
+// padding 0) and [lo] of Ep.  With W_r's columns as [hi | mid], hi hi + hi mid + mid hi is dl W_r
 // to 2^-15 of its terms (mid x mid and the third parts are left out: dx is rounded to bf16, half a
 // step 2^-8); the three parts against the exact bf16 x are dl^T x to fp32, in which dW_r leaves.
 constexpr int DL_TW = 2;
@@ -454,16 +454,16 @@ struct DlArgs {
   int E, Ep, k;
   ScoreRule rule;
   float* dl;            // fp32 tokens: [T, E]
-  bf16_t* planes;       // bf16 tokens: [Tp, 3 Ep]
+  bf16_t* planes;       // bf16 tokens: [Tp, 2 Ep]
   bf16_t* low;          // bf16 tokens: [Tp, Ep]
   uint32_t* zero;       // bf16 tokens: 256 words set to 0
   const float* w_r;     // bf16 tokens: W_r [E, d] to be turned by the workgroups from G on
-  bf16_t* wt;           // [d, 3 Ep]
+  bf16_t* wt;           // [d, 2 Ep]
   int d, G;
   float* db_part;       // [workgroups, E] sums over a workgroup's tokens, or NULL
 };
 
-// W_r [E, d] fp32 -> [d, 3 Ep] bf16, rows [hi | mid | hi] of W_r's columns: 64 x 64 of them, turned through LDS,
+// W_r [E, d] fp32 -> [d, 2 Ep] bf16, rows [hi | mid] of W_r's columns: 64 x 64 of them, turned through LDS,
 // read and written in 16-byte pieces.
 __device__ __forceinline__ void score_turn(const DlArgs& p, int at, float (*tile)[65]) {
   const int c0 = at % (p.d / 64) * 64, e0 = at / (p.d / 64) * 64;   // d is a multiple of 64
@@ -486,10 +486,9 @@ __device__ __forceinline__ void score_turn(const DlArgs& p, int at, float (*tile
       hi[q] = pack_bf2(u, v);
       mid[q] = pack_bf2(u - lo_bf(hi[q]), v - hi_bf(hi[q]));
     }
-    bf16_t* row = p.wt + (int64_t)(c0 + c) * 3 * p.Ep + e0 + e;
+    bf16_t* row = p.wt + (int64_t)(c0 + c) * 2 * p.Ep + e0 + e;
     *(u32x4*)row = hi;
     *(u32x4*)(row + p.Ep) = mid;
-    *(u32x4*)(row + 2 * p.Ep) = hi;
   }
 }
 
@@ -581,10 +580,9 @@ __global__ __launch_bounds__(256) void score_dl_kernel(DlArgs p) {
         if (e < E) p.dl[t * E + e] = dl[i];
       } else if (e < p.Ep) {
         const bf16_t hi = f2bf(dl[i]), mid = f2bf(dl[i] - bf2f(hi));
-        bf16_t* row = p.planes + t * 3 * p.Ep + e;
+        bf16_t* row = p.planes + t * 2 * p.Ep + e;
         row[0] = hi;
-        row[p.Ep] = hi;
-        row[2 * p.Ep] = mid;
+        row[p.Ep] = mid;
         p.low[t * p.Ep + e] = f2bf(dl[i] - bf2f(hi) - bf2f(mid));
       }
     }
@@ -673,7 +671,7 @@ __global__ __launch_bounds__(512) void score_bwd_few_kernel(DlArgs p, const bf16
 // workgroups, each with a plane of its own; split z runs on XCD z (Z = 8), so that a token row of
 // x crosses into one L2 only.
 struct DwArgs {
-  const bf16_t* planes;   // [Tp, 3 Ep]: hi | hi | mid
+  const bf16_t* planes;   // [Tp, 2 Ep]: hi | mid
   const bf16_t* low;      // [Tp, Ep]
   const bf16_t* x;        // [T, d]
   const bf16_t* zero;     // 1 KB of zeros: rows past T of x
@@ -684,10 +682,10 @@ struct DwArgs {
 constexpr int DW_M = 256, DW_N = 256, DW_K = 32, DW_S = 2, DW_ROW = 512;   // bytes of a staged row
 constexpr int DW_TILE = DW_K * DW_ROW, DW_STAGE = 4 * DW_TILE, DW_LDS = DW_S * DW_STAGE;
 
-__global__ __launch_bounds__(512) void score_dw_mfma_kernel(DwArgs p) {
+__device__ __forceinline__ void score_dw_body(const DwArgs& p, const int block) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
-  const int z = blockIdx.x % p.Z, tile = blockIdx.x / p.Z;
+  const int z = block % p.Z, tile = block / p.Z;
   const int mt = (p.E + DW_M - 1) / DW_M;
   const int m0 = (tile % mt) * DW_M, n0 = (tile / mt) * DW_N;
   const int64_t steps = p.Tp / DW_K, s0 = steps * z / p.Z;
@@ -711,10 +709,10 @@ __global__ __launch_bounds__(512) void score_dw_mfma_kernel(DwArgs p) {
     for (int c = 0; c < 2; ++c) {
       const int64_t t = r0 + 2 * (8 * c + wave) + crow;
       const uint32_t to = __builtin_amdgcn_readfirstlane(st + (8 * c + wave) * 1024);
-      const bf16_t* row = p.planes + t * 3 * p.Ep + acol[c];
+      const bf16_t* row = p.planes + t * 2 * p.Ep + acol[c];
       dma16_at(t < p.T ? p.x + t * p.d + bcol[c] : p.zero + (lane & 31) * 8, to);
       dma16_at(row, to + DW_TILE);
-      dma16_at(row + 2 * p.Ep, to + 2 * DW_TILE);
+      dma16_at(row + p.Ep, to + 2 * DW_TILE);
       dma16_at(p.low + t * p.Ep + acol[c], to + 3 * DW_TILE);
     }
   };
@@ -788,6 +786,30 @@ __global__ __launch_bounds__(512) void score_dw_mfma_kernel(DwArgs p) {
     }
     __builtin_amdgcn_wave_barrier();
   }
+}
+
+// dW_r's workgroups (below nw; up to nb, a multiple of 8 that keeps the rest's XCDs, they are none) and dx's tiles in one
+// launch: neither needs the other, and for few tokens neither fills the chip (the whole gradient, us before and after:
+// 64 tokens, d 2048, 256 experts 29 -> 19; 2,000 tokens, d 1024, 256 experts 47 -> 37; 8,192 tokens, d 4096, 512
+// experts 183 for the two either way).
+template <int FM, int S>
+__global__ __launch_bounds__(512) void score_products_kernel(Fp8Args a, DwArgs q, int nw, int nb) {
+  const int b = (int)blockIdx.x;
+  if (b >= nb) fp8_tile_body<FM, TILE_ADD, S, false>(a, b - nb);
+  else if (b < nw) score_dw_body(q, b);
+}
+
+template <int FM, int S>
+static hipError_t run_products(const Fp8Args& a, const DwArgs& q, int nw, hipStream_t st) {
+  constexpr int tile = fp8_tile_lds<FM, TILE_ADD, S>(), lds = tile > DW_LDS ? tile : DW_LDS;
+  static_assert(lds <= 160 * 1024, "LDS");
+  auto kern = score_products_kernel<FM, S>;
+  hipError_t err = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (err != hipSuccess) return err;
+  const int nb = (nw + 7) / 8 * 8;
+  const int64_t tiles = (a.a_rows + 64 * FM - 1) / (64 * FM) * ((a.N + 255) / 256);
+  kern<<<(unsigned)(nb + (tiles + 7) / 8 * 8), 512, lds, st>>>(a, q, nw, nb);
+  return hipGetLastError();
 }
 
 // fp32 tokens: dx [T, d] = dx_in + dl [T, E] W_r [E, d], and partial planes of dW_r [E, d] = dl^T x, on the
@@ -889,6 +911,7 @@ __global__ __launch_bounds__(256) void score_sum_kernel(const float* __restrict_
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= n) return;
     f32x4 s = *(const f32x4*)(part + i);
+#pragma unroll 8
     for (int z = 1; z < Z; ++z) s += *(const f32x4*)(part + z * n + i);
     *(f32x4*)(dw + i) = s;
     return;
@@ -909,12 +932,20 @@ __global__ __launch_bounds__(256) void score_sum_kernel(const float* __restrict_
   }
 }
 
+// fp32: about four workgroups a CU.  bf16: the least estimated time of one round of steps of 32 tokens, 1.3 us each,
+// and of the planes, written and read once.
 static int dw_splits(bool f32, int64_t T, int E, int d) {
   const int m = f32 ? GB : DW_M, n = f32 ? GB : DW_N;
   const int64_t tiles = (int64_t)((E + m - 1) / m) * ((d + n - 1) / n);
-  // fp32: about four workgroups a CU; bf16: one, and at least 8 stages of each
-  const int64_t most = f32 ? std::min<int64_t>(1024 / tiles, T / 128) : std::min<int64_t>(256 / tiles, T / 128);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(8, most));
+  if (f32) return (int)std::max<int64_t>(1, std::min<int64_t>({8, 1024 / tiles, T / 128}));
+  const int64_t steps = (T + DW_K - 1) / DW_K;
+  int best = 1;
+  double least = 1e300;
+  for (int Z = 1; Z == 1 || (Z <= 64 && Z * tiles <= 256 && Z * 4 <= steps); Z *= 2) {
+    const double t = (double)((steps + Z - 1) / Z) * 1.3 + (Z > 1 ? 2.0 + (double)Z * E * d * 8 / 4.5e6 : 0.0);
+    if (t < least) { least = t; best = Z; }
+  }
+  return best;
 }
 
 struct ScoreBwdLayout {
@@ -930,9 +961,9 @@ static ScoreBwdLayout score_bwd_layout(bool f32, int64_t T, int E, int d) {
   L.Z = dw_splits(f32, T, E, d);
   L.G = (int)((L.Tp + 4 * DL_TW - 1) / (4 * DL_TW));
   size_t o = 0;
-  L.dl = o; o += al(f32 ? (size_t)T * E * 4 : (size_t)L.Tp * 3 * L.Ep * 2);
+  L.dl = o; o += al(f32 ? (size_t)T * E * 4 : (size_t)L.Tp * 2 * L.Ep * 2);
   L.low = o; o += f32 ? 0 : al((size_t)L.Tp * L.Ep * 2);
-  L.wt = o; o += f32 ? 0 : al((size_t)d * 3 * L.Ep * 2);
+  L.wt = o; o += f32 ? 0 : al((size_t)d * 2 * L.Ep * 2);
   L.zero = o; o += 1024;
   L.dw = o; o += al((size_t)L.Z * E * d * 4);
   L.db = o; o += al((size_t)L.G * E * 4);
@@ -994,25 +1025,28 @@ hipError_t launch_route_scored_bwd(bool f32, const ScoreRule& rule, const float*
     score_dw_kernel<<<dim3((d + GB - 1) / GB, (E + GB - 1) / GB, L.Z), 256, 0, st>>>(p.dl, (const float*)x, T, E,
                                                                                     d, part);
   } else {
-    // dx: at most 2^18 rows a launch (32-bit offsets inside the operands)
-    for (int64_t t0 = 0; t0 < T; t0 += (int64_t)1 << 18) {
+    const DwArgs q{p.planes, p.low, (const bf16_t*)x, (const bf16_t*)p.zero, T, L.Tp, E, L.Ep, d, L.Z, part};
+    int nw = (int)((int64_t)((E + DW_M - 1) / DW_M) * ((d + DW_N - 1) / DW_N) * L.Z);
+    // dx: at most 2^18 rows a launch (32-bit offsets inside the operands), dW_r beside the first
+    for (int64_t t0 = 0; t0 < T; t0 += (int64_t)1 << 18, nw = 0) {
       Fp8Args a{};
-      a.A = (const uint8_t*)(p.planes + t0 * 3 * L.Ep);
+      a.A = (const uint8_t*)(p.planes + t0 * 2 * L.Ep);
       a.W0 = (const uint8_t*)p.wt;
       a.a_rows = std::min<int64_t>(T - t0, (int64_t)1 << 18);
       a.C = a.a_rows;
-      a.K = 6 * L.Ep;
+      a.K = 4 * L.Ep;
       a.N = d;
+      a.Z = 1;
+      a.group = FP8_GROUP;
       a.out = (bf16_t*)dx + t0 * d;
       a.add = dx_in ? (const bf16_t*)dx_in + t0 * d : nullptr;
-      if ((err = launch_tile_add(a, st)) != hipSuccess) return err;
+      const int fm = tile_add_height(a.a_rows, d, 6 * L.Ep);
+      err = fm == 1   ? run_products<1, 3>(a, q, nw, st)
+            : fm == 2 ? run_products<2, 3>(a, q, nw, st)
+            : fm == 3 ? run_products<3, 2>(a, q, nw, st)
+                      : run_products<4, 2>(a, q, nw, st);
+      if (err != hipSuccess) return err;
     }
-    const DwArgs a{p.planes, p.low, (const bf16_t*)x, (const bf16_t*)p.zero, T, L.Tp, E, L.Ep, d, L.Z, part};
-    if ((err = hipFuncSetAttribute((const void*)score_dw_mfma_kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                   DW_LDS)) != hipSuccess)
-      return err;
-    const int64_t tiles = (int64_t)((E + DW_M - 1) / DW_M) * ((d + DW_N - 1) / DW_N);
-    score_dw_mfma_kernel<<<(unsigned)(tiles * L.Z), 512, DW_LDS, st>>>(a);
   }
   if ((err = hipGetLastError()) != hipSuccess) return err;
   const int64_t n = (int64_t)E * d;   // d is a multiple of 8

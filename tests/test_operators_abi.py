@@ -94,9 +94,9 @@ def test_route_scored_refusals():
     assert route_bwd(s, r, n=moe.workspace_bytes(s, moe.OP_ROUTE_BACKWARD) - 1) == _lib.MOE_ERR_WORKSPACE
     many = shape("f32", T=(1 << 21) + 1, d=8, f=8)
     assert route(many, r) == _lib.MOE_ERR_SHAPE and route_bwd(many, r) == _lib.MOE_ERR_SHAPE
-    wide = shape(T=1, d=64 * 10923, E=1024, f=64)      # d * 6 E is past 2^32
+    wide = shape(T=1, d=64 * 16384, E=1024, f=64)      # d * 4 E is 2^32
     assert route_bwd(wide, r) == _lib.MOE_ERR_SHAPE
-    assert route_bwd(shape(T=1, d=64 * 10922, E=1024, f=64), r, n=0) == _lib.MOE_ERR_WORKSPACE
+    assert route_bwd(shape(T=1, d=64 * 16383, E=1024, f=64), r, n=0) == _lib.MOE_ERR_WORKSPACE
     with pytest.raises(KeyError):
         moe.make_router(score="tanh")
 
