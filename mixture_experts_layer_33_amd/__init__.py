@@ -75,7 +75,7 @@ def moe_route(shape, x, w_router, b_router, topk_idx, topk_gate, expert_count, w
 def moe_dispatch(shape, x, topk_idx, ring_head, ring_x, ring_x_scale, expert_offset, copy_slot,
                  slot_copy, ws, stream=None):
     if shape.dtype == MOE_FP8:
-        T, d, E, k, C, dev = (shape.tokens, shape.hidden, shape.experts, shape.top_k, shape.capacity, ring_x.device)
+        T, d, E, k, C, dev = (shape.tokens, shape.hidden, shape.experts, shape.top_k, shape.capacity, ring_x.get_device())
         i32 = torch.int32
         args = (_a("x", x, torch.bfloat16, (T, d), dev), _a("topk_idx", topk_idx, i32, (T, k), dev),
                 int(ring_head), _a("ring_x", ring_x, torch.uint8, (C, d), dev),
@@ -94,7 +94,7 @@ def moe_expert_ffn(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate
     if shape.dtype == MOE_FP8:
         args = _ffn_fp8_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
                              w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws)
-        return _on(ring_x.device, stream, "moe_expert_ffn", lib().moe_expert_ffn, shape, *args)
+        return _on(ring_x.get_device(), stream, "moe_expert_ffn", lib().moe_expert_ffn, shape, *args)
     check("moe_expert_ffn", lib().moe_expert_ffn(
         shape, _p(ring_x), _p(ring_x_scale), _p(expert_offset), int(ring_head), _p(w_gate),
         _p(w_up), _p(w_down), _p(w_gate_scale), _p(w_up_scale), _p(w_down_scale), _p(ring_y),
@@ -113,7 +113,7 @@ def moe_expert_ffn_timed(shape, ring_x, ring_x_scale, expert_offset, ring_head, 
     if shape.dtype == MOE_FP8:
         args = _ffn_fp8_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
                              w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws)
-        return _on(ring_x.device, stream, "moe_expert_ffn_timed", lib().moe_expert_ffn_timed,
+        return _on(ring_x.get_device(), stream, "moe_expert_ffn_timed", lib().moe_expert_ffn_timed,
                    shape, *args, ctypes.cast(arr, ctypes.c_void_p))
     check("moe_expert_ffn_timed", lib().moe_expert_ffn_timed(
         shape, _p(ring_x), _p(ring_x_scale), _p(expert_offset), int(ring_head), _p(w_gate),
@@ -227,22 +227,26 @@ def quantize_mx(src: torch.Tensor, stream=None):
 # These calls check every tensor (type, shape, contiguity, one device) and run on that device,
 # on `stream` or its current stream.
 
-try:   # the raw handle of a device's current stream, without building a Stream object (2 us a call)
-    _raw_stream = torch._C._cuda_getCurrentRawStream
+try:   # the current device and its stream's raw handle, without building objects (2 us a call)
+    _raw_stream, _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 except AttributeError:
+    _current = torch.cuda.current_device
+
     def _raw_stream(index: int) -> int:
         return torch.cuda.current_stream(index).cuda_stream
 
 
-def _on(dev: torch.device, stream, fn: str, c_fn, *args):
-    """c_fn(*args, raw stream) with `dev` current; raises MoeError on a status."""
-    if dev.type != "cuda":
+def _on(index: int, stream, fn: str, c_fn, *args):
+    """c_fn(*args, raw stream) with device `index` current; raises MoeError on a status."""
+    if index < 0:
         raise ValueError("libmoe takes device tensors only")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {dev}")
-    index = dev.index
-    raw = _raw_stream(index) if stream is None else stream.cuda_stream
-    if index == torch.cuda.current_device():
+    if stream is None:
+        raw = _raw_stream(index)
+    elif stream.device.index == index:
+        raw = stream.cuda_stream
+    else:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on device {index}")
+    if index == _current():
         st = c_fn(*args, raw)
     else:
         with torch.cuda.device(index):
@@ -251,13 +255,13 @@ def _on(dev: torch.device, stream, fn: str, c_fn, *args):
         check(fn, st)
 
 
-def _a(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple, dev: torch.device):
-    """The address of an argument after its checks (None for None)."""
+def _a(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple, index: int):
+    """The address of an argument after its checks (None for None); index: its device, -1 the host."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev:
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
         return t.data_ptr()
-    raise ValueError(f"{name}: needs a contiguous {dtype} tensor {list(shape)} on {dev}, got {t.dtype} {list(t.shape)} on "
+    raise ValueError(f"{name}: needs a contiguous {dtype} tensor {list(shape)} on device {index}, got {t.dtype} {list(t.shape)} on "
                      f"{t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
@@ -265,11 +269,11 @@ def _act(shape: MoeShape) -> torch.dtype:
     return torch.float32 if shape.dtype == MOE_F32 else torch.bfloat16
 
 
-def _ws_arg(name: str, ws: Optional[torch.Tensor], dev: torch.device):
+def _ws_arg(name: str, ws: Optional[torch.Tensor], index: int):
     if ws is None:
         return None, 0
-    if ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"{name}: needs a contiguous tensor on {dev}")
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"{name}: needs a contiguous tensor on device {index}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -284,7 +288,7 @@ def make_router(score: str = "softmax", groups: int = 1, top_groups: Optional[in
 
 def moe_route_scored(shape, router, x, w_router, b_router, balance, topk_idx, topk_gate, expert_count,
                      logits, ws, stream=None):
-    T, d, E, k, dev = shape.tokens, shape.hidden, shape.experts, shape.top_k, w_router.device
+    T, d, E, k, dev = shape.tokens, shape.hidden, shape.experts, shape.top_k, w_router.get_device()
     f32, i32 = torch.float32, torch.int32
     args = (_a("x", x, _act(shape), (T, d), dev), _a("w_router", w_router, f32, (E, d), dev),
             _a("b_router", b_router, f32, (E,), dev), _a("balance", balance, f32, (E,), dev),
@@ -296,7 +300,7 @@ def moe_route_scored(shape, router, x, w_router, b_router, balance, topk_idx, to
 
 def moe_route_scored_backward(shape, router, dgate, dlogits, x, w_router, logits, topk_idx, dx_in, dx,
                               dw_router, db_router, ws, stream=None):
-    T, d, E, k, dev = shape.tokens, shape.hidden, shape.experts, shape.top_k, w_router.device
+    T, d, E, k, dev = shape.tokens, shape.hidden, shape.experts, shape.top_k, w_router.get_device()
     act, f32 = _act(shape), torch.float32
     args = (_a("dgate", dgate, f32, (T, k), dev), _a("dlogits", dlogits, f32, (T, E), dev),
             _a("x", x, act, (T, d), dev), _a("w_router", w_router, f32, (E, d), dev),
@@ -312,7 +316,7 @@ def moe_backward_experts(shape, dy, topk_idx, topk_gate, ring_x, expert_offset, 
                          ws, stream=None):
     """moe_backward without the router's part: dx of the experts alone, and the gates' gradient."""
     T, d, E, k, f, C = (shape.tokens, shape.hidden, shape.experts, shape.top_k, shape.ffn, shape.capacity)
-    dev, bf, f32, i32 = w_gate.device, torch.bfloat16, torch.float32, torch.int32
+    dev, bf, f32, i32 = w_gate.get_device(), torch.bfloat16, torch.float32, torch.int32
     args = (_a("dy", dy, bf, (T, d), dev), _a("topk_idx", topk_idx, i32, (T, k), dev),
             _a("topk_gate", topk_gate, f32, (T, k), dev), _a("ring_x", ring_x, bf, (C, d), dev),
             _a("expert_offset", expert_offset, i32, (E + 1,), dev),
@@ -335,7 +339,7 @@ def _scale_spec(shape: MoeShape, rows: int):
 
 def _ffn_fp8_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
                   w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws):
-    d, E, f, C, dev = shape.hidden, shape.experts, shape.ffn, shape.capacity, ring_x.device
+    d, E, f, C, dev = shape.hidden, shape.experts, shape.ffn, shape.capacity, ring_x.get_device()
     u8, f32, bf = torch.uint8, torch.float32, torch.bfloat16
     wide, tall = (E, f // 128, d // 128), (E, d // 128, f // 128)
     return (_a("ring_x", ring_x, u8, (C, d), dev),
@@ -349,7 +353,7 @@ def _ffn_fp8_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate,
 
 
 def moe_add_rmsnorm(shape, x, residual, weight, eps, h, y, y8, y8_scale, rstd, stream=None):
-    T, d, dev = shape.tokens, shape.hidden, weight.device
+    T, d, dev = shape.tokens, shape.hidden, weight.get_device()
     act, f32 = _act(shape), torch.float32
     sdt, sshape = _scale_spec(shape, T)
     args = (_a("x", x, act, (T, d), dev), _a("residual", residual, act, (T, d), dev),
@@ -360,7 +364,7 @@ def moe_add_rmsnorm(shape, x, residual, weight, eps, h, y, y8, y8_scale, rstd, s
 
 
 def moe_add_rmsnorm_backward(shape, dy, dh, h, weight, rstd, dx, dweight, ws, stream=None):
-    T, d, dev = shape.tokens, shape.hidden, weight.device
+    T, d, dev = shape.tokens, shape.hidden, weight.get_device()
     act, f32 = _act(shape), torch.float32
     args = (_a("dy", dy, act, (T, d), dev), _a("dh", dh, act, (T, d), dev), _a("h", h, act, (T, d), dev),
             _a("weight", weight, f32, (d,), dev), _a("rstd", rstd, f32, (T,), dev),
@@ -372,7 +376,7 @@ def moe_add_rmsnorm_backward(shape, dy, dh, h, weight, rstd, dx, dweight, ws, st
 def moe_dispatch_q(shape, x8, x8_scale, topk_idx, ring_head, ring_x, ring_x_scale, expert_offset,
                    copy_slot, slot_copy, ws, stream=None):
     """moe_dispatch of 8-bit rows (moe_add_rmsnorm's y8 and its scales)."""
-    T, d, E, k, C, dev = (shape.tokens, shape.hidden, shape.experts, shape.top_k, shape.capacity, ring_x.device)
+    T, d, E, k, C, dev = (shape.tokens, shape.hidden, shape.experts, shape.top_k, shape.capacity, ring_x.get_device())
     i32, u8 = torch.int32, torch.uint8
     args = (_a("x8", x8, u8, (T, d), dev), _a("x8_scale", x8_scale, *_scale_spec(shape, T), dev),
             _a("topk_idx", topk_idx, i32, (T, k), dev), int(ring_head),
@@ -403,8 +407,9 @@ def quantize_fp8(src: torch.Tensor, row_block: int = 128, stream=None):
     else:
         shape = (-(-rows // 128), cols // 128)
     scales = torch.empty(shape, dtype=torch.float32, device=dev)
-    p = _a("src", src, torch.bfloat16, src.shape, dev)
-    _on(dev, stream, "moe_quantize_fp8", lib().moe_quantize_fp8, p, rows, cols, row_block, codes.data_ptr(), scales.data_ptr())
+    at = src.get_device()
+    p = _a("src", src, torch.bfloat16, src.shape, at)
+    _on(at, stream, "moe_quantize_fp8", lib().moe_quantize_fp8, p, rows, cols, row_block, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -419,7 +424,7 @@ def moe_matmul_fp8(a, a_scale, w, w_scale, out, ws=None, stream=None):
     quantize_fp8: a_scale [K/128, M] (row_block 1), w_scale [ceil(N/128), K/128]."""
     if a.dim() != 2 or w.dim() != 2 or out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("moe_matmul_fp8: two matrices of codes, and an output in bfloat16 or float32")
-    dev, (M, K), N = w.device, a.shape, w.shape[0]
+    dev, (M, K), N = w.get_device(), a.shape, w.shape[0]
     u8, f32 = torch.uint8, torch.float32
     args = (_a("a", a, u8, (M, K), dev), _a("a_scale", a_scale, f32, (K // 128, M), dev),
             _a("w", w, u8, (N, K), dev), _a("w_scale", w_scale, f32, (-(-N // 128), K // 128), dev),
