@@ -14,28 +14,50 @@
 
 namespace moe {
 
-// Eight consecutive elements of an act row as fp32.
+// Eight consecutive elements of an act row: as they are in memory, and as fp32.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
+struct Raw8 {
+  u32x4 w[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load_raw(const void* p, int64_t i) {
+  Raw8<F32> r;
   if constexpr (F32) {
-    const f32x4 a = *(const f32x4*)((const float*)p + i), b = *(const f32x4*)((const float*)p + i + 4);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) { v[q] = a[q]; v[4 + q] = b[q]; }
+    r.w[0] = *(const u32x4*)((const float*)p + i);
+    r.w[1] = *(const u32x4*)((const float*)p + i + 4);
   } else {
-    const u32x4 w = *(const u32x4*)((const bf16_t*)p + i);
+    r.w[0] = *(const u32x4*)((const bf16_t*)p + i);
+  }
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void widen8(const Raw8<F32>& r, float (&v)[8]) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) { v[2 * q] = lo_bf(w[q]); v[2 * q + 1] = hi_bf(w[q]); }
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (F32) {
+      v[q] = __uint_as_float(r.w[0][q]);
+      v[4 + q] = __uint_as_float(r.w[1][q]);
+    } else {
+      v[2 * q] = lo_bf(r.w[0][q]);
+      v[2 * q + 1] = hi_bf(r.w[0][q]);
+    }
   }
 }
+template <bool F32>
+__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
+  widen8<F32>(load_raw<F32>(p, i), v);
+}
 
+// Rows are written past the caches' retention (8,192 x 7168 with 8-bit rows: 111 -> 107 us).
 template <bool F32>
 __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
   if constexpr (F32) {
-    *(f32x4*)((float*)p + i) = f32x4{v[0], v[1], v[2], v[3]};
-    *(f32x4*)((float*)p + i + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4*)((float*)p + i));
+    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, (f32x4*)((float*)p + i + 4));
   } else {
-    *(u32x4*)((bf16_t*)p + i) = u32x4{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]),
-                                      pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7])};
+    __builtin_nontemporal_store(
+        u32x4{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7])},
+        (u32x4*)((bf16_t*)p + i));
   }
 }
 
@@ -129,8 +151,8 @@ __device__ __forceinline__ void norm_out(const NormArgs& p, int64_t t, int v, bo
   }
 }
 
-// Bound by memory: x, r, h, y and the codes each cross once (8,192 x 7168 bf16 with 8-bit rows: 111 us, the
-// 4.8 TB/s of a large copy).  For a few rows by latency: two reads and the sum (6 us for 8).
+// Bound by memory: x, r, h, y and the codes each cross once (8,192 x 7168 bf16 with 8-bit rows: 107 us, 5.0 TB/s;
+// a large copy reaches 4.8).  For a few rows by latency: two reads and the sum (6 us for 8).
 //
 // LANES threads per row, 256 threads per workgroup, NV vectors of 8 per thread in registers;
 // NV = 0: a row too wide for that is read twice (every element by the thread that
@@ -203,12 +225,18 @@ hipError_t launch_add_rmsnorm(bool f32, int q, const void* x, const void* residu
 
 // ----------------------------------------------------------------------------- gradient
 // A workgroup takes rows b, b + G, ... and keeps its columns' share of dw in registers; the
-// G partial rows are then added in order.  Bound by memory: 8,192 x 4096 bf16 with dh takes 54 us (5.0 TB/s) and
-// 5 us for the partial rows; two workgroups a CU, so that one's row sum is hidden by the other's reads.
+// G partial rows are then added in order.  Bound by memory: 8,192 x 4096 bf16 with dh takes 38 us (7.0 TB/s; 55
+// without the next row's reads under way during a row's sum, 41 with stores that stay in the caches) and
+// 5 us for the partial rows.
 constexpr int NB_G = 512;
 
 int norm_bwd_groups(int64_t T) { return (int)std::min<int64_t>(T, NB_G); }
 size_t norm_bwd_workspace_bytes(int64_t T, int d) { return (size_t)norm_bwd_groups(T) * d * 4; }
+
+__device__ __forceinline__ void store_part(float* at, const float (&v)[8]) {
+  *(f32x4*)at = f32x4{v[0], v[1], v[2], v[3]};
+  *(f32x4*)(at + 4) = f32x4{v[4], v[5], v[6], v[7]};
+}
 
 struct NormBwdArgs {
   const void* dy;
@@ -223,21 +251,19 @@ struct NormBwdArgs {
 };
 
 template <bool F32>
-__device__ __forceinline__ void norm_bwd_out(const NormBwdArgs& p, int64_t at, const float (&q)[8],
+__device__ __forceinline__ void norm_bwd_out(const NormBwdArgs& p, int64_t at, const Raw8<F32>& dh, const float (&q)[8],
                                              const float (&xh)[8], float m, float rstd) {
   float o[8];
-  if (p.dh) load8<F32>(p.dh, at, o);
-  else {
+  widen8<F32>(dh, o);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = 0.f;
-  }
+  for (int i = 0; i < 8; ++i) o[i] = p.dh ? o[i] : 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] += rstd * (q[i] - xh[i] * m);
   store8<F32>(p.dx, at, o);
 }
 
 template <bool F32, int NV>
-__global__ __launch_bounds__(256) void rmsnorm_bwd_kernel(NormBwdArgs p) {
+__global__ __launch_bounds__(256, 2) void rmsnorm_bwd_kernel(NormBwdArgs p) {
   __shared__ float red[4];
   const int tid = threadIdx.x, nv = p.d / 8;
   constexpr int KV = NV > 0 ? NV : 1;
@@ -248,15 +274,25 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_kernel(NormBwdArgs p) {
       const int v = tid + 256 * i;
       if (v < nv) load8<true>(p.w, v * 8, w[i]);
     }
+    // The next row is requested before this row's sum is joined, and dh before it is needed.  Loads are
+    // unconditional (past the row's or the batch's end the last place again): a branch would make them wait.
+    Raw8<F32> dy[NV], hh[NV], dh[NV];
+    float rstd = p.rstd[blockIdx.x];
+    const void* add = p.dh ? p.dh : p.dy;
+    auto at = [&](int64_t t, int i) { return t * p.d + min(tid + 256 * i, nv - 1) * 8; };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      dy[i] = load_raw<F32>(p.dy, at(blockIdx.x, i));
+      hh[i] = load_raw<F32>(p.h, at(blockIdx.x, i));
+    }
     for (int64_t t = blockIdx.x; t < p.T; t += p.G) {
-      const float rstd = p.rstd[t];
       float q[NV][8], xh[NV][8], c = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int v = tid + 256 * i;
-        if (v < nv) {
-          load8<F32>(p.dy, t * p.d + v * 8, q[i]);
-          load8<F32>(p.h, t * p.d + v * 8, xh[i]);
+        dh[i] = load_raw<F32>(add, at(t, i));
+        widen8<F32>(dy[i], q[i]);
+        widen8<F32>(hh[i], xh[i]);
+        if (tid + 256 * i < nv) {
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             xh[i][u] *= rstd;
@@ -266,18 +302,26 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_kernel(NormBwdArgs p) {
           }
         }
       }
+      const int64_t next = min(t + p.G, p.T - 1);
+      const float rstd_next = p.rstd[next];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        dy[i] = load_raw<F32>(p.dy, at(next, i));
+        hh[i] = load_raw<F32>(p.h, at(next, i));
+      }
       const float m = row_sum<256>(c, red) / (float)p.d;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = tid + 256 * i;
-        if (v < nv) norm_bwd_out<F32>(p, t * p.d + v * 8, q[i], xh[i], m, rstd);
+        if (v < nv) norm_bwd_out<F32>(p, t * p.d + v * 8, dh[i], q[i], xh[i], m, rstd);
       }
+      rstd = rstd_next;
     }
     if (p.part)
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = tid + 256 * i;
-        if (v < nv) store8<true>(p.part, (int64_t)blockIdx.x * p.d + v * 8, dw[i]);
+        if (v < nv) store_part(p.part + (int64_t)blockIdx.x * p.d + v * 8, dw[i]);
       }
   } else {
     // wide rows: read twice; the workgroup's own row of partials is kept in memory
@@ -306,43 +350,45 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_kernel(NormBwdArgs p) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) o[u] = dw[0][u];
           }
-          store8<true>(p.part, at, o);
+          store_part(p.part + at, o);
         }
       }
       const float m = row_sum<256>(c, red) / (float)p.d;
       for (int v = tid; v < nv; v += 256) {
         term(v);
-        norm_bwd_out<F32>(p, t * p.d + v * 8, q, xh, m, rstd);
+        const int64_t at = t * p.d + v * 8;
+        norm_bwd_out<F32>(p, at, load_raw<F32>(p.dh ? p.dh : p.dy, at), q, xh, m, rstd);
       }
     }
   }
 }
 
-// out[c] = sum over g of part[g, c]: eight threads share a column, each adds rows g = its number
-// mod 8 ascending, then the eight sums in order.  One thread per column left 16 workgroups
-// waiting for 512 loads in turn (131 us of the 187 us gradient at 8,192 x 4,096).
-__global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict__ part, int G, int64_t d,
-                                                         float* __restrict__ out) {
-  __shared__ float red[8][32];
+// out[c] = sum over g of part[g, c]: 32 threads share a column, each adds rows g = its number
+// mod 32 ascending, then the 32 sums in order.  Bound by the latency of a thread's loads: one thread per
+// column took 131 us of the 187 us gradient at 8,192 x 4096, eight 4.9.
+constexpr int CS = 32;
+__global__ __launch_bounds__(32 * CS) void column_sum_kernel(const float* __restrict__ part, int G, int64_t d,
+                                                             float* __restrict__ out) {
+  __shared__ float red[CS][33];
   const int cl = threadIdx.x & 31, r = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + cl;
   float s = 0.f;
   if (c < d) {
-#pragma unroll 8
-    for (int g = r; g < G; g += 8) s += part[(int64_t)g * d + c];
+#pragma unroll 16
+    for (int g = r; g < G; g += CS) s += part[(int64_t)g * d + c];
   }
   red[r][cl] = s;
   __syncthreads();
   if (r == 0 && c < d) {
     s = red[0][cl];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][cl];
+    for (int i = 1; i < CS; ++i) s += red[i][cl];
     out[c] = s;
   }
 }
 
 hipError_t launch_column_sum(const float* part, int G, int64_t d, float* out, hipStream_t st) {
-  column_sum_kernel<<<(unsigned)((d + 31) / 32), 256, 0, st>>>(part, G, d, out);
+  column_sum_kernel<<<(unsigned)((d + 31) / 32), 32 * CS, 0, st>>>(part, G, d, out);
   return hipGetLastError();
 }
 
