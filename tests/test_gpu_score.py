@@ -59,6 +59,8 @@ CASES = [  # dtype, T, d, E, k, rule
     ("bf16", 2, 192, 1024, 32, R("softmax", 64, 17, 2)), ("bf16", 64, 64, 1, 1, R()), ("bf16", 40, 128, 33, 32, R("sigmoid", 11, 11, 2)),
     ("bf16", 7, 128, 500, 10, R("sigmoid", 50, 7, 1)), ("f32", 19, 72, 16, 4, R("sigmoid", 4, 2, 2, True, 2.5)), ("f32", 66, 128, 130, 3, R(renormalise=False)),
 ]
+CASES += [("bf16", 9, 7168, 256, 8, R("sigmoid", 8, 4, 2, True, 2.5)), ("bf16", 100, 4096, 512, 10, R(renormalise=False)),
+          ("bf16", 65, 2048, 1000, 16, R("sigmoid", 10, 5, 2, True)), ("bf16", 31, 1024, 70, 4, R("softmax", 7, 3, 2, False))]
 IDS = [f"{c[0]}-{c[1]}x{c[2]}-E{c[3]}k{c[4]}-{c[5].score}{c[5].groups}.{c[5].top_groups}.{c[5].group_top}{'r' if c[5].renormalise else ''}" for c in CASES]
 
 
@@ -166,7 +168,8 @@ def backward(dtype, s, rule, dg, dlog, x, w, logits, idx, dx_in, db=True):
     return dx, dw, dbv, ws
 
 
-BCASES = CASES + [("bf16", 700, 512, 160, 6, R(renormalise=False)), ("bf16", 257, 320, 512, 10, R("sigmoid")), ("f32", 300, 72, 40, 4, R("sigmoid"))]
+BCASES = CASES + [("bf16", 16, 320, 1000, 32, R(renormalise=False)), ("bf16", 16, 128, 64, 2, R("sigmoid")), ("bf16", 17, 128, 128, 2, R()),
+                  ("bf16", 3000, 128, 72, 4, R(renormalise=False)), ("bf16", 700, 512, 160, 6, R(renormalise=False)), ("bf16", 257, 320, 512, 10, R("sigmoid")), ("f32", 300, 72, 40, 4, R("sigmoid"))]
 BIDS = [f"{c[0]}-{c[1]}x{c[2]}-E{c[3]}k{c[4]}-{c[5].score}{'r' if c[5].renormalise else ''}" for c in BCASES]
 
 
@@ -335,10 +338,11 @@ def test_no_tokens():
     assert (cnt == 0).all() and (dw == 0).all() and (db == 0).all()
 
 
-def test_side_stream_graph_and_repeats():
-    print("\n[case] route_scored graph", flush=True)
+@pytest.mark.parametrize("T,d", [(3, 256), (12, 2048), (70, 256)])
+def test_side_stream_graph_and_repeats(T, d):
+    print(f"\n[case] route_scored graph {T}x{d}", flush=True)
     rule = R("sigmoid", 8, 4, 2, True, 2.5)
-    T, d, E, k = 70, 256, 64, 6
+    E, k = 64, 6
     x, w, _, bal, _ = draw("bf16", T, d, E, k, rule, 8, True)
     s, idx, gate, cnt, logits = run("bf16", x, w, None, bal, k, rule)
     ws, wb = moe.workspace(s, moe.OP_ROUTE, DEV), moe.workspace(s, moe.OP_ROUTE_BACKWARD, DEV)
