@@ -379,6 +379,135 @@ __global__ __launch_bounds__(256) void router_small_kernel(const bf16_t* __restr
   }
 }
 
+// Logits of many tokens over 128 or more experts: partial planes of x W_r^T by 128 x 128 tiles, eight wavefronts of 64
+// tokens x 32 experts, K in slices of 64 through two LDS buffers, W_r split into its three bf16 parts in
+// registers (route_body.h).  The 32 x 32 wavefront tiles of the plain router read 4 KB of LDS for three MFMAs, this one
+// 5 KB for six, and the next slice's parts are made and stored among a slice's MFMAs (its loads were issued
+// two slices ahead).  hi's products have their own sum; mid's and lo's share one, 2^-8 of it.  Split z runs on XCD z
+// (8 splits), so that each byte of x and W_r enters one L2 only.  The whole call, against the plain router's logits: 8,192
+// tokens, d 7168, 512 experts 220 -> 194 us, 2,048 tokens, 256 experts 40 -> 37; a slice takes 1.5 us, its MFMAs 0.7.
+// Rows of 128 bytes are swizzled by r / 2 (a 128-bit read is served in groups like rows 0-3, 12-15, 20-27, whose 16 places
+// are then distinct; by r they meet in pairs).
+__device__ __forceinline__ int lswz(int r, int c) { return r * RM_K + ((c ^ ((r >> 1) & 7)) << 4); }
+constexpr int LG_T = 128, LG_BUF = 4 * LG_T * RM_K, LG_LDS = 2 * LG_BUF;
+__global__ __launch_bounds__(512) void score_logits_kernel(const bf16_t* __restrict__ x, const float* __restrict__ w_r,
+                                                           float* __restrict__ planes, int64_t T, int d, int E, int KS) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int ne = (E + LG_T - 1) / LG_T, z = (int)(blockIdx.x % KS);
+  int tile = (int)(blockIdx.x / KS);
+  if (KS == 1) {   // XCD b % 8 takes a run of tiles, so that a token tile's expert tiles meet in one L2
+    const int n = (int)gridDim.x, b = tile & 7, j = tile >> 3;
+    tile = b * (n / 8) + min(b, n % 8) + j;
+  }
+  const int e0 = tile % ne * LG_T;
+  const int64_t t0 = (int64_t)(tile / ne) * LG_T;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 2, wn = wave & 3, lr = lane & 31, lg = lane >> 5;
+  const int KA = d / 64, kb = (int)((int64_t)KA * z / KS), KT = (int)((int64_t)KA * (z + 1) / KS) - kb;
+  const bf16_t* xs[2];
+  const float* ws[2];
+  int at[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {   // piece q: row q / 8, elements 8 (q % 8) .. + 7 of a slice
+    const int q = tid + 512 * i, r = q / 8, c = q % 8;
+    xs[i] = x + min(t0 + r, T - 1) * d + (int64_t)kb * 64 + c * 8;
+    ws[i] = w_r + (int64_t)min(e0 + r, E - 1) * d + (int64_t)kb * 64 + c * 8;
+    at[i] = lswz(r, c);
+  }
+  u32x4 rx[2][2];
+  f32x4 rw[2][2][2];
+  auto load = [&](int kt, auto set) __attribute__((always_inline)) {
+    constexpr int P = decltype(set)::value;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      rx[P][i] = *(const u32x4*)(xs[i] + kt * 64);
+      rw[P][i][0] = *(const f32x4*)(ws[i] + kt * 64);
+      rw[P][i][1] = *(const f32x4*)(ws[i] + kt * 64 + 4);
+    }
+  };
+  auto store = [&](int i, auto set) __attribute__((always_inline)) {   // piece i of the set's slice to its buffer
+    constexpr int P = decltype(set)::value;
+    uint8_t* to = lds + P * LG_BUF + at[i];
+    u32x4 h, m, l;
+    router_split8(rw[P][i], h, m, l);
+    *(u32x4*)to = rx[P][i];
+    *(u32x4*)(to + LG_T * RM_K) = h;
+    *(u32x4*)(to + 2 * LG_T * RM_K) = m;
+    *(u32x4*)(to + 3 * LG_T * RM_K) = l;
+  };
+  f32x16 acc[2][2];   // [token half][hi | mid, lo]
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][p][r] = 0.f;
+  // Slice kt (buffer P); slice kt + 1 is in the other set, kt + 2 goes into this one.
+  auto step = [&](int kt, auto set, auto more, auto next) __attribute__((always_inline)) {
+    constexpr int P = decltype(set)::value;
+    using Other = std::integral_constant<int, 1 - P>;
+    if constexpr (decltype(more)::value) load(kt + 2, set);
+    // Scheduling barriers: the loads stay here, the stores, which wait for the loads before, come late in the slice.
+    // (Reading a quarter's fragments before the MFMAs of the quarter before measured no better.)
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t* b = lds + P * LG_BUF;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const int c = kk * 2 + lg;
+      auto frag = [&](int row) __attribute__((always_inline)) {
+        return __builtin_bit_cast(bf16x8, *(const u32x4*)(b + lswz(row, c)));
+      };
+      const bf16x8 a0 = frag(wm * 64 + lr), a1 = frag(wm * 64 + 32 + lr);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        const bf16x8 w = frag((p + 1) * LG_T + wn * 32 + lr);
+        acc[0][p > 0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a0, w, acc[0][p > 0], 0, 0, 0);
+        acc[1][p > 0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a1, w, acc[1][p > 0], 0, 0, 0);
+      }
+      if constexpr (decltype(next)::value) {
+        if (kk == 2) store(0, Other{});
+        if (kk == 3) store(1, Other{});
+      }
+      if (kk > 0) __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();
+  };
+  using A = std::integral_constant<int, 0>;
+  using B = std::integral_constant<int, 1>;
+  using Yes = std::true_type;
+  using No = std::false_type;
+  load(0, A{});
+  if (KT > 1) load(1, B{});
+  store(0, A{});
+  store(1, A{});
+  __syncthreads();
+  int kt = 0;
+  for (; kt + 3 < KT; kt += 2) {
+    step(kt, A{}, Yes{}, Yes{});
+    step(kt + 1, B{}, Yes{}, Yes{});
+  }
+  if (KT - kt == 3) {
+    step(kt, A{}, Yes{}, Yes{});
+    step(kt + 1, B{}, No{}, Yes{});
+    step(kt + 2, A{}, No{}, No{});
+  } else if (KT - kt == 2) {
+    step(kt, A{}, No{}, Yes{});
+    step(kt + 1, B{}, No{}, No{});
+  } else {
+    step(kt, A{}, No{}, No{});
+  }
+  const int e = e0 + wn * 32 + lr;
+  if (e >= E) return;
+  float* out = planes + (int64_t)z * T * E;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int64_t t = t0 + wm * 64 + 32 * i + 8 * (r / 4) + 4 * lg + (r % 4);
+      if (t < T) out[t * E + e] = acc[i][0][r] + acc[i][1][r];
+    }
+}
+
 // K splits of 64 x 64 logit tiles where the 128 x 128 tiles (or the plain router's fewer splits) would leave
 // half of the CUs idle, at least four slices of 64 each; 0: the plain router's choice.  (256 experts, d 7168, the
 // whole call: 9 tokens 33 -> 16 us, 400 tokens 35 -> 24; 128 experts, d 4096, 200 tokens 23 -> 15.)
@@ -408,6 +537,14 @@ hipError_t launch_route_scored(const void* x, bool x_f32, const float* w_r, cons
   } else if (const int fine = x_f32 ? 0 : fine_splits(T, E, d)) {
     ks = fine;
     err = launch_router_logits_64(x, w_r, T, d, E, ks, planes, st);
+  } else if (!x_f32 && router_big(E)) {
+    ks = router_ksplit(T, E, d);
+    if ((err = hipFuncSetAttribute((const void*)score_logits_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, LG_LDS)) !=
+        hipSuccess)
+      return err;
+    const int64_t tiles = ((T + LG_T - 1) / LG_T) * ((E + LG_T - 1) / LG_T);
+    score_logits_kernel<<<(unsigned)(tiles * ks), 512, LG_LDS, st>>>((const bf16_t*)x, w_r, planes, T, d, E, ks);
+    err = hipGetLastError();
   } else {
     err = launch_router_logits(x, x_f32, w_r, T, d, E, planes, &ks, st);
   }

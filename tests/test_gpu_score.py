@@ -82,6 +82,16 @@ def test_forward(case, balanced):
     assert torch.equal(idx, idx2) and same_bits(gate, gate2) and torch.equal(cnt, cnt2)
 
 
+# 128 x 128 tiles of the logits: one to many slices of 64, with K splits, ragged tiles
+LOTS = [("bf16", 16500, 64, 130, 4, R("sigmoid")), ("bf16", 8200, 128, 257, 3, R()), ("bf16", 8200, 192, 260, 6, R("sigmoid", 4, 2, 2)),
+        ("bf16", 8321, 320, 300, 2, R(renormalise=False)), ("bf16", 5000, 1088, 300, 8, R("sigmoid", 10, 5, 1)), ("bf16", 2048, 3136, 256, 8, R("sigmoid", 8, 4, 2, True, 2.5))]
+
+
+@pytest.mark.parametrize("case", LOTS, ids=[f"{c[1]}x{c[2]}-E{c[3]}" for c in LOTS])
+def test_forward_of_many_tokens(case):
+    test_forward(case, True)
+
+
 def test_softmax_without_groups_is_the_plain_router():
     """The rule that moe_route has gives its choice bit for bit, and its gates within rounding."""
     print("\n[case] route_scored against route", flush=True)
