@@ -102,44 +102,6 @@ __device__ __forceinline__ void wait_stages(int n) {
   else wait_stages<L, MOST - 1>(n);
 }
 
-// Row tile mt of 16 rows in expert-major order, found by every wavefront for itself from the segment offsets
-// (lane l counts the tiles of experts l V .. l V + V - 1): a separate launch for a tile list costs more
-// than a few tokens' products can spare (4.7 of 75 us).  False past the last tile.
-__device__ __forceinline__ bool thin_tile(const int32_t* offset, int E, int mt, int& e, int& row0, int32_t& seg,
-                                          int& rows) {
-  const int lane = threadIdx.x & 63, V = (E + 63) / 64, e0 = lane * V;
-  auto at = [&](int i) { return offset[min(e0 + i, E)]; };
-  int n = 0;
-  int32_t lo = at(0);
-  for (int i = 1; i <= V; ++i) {
-    const int32_t hi = at(i);
-    n += (hi - lo + 15) / 16;
-    lo = hi;
-  }
-  int incl = n;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int v = __shfl_up(incl, o, 64);
-    if (lane >= o) incl += v;
-  }
-  const unsigned long long past = __ballot(incl > mt);
-  if (past == 0) return false;
-  const int owner = __builtin_ctzll(past);
-  int left = mt - (__builtin_amdgcn_readlane(incl, owner) - __builtin_amdgcn_readlane(n, owner));
-  for (int i = owner * V;; ++i) {   // ends: the owner's experts hold tile `left`
-    const int32_t a = offset[i], b = offset[i + 1];
-    const int t = (b - a + 15) / 16;
-    if (left < t) {
-      e = i;
-      row0 = 16 * left;
-      seg = a;
-      rows = min(16, b - a - row0);
-      return true;
-    }
-    left -= t;
-  }
-}
-
 // Few token rows: a weight stream.  16 token rows x 32 W weight rows, W wavefronts, each with 32 weight rows
 // (SWIGLU: 16 gate and the matching 16 up rows, W = 4: 64 columns a workgroup, half a block of H, so that twice
 // the workgroups fill the chip; h leaves in fp32 for quantise_h_kernel: 46 -> 36 us for the gate and up
@@ -173,9 +135,12 @@ __global__ __launch_bounds__(64 * W) void fp8_thin_kernel(Fp8Args p) {
   int e = 0, row0 = 16 * mt, rows = 16;
   int32_t seg = 0;
   if (p.offset) {
-    if (!thin_tile(p.offset, p.E, mt, e, row0, seg, rows)) return;
+    const SegmentTiles st = segment_tiles<16>(p.offset, p.E);
+    if (mt >= st.total) return;
+    int first;
+    find_segment<16>(st, mt, e, first, seg, rows);
     auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-    e = uni(e); row0 = uni(row0); seg = uni(seg); rows = uni(rows);
+    e = uni(e); row0 = uni(16 * (mt - first)); seg = uni(seg); rows = uni(min(16, rows - row0));
   } else {
     rows = (int)min((int64_t)16, p.a_rows - row0);
   }
@@ -445,11 +410,11 @@ hipError_t launch_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8
 
 // How the experts' products run.  The host knows the mean rows of an expert, not their spread.
 //   * `few`: fewer than THIN_FEW workgroups of 128 columns over all 16-row tiles: the thin kernel (4 experts x
-//     16 rows, d 7168, f 2048: 47 us against 65 with tiles of 64 rows; 64 experts x 8 rows: 309 us
+//     16 rows, d 7168, f 2048: 47 us against 65 with a list of tiles of 64 rows; 64 experts x 8 rows: 309 us
 //     either way, and a batch that falls on one expert would read its weights once per 16 rows).
 //   * else tiles of 64 fm rows, the least estimated time of both products: rounds of 256 workgroups times the
 //     blocks of one (dense_plan's times), or the weights at the rate that height streams them at
-//     (5.3, 5.1, 4.6, 4.5 TB/s: the lower tiles keep three stages).  A tile list is shared by both products.
+//     (5.3, 5.1, 4.6, 4.5 TB/s: the lower tiles keep three stages).
 //     Measured at 64 experts, d 4096, f 2048, us for fm = 1 | 2 | 3 | 4: 32 rows 310 | 313 | 363 | 371, 64 rows 344 |
 //     325 | 370 | 377, 128 rows 470 | 404 | 390 | 394, 200 rows 621 | 477 | 562 | 434, 300 rows 872 | 667 | 652 | 713.
 constexpr int64_t THIN_FEW = 200;
@@ -473,7 +438,7 @@ struct FfnFp8Layout {
   size_t tiles, h, hs, h32, total;
   int fm;
   int64_t mt;   // bound on the row tiles: every tile holds a row
-  bool few;
+  bool few, list;
 };
 static FfnFp8Layout ffn_fp8_layout(int64_t n, int64_t C, int d, int E, int f) {
   auto al = [](size_t b) { return (b + 255) & ~(size_t)255; };
@@ -481,8 +446,10 @@ static FfnFp8Layout ffn_fp8_layout(int64_t n, int64_t C, int d, int E, int f) {
   L.few = std::min<int64_t>(max_tiles_for(n, E, 16), n) * (f / 128) < THIN_FEW;
   L.fm = L.few ? 0 : ffn_tile(n, d, E, f);
   L.mt = std::min<int64_t>(max_tiles_for(n, E, L.few ? 16 : 64 * L.fm), n);
+  // many workgroups: their row tiles come from a list (2,048 tokens over 256 experts, 17 thousand: 1,948 -> 1,926 us)
+  L.list = !L.few && L.mt * (f / 128 + (d + 255) / 256) > 4096;
   size_t o = 0;
-  L.tiles = o; o += al((size_t)(2 * L.mt + 64) * 4);
+  L.tiles = o; o += L.list ? al((size_t)(2 * L.mt + 64) * 4) : 0;
   L.h = o; o += al((size_t)C * f);
   L.hs = o; o += al((size_t)C * (f / 128) * 4);
   L.h32 = o; o += L.few ? al((size_t)n * f * 4) : 0;
@@ -500,12 +467,11 @@ hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const i
                           void* saved_au, void* ws, hipEvent_t* events, hipStream_t st) {
   const FfnFp8Layout L = ffn_fp8_layout(n, C, d, E, f);
   uint8_t* w = (uint8_t*)ws;
-  int32_t* ntiles = (int32_t*)(w + L.tiles);
-  int32_t* tiles = ntiles + 64;
   auto mark = [&](int i) { return events ? hipEventRecord(events[i], st) : hipSuccess; };
   const int fm = L.fm;
   const int64_t mt = L.mt;
-  hipError_t err = fm ? launch_build_tiles(expert_offset, E, 64 * fm, tiles, ntiles, st) : hipSuccess;
+  int32_t* ntiles = (int32_t*)(w + L.tiles);
+  hipError_t err = L.list ? launch_build_tiles(expert_offset, E, 64 * fm, ntiles + 64, ntiles, st) : hipSuccess;
   if (err != hipSuccess || (err = mark(0)) != hipSuccess) return err;
   const bool once = n <= 64 * fm * (int64_t)E;   // about one row tile per expert: each weight is read once
   Fp8Args p{};
@@ -519,7 +485,7 @@ hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const i
   p.K = d;
   p.N = f;
   p.offset = expert_offset;
-  p.tiles = tiles;
+  p.tiles = L.list ? ntiles + 64 : nullptr;
   p.ntiles = ntiles;
   p.head = head;
   p.C = C;

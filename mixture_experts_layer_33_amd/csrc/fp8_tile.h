@@ -26,7 +26,7 @@ struct Fp8Args {
   int64_t a_rows;
   int K, N;
   const int32_t* offset;   // ring segments; NULL: one product of all a_rows rows
-  const int32_t* tiles;
+  const int32_t* tiles;    // the row tiles' list, or NULL: found from the offsets
   const int32_t* ntiles;
   int64_t head, C;
   void* out;               // SWIGLU: H codes [C, N]; else bf16 or fp32 [C, N]
@@ -34,12 +34,74 @@ struct Fp8Args {
   bf16_t* saved_au;        // SWIGLU: [C, 2N] or NULL
   const bf16_t* add;       // TILE_ADD: [C, N] or NULL (may be out)
   int Z;                   // K splits of a dense product (1 elsewhere)
-  int E;                   // experts (the thin kernel)
+  int E;                   // experts
   float* h32;              // the thin kernel's h in fp32 [n, N], segment order
   int group;               // row tiles that take the same column tile one after another
 };
 
 constexpr int FP8_GROUP = 4;   // row tiles that take a column tile one after another
+
+// The row tiles of all experts' segments, BM rows each, in expert order, found by every wavefront for itself from
+// the offsets (lane l counts the tiles of experts l V .. l V + V - 1): a launch that writes a list of them costs 5 us
+// (16 experts x 64 rows, d 1024, f 512: 23 -> 20 us), this scan 0.3 us more in each workgroup than reading the list.
+struct SegmentTiles {
+  const int32_t* offset;
+  int32_t o[5];               // V <= 4: the offsets around this lane's experts
+  int V, n, incl, total;      // this lane's tiles, those up to it, all
+};
+// Inclusive sum over the lanes, in VALU moves: within rows of 16, then their last lanes into the rows behind.
+__device__ __forceinline__ int lanes_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr:1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2 and 3
+  return v;
+}
+template <int BM>
+__device__ __forceinline__ SegmentTiles segment_tiles(const int32_t* offset, int E) {
+  SegmentTiles s{offset, {}, (E + 63) / 64, 0, 0, 0};
+  const int e0 = (threadIdx.x & 63) * s.V;
+#pragma unroll
+  for (int i = 0; i < 5; ++i) s.o[i] = offset[min(e0 + i, E)];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < s.V) s.n += (s.o[i + 1] - s.o[i] + BM - 1) / BM;
+  int32_t lo = s.o[4];
+  for (int i = 5; i <= s.V; ++i) {
+    const int32_t hi = offset[min(e0 + i, E)];
+    s.n += (hi - lo + BM - 1) / BM;
+    lo = hi;
+  }
+  s.incl = lanes_scan(s.n);
+  s.total = __builtin_amdgcn_readlane(s.incl, 63);
+  return s;
+}
+// The expert e of tile mt < total, its first tile, its segment's start and its rows.
+template <int BM>
+__device__ __forceinline__ void find_segment(const SegmentTiles& s, int mt, int& e, int& first, int32_t& seg, int& rows) {
+  const int owner = __builtin_ctzll(__ballot(s.incl > mt));
+  first = __builtin_amdgcn_readlane(s.incl, owner) - __builtin_amdgcn_readlane(s.n, owner);
+  e = owner * s.V;
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (!found && i < s.V) {
+      seg = __builtin_amdgcn_readlane(s.o[i], owner);
+      rows = __builtin_amdgcn_readlane(s.o[i + 1], owner) - seg;
+      const int t = (rows + BM - 1) / BM;
+      found = mt < first + t;
+      if (!found) { first += t; ++e; }
+    }
+  while (!found) {   // V > 4; ends: the owner's experts hold tile mt
+    seg = s.offset[e];
+    rows = s.offset[e + 1] - seg;
+    const int t = (rows + BM - 1) / BM;
+    found = mt < first + t;
+    if (!found) { first += t; ++e; }
+  }
+}
 
 // Lane l's 32 bytes of a row's block.  (Which of the block's 128 positions a lane's byte is does
 // not matter as long as both operands agree.)
@@ -101,7 +163,9 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Args& p, const int block)
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
   constexpr int CB = SWIGLU ? 1 : 2;             // output blocks of 128 columns per tile
   const int nblk = (p.N + 127) / 128, nct = (nblk + CB - 1) / CB;
-  const int nmt = p.offset ? *p.ntiles : (int)((p.a_rows + BM - 1) / BM);
+  SegmentTiles st{};
+  if (p.offset && !p.tiles) st = segment_tiles<BM>(p.offset, p.E);
+  const int nmt = p.tiles ? *p.ntiles : p.offset ? st.total : (int)((p.a_rows + BM - 1) / BM);
   // Tile order: XCD x (workgroup b runs on XCD b % 8) takes one run of the logical tiles.  An expert's
   // row tiles form groups of `group`; inside a group the column tile is the slower index, so that
   // tiles running together on an XCD share both their token rows and their weight rows in its L2
@@ -114,11 +178,17 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Args& p, const int block)
   int e = 0, t0 = 0, R = nmt, mt = T / nct;      // expert, its first row tile, its row tiles
   int32_t seg = 0;
   int64_t all = p.a_rows;                        // its rows
-  if (p.offset) {
+  if (p.tiles) {
     e = p.tiles[2 * mt];
     t0 = mt - p.tiles[2 * mt + 1] / BM;
     seg = p.offset[e];
     all = p.offset[e + 1] - seg;
+    R = (int)((all + BM - 1) / BM);
+  } else if (p.offset) {
+    int n;
+    find_segment<BM>(st, mt, e, t0, seg, n);
+    auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    e = uni(e); t0 = uni(t0); seg = uni(seg); all = uni(n);
     R = (int)((all + BM - 1) / BM);
   }
   const int local = T - t0 * nct, grp = local / (p.group * nct), rem = local - grp * p.group * nct;

@@ -5,7 +5,8 @@
 //   group score = sum of its group_top largest c; the top_groups best groups are kept;
 //   S = k largest c in them (ties to the lower id);  g = scale s_S (/ sum_S s)
 //
-// The logits come from the router's MFMA kernels (route.hip); here one wavefront owns a token.
+// The logits come in partial planes, a K split each, by kernels for few, some and many tokens (here and in route.hip);
+// the selection adds them, one wavefront per token.
 #include <algorithm>
 
 #include "common.h"
@@ -109,7 +110,7 @@ struct SelectArgs {
   ScoreRule rule;
   int32_t* topk_idx;
   float* topk_gate;
-  int32_t* count;        // [E]; with several workgroups block 0 clears it for score_count_kernel
+  int32_t* count;        // [E]; with several workgroups the first clears it for score_count_kernel
   float* logits;
 };
 

@@ -66,20 +66,26 @@ def test_experts_in_a_long_ring(counts, f):
     assert bool((y[other] == 7).all())
 
 
-def test_1024_experts():
-    print("\n[case] expert_ffn fp8 of 1,024 experts", flush=True)
-    counts = [0] * 1024
-    for e, c in ((0, 1), (15, 2), (16, 3), (500, 20), (777, 1), (1023, 5)):
-        counts[e] = c
-    s, q, qs, slot, ring, rs, off, wt = expert_case(counts, 128, 128, 9, 6)
+# a few rows; some hundreds (row tiles found from the offsets); many workgroups (row tiles from a list)
+@pytest.mark.parametrize("rows,f,most", [(32, 128, 20), (330, 128, 70), (1500, 512, 130)])
+def test_1024_experts(rows, f, most):
+    print(f"\n[case] expert_ffn fp8 of 1,024 experts, {rows} rows", flush=True)
+    rng = np.random.default_rng(rows)
+    counts = np.zeros(1024, dtype=int)
+    counts[[0, 15, 16, 500, 1023]] = 1, 2, 3, most, 5
+    np.add.at(counts, rng.integers(0, 1024, rows - most), 1)
+    s, q, qs, slot, ring, rs, off, wt = expert_case(list(counts), 128, f, 9, 6)
     y, _ = experts(s, ring, rs, off, 9, wt)
-    lo = 0
-    for e, c in enumerate(counts):
-        if c:
-            r = slice(lo, lo + c)
+    starts = np.concatenate([[0], np.cumsum(counts)])
+    for e in (0, 1, 15, 16, 63, 64, 499, 500, 501, 777, 1022, 1023):
+        r = slice(starts[e], starts[e + 1])
+        if counts[e]:
             W = [ops.spread_blocks(codes(w[e]), host(sw[e])) for w, sw in wt]
             ffn_within(host(y[slot[r]]), ops.spread_rows(codes(q[r]), host(qs[:, r]).T), W, f"expert {e}")
-        lo += c
+    # every row was written, and nothing else
+    other = torch.ones(s.capacity, dtype=torch.bool, device=DEV)
+    other[slot] = False
+    assert bool((y[other] == 7).all()) and bool(y[slot].isfinite().all()) and bool((y[slot] != 7).any(1).all())
 
 
 def test_norm_of_more_than_2_31_elements():
