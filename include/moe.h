@@ -270,6 +270,8 @@ int moe_decode_noalloc(const moe_shape* shape, const void* x, const float* w_rou
  *   du = g dh a s  (s = sigmoid(a)),   dx_t += W_gate[e]^T da + W_up[e]^T du,
  *   dW_down[e] += g dy_t h^T,  dW_gate[e] += da x_t^T,  dW_up[e] += du x_t^T;
  *   router: dl_j = g_j (dg_j - sum_i g_i dg_i),  dW_r[e_j] += dl_j x_t,  dx_t += dl_j W_r[e_j].
+ * The router part is that of gates renormalised from a softmax, unscaled (moe_route's): gates of
+ * another moe_router rule take moe_backward_experts and moe_route_scored_backward.
  * In:  dy [T,d] bf16; x [T,d] bf16; w_router [E,d]; topk_idx, topk_gate; ring_x,
  *      expert_offset, copy_slot, slot_copy, ring_head from moe_dispatch; saved_au from
  *      moe_expert_ffn; w_gate, w_up, w_down bf16.
@@ -301,6 +303,8 @@ int moe_check_shape(const moe_shape* shape);
  *   dx_t += Q_f(W_gate)^T Q_f(da) + Q_f(W_up)^T Q_f(du)   (weights along f)
  *   dW_down[e] = Q_t(dY_e)^T Q_t(g H_e),  dW_gate[e] = Q_t(dA_e)^T Q_t(X_e),
  *   dW_up[e] = Q_t(dU_e)^T Q_t(X_e)
+ * The router part is moe_backward's, for moe_route's gates: a layer in MXFP8 that routes by
+ * another moe_router rule has no backward.
  * Q_t: along the token axis, each expert's copies in ring-segment order in blocks of 32
  * aligned to the segment's last slot (the first block partial).  dg, da, du, the router
  * gradient and dx's router term as in moe_backward; saved_au from the MXFP8 forward's

@@ -15,7 +15,7 @@ import torch
 
 from ._lib import (DTYPES, MOE_BF16, MOE_F32, MOE_FP8, MOE_MXFP8, OP_BACKWARD, OP_COMBINE,
                    OP_DECODE, OP_DISPATCH, OP_EXPERT_FFN, OP_FORWARD, OP_NORM_BACKWARD, OP_ROUTE,
-                   OP_ROUTE_BACKWARD, SCORES, LIB_PATH, MoeError, MoeRouter, MoeShape, check, lib)
+                   OP_ROUTE_BACKWARD, SCORE_SOFTMAX, SCORES, LIB_PATH, MoeError, MoeRouter, MoeShape, check, lib)
 
 __all__ = ["make_shape", "check_shape", "workspace_bytes", "moe_route", "moe_dispatch", "moe_expert_ffn",
            "moe_expert_ffn_timed",
@@ -438,10 +438,17 @@ class Layer:
     """Buffers of one layer shape, and the forward / backward / decode as chained C calls.
 
     Expert weights are passed per call; for MXFP8 pass their MX codes and scales, for FP8 those of
-    quantize_fp8.  With a `router` (make_router) the layer routes by moe_route_scored."""
+    quantize_fp8.  With a `router` (make_router) the layer routes by moe_route_scored.
+
+    The layer remembers the rule of the last call that routed (route, forward, forward_fused, decode), and a
+    backward of other gates raises ValueError.  A replayed graph's forward is not seen: capture the backward with
+    it, or route eagerly last."""
     shape: MoeShape
     device: torch.device
     bufs: Dict[str, torch.Tensor] = field(default_factory=dict)
+    # the rule that made topk_gate (and, of a router, logits): the bytes of its MoeRouter, b"" for
+    # moe_route's, None as long as no call of this layer has routed
+    routed: Optional[bytes] = None
 
     @classmethod
     def create(cls, T, d, E, k, f, C=None, fs=0, dtype="bf16", device="cuda"):
@@ -462,6 +469,19 @@ class Layer:
         n = max(workspace_bytes(self.shape, op), 256)
         return self._buf(f"ws{op}", (n,), torch.uint8)
 
+    def _check_rule(self, fn, router=None):
+        """Refuse the gradient of gates that another rule than `router` (None: moe_route's) has made."""
+        if self.routed is None:
+            return
+        if router is not None:
+            if bytes(router) != self.routed:
+                raise ValueError(f"{fn}: the tokens were routed by another router, or by none")
+        elif self.routed:
+            r = MoeRouter.from_buffer_copy(self.routed)
+            if r.score != SCORE_SOFTMAX or not r.renormalise or r.scale != 1.0:
+                raise ValueError(f"{fn}: the tokens were routed by a router whose gates have another gradient than moe_route's "
+                                 "(renormalised softmax, scale 1)")
+
     def route(self, x, w_router, b_router=None, router=None, balance=None):
         s = self.shape
         T, k, E = s.tokens, s.top_k, s.experts
@@ -471,10 +491,12 @@ class Layer:
         if router is not None:
             moe_route_scored(s, router, x, w_router, b_router, balance, idx, gate, cnt,
                              self._buf("logits", (T, E), torch.float32), self._ws(OP_ROUTE))
+            self.routed = bytes(router)
             return idx, gate, cnt
         if balance is not None:
             raise ValueError("a balance bias needs a router (make_router)")
         moe_route(s, x, w_router, b_router, idx, gate, cnt, self._ws(OP_ROUTE))
+        self.routed = b""
         return idx, gate, cnt
 
     def add_rmsnorm(self, x, residual, weight, eps=1e-6):
@@ -568,6 +590,7 @@ class Layer:
                     t["topk_gate"], t["expert_count"], t["ring_x"], t["expert_offset"],
                     t["copy_slot"], t["slot_copy"], t["ring_y"], au, t["y"], self._ws(OP_FORWARD),
                     spin_limit)
+        self.routed = b""
         return t["y"]
 
     def forward_status(self) -> int:
@@ -583,10 +606,14 @@ class Layer:
         gate = self._buf("topk_gate", (s.tokens, s.top_k), torch.float32)
         moe_decode(s, x, w_router, b_router, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, y, idx,
                    gate, self._ws(OP_DECODE))
+        self.routed = b""
         return y, idx, gate
 
     def backward_mx(self, dy, x, w_router, w_gu_t, w_gu_t_scale, w_down_t, w_down_t_scale, head=0):
-        """The MXFP8 layer's gradients after forward(..., save_au=True) with the same buffers."""
+        """The MXFP8 layer's gradients after forward(..., save_au=True) with the same buffers.  Its router part is
+        that of moe_route's gates: after a forward with another router (sigmoid or plain softmax scores, a scale) it
+        raises ValueError."""
+        self._check_rule("backward_mx")
         s = self.shape
         b = self.bufs
         dx = self._buf("dx", (s.tokens, s.hidden), torch.bfloat16)
@@ -601,10 +628,11 @@ class Layer:
 
     def backward(self, dy, x, w_router, w_gate, w_up, w_down, head=0, router=None, dlogits=None):
         """Gradients after a forward(..., save_au=True) with the same buffers (and the same
-        `router`; then dlogits is a further gradient of the logits, and the bias's gradient is
-        left in bufs["db_router"]).  After an FP8 forward the weights are the bf16 ones: the
-        tokens are dispatched again in bf16, and the forward's rounding to 8 bits counts as
-        the identity."""
+        `router`, another one raises ValueError; then dlogits is a further gradient of the logits,
+        and the bias's gradient is left in bufs["db_router"]).  After an FP8 forward the weights
+        are the bf16 ones: the tokens are dispatched again in bf16, and the forward's rounding to
+        8 bits counts as the identity."""
+        self._check_rule("backward", router)
         s = self.shape
         b = self.bufs
         ring = b.get("ring_x")
