@@ -109,7 +109,8 @@ typedef struct moe_shape {
  * In:  x [T,d] act (bf16 for MOE_MXFP8), w_router [E,d] f32, b_router [E] f32 or NULL.
  * Out: topk_idx [T,k] int32, ascending expert id per token; topk_gate [T,k] f32;
  *      expert_count [E] int32 = copies routed to each expert.
- * workspace: moe_workspace_bytes(shape, MOE_OP_ROUTE) bytes (router logits).
+ * workspace: moe_workspace_bytes(shape, MOE_OP_ROUTE) bytes, a size that serves moe_route_scored too;
+ * moe_route refuses one only where its own planes of router logits do not fit.
  */
 int moe_route(const moe_shape* shape, const void* x, const float* w_router,
               const float* b_router, int32_t* topk_idx, float* topk_gate,

@@ -133,7 +133,8 @@ int moe_route(const moe_shape* s, const void* x, const float* w_router, const fl
     if (missing_tok(x, T) || !w_router || missing_tok(topk_idx, T) || missing_tok(topk_gate, T) ||
         !expert_count || !workspace)
       return MOE_ERR_NULL;
-    if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_ROUTE)) return MOE_ERR_WORKSPACE;
+    // its own logit planes: MOE_OP_ROUTE's size also covers moe_route_scored, which may keep more of them
+    if (workspace_bytes < align256(moe::route_workspace_bytes(T, s->experts, s->hidden))) return MOE_ERR_WORKSPACE;
     if (s->tokens == 0) return hip_status(zero_words(expert_count, (size_t)s->experts, stream));
     return hip_status(moe::launch_route(x, s->dtype == MOE_F32, w_router, b_router, s->tokens,
                                         s->hidden, s->experts, s->top_k, (float*)workspace,
