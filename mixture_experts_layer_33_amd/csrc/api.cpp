@@ -498,7 +498,7 @@ int moe_add_rmsnorm_backward(const moe_shape* s, const void* dy, const void* dh,
 
 // ------------------------------------------------------------------ scored routing
 namespace {
-// fp32 tokens: one grid dimension holds tiles of 64 of them (65,535 at most).
+// fp32 tokens: the gradient's tiles of 64 of them are one grid dimension (65,536 at most).
 constexpr int64_t SCORED_F32_ROWS = (int64_t)1 << 21;
 
 int check_router(const moe_shape* s, const moe_router* r, moe::ScoreRule* rule) {

@@ -232,26 +232,34 @@ size_t route_workspace_bytes(int64_t T, int E, int d) {
   return logits_bytes(T, E, d);
 }
 
+// A device's grid holds 65,536 tiles in y: more tokens take several launches, whose planes follow one another (so many
+// tokens are one K split, one plane).
+constexpr int64_t GRID_TILES = 65535;
+
 hipError_t launch_router_logits(const void* x, bool x_f32, const float* w_r, int64_t T, int d, int E,
                                 float* logits, int* planes, hipStream_t st) {
   int& ks = *planes;
-  ks = 1;
-  if (x_f32) {
-    dim3 g1((E + RT_N - 1) / RT_N, (unsigned)((T + RT_M - 1) / RT_M));
-    router_logits_kernel<true><<<g1, 256, 0, st>>>(x, w_r, logits, T, d, E);
-  } else {
-    // d % 64 == 0 for bf16 layers
-    ks = router_ksplit(T, E, d);
-    if (router_big(E)) {
-      hipError_t e = hipFuncSetAttribute((const void*)router_mfma2_kernel,
-                                         hipFuncAttributeMaxDynamicSharedMemorySize, R2_LDS);
-      if (e != hipSuccess) return e;
-      router_mfma2_kernel<<<dim3((unsigned)((E + 127) / 128), (unsigned)((T + 127) / 128), (unsigned)ks),
-                            R2_NT, R2_LDS, st>>>((const bf16_t*)x, w_r, logits, T, d, E);
-    } else {
-      router_mfma_kernel<64><<<dim3((unsigned)((E + 63) / 64), (unsigned)((T + 63) / 64), (unsigned)ks),
-                               256, 0, st>>>((const bf16_t*)x, w_r, logits, T, d, E);
-    }
+  ks = x_f32 ? 1 : router_ksplit(T, E, d);   // d % 64 == 0 for bf16 layers
+  const bool big = !x_f32 && router_big(E);
+  const int64_t bm = big ? R2_BM : RT_M;
+  if (big) {
+    hipError_t e = hipFuncSetAttribute((const void*)router_mfma2_kernel,
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, R2_LDS);
+    if (e != hipSuccess) return e;
+  }
+  if (ks > 1 && T > GRID_TILES * bm) return hipErrorInvalidValue;
+  for (int64_t t0 = 0; t0 < T; t0 += GRID_TILES * bm) {
+    const int64_t n = std::min(T - t0, GRID_TILES * bm);
+    const unsigned mt = (unsigned)((n + bm - 1) / bm);
+    float* out = logits + t0 * E;
+    if (x_f32)
+      router_logits_kernel<true><<<dim3((E + RT_N - 1) / RT_N, mt), 256, 0, st>>>((const float*)x + t0 * d, w_r, out, n, d, E);
+    else if (big)
+      router_mfma2_kernel<<<dim3((unsigned)((E + 127) / 128), mt, (unsigned)ks), R2_NT, R2_LDS, st>>>(
+          (const bf16_t*)x + t0 * d, w_r, out, n, d, E);
+    else
+      router_mfma_kernel<64><<<dim3((unsigned)((E + 63) / 64), mt, (unsigned)ks), 256, 0, st>>>(
+          (const bf16_t*)x + t0 * d, w_r, out, n, d, E);
   }
   return hipGetLastError();
 }
