@@ -133,7 +133,7 @@ int moe_route(const moe_shape* shape, const void* x, const float* w_router,
  *      copy_slot [T,k] int32 absolute slot of each copy;
  *      slot_copy [C] int32 copy id t*k+j held by each used slot (other slots untouched).
  * workspace: moe_workspace_bytes(shape, MOE_OP_DISPATCH) bytes.  MOE_FP8: x and ring_x are aligned to
- * 16 bytes, ring_x_scale to 4 (MOE_ERR_ALIGN).
+ * 16 bytes, ring_x_scale to 4 (MOE_ERR_ALIGN); fewer than 2^24 tokens (MOE_ERR_SHAPE).
  */
 int moe_dispatch(const moe_shape* shape, const void* x, const int32_t* topk_idx,
                  int64_t ring_head, void* ring_x, uint8_t* ring_x_scale,
@@ -489,7 +489,7 @@ int moe_backward_experts(const moe_shape* shape, const void* dy, const int32_t* 
  * moe_dispatch_q: moe_dispatch of rows that are 8-bit already (moe_add_rmsnorm's y8): x8 [T,d]
  * codes and x8_scale [d/128][T] (MOE_FP8: f32; MOE_MXFP8: 4 bytes each) are copied into the
  * ring; every other argument as moe_dispatch.  MOE_MXFP8 and MOE_FP8 only (MOE_ERR_DTYPE).
- * x8 and ring_x are aligned to 16 bytes (MOE_ERR_ALIGN).
+ * x8 and ring_x are aligned to 16 bytes (MOE_ERR_ALIGN); fewer than 2^24 tokens (MOE_ERR_SHAPE).
  */
 int moe_dispatch_q(const moe_shape* shape, const uint8_t* x8, const uint8_t* x8_scale,
                    const int32_t* topk_idx, int64_t ring_head, void* ring_x,

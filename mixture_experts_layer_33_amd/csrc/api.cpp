@@ -37,6 +37,9 @@ hipError_t zero_words(void* p, size_t words, hipStream_t st) {
 
 bool bad_dtype(int dt) { return dt != MOE_F32 && dt != MOE_BF16 && dt != MOE_MXFP8 && dt != MOE_FP8; }
 
+// A workgroup of 256 threads per token, and a grid of fewer than 2^32 threads (the 8-bit rows' dispatches).
+constexpr int64_t DISPATCH_ROWS = ((int64_t)1 << 24) - 1;
+
 bool unaligned(const void* p, uintptr_t a = 16) { return (uintptr_t)p % a != 0; }
 
 // Shape checks common to the forward calls.  K-dimension multiples follow the
@@ -158,6 +161,7 @@ int moe_dispatch(const moe_shape* s, const void* x, const int32_t* topk_idx, int
     if (s->dtype == MOE_FP8 && (unaligned(x) || unaligned(ring_x) || unaligned(ring_x_scale, 4)))
       return MOE_ERR_ALIGN;
     if (ring_head < 0 || ring_head >= s->capacity) return MOE_ERR_SHAPE;
+    if (s->dtype == MOE_FP8 && s->tokens > DISPATCH_ROWS) return MOE_ERR_SHAPE;
     if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_DISPATCH)) return MOE_ERR_WORKSPACE;
     if (s->tokens == 0)   // no copies: every expert's segment is empty
       return hip_status(zero_words(expert_offset, (size_t)s->experts + 1, stream));
@@ -627,7 +631,7 @@ int moe_dispatch_q(const moe_shape* s, const uint8_t* x8, const uint8_t* x8_scal
       return MOE_ERR_NULL;
     if (unaligned(x8) || unaligned(ring_x) || unaligned(x8_scale, 4) || unaligned(ring_x_scale, 4))
       return MOE_ERR_ALIGN;
-    if (ring_head < 0 || ring_head >= s->capacity) return MOE_ERR_SHAPE;
+    if (ring_head < 0 || ring_head >= s->capacity || T > DISPATCH_ROWS) return MOE_ERR_SHAPE;
     if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_DISPATCH)) return MOE_ERR_WORKSPACE;
     if (T == 0) return hip_status(zero_words(expert_offset, (size_t)s->experts + 1, stream));
     return hip_status(moe::launch_dispatch(

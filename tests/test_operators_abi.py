@@ -263,3 +263,14 @@ def test_host_code_under_address_sanitizer(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120,
                        env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0:halt_on_error=1"))
     assert r.returncode == 0 and "ok: 0 failure(s)" in r.stdout and "AddressSanitizer" not in r.stderr, r.stdout + r.stderr
+
+
+def test_dispatch_of_more_tokens_than_a_grid_holds():
+    """A workgroup of 256 threads per token, fewer than 2^32 threads: up to 2^24 - 1 tokens."""
+    for ty in ("fp8", "mxfp8"):
+        for T, want in ((1 << 24, _lib.MOE_ERR_SHAPE), ((1 << 24) - 1, _lib.MOE_ERR_WORKSPACE)):
+            s = shape(ty, T=T, d=128, f=128, k=1, C=T)
+            assert L().moe_check_shape(s) == _lib.MOE_OK
+            assert L().moe_dispatch_q(s, FAKE, FAKE, FAKE, 0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0, None) == want
+            if ty == "fp8":
+                assert L().moe_dispatch(s, FAKE, FAKE, 0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0, None) == want
