@@ -502,7 +502,8 @@ int moe_dispatch_q(const moe_shape* shape, const uint8_t* x8, const uint8_t* x8_
  * scales, scale = max(amax, 2^-100) / 448 per block, code = RNE_E4M3(v / scale) (a block that
  * holds an infinity or a NaN: scale NaN).  row_block 1: one block per row and 128
  * columns, scales [cols/128][rows]; row_block 128: one per 128 x 128, the last block of
- * rows may be short, scales [ceil(rows/128)][cols/128].  At most 2^37 elements.  src and codes are aligned to 16
+ * rows may be short, scales [ceil(rows/128)][cols/128].  At most 2^37 elements, and
+ * with row_block 128 fewer than 2^24 blocks (MOE_ERR_SHAPE).  src and codes are aligned to 16
  * bytes (MOE_ERR_ALIGN).
  */
 int moe_quantize_fp8(const void* src_bf16, int64_t rows, int64_t cols, int row_block,

@@ -648,6 +648,8 @@ int moe_quantize_fp8(const void* src_bf16, int64_t rows, int64_t cols, int row_b
   try {
     if (row_block != 1 && row_block != 128) return MOE_ERR_SHAPE;
     if (rows < 0 || cols <= 0 || cols % 128 || rows > ((int64_t)1 << 37) / cols) return MOE_ERR_SHAPE;
+    // a workgroup of 256 threads per block of 128 x 128, and a grid of fewer than 2^32 threads
+    if (row_block == 128 && (rows + 127) / 128 * (cols / 128) >= (int64_t)1 << 24) return MOE_ERR_SHAPE;
     if (rows == 0) return MOE_OK;
     if (!src_bf16 || !codes || !scales) return MOE_ERR_NULL;
     if (unaligned(src_bf16) || unaligned(codes) || unaligned(scales, 4)) return MOE_ERR_ALIGN;

@@ -274,3 +274,12 @@ def test_dispatch_of_more_tokens_than_a_grid_holds():
             assert L().moe_dispatch_q(s, FAKE, FAKE, FAKE, 0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0, None) == want
             if ty == "fp8":
                 assert L().moe_dispatch(s, FAKE, FAKE, 0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0, None) == want
+
+
+def test_quantise_more_blocks_than_a_grid_holds():
+    """A workgroup of 256 threads per block of 128 x 128, fewer than 2^32 threads; a short last block of rows counts whole."""
+    q = L().moe_quantize_fp8
+    assert q(FAKE, 1, 1 << 31, 128, FAKE, FAKE, None) == _lib.MOE_ERR_SHAPE
+    assert q(FAKE, 129, 1 << 30, 128, FAKE, FAKE, None) == _lib.MOE_ERR_SHAPE
+    assert q(FAKE, 1, (1 << 31) - 128, 128, ODD, FAKE, None) == _lib.MOE_ERR_ALIGN
+    assert q(FAKE, 1, 1 << 31, 1, ODD, FAKE, None) == _lib.MOE_ERR_ALIGN       # rows: a bounded grid takes them in turn
