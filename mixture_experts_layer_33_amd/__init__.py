@@ -399,14 +399,17 @@ def quantize_fp8(src: torch.Tensor, row_block: int = 128, stream=None):
     rows = math.prod(src.shape[:-1])
     if row_block == 128 and src.dim() > 2 and src.shape[-2] % 128:
         raise ValueError("the rows of each matrix of a stack must be a multiple of 128")
-    codes = torch.empty(src.shape, dtype=torch.uint8, device=dev)
     if row_block == 1:
         shape = (cols // 128, rows)
     elif src.dim() > 2:
         shape = (*src.shape[:-2], src.shape[-2] // 128, cols // 128)
     else:
         shape = (-(-rows // 128), cols // 128)
-    scales = torch.empty(shape, dtype=torch.float32, device=dev)
+    # memory of the stream that writes it: a block that the current stream has freed may still be
+    # written by what runs there
+    with torch.cuda.stream(stream):
+        codes = torch.empty(src.shape, dtype=torch.uint8, device=dev)
+        scales = torch.empty(shape, dtype=torch.float32, device=dev)
     at = src.get_device()
     p = _a("src", src, torch.bfloat16, src.shape, at)
     _on(at, stream, "moe_quantize_fp8", lib().moe_quantize_fp8, p, rows, cols, row_block, codes.data_ptr(), scales.data_ptr())

@@ -527,3 +527,23 @@ def test_fp8_workload_size_smoke():
             W = [ops.spread_blocks(codes(w[e]), host(sw[e])) for w, sw in wt]
             ffn_within(host(y[slot[m]])[None], X[r:r + 1], W, f"row {m}")
     assert math.isfinite(float(y[slot].float().abs().max()))
+
+
+def test_quantise_on_another_stream_than_the_current_one():
+    """The outputs are not memory that the current stream has freed and still has to write."""
+    print("\n[case] quantize_fp8 beside a busy current stream", flush=True)
+    M, K = 2048, 2048
+    src = randn(gen(3), M, K, dtype=BF)
+    want = [(r, moe.quantize_fp8(src, r)) for r in (1, 128)]
+    busy, side = torch.empty(1 << 30, dtype=torch.uint8, device=DEV), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for r, (codes_, scales_) in want:
+        gone = [torch.empty_like(codes_), torch.empty_like(scales_)]
+        for i in range(20):
+            busy.fill_(i)                 # some milliseconds in front of the last writes
+        for t in gone:
+            t.fill_(7)
+        del t, gone
+        q, s = moe.quantize_fp8(src, r, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(q, codes_) and torch.equal(s, scales_)
