@@ -1086,6 +1086,9 @@ static int dw_splits(bool f32, int64_t T, int E, int d) {
   return best;
 }
 
+// One launch, without a workspace (score_bwd_few_kernel).
+static bool bwd_few(bool f32, int64_t T) { return !f32 && T <= 16; }
+
 struct ScoreBwdLayout {
   size_t dl, low, wt, zero, dw, db, total;
   int64_t Tp;
@@ -1093,17 +1096,21 @@ struct ScoreBwdLayout {
 };
 static ScoreBwdLayout score_bwd_layout(bool f32, int64_t T, int E, int d) {
   auto al = [](size_t b) { return (b + 255) & ~(size_t)255; };
-  ScoreBwdLayout L;
+  ScoreBwdLayout L{};
   L.Ep = (E + 63) / 64 * 64;
   L.Tp = f32 ? T : (T + DW_K - 1) / DW_K * DW_K;
   L.Z = dw_splits(f32, T, E, d);
   L.G = (int)((L.Tp + 4 * DL_TW - 1) / (4 * DL_TW));
   size_t o = 0;
+  if (bwd_few(f32, T)) {   // keeps nothing: the least a call asks for
+    L.total = 256;
+    return L;
+  }
   L.dl = o; o += al(f32 ? (size_t)T * E * 4 : (size_t)L.Tp * 2 * L.Ep * 2);
   L.low = o; o += f32 ? 0 : al((size_t)L.Tp * L.Ep * 2);
   L.wt = o; o += f32 ? 0 : al((size_t)d * 2 * L.Ep * 2);
   L.zero = o; o += 1024;
-  L.dw = o; o += al((size_t)L.Z * E * d * 4);
+  L.dw = o; o += L.Z > 1 ? al((size_t)L.Z * E * d * 4) : 0;   // one split writes dW_r itself
   L.db = o; o += al((size_t)L.G * E * 4);
   L.total = o;
   return L;
@@ -1125,7 +1132,7 @@ hipError_t launch_route_scored_bwd(bool f32, const ScoreRule& rule, const float*
                  (bf16_t*)(w + L.dl), (bf16_t*)(w + L.low), (uint32_t*)(w + L.zero),
                  w_r, (bf16_t*)(w + L.wt), d, L.G, db ? dbp : nullptr};
   const int vpl = (E + 63) / 64;
-  if (!f32 && T <= 16) {
+  if (bwd_few(f32, T)) {
 #define FEW(V, N)                                                                                                \
   {                                                                                                             \
     hipError_t e_ = hipFuncSetAttribute((const void*)score_bwd_few_kernel<V, N>,                                 \

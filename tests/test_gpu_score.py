@@ -378,3 +378,24 @@ def test_side_stream_graph_and_repeats(T, d):
         both()
         torch.cuda.synchronize()
         assert all(same_bits(a, b) for a, b in zip(got, (*out, dx, dw, db)))
+
+
+@pytest.mark.parametrize("case", [("bf16", 1, 128, 64, 4), ("bf16", 16, 256, 500, 8), ("bf16", 17, 256, 500, 8), ("bf16", 4100, 256, 72, 4),
+                                  ("f32", 30, 64, 20, 3), ("f32", 3000, 64, 20, 3)], ids=str)
+def test_backward_keeps_to_its_workspace(case):
+    dtype, T, d, E, k = case
+    print(f"\n[case] route_scored backward workspace {case}", flush=True)
+    rule = R("sigmoid", renormalise=False)
+    x, w, _, _, _ = draw(dtype, T, d, E, k, rule, 8, False)
+    s, idx, gate, _, logits = run(dtype, x, w, None, None, k, rule)
+    dg = randn(gen(2), T, k)
+    n = moe.workspace_bytes(s, moe.OP_ROUTE_BACKWARD)
+    outs = []
+    for fill in (0, 255):
+        buf = torch.full((n + 65536,), fill, dtype=torch.uint8, device=DEV)
+        dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(E, device=DEV)
+        moe.moe_route_scored_backward(s, make(rule), dg, None, x, w, logits, idx, None, dx, dw, db, buf[:n])
+        torch.cuda.synchronize()
+        assert (buf[n:] == fill).all()
+        outs.append((dx, dw, db))
+    assert all(same_bits(a, b) for a, b in zip(*outs))

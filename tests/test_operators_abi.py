@@ -283,3 +283,15 @@ def test_quantise_more_blocks_than_a_grid_holds():
     assert q(FAKE, 129, 1 << 30, 128, FAKE, FAKE, None) == _lib.MOE_ERR_SHAPE
     assert q(FAKE, 1, (1 << 31) - 128, 128, ODD, FAKE, None) == _lib.MOE_ERR_ALIGN
     assert q(FAKE, 1, 1 << 31, 1, ODD, FAKE, None) == _lib.MOE_ERR_ALIGN       # rows: a bounded grid takes them in turn
+
+
+def test_route_backward_asks_for_what_it_uses():
+    """Up to 16 bf16 tokens nothing is kept (256 bytes are asked for all the same); one split of dW_r has no planes."""
+    def need(dtype, T):
+        return moe.workspace_bytes(shape(dtype, T=T, d=7168, E=512, k=8), moe.OP_ROUTE_BACKWARD)
+    for ty in ("bf16", "fp8", "mxfp8"):
+        assert [need(ty, T) for T in (1, 4, 5, 16)] == [256] * 4
+        turned, plane = 7168 * 2 * 512 * 2, 512 * 7168 * 4      # W_r's parts; a plane of dW_r
+        assert turned < need(ty, 17) < turned + (1 << 20) < turned + plane
+        assert need(ty, 8192) >= turned + plane
+    assert need("f32", 1) < 1 << 20 and need("f32", 0) == need("bf16", 0) == 0
