@@ -547,3 +547,24 @@ def test_quantise_on_another_stream_than_the_current_one():
         q, s = moe.quantize_fp8(src, r, stream=side)
         torch.cuda.synchronize()
         assert torch.equal(q, codes_) and torch.equal(s, scales_)
+
+
+@pytest.mark.parametrize("M,K", [(1, 512), (16, 512), (40, 512), (200, 512), (600, 512), (16, 8192), (200, 8192)])
+def test_bf16_matmul_keeps_rows_apart(M, K):
+    """As with the fp32 output, on the 8-bit matrix instruction, and through the joined planes of a split K."""
+    print(f"\n[case] matmul_fp8 scales, bf16 {M}x{K}", flush=True)
+    N = 384
+    assert (moe.matmul_fp8_workspace(M, N, K, DEV) is not None) == (K == 8192)
+    a, sa, w, sw = operands(M, N, K, 4)
+    sa = sa * 2.0 ** ((torch.arange(M, device=DEV) % 5) * 10 - 20)[None]
+    sw = sw * 2.0 ** ((torch.arange(3, device=DEV) % 3) * 20 - 20)[:, None]
+    out = matmul(a, sa, w, sw, BF)
+    check_product(out, a, sa, w, sw)
+    sa2, sw2 = sa.clone(), sw.clone()
+    sa2[1, M // 2] = float("nan")
+    out2 = matmul(a, sa2, w, sw, BF)
+    rest = [m for m in range(M) if m != M // 2]
+    assert torch.isnan(out2[M // 2]).all() and same_bits(out2[rest], out[rest])
+    sw2[1, 2] = float("nan")
+    out3 = matmul(a, sa, w, sw2, BF)
+    assert torch.isnan(out3[:, 128:256]).all() and same_bits(out3[:, :128], out[:, :128]) and same_bits(out3[:, 256:], out[:, 256:])

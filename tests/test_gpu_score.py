@@ -399,3 +399,23 @@ def test_backward_keeps_to_its_workspace(case):
         assert (buf[n:] == fill).all()
         outs.append((dx, dw, db))
     assert all(same_bits(a, b) for a, b in zip(*outs))
+
+
+def test_balance_masks_inside_groups():
+    """A balance of -inf leaves group 0 and one expert of group 1: every group but the first then scores -inf (group 1
+    for want of a second), the tie goes to the lower id, and the choice is of the experts that are left.  With as many
+    experts left as are chosen, the choice is theirs whatever the logits."""
+    E, inf = 16, float("inf")
+    for rule in (R("sigmoid", 4, 2, 2), R("softmax", 4, 2, 2, False), R("sigmoid", 4, 2, 1)):
+        for k, left in ((3, 5), (5, 5), (2, 5)):
+            print(f"\n[case] route_scored balance masks {rule} k={k}", flush=True)
+            x, w, _, _, l = draw("bf16", 12, 64, E, k, rule, 3, False)
+            bal = torch.zeros(E, device=DEV)
+            bal[left:] = -inf
+            _, idx, gate, cnt, _ = run("bf16", x, w, None, bal, k, rule)
+            assert (idx < left).all() and (idx[:, 1:] > idx[:, :-1]).all() and int(cnt[:left].sum()) == 12 * k and (cnt[left:] == 0).all()
+            want = ops.choose(l, rule, k, host(bal))
+            assert np.array_equal(idx.cpu().numpy(), want)
+            g = ops.gates(l, want, rule)
+            within(host(gate), g, abs(g) * 2.0 ** -12, "gates")
+            assert (gate > 0).all()
