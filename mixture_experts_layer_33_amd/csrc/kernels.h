@@ -44,8 +44,6 @@ size_t norm_bwd_workspace_bytes(int64_t T, int d);
 hipError_t launch_rmsnorm_bwd(bool f32, const void* dy, const void* dh, const void* h, const float* w,
                               const float* rstd, int64_t T, int d, void* dx, float* dw, float* part,
                               hipStream_t st);
-// out[c] = sum over g < G of part[g, c], c < d
-hipError_t launch_column_sum(const float* part, int G, int64_t d, float* out, hipStream_t st);
 
 // dispatch.  Rows as they are (elem_bytes 4, 2), bf16 rows quantised to MX or FP8, or 8-bit
 // rows with their scale words x_scale [d/128][T] as they are
@@ -63,9 +61,8 @@ size_t matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w,
                              const float* w_scale, int64_t M, int64_t N, int64_t K, bool f32_out,
                              void* out, void* ws, hipStream_t st);
-// out = round(add + A W^T) of bf16 rows (the tile of the FP8 products)
-struct Fp8Args;
-int tile_add_height(int64_t M, int64_t N, int64_t K);   // in 64 rows
+// height of the tiles of a product of M rows that the FP8 products' tile computes (the router gradient's dx), in 64 rows
+int tile_add_height(int64_t M, int64_t N, int64_t K);
 size_t ffn_fp8_workspace_bytes(int64_t n, int64_t C, int d, int E, int f);
 hipError_t launch_ffn_fp8(const void* ring_x, const float* ring_x_scale, const int32_t* expert_offset,
                           int64_t head, int64_t C, int64_t n, int d, int E, int f,

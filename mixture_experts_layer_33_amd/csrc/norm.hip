@@ -387,7 +387,7 @@ __global__ __launch_bounds__(32 * CS) void column_sum_kernel(const float* __rest
   }
 }
 
-hipError_t launch_column_sum(const float* part, int G, int64_t d, float* out, hipStream_t st) {
+static hipError_t launch_column_sum(const float* part, int G, int64_t d, float* out, hipStream_t st) {
   column_sum_kernel<<<(unsigned)((d + 31) / 32), 32 * CS, 0, st>>>(part, G, d, out);
   return hipGetLastError();
 }
