@@ -108,9 +108,6 @@ __device__ __forceinline__ void find_segment(const SegmentTiles& s, int mt, int&
 __device__ __forceinline__ i32x8 fp8_join(u32x4 a, u32x4 b) {
   return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
-__device__ __forceinline__ i32x8 fp8_frag(const uint8_t* p) {
-  return fp8_join(*(const u32x4*)p, *(const u32x4*)(p + 16));
-}
 __device__ __forceinline__ f32x4 fp8_mfma16(i32x8 w, i32x8 a) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
