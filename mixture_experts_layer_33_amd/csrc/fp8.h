@@ -58,12 +58,17 @@ __device__ __forceinline__ u32x2 fp8_encode8(const float (&v)[8], float s) {
   return u32x2{fp8_encode4(v[0], v[1], v[2], v[3], s), fp8_encode4(v[4], v[5], v[6], v[7], s)};
 }
 
-// H's codes: times the scale's reciprocal, which may take a value that lies within the last bit of a
-// rounding border to its other side.  H stays inside the experts' products, and a division per
-// value would cost a gate/up tile's epilogue some ten instructions where one will do.
+// H's codes: the same quotient, from the scale's rounded reciprocal r and one correction by the exact remainder of v r
+// (Markstein's theorem: the result is the rounded v / s).  As plain divisions, some ten instructions each, a
+// gate/up tile's epilogue took 6 % of a call (4,096 rows over 16 experts, d 1024, f 2048: 150 -> 159 us; so 145), and v r
+// alone takes values that lie within a last bit of a rounding border to its other side.
 __device__ __forceinline__ uint32_t h_encode4(float a, float b, float c, float d, float s) {
   const float r = 1.0f / s;
-  auto q = [r](float v) { return __builtin_amdgcn_fmed3f(v * r, -FP8_MAX, FP8_MAX); };
+  auto quotient = [r, s](float v) {
+    const float q = v * r;
+    return fmaf(fmaf(-q, s, v), r, q);
+  };
+  auto q = [&](float v) { return __builtin_amdgcn_fmed3f(quotient(v), -FP8_MAX, FP8_MAX); };
   const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q(a), q(b), 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q(c), q(d), lo, true);
 }

@@ -568,3 +568,43 @@ def test_bf16_matmul_keeps_rows_apart(M, K):
     sw2[1, 2] = float("nan")
     out3 = matmul(a, sa, w, sw2, BF)
     assert torch.isnan(out3[:, 128:256]).all() and same_bits(out3[:, :128], out[:, :128]) and same_bits(out3[:, 256:], out[:, 256:])
+
+
+@pytest.mark.parametrize("save", [False, True])
+@pytest.mark.parametrize("M", [3, 64, 4000])
+def test_codes_of_h_are_those_of_the_quotient(M, save):
+    """H = RNE_E4M3(h / scale) bit for bit where h / scale is next to a tie.  One product per sum, gates large enough that
+    silu(a) = a, and W_down = identity: every step up to the quotient is one fp32 rounding, and the output is code times scale,
+    rounded.  The ratios to the row's maximum are ties (21, 25, 27 / 16 times a power of two), which the rounded
+    scale moves by a last bit."""
+    print(f"\n[case] expert_ffn fp8 codes of h, {M} rows save={save}", flush=True)
+    F = np.float32
+    d = f = 128
+    C = M + 5
+    cg, cu = np.ones(f, F), np.ones(f, F)
+    for i in range(f - 1):
+        cg[i], cu[i] = ((1.5, 0.875), (1.25, 1.25), (1.5, 1.125))[i % 3]
+        cu[i] *= 2.0 ** (i % 12 - 6)
+    cu[f - 1] = 448
+    as_codes = lambda v: torch.from_numpy(v).to(DEV).to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
+    wg, wu = np.zeros((1, f, d), F), np.zeros((1, f, d), F)
+    wg[0, :, 0], wu[0, :, 0] = cg, cu
+    sg, su = F(64), F(0.7)
+    sx = np.random.default_rng(4).uniform(1, 2, C).astype(F)
+    ring = torch.zeros(C, d, dtype=torch.uint8, device=DEV)
+    ring[:, 0] = 0x38                                     # 1.0
+    one = lambda s: torch.full((1, 1, 1), float(s), device=DEV)  # noqa: E731
+    s = moe.make_shape(M, d, 1, 1, f, C=C, dtype="fp8")
+    off = torch.tensor([0, M], dtype=torch.int32, device=DEV)
+    wt = [(as_codes(wg), one(sg)), (as_codes(wu), one(su)), (as_codes(np.eye(d, dtype=F)[None]), one(1))]
+    head = 3
+    y, _ = experts(s, ring, torch.from_numpy(sx[None]).to(DEV), off, head, wt, save)
+    slot = (head + np.arange(M)) % C
+    a, u = cg * (sx[slot] * sg)[:, None], cu * (sx[slot] * su)[:, None]
+    h = a * u
+    scale = h.max(1, keepdims=True) / F(448)
+    q = h / scale
+    assert h.dtype == scale.dtype == q.dtype == F and (a > 32).all()
+    assert (ops.e4m3(q) != ops.e4m3(h * (F(1) / scale))).any()     # a reciprocal takes some to the other side
+    want = torch.from_numpy(ops.e4m3(q).astype(F) * scale).bfloat16()
+    assert same_bits(y[torch.from_numpy(slot).to(DEV)].cpu(), want)
