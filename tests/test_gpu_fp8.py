@@ -608,3 +608,27 @@ def test_codes_of_h_are_those_of_the_quotient(M, save):
     assert (ops.e4m3(q) != ops.e4m3(h * (F(1) / scale))).any()     # a reciprocal takes some to the other side
     want = torch.from_numpy(ops.e4m3(q).astype(F) * scale).bfloat16()
     assert same_bits(y[torch.from_numpy(slot).to(DEV)].cpu(), want)
+
+
+@pytest.mark.parametrize("M", [1, 5, 40])
+def test_gate_and_up_sums_of_few_rows_are_fp32(M):
+    """Products that cancel, of 448 x 448 and of 1 x 1 in the same eights: A and U are what the small ones leave, exactly (every
+    sum on the way is a whole number below 2^24), where sums on a grid of 2^-13 of the large ones would lose them."""
+    print(f"\n[case] expert_ffn fp8 cancelling products, {M} rows", flush=True)
+    d, f = 256, 128
+    x, w = np.ones((M, d)), np.zeros((1, f, d))
+    r = np.random.default_rng(M)
+    for c in range(0, d, 16):                        # +L among eight positions, -L among the eight behind
+        x[:, c] = x[:, c + 8] = 448
+        w[0, :, c], w[0, :, c + 8] = 448, -448
+        w[0, :, c + 1:c + 8] = r.integers(-1, 2, size=(f, 7))
+    e4 = lambda v: torch.from_numpy(v).to(DEV, torch.float32).to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
+    ring = torch.zeros(M + 2, d, dtype=torch.uint8, device=DEV)
+    ring[:M] = e4(x)
+    s = moe.make_shape(M, d, 1, 1, f, C=M + 2, dtype="fp8")
+    one = torch.ones(1, 1, d // 128, device=DEV)
+    wt = [(e4(w), one), (e4(w[:, ::-1].copy()), one), (e4(np.zeros((1, d, f))), torch.ones(1, d // 128, 1, device=DEV))]
+    y, au = experts(s, ring, torch.ones(d // 128, M + 2, device=DEV), torch.tensor([0, M], dtype=torch.int32, device=DEV), 0, wt, True)
+    A = x @ w[0].T
+    assert abs(A).max() <= 112 and (abs(A) > 8).any()        # whole numbers that bf16 holds
+    assert np.array_equal(host(au[:M]), np.concatenate([A, A[:, ::-1]], axis=1))
