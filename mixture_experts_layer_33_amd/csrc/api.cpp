@@ -194,7 +194,7 @@ int moe_expert_ffn_timed(const moe_shape* s, const void* ring_x, const uint8_t* 
         (unaligned(ring_x) || unaligned(w_gate) || unaligned(w_up) || unaligned(w_down) ||
          unaligned(ring_y) || unaligned(saved_au) || unaligned(workspace) ||
          unaligned(ring_x_scale, 4) || unaligned(w_gate_scale, 4) || unaligned(w_up_scale, 4) ||
-         unaligned(w_down_scale, 4)))
+         unaligned(w_down_scale, 4) || unaligned(expert_offset, 4)))
       return MOE_ERR_ALIGN;
     if (ring_head < 0 || ring_head >= s->capacity) return MOE_ERR_SHAPE;
     if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_EXPERT_FFN)) return MOE_ERR_WORKSPACE;

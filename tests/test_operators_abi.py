@@ -295,3 +295,8 @@ def test_route_backward_asks_for_what_it_uses():
         assert turned < need(ty, 17) < turned + (1 << 20) < turned + plane
         assert need(ty, 8192) >= turned + plane
     assert need("f32", 1) < 1 << 20 and need("f32", 0) == need("bf16", 0) == 0
+
+
+def test_fp8_experts_refuse_misaligned_offsets():
+    s = shape("fp8")
+    assert L().moe_expert_ffn(s, FAKE, FAKE, FAKE + 2, 0, *([FAKE] * 7), None, FAKE, 1 << 30, None) == _lib.MOE_ERR_ALIGN
