@@ -129,8 +129,9 @@ template <int KIND, int W, int S>
 __global__ __launch_bounds__(64 * W) void fp8_thin_kernel(Fp8Args p) {
   using SL = ThinStage<W, S>;
   constexpr bool SWIGLU = KIND >= FP8_SWIGLU;
-  // fp32 sums (one token's experts, 8 of 64, d 7168, f 2048: 60.3 us against 59.2; its output's error 1.66e-3, that of its
-  // rounding, against 1.9e-3 to 2.3e-3)
+  // fp32 sums for the gate and up products (one token's experts, 8 of 64, d 7168, f 2048: 60.3 us a call against 59.2, 8 experts x
+  // 8 rows, d 2048, f 768, weights in the caches: 17.8 against 16.2; the output's error 1.66e-3, that of its rounding,
+  // against 1.9e-3 to 2.3e-3)
   constexpr bool WIDE = KIND == FP8_F32 || SWIGLU;
   constexpr int L = SL::L, COLS = SWIGLU ? 16 * W : 32 * W;
   static_assert(!SWIGLU || W == 4, "half a block of H");
