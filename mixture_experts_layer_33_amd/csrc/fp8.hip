@@ -109,7 +109,7 @@ __device__ __forceinline__ void wait_stages(int n) {
 
 // Few token rows: a weight stream.  16 token rows x 32 W weight rows, W wavefronts, each with 32 weight rows
 // (SWIGLU: 16 gate and the matching 16 up rows, W = 4: 64 columns a workgroup, half a block of H, so that twice
-// the workgroups fill the chip; h leaves in fp32 for quantise_h_kernel: 46 -> 36 us for the gate and up
+// the workgroups fill the chip; h leaves in fp32 for quantise_h_kernel: 46 -> 37 us for the gate and up
 // products of one token, 8 of 64 experts, d 7168, f 2048).  The work is one pass over the weights, so what counts is bytes in flight: S stages
 // of whole 128-byte lines are copied global -> LDS, S - 1 of them ahead.  The same stream read straight
 // into registers in the MFMA's layout asks for each line in halves by 16 rows and ran at 3.7 TB/s where
