@@ -44,6 +44,12 @@
  *     multiples of 128.  Scale arguments typed uint8_t* take the address of these floats.
  *     moe_route, moe_dispatch, moe_expert_ffn and moe_combine take MOE_FP8; so do the
  *     calls below that say so.
+ *   - With MOE_MXFP4 the expert weights are E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ *     negatives), two a byte, the even column in the low half: a matrix [rows, cols] is [rows, cols/2]
+ *     bytes, with one E8M0 byte per 32 columns in the MX scale layout above.  Everything else is as
+ *     with MOE_MXFP8: bf16 router and tokens, ring_x and H in MX E4M3.  d and f are multiples of 128.
+ *     moe_route, moe_route_scored, moe_add_rmsnorm, moe_dispatch, moe_dispatch_q, moe_expert_ffn
+ *     (saved_au NULL) and moe_combine take it, and moe_decode_mxfp4; it has no backward.
  *   - The caller owns every buffer.  The library allocates nothing, keeps no
  *     pointer after return, and only enqueues work on `stream`: there is no
  *     host synchronisation and no device-to-host copy inside any call.
@@ -81,7 +87,7 @@ enum moe_status {
   MOE_ERR_ALIGN = 8       /* a tensor is not aligned to 16 bytes (calls that say so) */
 };
 
-enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP8 = 2, MOE_FP8 = 3 };
+enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP8 = 2, MOE_FP8 = 3, MOE_MXFP4 = 4 };
 
 enum moe_op {
   MOE_OP_ROUTE = 0, MOE_OP_DISPATCH = 1, MOE_OP_EXPERT_FFN = 2,
@@ -124,15 +130,15 @@ int moe_route(const moe_shape* shape, const void* x, const float* w_router,
  *   slot = (ring_head + rank(c)) mod C,
  * where rank orders copies by (expert, token): segments are expert-contiguous
  * and hold their tokens in ascending order.
- * In:  x [T,d] act (bf16 for MOE_MXFP8 and MOE_FP8), topk_idx [T,k], ring_head in [0, C).
- * Out: ring_x [C,d] act (MOE_MXFP8, MOE_FP8: E4M3 codes, each row quantised along d)
+ * In:  x [T,d] act (bf16 for the 8-bit and 4-bit layers), topk_idx [T,k], ring_head in [0, C).
+ * Out: ring_x [C,d] act (MOE_MXFP8, MOE_MXFP4, MOE_FP8: E4M3 codes, each row quantised along d)
  *        — only the T*k used slots are written;
- *      ring_x_scale [d/128][C][4] E8M0 bytes (MOE_MXFP8), [d/128][C] f32 (MOE_FP8: codes and
+ *      ring_x_scale [d/128][C][4] E8M0 bytes (MOE_MXFP8, MOE_MXFP4), [d/128][C] f32 (MOE_FP8: codes and
  *      scales of moe_quantize_fp8 with row_block 1), else NULL;
  *      expert_offset [E+1] int32, segment starts relative to the head (offset[E] = T*k);
  *      copy_slot [T,k] int32 absolute slot of each copy;
  *      slot_copy [C] int32 copy id t*k+j held by each used slot (other slots untouched).
- * workspace: moe_workspace_bytes(shape, MOE_OP_DISPATCH) bytes.  MOE_FP8: x and ring_x are aligned to
+ * workspace: moe_workspace_bytes(shape, MOE_OP_DISPATCH) bytes.  MOE_FP8, MOE_MXFP4: x and ring_x are aligned to
  * 16 bytes, ring_x_scale to 4 (MOE_ERR_ALIGN); fewer than 2^24 tokens (MOE_ERR_SHAPE).
  */
 int moe_dispatch(const moe_shape* shape, const void* x, const int32_t* topk_idx,
@@ -148,6 +154,8 @@ int moe_dispatch(const moe_shape* shape, const void* x, const int32_t* topk_idx,
  * H is bf16 (fp32 for MOE_F32; 8-bit along f for MOE_MXFP8 and MOE_FP8) and lives in the workspace.
  * MOE_FP8: a block of 128's sum comes from the 8-bit matrix instruction, to 2^-13 of the largest of every eight products
  * (few rows: the gate and up products have fp32 sums); code = RNE_E4M3(h / scale) as in moe_quantize_fp8.
+ * MOE_MXFP4: as MOE_MXFP8 with 4-bit weights (the 8-bit by 4-bit matrix instruction; its sums differ from the 8-bit
+ * one's in the last bits).
  * In:  ring_x (+ ring_x_scale), expert_offset, ring_head; w_gate, w_up [E,f,d] and
  *      w_down [E,d,f] act, or E4M3 codes with w_gate_scale/w_up_scale [d/128][E*f][4]
  *      and w_down_scale [f/128][E*d][4] for MOE_MXFP8, as moe_quantize_mx writes them for
@@ -157,7 +165,7 @@ int moe_dispatch(const moe_shape* shape, const void* x, const int32_t* topk_idx,
  *      saved_au [C,2f] bf16 (A then U per slot) when not NULL — the backward's input
  *      (MOE_BF16, MOE_MXFP8 and MOE_FP8: the gate/up fp32 accumulations rounded to bf16; NULL
  *      for MOE_F32).
- * workspace: moe_workspace_bytes(shape, MOE_OP_EXPERT_FFN) bytes.  MOE_FP8: tensors and workspace
+ * workspace: moe_workspace_bytes(shape, MOE_OP_EXPERT_FFN) bytes.  MOE_FP8, MOE_MXFP4: tensors and workspace
  * are aligned to 16 bytes, scales and offsets to 4 (MOE_ERR_ALIGN).
  */
 int moe_expert_ffn(const moe_shape* shape, const void* ring_x, const uint8_t* ring_x_scale,
@@ -381,12 +389,12 @@ int moe_quantize_mx_both(const void* src_bf16, int64_t batch, int64_t rows, int6
  * Out: h [T,d] act or NULL (may be x or residual itself: each element is read before it is
  *      written); y [T,d] act or NULL; y8 [T,d] E4M3 codes of the unrounded y with y8_scale,
  *      or both NULL: MOE_FP8: scale = max(amax, 2^-100) / 448 per row and 128 columns, f32
- *      [d/128][T], code = RNE_E4M3(y / scale); MOE_MXFP8: codes and E8M0 bytes as
+ *      [d/128][T], code = RNE_E4M3(y / scale); MOE_MXFP8 and MOE_MXFP4: codes and E8M0 bytes as
  *      moe_quantize_mx writes them, [d/128][T][4].  A block that holds an infinity or a NaN
  *      gets the scale NaN (E8M0 byte 255).  y or y8 must be given.  rstd [T] f32 or NULL
  *      (moe_add_rmsnorm_backward needs it).
- * Apart from h no output may overlap an input or another output.  y8 needs MOE_MXFP8 or
- * MOE_FP8 (MOE_ERR_DTYPE).  Tensors are aligned to 16 bytes (MOE_ERR_ALIGN); rstd and
+ * Apart from h no output may overlap an input or another output.  y8 needs MOE_MXFP8,
+ * MOE_MXFP4 or MOE_FP8 (MOE_ERR_DTYPE).  Tensors are aligned to 16 bytes (MOE_ERR_ALIGN); rstd and
  * y8_scale to 4.  eps that is negative, NaN or infinite, or more than 2^23 tokens: MOE_ERR_SHAPE.
  * A row whose sum of squares is above fp32's range has rstd 0; a row of zeros with eps 0 has
  * rstd infinite and y NaN.
@@ -489,8 +497,8 @@ int moe_backward_experts(const moe_shape* shape, const void* dy, const int32_t* 
 
 /* ------------------------------------------------------------------ FP8, scales per 128
  * moe_dispatch_q: moe_dispatch of rows that are 8-bit already (moe_add_rmsnorm's y8): x8 [T,d]
- * codes and x8_scale [d/128][T] (MOE_FP8: f32; MOE_MXFP8: 4 bytes each) are copied into the
- * ring; every other argument as moe_dispatch.  MOE_MXFP8 and MOE_FP8 only (MOE_ERR_DTYPE).
+ * codes and x8_scale [d/128][T] (MOE_FP8: f32; MOE_MXFP8 and MOE_MXFP4: 4 bytes each) are copied into the
+ * ring; every other argument as moe_dispatch.  MOE_MXFP8, MOE_MXFP4 and MOE_FP8 only (MOE_ERR_DTYPE).
  * x8 and ring_x are aligned to 16 bytes (MOE_ERR_ALIGN); fewer than 2^24 tokens (MOE_ERR_SHAPE).
  */
 int moe_dispatch_q(const moe_shape* shape, const uint8_t* x8, const uint8_t* x8_scale,
@@ -528,6 +536,58 @@ int moe_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w,
                    const float* w_scale, int64_t M, int64_t N, int64_t K, int out_dtype,
                    void* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
 size_t moe_matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* ------------------------------------------------------------------ MXFP4 weights
+ * moe_quantize_mxfp4: a bf16 matrix [rows, cols] (cols % 128 == 0) to MXFP4 along cols: per block of 32,
+ * X = floor(log2 amax) - 2 clamped to -127 below (-127 for a block of zeros), code =
+ * RNE_E2M1(clamp(v / 2^X, +-6)), scale = X + 127; a block that holds an infinity or a NaN: scale byte 255
+ * (NaN), codes 0.
+ * Out: codes [rows, cols/2], scales [cols/128][rows][4].  At most 2^37 elements (MOE_ERR_SHAPE).  src and
+ * codes are aligned to 16 bytes, scales to 4 (MOE_ERR_ALIGN).
+ */
+int moe_quantize_mxfp4(const void* src_bf16, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
+                       hipStream_t stream);
+
+/*
+ * moe_matmul_mxfp4: out = X W^T of bf16 rows and an MXFP4 matrix in nn.Linear layout,
+ *   out[m,n] = sum_b 2^(w_scale[n,b] - 127) sum_{i in block b of 32} x[m,i] w[n,i],
+ * products exact, sums in fp32, one rounding.  out may not overlap an input.  A scale byte of 252 or more gives
+ * values past bf16's range, which count as infinite (255: NaN).
+ * In:  x [M,K] bf16; w [N,K/2] codes, w_scale [K/128][N][4] (moe_quantize_mxfp4).  K % 128 == 0; M K and
+ *      N K < 2^32, M N < 2^38.
+ * Out: out [M,N]: out_dtype MOE_BF16 or MOE_F32 (MOE_ERR_DTYPE otherwise).
+ * M = 0 or N = 0: nothing is written.
+ * workspace: moe_matmul_mxfp4_workspace_bytes(M, N, K) bytes (NULL if that is 0).  x and w are aligned to 16
+ * bytes, out to its element, w_scale to 4 (MOE_ERR_ALIGN).
+ */
+int moe_matmul_mxfp4(const void* x, const uint8_t* w, const uint8_t* w_scale, int64_t M, int64_t N, int64_t K,
+                     int out_dtype, void* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t moe_matmul_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * moe_decode_mxfp4: the whole layer for a few tokens with MXFP4 weights (the output-parallel decode of the
+ * toolnavs.com warp-decode page, for this weight format and with moe_route_scored's rules):
+ *   S_t, g_t by `router` (as moe_route_scored);  y_t = sum_j g_tj E_{S_tj}(x_t) + E_shared(x_t),
+ * x in bf16 as it is (no 8-bit rows), products exact, sums in fp32; the inner h, times its gate, is held to 2^-16 of
+ * its value; y is rounded once.  topk_idx and topk_gate are bit for bit moe_route_scored's.
+ * In:  x [T,d] bf16, T = shape->tokens in 1..16; w_router [E,d] f32, b_router and balance [E] f32 or NULL;
+ *      w_gate, w_up [E,f,d/2] and w_down [E,d,f/2] codes, w_gate_scale and w_up_scale [d/128][E*f][4],
+ *      w_down_scale [f/128][E*d][4]; the shared expert's ws_gate, ws_up [fs,d/2], ws_down [d,fs/2] and scales
+ *      likewise, read only when fs = shape->shared_ffn > 0.  Weights are finite (scale bytes up to 251): an expert's
+ *      infinity or NaN may reach every token of the call.
+ * Out: y [T,d] bf16; topk_idx [T,k] int32, ascending; topk_gate [T,k] f32.
+ * No output may overlap an input or another output.
+ * MOE_MXFP4 only; top_k <= 16, d <= 8192, f and fs <= 65536, fs a multiple of 128 (MOE_ERR_SHAPE otherwise).
+ * workspace: moe_workspace_bytes(shape, MOE_OP_DECODE) bytes (no initial contents needed).  x, w_router, weights and
+ * workspace are aligned to 16 bytes, y to 2, everything else to 4 (MOE_ERR_ALIGN).
+ */
+int moe_decode_mxfp4(const moe_shape* shape, const moe_router* router, const void* x, const float* w_router,
+                     const float* b_router, const float* balance, const uint8_t* w_gate, const uint8_t* w_up,
+                     const uint8_t* w_down, const uint8_t* w_gate_scale, const uint8_t* w_up_scale,
+                     const uint8_t* w_down_scale, const uint8_t* ws_gate, const uint8_t* ws_up,
+                     const uint8_t* ws_down, const uint8_t* ws_gate_scale, const uint8_t* ws_up_scale,
+                     const uint8_t* ws_down_scale, void* y, int32_t* topk_idx, float* topk_gate, void* workspace,
+                     size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -13,7 +13,7 @@ from typing import Dict, Optional
 
 import torch
 
-from ._lib import (DTYPES, MOE_BF16, MOE_F32, MOE_FP8, MOE_MXFP8, OP_BACKWARD, OP_COMBINE,
+from ._lib import (DTYPES, MOE_BF16, MOE_F32, MOE_FP8, MOE_MXFP4, MOE_MXFP8, OP_BACKWARD, OP_COMBINE,
                    OP_DECODE, OP_DISPATCH, OP_EXPERT_FFN, OP_FORWARD, OP_NORM_BACKWARD, OP_ROUTE,
                    OP_ROUTE_BACKWARD, SCORE_SOFTMAX, SCORES, LIB_PATH, MoeError, MoeRouter, MoeShape, check, lib)
 
@@ -24,6 +24,7 @@ __all__ = ["make_shape", "check_shape", "workspace_bytes", "moe_route", "moe_dis
            "make_router", "moe_route_scored", "moe_route_scored_backward", "moe_backward_experts",
            "moe_add_rmsnorm", "moe_add_rmsnorm_backward", "moe_dispatch_q", "quantize_fp8",
            "moe_matmul_fp8", "matmul_fp8_workspace",
+           "quantize_mxfp4", "moe_matmul_mxfp4", "matmul_mxfp4_workspace", "moe_decode_mxfp4",
            "MoeError",
            "LIB_PATH"]
 
@@ -74,7 +75,7 @@ def moe_route(shape, x, w_router, b_router, topk_idx, topk_gate, expert_count, w
 
 def moe_dispatch(shape, x, topk_idx, ring_head, ring_x, ring_x_scale, expert_offset, copy_slot,
                  slot_copy, ws, stream=None):
-    if shape.dtype == MOE_FP8:
+    if shape.dtype in (MOE_FP8, MOE_MXFP4):
         T, d, E, k, C, dev = (shape.tokens, shape.hidden, shape.experts, shape.top_k, shape.capacity, ring_x.get_device())
         i32 = torch.int32
         args = (_a("x", x, torch.bfloat16, (T, d), dev), _a("topk_idx", topk_idx, i32, (T, k), dev),
@@ -91,9 +92,9 @@ def moe_dispatch(shape, x, topk_idx, ring_head, ring_x, ring_x_scale, expert_off
 
 def moe_expert_ffn(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
                    w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws, stream=None):
-    if shape.dtype == MOE_FP8:
-        args = _ffn_fp8_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
-                             w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws)
+    if shape.dtype in (MOE_FP8, MOE_MXFP4):
+        args = _ffn_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
+                         w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws)
         return _on(ring_x.get_device(), stream, "moe_expert_ffn", lib().moe_expert_ffn, shape, *args)
     check("moe_expert_ffn", lib().moe_expert_ffn(
         shape, _p(ring_x), _p(ring_x_scale), _p(expert_offset), int(ring_head), _p(w_gate),
@@ -110,9 +111,9 @@ def moe_expert_ffn_timed(shape, ring_x, ring_x_scale, expert_offset, ring_head, 
         if e.cuda_event == 0:
             e.record()
     arr = (ctypes.c_void_p * 3)(*[e.cuda_event for e in events])
-    if shape.dtype == MOE_FP8:
-        args = _ffn_fp8_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
-                             w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws)
+    if shape.dtype in (MOE_FP8, MOE_MXFP4):
+        args = _ffn_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
+                         w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws)
         return _on(ring_x.get_device(), stream, "moe_expert_ffn_timed", lib().moe_expert_ffn_timed,
                    shape, *args, ctypes.cast(arr, ctypes.c_void_p))
     check("moe_expert_ffn_timed", lib().moe_expert_ffn_timed(
@@ -331,23 +332,31 @@ def moe_backward_experts(shape, dy, topk_idx, topk_gate, ring_x, expert_offset, 
 
 
 def _scale_spec(shape: MoeShape, rows: int):
-    """Type and shape of the scales of 8-bit rows [rows, d]."""
+    """Type and shape of the scales of 8-bit rows [rows, d] (one fp32 per 128 columns, or four E8M0 bytes)."""
     if shape.dtype == MOE_FP8:
         return torch.float32, (shape.hidden // 128, rows)
     return torch.uint8, (shape.hidden // 128, rows, 4)
 
 
-def _ffn_fp8_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
-                  w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws):
+def _weight_specs(shape: MoeShape):
+    """Columns in a byte of codes, type and shapes of the scales of W_gate or W_up and of W_down: FP8 and MXFP4."""
+    d, E, f = shape.hidden, shape.experts, shape.ffn
+    if shape.dtype == MOE_MXFP4:
+        return 2, torch.uint8, (d // 128, E * f, 4), (f // 128, E * d, 4)
+    return 1, torch.float32, (E, f // 128, d // 128), (E, d // 128, f // 128)
+
+
+def _ffn_args(shape, ring_x, ring_x_scale, expert_offset, ring_head, w_gate, w_up, w_down,
+              w_gate_scale, w_up_scale, w_down_scale, ring_y, saved_au, ws):
     d, E, f, C, dev = shape.hidden, shape.experts, shape.ffn, shape.capacity, ring_x.get_device()
-    u8, f32, bf = torch.uint8, torch.float32, torch.bfloat16
-    wide, tall = (E, f // 128, d // 128), (E, d // 128, f // 128)
+    u8, bf = torch.uint8, torch.bfloat16
+    per, sdt, wide, tall = _weight_specs(shape)
     return (_a("ring_x", ring_x, u8, (C, d), dev),
-            _a("ring_x_scale", ring_x_scale, f32, (d // 128, C), dev),
+            _a("ring_x_scale", ring_x_scale, *_scale_spec(shape, C), dev),
             _a("expert_offset", expert_offset, torch.int32, (E + 1,), dev), int(ring_head),
-            _a("w_gate", w_gate, u8, (E, f, d), dev), _a("w_up", w_up, u8, (E, f, d), dev),
-            _a("w_down", w_down, u8, (E, d, f), dev), _a("w_gate_scale", w_gate_scale, f32, wide, dev),
-            _a("w_up_scale", w_up_scale, f32, wide, dev), _a("w_down_scale", w_down_scale, f32, tall, dev),
+            _a("w_gate", w_gate, u8, (E, f, d // per), dev), _a("w_up", w_up, u8, (E, f, d // per), dev),
+            _a("w_down", w_down, u8, (E, d, f // per), dev), _a("w_gate_scale", w_gate_scale, sdt, wide, dev),
+            _a("w_up_scale", w_up_scale, sdt, wide, dev), _a("w_down_scale", w_down_scale, sdt, tall, dev),
             _a("ring_y", ring_y, bf, (C, d), dev), _a("saved_au", saved_au, bf, (C, 2 * f), dev),
             *_ws_arg("ws", ws, dev))
 
@@ -436,12 +445,70 @@ def moe_matmul_fp8(a, a_scale, w, w_scale, out, ws=None, stream=None):
     _on(dev, stream, "moe_matmul_fp8", lib().moe_matmul_fp8, *args)
 
 
+def quantize_mxfp4(src: torch.Tensor, stream=None):
+    """(codes uint8 [..., cols/2], scales uint8 [cols/128, rows, 4]) of a bf16 tensor, MXFP4 along its last dimension
+    (rows: all leading dimensions)."""
+    if src.dim() < 2:
+        raise ValueError("quantize_mxfp4 takes matrices")
+    cols = src.shape[-1]
+    rows, at = math.prod(src.shape[:-1]), src.get_device()
+    p = _a("src", src, torch.bfloat16, src.shape, at)
+    with torch.cuda.stream(stream):   # memory of the stream that writes it (as quantize_fp8)
+        codes = torch.empty((*src.shape[:-1], cols // 2), dtype=torch.uint8, device=src.device)
+        scales = torch.empty((cols // 128, rows, 4), dtype=torch.uint8, device=src.device)
+    _on(at, stream, "moe_quantize_mxfp4", lib().moe_quantize_mxfp4, p, rows, cols, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def matmul_mxfp4_workspace(M: int, N: int, K: int, device) -> Optional[torch.Tensor]:
+    """The workspace moe_matmul_mxfp4 needs for these sizes (None if it needs none)."""
+    n = int(lib().moe_matmul_mxfp4_workspace_bytes(M, N, K))
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def moe_matmul_mxfp4(x, w, w_scale, out, ws=None, stream=None):
+    """out [M, N] (bf16 or fp32) = X W^T of bf16 rows x [M, K] and MXFP4 codes w [N, K/2] with the scales of
+    quantize_mxfp4, w_scale [K/128, N, 4]."""
+    if x.dim() != 2 or w.dim() != 2 or out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("moe_matmul_mxfp4: a matrix of rows, a matrix of codes, and an output in bfloat16 or float32")
+    dev, (M, K), N = w.get_device(), x.shape, w.shape[0]
+    u8 = torch.uint8
+    args = (_a("x", x, torch.bfloat16, (M, K), dev), _a("w", w, u8, (N, K // 2), dev),
+            _a("w_scale", w_scale, u8, (K // 128, N, 4), dev), M, N, K,
+            MOE_F32 if out.dtype is torch.float32 else MOE_BF16, _a("out", out, out.dtype, (M, N), dev),
+            *_ws_arg("ws", ws, dev))
+    _on(dev, stream, "moe_matmul_mxfp4", lib().moe_matmul_mxfp4, *args)
+
+
+def moe_decode_mxfp4(shape, router, x, w_router, b_router, balance, w_gate, w_up, w_down, w_gate_scale, w_up_scale,
+                     w_down_scale, ws_gate, ws_up, ws_down, ws_gate_scale, ws_up_scale, ws_down_scale, y, topk_idx,
+                     topk_gate, ws, stream=None):
+    """The whole layer for 1 to 16 tokens with MXFP4 weights; the ws_ arguments (a shared expert) are None if
+    shape.shared_ffn is 0."""
+    T, d, E, k, f, fs = shape.tokens, shape.hidden, shape.experts, shape.top_k, shape.ffn, shape.shared_ffn
+    dev, f32, u8 = w_router.get_device(), torch.float32, torch.uint8
+    wide, tall = (d // 128, E * f, 4), (f // 128, E * d, 4)
+    args = (_a("x", x, torch.bfloat16, (T, d), dev), _a("w_router", w_router, f32, (E, d), dev),
+            _a("b_router", b_router, f32, (E,), dev), _a("balance", balance, f32, (E,), dev),
+            _a("w_gate", w_gate, u8, (E, f, d // 2), dev), _a("w_up", w_up, u8, (E, f, d // 2), dev),
+            _a("w_down", w_down, u8, (E, d, f // 2), dev), _a("w_gate_scale", w_gate_scale, u8, wide, dev),
+            _a("w_up_scale", w_up_scale, u8, wide, dev), _a("w_down_scale", w_down_scale, u8, tall, dev),
+            _a("ws_gate", ws_gate, u8, (fs, d // 2), dev), _a("ws_up", ws_up, u8, (fs, d // 2), dev),
+            _a("ws_down", ws_down, u8, (d, fs // 2), dev),
+            _a("ws_gate_scale", ws_gate_scale, u8, (d // 128, fs, 4), dev),
+            _a("ws_up_scale", ws_up_scale, u8, (d // 128, fs, 4), dev),
+            _a("ws_down_scale", ws_down_scale, u8, (fs // 128, d, 4), dev),
+            _a("y", y, torch.bfloat16, (T, d), dev), _a("topk_idx", topk_idx, torch.int32, (T, k), dev),
+            _a("topk_gate", topk_gate, f32, (T, k), dev), *_ws_arg("ws", ws, dev))
+    _on(dev, stream, "moe_decode_mxfp4", lib().moe_decode_mxfp4, shape, router, *args)
+
+
 @dataclass
 class Layer:
     """Buffers of one layer shape, and the forward / backward / decode as chained C calls.
 
     Expert weights are passed per call; for MXFP8 pass their MX codes and scales, for FP8 those of
-    quantize_fp8.  With a `router` (make_router) the layer routes by moe_route_scored.
+    quantize_fp8, for MXFP4 those of quantize_mxfp4.  With a `router` (make_router) the layer routes by moe_route_scored.
 
     The layer remembers the rule of the last call that routed (route, forward, forward_fused, decode), and a
     backward of other gates raises ValueError.  A replayed graph's forward is not seen: capture the backward with
@@ -510,7 +577,7 @@ class Layer:
         h, y = self._buf("norm_h", (T, d), self.act_dtype), self._buf("norm_y", (T, d), self.act_dtype)
         rstd = self._buf("norm_rstd", (T,), torch.float32)
         y8 = ys = None
-        if s.dtype in (MOE_MXFP8, MOE_FP8):
+        if s.dtype in (MOE_MXFP8, MOE_MXFP4, MOE_FP8):
             sdt, sshape = _scale_spec(s, T)
             y8, ys = self._buf("norm_y8", (T, d), torch.uint8), self._buf("norm_y8_scale", sshape, sdt)
         moe_add_rmsnorm(s, x, residual, weight, eps, h, y, y8, ys, rstd)
@@ -526,9 +593,9 @@ class Layer:
         return dx, dw
 
     def dispatch(self, x, topk_idx, head=0, x_scale=None):
-        """With x_scale: x are 8-bit rows (add_rmsnorm's y8 and y8_scale) in an MXFP8 or FP8 layer."""
+        """With x_scale: x are 8-bit rows (add_rmsnorm's y8 and y8_scale) in an MXFP8, MXFP4 or FP8 layer."""
         s = self.shape
-        mx = s.dtype in (MOE_MXFP8, MOE_FP8)
+        mx = s.dtype in (MOE_MXFP8, MOE_MXFP4, MOE_FP8)
         if x.dtype is not (self.act_dtype if x_scale is None else torch.uint8):
             raise ValueError("dispatch takes act rows, or 8-bit rows with their scales")
         ring = self._buf("ring_x", (s.capacity, s.hidden), torch.uint8 if mx else self.act_dtype)
@@ -602,11 +669,22 @@ class Layer:
         return 0 if ws is None else int(ws[8:12].view(torch.int32).item())
 
     def decode(self, x, w_router, b_router, w_gate, w_up, w_down, ws_gate=None, ws_up=None,
-               ws_down=None):
+               ws_down=None, scales=(None, None, None), shared_scales=(None, None, None), router=None,
+               balance=None):
+        """(y, topk_idx, topk_gate) of a few tokens.  An MXFP4 layer takes the weights' scales and any `router`
+        (without one: softmax scores, renormalised gates); a bf16 layer neither."""
         s = self.shape
         y = self._buf("y", (s.tokens, s.hidden), torch.bfloat16)
         idx = self._buf("topk_idx", (s.tokens, s.top_k), torch.int32)
         gate = self._buf("topk_gate", (s.tokens, s.top_k), torch.float32)
+        if s.dtype == MOE_MXFP4:
+            router = make_router() if router is None else router
+            moe_decode_mxfp4(s, router, x, w_router, b_router, balance, w_gate, w_up, w_down, *scales, ws_gate, ws_up,
+                             ws_down, *shared_scales, y, idx, gate, self._ws(OP_DECODE))
+            self.routed = bytes(router)
+            return y, idx, gate
+        if router is not None or balance is not None or any(t is not None for t in (*scales, *shared_scales)):
+            raise ValueError("decode: a router, a balance bias and scales need an MXFP4 layer")
         moe_decode(s, x, w_router, b_router, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, y, idx,
                    gate, self._ws(OP_DECODE))
         self.routed = b""

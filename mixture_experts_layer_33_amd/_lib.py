@@ -10,12 +10,12 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 (MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_CAPACITY, MOE_ERR_WORKSPACE, MOE_ERR_HIP, MOE_ERR_DTYPE,
  MOE_ERR_SCRATCH, MOE_ERR_ALIGN) = range(9)
-MOE_F32, MOE_BF16, MOE_MXFP8, MOE_FP8 = 0, 1, 2, 3
+MOE_F32, MOE_BF16, MOE_MXFP8, MOE_FP8, MOE_MXFP4 = range(5)
 (OP_ROUTE, OP_DISPATCH, OP_EXPERT_FFN, OP_COMBINE, OP_DECODE, OP_BACKWARD, OP_FORWARD,
  OP_NORM_BACKWARD, OP_ROUTE_BACKWARD) = range(9)
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
-DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp8": MOE_MXFP8, "fp8": MOE_FP8}
+DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp8": MOE_MXFP8, "fp8": MOE_FP8, "mxfp4": MOE_MXFP4}
 SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 
 
@@ -63,8 +63,13 @@ SIGNATURES = {
     "moe_quantize_fp8": [P, I64, I64, C.c_int, P, P, P],
     "moe_matmul_fp8": [P, P, P, P, I64, I64, I64, C.c_int, P, P, SZ, P],
     "moe_matmul_fp8_workspace_bytes": [I64, I64, I64],
+    "moe_quantize_mxfp4": [P, I64, I64, P, P, P],
+    "moe_matmul_mxfp4": [P, P, P, I64, I64, I64, C.c_int, P, P, SZ, P],
+    "moe_matmul_mxfp4_workspace_bytes": [I64, I64, I64],
+    "moe_decode_mxfp4": [SHP, RTP] + [P] * 20 + [SZ, P],
 }
-_RESTYPE = {"moe_workspace_bytes": SZ, "moe_matmul_fp8_workspace_bytes": SZ, "moe_status_string": C.c_char_p}
+_RESTYPE = {"moe_workspace_bytes": SZ, "moe_matmul_fp8_workspace_bytes": SZ,
+            "moe_matmul_mxfp4_workspace_bytes": SZ, "moe_status_string": C.c_char_p}
 
 _lib = None
 

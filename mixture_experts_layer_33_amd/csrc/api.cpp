@@ -35,7 +35,10 @@ hipError_t zero_words(void* p, size_t words, hipStream_t st) {
   return hipGetLastError();
 }
 
-bool bad_dtype(int dt) { return dt != MOE_F32 && dt != MOE_BF16 && dt != MOE_MXFP8 && dt != MOE_FP8; }
+bool bad_dtype(int dt) { return dt < MOE_F32 || dt > MOE_MXFP4; }
+// Rows (ring_x, H) in MX E4M3, and rows in 8 bits of either kind.
+bool mx_rows(int dt) { return dt == MOE_MXFP8 || dt == MOE_MXFP4; }
+bool coded_rows(int dt) { return mx_rows(dt) || dt == MOE_FP8; }
 
 // A workgroup of 256 threads per token, and a grid of fewer than 2^32 threads (the 8-bit rows' dispatches).
 constexpr int64_t DISPATCH_ROWS = ((int64_t)1 << 24) - 1;
@@ -43,7 +46,7 @@ constexpr int64_t DISPATCH_ROWS = ((int64_t)1 << 24) - 1;
 bool unaligned(const void* p, uintptr_t a = 16) { return (uintptr_t)p % a != 0; }
 
 // Shape checks common to the forward calls.  K-dimension multiples follow the
-// kernels' 128-byte K slices: bf16 needs d, f % 64; MX and FP8 need d, f % 128.
+// kernels' 128-byte K slices: bf16 needs d, f % 64; MX, FP8 and MXFP4 need d, f % 128.
 int check_shape(const moe_shape* s) {
   if (!s) return MOE_ERR_NULL;
   if (bad_dtype(s->dtype)) return MOE_ERR_DTYPE;
@@ -52,7 +55,7 @@ int check_shape(const moe_shape* s) {
   if (s->experts > MAX_E || s->top_k < 1 || s->top_k > s->experts || s->top_k > MAX_K)
     return MOE_ERR_SHAPE;
   if (s->tokens > (int64_t)1 << 30) return MOE_ERR_SHAPE;
-  const int q = s->dtype == MOE_MXFP8 || s->dtype == MOE_FP8 ? 128 : s->dtype == MOE_BF16 ? 64 : 8;
+  const int q = coded_rows(s->dtype) ? 128 : s->dtype == MOE_BF16 ? 64 : 8;
   if (s->hidden % q || s->ffn % q) return MOE_ERR_SHAPE;
   if (s->capacity < s->tokens * s->top_k) return MOE_ERR_CAPACITY;
   if (s->capacity > ((int64_t)1 << 31) - 1) return MOE_ERR_SHAPE;
@@ -63,13 +66,22 @@ int check_shape(const moe_shape* s) {
     const int64_t eb = s->dtype == MOE_BF16 ? 2 : 1;
     const int64_t row = (s->hidden > s->ffn ? s->hidden : s->ffn) * eb;
     if (s->capacity * row >= ((int64_t)1 << 32)) return MOE_ERR_SHAPE;
-    // ... and the FP8 products the rows of one expert's matrix likewise
-    if (s->dtype == MOE_FP8 && (int64_t)s->hidden * s->ffn >= ((int64_t)1 << 32)) return MOE_ERR_SHAPE;
+    // ... and the FP8 and MXFP4 products the rows of one expert's matrix likewise
+    if ((s->dtype == MOE_FP8 || s->dtype == MOE_MXFP4) && (int64_t)s->hidden * s->ffn >= ((int64_t)1 << 32)) return MOE_ERR_SHAPE;
   }
   return MOE_OK;
 }
 
 int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+
+// What moe_decode_mxfp4 takes of a shape that check_shape has passed: a wavefront's part of a token is registers (d), the
+// expert list 16 x 16 entries, and a shared expert's matrix is addressed with 32-bit offsets like a routed one's.
+int decode_mxfp4_shape(const moe_shape* s) {
+  if (s->tokens < 1 || s->tokens > 16 || s->top_k > 16 || s->hidden > 8192 || s->ffn > 65536 || s->shared_ffn > 65536 ||
+      s->shared_ffn % 128)
+    return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
 
 }  // namespace
 
@@ -88,6 +100,10 @@ size_t moe_workspace_bytes(const moe_shape* s, int op) {
       return align256(moe::ffn_workspace_bytes(n, C, s->hidden, s->experts, s->ffn, s->dtype));
     case MOE_OP_COMBINE: return 0;
     case MOE_OP_DECODE:
+      if (s->dtype == MOE_MXFP4)
+        return decode_mxfp4_shape(s) ? 0
+                                     : align256(moe::decode_mxfp4_workspace_bytes((int)T, s->hidden, s->experts, s->top_k,
+                                                                                  s->ffn, s->shared_ffn));
       return align256(moe::decode_workspace_bytes((int)T, s->experts, s->top_k, s->ffn,
                                                   s->shared_ffn));
     case MOE_OP_FORWARD:
@@ -98,7 +114,7 @@ size_t moe_workspace_bytes(const moe_shape* s, int op) {
     case MOE_OP_ROUTE_BACKWARD:
       return align256(moe::route_scored_bwd_workspace_bytes(s->dtype == MOE_F32, T, s->experts, s->hidden));
     case MOE_OP_BACKWARD:
-      if (s->dtype == MOE_FP8) return 0;
+      if (s->dtype == MOE_FP8 || s->dtype == MOE_MXFP4) return 0;
       if (s->dtype == MOE_MXFP8)
         return align256(moe::backward_mx_workspace_bytes(T, C, s->hidden, s->experts, s->top_k,
                                                          s->ffn));
@@ -157,17 +173,17 @@ int moe_dispatch(const moe_shape* s, const void* x, const int32_t* topk_idx, int
     if (missing_tok(x, T) || missing_tok(topk_idx, T) || !ring_x || !expert_offset ||
         missing_tok(copy_slot, T) || !slot_copy || !workspace)
       return MOE_ERR_NULL;
-    if ((s->dtype == MOE_MXFP8 || s->dtype == MOE_FP8) && !ring_x_scale) return MOE_ERR_NULL;
-    if (s->dtype == MOE_FP8 && (unaligned(x) || unaligned(ring_x) || unaligned(ring_x_scale, 4)))
-      return MOE_ERR_ALIGN;
+    if (coded_rows(s->dtype) && !ring_x_scale) return MOE_ERR_NULL;
+    const bool strict = s->dtype == MOE_FP8 || s->dtype == MOE_MXFP4;
+    if (strict && (unaligned(x) || unaligned(ring_x) || unaligned(ring_x_scale, 4))) return MOE_ERR_ALIGN;
     if (ring_head < 0 || ring_head >= s->capacity) return MOE_ERR_SHAPE;
-    if (s->dtype == MOE_FP8 && s->tokens > DISPATCH_ROWS) return MOE_ERR_SHAPE;
+    if (strict && s->tokens > DISPATCH_ROWS) return MOE_ERR_SHAPE;
     if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_DISPATCH)) return MOE_ERR_WORKSPACE;
     if (s->tokens == 0)   // no copies: every expert's segment is empty
       return hip_status(zero_words(expert_offset, (size_t)s->experts + 1, stream));
     return hip_status(moe::launch_dispatch(
         x, s->dtype == MOE_F32 ? 4 : 2,
-        s->dtype == MOE_MXFP8 ? moe::RowForm::mx : s->dtype == MOE_FP8 ? moe::RowForm::fp8 : moe::RowForm::plain,
+        mx_rows(s->dtype) ? moe::RowForm::mx : s->dtype == MOE_FP8 ? moe::RowForm::fp8 : moe::RowForm::plain,
         nullptr, topk_idx, s->tokens, s->hidden, s->experts, s->top_k, ring_head, s->capacity,
         ring_x, ring_x_scale, expert_offset, copy_slot, slot_copy, workspace, stream));
   } catch (...) {
@@ -186,11 +202,10 @@ int moe_expert_ffn_timed(const moe_shape* s, const void* ring_x, const uint8_t* 
     if (st) return st;
     if (!ring_x || !expert_offset || !w_gate || !w_up || !w_down || !ring_y || !workspace)
       return MOE_ERR_NULL;
-    const bool scaled = s->dtype == MOE_MXFP8 || s->dtype == MOE_FP8;
-    if (scaled && (!ring_x_scale || !w_gate_scale || !w_up_scale || !w_down_scale))
+    if (coded_rows(s->dtype) && (!ring_x_scale || !w_gate_scale || !w_up_scale || !w_down_scale))
       return MOE_ERR_NULL;
-    if (saved_au && s->dtype == MOE_F32) return MOE_ERR_DTYPE;
-    if (s->dtype == MOE_FP8 &&
+    if (saved_au && (s->dtype == MOE_F32 || s->dtype == MOE_MXFP4)) return MOE_ERR_DTYPE;
+    if ((s->dtype == MOE_FP8 || s->dtype == MOE_MXFP4) &&
         (unaligned(ring_x) || unaligned(w_gate) || unaligned(w_up) || unaligned(w_down) ||
          unaligned(ring_y) || unaligned(saved_au) || unaligned(workspace) ||
          unaligned(ring_x_scale, 4) || unaligned(w_gate_scale, 4) || unaligned(w_up_scale, 4) ||
@@ -461,7 +476,7 @@ int moe_add_rmsnorm(const moe_shape* s, const void* x, const void* residual, con
   try {
     int st = check_shape(s);
     if (st) return st;
-    const bool coded = s->dtype == MOE_MXFP8 || s->dtype == MOE_FP8;
+    const bool coded = coded_rows(s->dtype);
     if (!coded && (y8 || y8_scale)) return MOE_ERR_DTYPE;
     if (!weight || (!y8) != (!y8_scale)) return MOE_ERR_NULL;
     if (!(eps >= 0.f) || !std::isfinite(eps) || s->tokens > NORM_ROWS) return MOE_ERR_SHAPE;
@@ -624,7 +639,7 @@ int moe_dispatch_q(const moe_shape* s, const uint8_t* x8, const uint8_t* x8_scal
   try {
     int st = check_shape(s);
     if (st) return st;
-    if (s->dtype != MOE_MXFP8 && s->dtype != MOE_FP8) return MOE_ERR_DTYPE;
+    if (!coded_rows(s->dtype)) return MOE_ERR_DTYPE;
     const int64_t T = s->tokens;
     if (missing_tok(x8, T) || missing_tok(x8_scale, T) || missing_tok(topk_idx, T) || !ring_x ||
         !ring_x_scale || !expert_offset || missing_tok(copy_slot, T) || !slot_copy || !workspace)
@@ -690,6 +705,91 @@ int moe_matmul_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w, con
     if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
     return hip_status(moe::launch_matmul_fp8(a, a_scale, w, w_scale, M, N, K, out_dtype == MOE_F32, out,
                                              workspace, stream));
+  } catch (...) {
+    return MOE_ERR_HIP;
+  }
+}
+
+// ------------------------------------------------------------------ MXFP4
+int moe_quantize_mxfp4(const void* src_bf16, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
+                       hipStream_t stream) {
+  try {
+    if (rows < 0 || cols <= 0 || cols % 128 || rows > ((int64_t)1 << 37) / cols) return MOE_ERR_SHAPE;
+    if (rows == 0) return MOE_OK;
+    if (!src_bf16 || !codes || !scales) return MOE_ERR_NULL;
+    if (unaligned(src_bf16) || unaligned(codes) || unaligned(scales, 4)) return MOE_ERR_ALIGN;
+    return hip_status(moe::launch_quantize_mxfp4(src_bf16, rows, cols, codes, scales, stream));
+  } catch (...) {
+    return MOE_ERR_HIP;
+  }
+}
+
+namespace {
+int check_matmul_mxfp4(int64_t M, int64_t N, int64_t K) {
+  const int64_t top = ((int64_t)1 << 31) - 1;
+  if (M < 0 || N < 0 || K <= 0 || K % 128 || M > top || N > top || K > top) return MOE_ERR_SHAPE;
+  if (M * K >= ((int64_t)1 << 32) || N * K >= ((int64_t)1 << 32) || M * N >= (int64_t)1 << 38) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+}  // namespace
+
+size_t moe_matmul_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_matmul_mxfp4(M, N, K) != MOE_OK || M == 0 || N == 0) return 0;
+  return align256(moe::matmul_mxfp4_workspace_bytes(M, N, K));
+}
+
+int moe_matmul_mxfp4(const void* x, const uint8_t* w, const uint8_t* w_scale, int64_t M, int64_t N, int64_t K,
+                     int out_dtype, void* out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  try {
+    int st = check_matmul_mxfp4(M, N, K);
+    if (st) return st;
+    if (out_dtype != MOE_BF16 && out_dtype != MOE_F32) return MOE_ERR_DTYPE;
+    if (M == 0 || N == 0) return MOE_OK;
+    const size_t need = moe_matmul_mxfp4_workspace_bytes(M, N, K);
+    if (!x || !w || !w_scale || !out || (need && !workspace)) return MOE_ERR_NULL;
+    if (unaligned(x) || unaligned(w) || unaligned(w_scale, 4) || unaligned(out, out_dtype == MOE_F32 ? 4 : 2) ||
+        unaligned(workspace))
+      return MOE_ERR_ALIGN;
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    return hip_status(moe::launch_matmul_mxfp4(x, w, w_scale, M, N, K, out_dtype == MOE_F32, out, workspace, stream));
+  } catch (...) {
+    return MOE_ERR_HIP;
+  }
+}
+
+int moe_decode_mxfp4(const moe_shape* s, const moe_router* router, const void* x, const float* w_router,
+                     const float* b_router, const float* balance, const uint8_t* w_gate, const uint8_t* w_up,
+                     const uint8_t* w_down, const uint8_t* w_gate_scale, const uint8_t* w_up_scale,
+                     const uint8_t* w_down_scale, const uint8_t* ws_gate, const uint8_t* ws_up, const uint8_t* ws_down,
+                     const uint8_t* ws_gate_scale, const uint8_t* ws_up_scale, const uint8_t* ws_down_scale, void* y,
+                     int32_t* topk_idx, float* topk_gate, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  try {
+    int st = check_shape(s);
+    if (st) return st;
+    if (s->dtype != MOE_MXFP4) return MOE_ERR_DTYPE;
+    moe::ScoreRule rule;
+    if ((st = check_router(s, router, &rule)) || (st = decode_mxfp4_shape(s))) return st;
+    if (!x || !w_router || !w_gate || !w_up || !w_down || !w_gate_scale || !w_up_scale || !w_down_scale || !y ||
+        !topk_idx || !topk_gate || !workspace)
+      return MOE_ERR_NULL;
+    if (s->shared_ffn > 0 && (!ws_gate || !ws_up || !ws_down || !ws_gate_scale || !ws_up_scale || !ws_down_scale))
+      return MOE_ERR_NULL;
+    for (const void* p : {x, (const void*)w_router, (const void*)w_gate, (const void*)w_up, (const void*)w_down,
+                          (const void*)ws_gate, (const void*)ws_up, (const void*)ws_down, (const void*)workspace})
+      if (unaligned(p)) return MOE_ERR_ALIGN;
+    for (const void* p : {(const void*)w_gate_scale, (const void*)w_up_scale, (const void*)w_down_scale,
+                          (const void*)ws_gate_scale, (const void*)ws_up_scale, (const void*)ws_down_scale,
+                          (const void*)b_router, (const void*)balance, (const void*)topk_idx, (const void*)topk_gate})
+      if (unaligned(p, 4)) return MOE_ERR_ALIGN;
+    if (unaligned(y, 2)) return MOE_ERR_ALIGN;
+    if (workspace_bytes < moe_workspace_bytes(s, MOE_OP_DECODE)) return MOE_ERR_WORKSPACE;
+    const bool sh = s->shared_ffn > 0;
+    const moe::Mx4Weights w{w_gate, w_up, w_down, w_gate_scale, w_up_scale, w_down_scale};
+    const moe::Mx4Weights ws = sh ? moe::Mx4Weights{ws_gate, ws_up, ws_down, ws_gate_scale, ws_up_scale, ws_down_scale}
+                                  : moe::Mx4Weights{};
+    return hip_status(moe::launch_decode_mxfp4(x, w_router, b_router, balance, rule, w, ws, (int)s->tokens, s->hidden,
+                                               s->experts, s->top_k, s->ffn, s->shared_ffn, y, topk_idx, topk_gate,
+                                               workspace, stream));
   } catch (...) {
     return MOE_ERR_HIP;
   }

@@ -59,19 +59,19 @@ hipError_t launch_build_tiles(const int32_t* expert_offset, int E, int BM, int32
 }
 
 template <int BM, int BN, int WM, int WN, int KB, bool SWIGLU, bool MX, int S, int POL,
-          bool F32OUT = false, bool MXSAVE = false>
+          bool F32OUT = false, bool MXSAVE = false, bool B4 = false>
 __global__ __launch_bounds__(WM * WN * 64) void gg_mfma_kernel(GemmArgs p) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  gg_mfma_body<BM, BN, WM, WN, KB, SWIGLU, MX, S, POL, F32OUT, MXSAVE>(p, (int)blockIdx.x, lds);
+  gg_mfma_body<BM, BN, WM, WN, KB, SWIGLU, MX, S, POL, F32OUT, MXSAVE, B4>(p, (int)blockIdx.x, lds);
 }
 
 template <int BM, int BN, int WM, int WN, int KB, bool SWIGLU, bool MX, int S, int POL,
-          bool F32OUT = false, bool MXSAVE = false>
+          bool F32OUT = false, bool MXSAVE = false, bool B4 = false>
 static hipError_t run_mfma(const GemmArgs& a, int max_tiles, hipStream_t st) {
   const int nt = SWIGLU ? (a.N + BN / 2 - 1) / (BN / 2) : (a.N + BN - 1) / BN;
-  const size_t lds = std::max<size_t>((size_t)S * StageLayout<BM, BN, KB, MX, WM * WN>::SIZE,
+  const size_t lds = std::max<size_t>((size_t)S * StageLayout<BM, BN, KB, MX, WM * WN, B4>::SIZE,
                                       EpiLayout<BM, BN, SWIGLU, MX>::SIZE);
-  auto kern = gg_mfma_kernel<BM, BN, WM, WN, KB, SWIGLU, MX, S, POL, F32OUT, MXSAVE>;
+  auto kern = gg_mfma_kernel<BM, BN, WM, WN, KB, SWIGLU, MX, S, POL, F32OUT, MXSAVE, B4>;
   // opt in to more than 64 KB of LDS: a host-side attribute, set on every launch so that
   // nothing is kept between calls
   hipError_t err = hipFuncSetAttribute((const void*)kern,
@@ -181,6 +181,8 @@ hipError_t launch_ffn(int dtype, const void* ring_x, const uint8_t* ring_x_scale
                       const uint8_t* wg_scale, const uint8_t* wu_scale, const uint8_t* wd_scale,
                       void* ring_y, void* saved_au, void* ws, hipEvent_t* events,
                       hipStream_t st) {
+  const bool w4 = dtype == 4;   // MXFP4: MX rows and H, 4-bit weights
+  if (w4) dtype = 2;
   const bool big = use_big(dtype, n, E);
   const int BM = dtype == 0 ? FT_M : big ? MFMA_BM_BIG : MFMA_BM;
   const int max_tiles = max_tiles_for(n, E, BM);
@@ -248,6 +250,18 @@ hipError_t launch_ffn(int dtype, const void* ring_x, const uint8_t* ring_x_scale
   err = (P) == 3 ? run_mfma<__VA_ARGS__, 3, false, true>(G, max_tiles, st)     \
                  : run_mfma<__VA_ARGS__, 2, false, true>(G, max_tiles, st);
   const bool mxsave = dtype == 2 && saved_au != nullptr;
+  if (w4) {
+#define RUN_W4(P, G, ...)                                                                   \
+  err = (P) == 3 ? run_mfma<__VA_ARGS__, 3, false, false, true>(G, max_tiles, st)           \
+                 : run_mfma<__VA_ARGS__, 2, false, false, true>(G, max_tiles, st);
+    if (big) { RUN_W4(pol1, g1, MFMA_BM_BIG, 256, 4, 2, 128, true, true, 3) }
+    else { RUN_W4(pol1, g1, MFMA_BM, 256, 2, 4, 128, true, true, 4) }
+    if (err != hipSuccess || (err = mark(1)) != hipSuccess) return err;
+    if (big) { RUN_W4(pol2, g2, MFMA_BM_BIG, 256, 4, 2, 128, false, true, 3) }
+    else { RUN_W4(pol2, g2, MFMA_BM, 256, 2, 4, 128, false, true, 4) }
+#undef RUN_W4
+    return err != hipSuccess ? err : mark(2);
+  }
   if (big && mxsave) { RUN_POL_MXSAVE(pol1, g1, MFMA_BM_BIG, 256, 4, 2, 128, true, true, 2) }
   else if (big && dtype == 2) { RUN_POL(pol1, g1, MFMA_BM_BIG, 256, 4, 2, 128, true, true, 2) }
   else if (big) { RUN_POL(pol1, g1, MFMA_BM_BIG, 256, 4, 4, 128, true, false, 2) }

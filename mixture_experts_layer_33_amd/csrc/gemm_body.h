@@ -25,18 +25,19 @@ namespace moe {
 // chunks of a row are XOR-swizzled so that those 16 reads hit 16 distinct 16-byte
 // bank groups of the 256-byte bank line: by ((row >> 1) & 7) for 128-byte rows
 // (two rows per bank line), by ((row >> 2) & 3) for 64-byte rows (four rows per
-// bank line).  The bank-conflict counter reads zero for both.
+// bank line), by (row & 15) for 256-byte rows.  The bank-conflict counter reads zero for the first two.
 template <int KB>
 __device__ __forceinline__ int swz(int r, int c) {
-  static_assert(KB == 128 || KB == 64, "row slice");
-  if constexpr (KB == 128) return r * 128 + ((c ^ ((r >> 1) & 7)) << 4);
+  static_assert(KB == 256 || KB == 128 || KB == 64, "row slice");
+  if constexpr (KB == 256) return r * 256 + ((c ^ (r & 15)) << 4);
+  else if constexpr (KB == 128) return r * 128 + ((c ^ ((r >> 1) & 7)) << 4);
   else return r * 64 + ((c ^ ((r >> 2) & 3)) << 4);
 }
 
 struct GemmArgs {
   const uint8_t* A;        // ring rows [C, K] (bf16 or E4M3)
   const uint8_t* A_scale;  // MX: [C, K/32]
-  const uint8_t* B0;       // [E, N, K]: W_gate (SWIGLU) or W_down
+  const uint8_t* B0;       // [E, N, K]: W_gate (SWIGLU) or W_down (MXFP4: [E, N, K/2], two codes a byte)
   const uint8_t* B1;       // SWIGLU: W_up [E, N, K]
   const uint8_t* B0_scale; // MX: [E, N, K/32]
   const uint8_t* B1_scale;
@@ -97,13 +98,18 @@ __device__ __forceinline__ void wait_vm() {
 // each (BM / 64 for A, then BN / 64 for B); the count is padded to a multiple of the
 // wave count with clamped duplicates written past the B dwords, so that every wave
 // issues the same copies.  S stages form a ring.
-template <int BM, int BN, int KB, bool MX, int NW>
+// B4 (MXFP4 weights): B rows are half as long, and a stage of KB = 256 elements holds two scale dwords
+// per row, those of all A rows and B rows for its first 128 columns, then for its second.
+template <int BM, int BN, int KB, bool MX, int NW, bool B4 = false>
 struct StageLayout {
-  static constexpr int NSC = MX ? (BM / 64 + BN / 64 + NW - 1) / NW : 0;   // scale copies per wave
+  static constexpr int NG = B4 ? KB / 128 : 1;                               // scale dwords per row
+  static constexpr int KBB = B4 ? KB / 2 : KB;                               // bytes of a B row's slice
+  static constexpr int NSC = MX ? (NG * (BM / 64 + BN / 64) + NW - 1) / NW : 0;   // scale copies per wave
   static constexpr int A = 0;
   static constexpr int B = BM * KB;
-  static constexpr int ASC = B + BN * KB;
+  static constexpr int ASC = B + BN * KBB;
   static constexpr int BSC = ASC + (MX ? BM * 4 : 0);
+  static constexpr int GSC = (BM + BN) * 4;                                  // from one 128 columns' dwords to the next's
   static constexpr int SIZE = ASC + NSC * NW * 256;
 };
 
@@ -129,8 +135,9 @@ struct EpiLayout {
 // MXSAVE (SWIGLU + MX): also write the saved A|U planes (bf16 takes them whenever
 // p.saved_au is set; the MX tiles have no registers to spare for that choice at run time:
 // the accumulators would stay live across the extra planes and spill).
+// B4 (with MX): B0 and B1 hold MXFP4 codes; the mixed E4M3 x E2M1 MFMA takes them as they are.
 template <int BM, int BN, int WM, int WN, int KB, bool SWIGLU, bool MX, int S, int POL,
-          bool F32OUT = false, bool MXSAVE = false>
+          bool F32OUT = false, bool MXSAVE = false, bool B4 = false>
 __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* lds) {
   constexpr int EB = MX ? 1 : 2;                 // element bytes
   constexpr int WTM = BM / WM, WTN = BN / WN;    // wave tile
@@ -138,8 +145,9 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
   constexpr int CH = KB / 16;                    // 16-byte chunks per row slice
   constexpr int RPC = 64 / CH;                   // rows per 1 KB copy
   constexpr int NW = WM * WN, NT = NW * 64;      // waves, threads
-  using SL = StageLayout<BM, BN, KB, MX, NW>;
-  constexpr int NA = BM * KB / (NW * 1024), NB = BN * KB / (NW * 1024);   // 1 KB copies per wave
+  using SL = StageLayout<BM, BN, KB, MX, NW, B4>;
+  constexpr int KBB = SL::KBB, CHB = KBB / 16, RPCB = 64 / CHB;   // the same of a B row
+  constexpr int NA = BM * KB / (NW * 1024), NB = BN * KBB / (NW * 1024);   // 1 KB copies per wave
   // MX scale copies: copy k of the tile (wave k mod NW) brings 64 rows' dwords, A rows
   // for k < SCA, then B rows.  Per stage that is BM / 64 + BN / 64 whole-wave copies
   // (one per wave in both tile shapes) where a copy of A and of B rows per wave took
@@ -148,8 +156,9 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
   constexpr int SCA = MX ? BM / 64 : 0, SCB = MX ? BN / 64 : 0;
   constexpr int NSC = SL::NSC;
   constexpr int L = NA + NB + NSC;               // copies per wave per stage
-  static_assert(BM * KB % (NW * 1024) == 0 && BN * KB % (NW * 1024) == 0, "tile / wave mismatch");
-  static_assert(!MX || KB == 128, "MX stages hold whole 128-element scale groups");
+  static_assert(BM * KB % (NW * 1024) == 0 && BN * KBB % (NW * 1024) == 0, "tile / wave mismatch");
+  static_assert(!B4 || (MX && !MXSAVE), "4-bit weights beside MX rows, forward only");
+  static_assert(!MX || KB == 128 || (B4 && KB == 256), "MX stages hold whole 128-element scale groups");
   static_assert(NW == 4 || NW == 8 || (NW == 16 && !MX), "four or eight waves, sixteen without scales");
   static_assert(!MX || (BM % 64 == 0 && BN % 64 == 0), "scale copies of 64 rows");
   static_assert(!SWIGLU || (FN % 2 == 0), "gate/up fragments come in pairs");
@@ -176,6 +185,7 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // wave-uniform
   const int wm = wave / WN, wn = wave % WN;
   const uint32_t Kb = (uint32_t)p.K * EB;                 // row bytes
+  const uint32_t Kbb = B4 ? Kb / 2 : Kb;                  // of a B row
 
 
   // Copy i of this wave fills 16-byte chunks j = (NW i + wave) * 64 + lane of a tile:
@@ -194,12 +204,12 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
   const uint8_t* b_base[NB];
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
-    const int j = (NW * i + wave) * 64 + lane, r = j / CH;
-    const int c = (swz<KB>(r, j % CH) - r * KB) >> 4;
-    const bool up = SWIGLU && (NW * i + wave) * RPC >= BN / 2;
+    const int j = (NW * i + wave) * 64 + lane, r = j / CHB;
+    const int c = (swz<KBB>(r, j % CHB) - r * KBB) >> 4;
+    const bool up = SWIGLU && (NW * i + wave) * RPCB >= BN / 2;
     const int rr = up ? r - BN / 2 : r;
-    b_base[i] = (up ? p.B1 : p.B0) + (int64_t)e * p.N * Kb;
-    b_off[i] = (uint32_t)min(n0 + rr, p.N - 1) * Kb + c * 16;
+    b_base[i] = (up ? p.B1 : p.B0) + (int64_t)e * p.N * Kbb;
+    b_off[i] = (uint32_t)min(n0 + rr, p.N - 1) * Kbb + c * 16;
   }
   uint32_t sc_off[NSC > 0 ? NSC : 1];
   const uint8_t* sc_base[NSC > 0 ? NSC : 1];
@@ -207,10 +217,11 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
   if (MX) {
 #pragma unroll
     for (int i = 0; i < NSC; ++i) {
-      const int k = NW * i + wave;              // the tile's scale copy k (wave-uniform)
+      const int kg = NW * i + wave;             // the tile's scale copy kg (wave-uniform)
+      const int grp = SL::NG > 1 ? kg / (SCA + SCB) : 0, k = SL::NG > 1 ? kg % (SCA + SCB) : kg;
       if (k < SCA) {
         const int r = 64 * k + lane;
-        sc_base[i] = p.A_scale;
+        sc_base[i] = p.A_scale + (SL::NG > 1 ? (size_t)min(grp, SL::NG - 1) * p.a_rows * 4 : 0);
         sc_rows[i] = p.a_rows;
         sc_off[i] = (uint32_t)ring_slot(p.head, seg, row0 + min(r, rows - 1), p.C) * 4;
       } else {
@@ -218,7 +229,8 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
         const int r = 64 * kb + lane;
         const bool up = SWIGLU && 64 * kb >= BN / 2;
         const int rr = up ? r - BN / 2 : r;
-        sc_base[i] = (up ? p.B1_scale : p.B0_scale) + (int64_t)e * p.N * 4;
+        sc_base[i] = (up ? p.B1_scale : p.B0_scale) + (int64_t)e * p.N * 4 +
+                     (SL::NG > 1 ? (size_t)min(grp, SL::NG - 1) * p.b_rows * 4 : 0);
         sc_rows[i] = p.b_rows;
         sc_off[i] = (uint32_t)min(n0 + rr, p.N - 1) * 4;
       }
@@ -238,11 +250,11 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
       dma16(p.A + (size_t)kt * KB, a_off[c], __builtin_amdgcn_readfirstlane(st + SL::A + (NW * c + wave) * 1024));
     } else if (c < NA + NB) {
       const int i = c - NA;
-      if (POL & 1) dma16nt(b_base[i] + (size_t)kt * KB, b_off[i], __builtin_amdgcn_readfirstlane(st + SL::B + (NW * i + wave) * 1024));
-      else dma16(b_base[i] + (size_t)kt * KB, b_off[i], __builtin_amdgcn_readfirstlane(st + SL::B + (NW * i + wave) * 1024));
+      if (POL & 1) dma16nt(b_base[i] + (size_t)kt * KBB, b_off[i], __builtin_amdgcn_readfirstlane(st + SL::B + (NW * i + wave) * 1024));
+      else dma16(b_base[i] + (size_t)kt * KBB, b_off[i], __builtin_amdgcn_readfirstlane(st + SL::B + (NW * i + wave) * 1024));
     } else {
       const int i = c - NA - NB;
-      dma4(sc_base[i] + (size_t)kt * sc_rows[i] * 4, sc_off[i],
+      dma4(sc_base[i] + (size_t)kt * SL::NG * sc_rows[i] * 4, sc_off[i],
            __builtin_amdgcn_readfirstlane(st + SL::ASC + (NW * i + wave) * 256));
     }
   };
@@ -291,9 +303,12 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
   // MFMAs of sub-step kk, except for MX waves of 64 x 128 (eight waves in 256 x 256),
   // whose two register sets would not fit beside the accumulators: there each sub-step
   // reads its own fragments first and the SIMD's other wave covers the LDS latency.
-  constexpr bool PF = !(MX && NW == 8 && FM * FN >= 8);
+  // (E2M1 fragments are half that size, and fit.)
+  constexpr bool PF = B4 || !(MX && NW == 8 && FM * FN >= 8);
   using Frag = std::conditional_t<MX, i32x8, bf16x8>;
-  Frag af[2][FM], bfr[2][FN];
+  using FragB = std::conditional_t<B4, u32x4, Frag>;
+  Frag af[2][FM];
+  FragB bfr[2][FN];
   int sa[2][FM], sb[2][FN];
   auto stage_ptrs = [&](int buf, const uint8_t*& as, const uint8_t*& bs, const uint32_t*& asc,
                         const uint32_t*& bsc) __attribute__((always_inline)) {
@@ -301,6 +316,10 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
     bs = lds + buf * SL::SIZE + SL::B;
     asc = (const uint32_t*)(lds + buf * SL::SIZE + SL::ASC);
     bsc = (const uint32_t*)(lds + buf * SL::SIZE + SL::BSC);
+  };
+  // the E2M1 operand's upper registers are not read
+  auto widened = [](u32x4 v) __attribute__((always_inline)) {
+    return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
   };
   // fragment q of sub-step kk of ring buffer buf into register set `set`: q < FM is
   // A fragment q, else B fragment q - FM
@@ -316,6 +335,18 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
     if constexpr (!MX) {
       const bf16x8 v = __builtin_bit_cast(bf16x8, *(const u32x4*)(base + swz<KB>(r, kk * 2 + lg)));
       if (isa) af[set][q] = v; else bfr[set][q - FM] = v;
+    } else if constexpr (B4) {
+      // E2M1 operand: lane group g holds the 32 codes (16 bytes) of scale block g of the 64-wide K step
+      const int blk = kk * 2 + lg;
+      const int sc = (int)(((isa ? asc : bsc)[blk / 4 * (SL::GSC / 4) + r] >> (8 * (blk & 3))) & 0xffu);
+      if (isa) {
+        const u32x4 lo = *(const u32x4*)(base + swz<KB>(r, kk * 4 + lg)), hi = *(const u32x4*)(base + swz<KB>(r, kk * 4 + 2 + lg));
+        af[set][q] = i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+        sa[set][q] = sc;
+      } else {
+        bfr[set][q - FM] = *(const u32x4*)(base + swz<KBB>(r, blk));
+        sb[set][q - FM] = sc;
+      }
     } else {
       // Operand layout of the 32x32x64 E4M3 MFMA: of a lane's 32 bytes, bytes
       // 0-15 belong to the first 32-element scale block of the 64-wide K step and
@@ -345,6 +376,9 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
       if (i < NL) {
         if constexpr (!MX)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[set][i], bfr[set][j], acc[i][j], 0, 0, 0);
+        else if constexpr (B4)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              af[set][i], widened(bfr[set][j]), acc[i][j], 0, 4, 0, sa[set][i], 0, sb[set][j]);
         else
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
               af[set][i], bfr[set][j], acc[i][j], 0, 0, 0, sa[set][i], 0, sb[set][j]);
@@ -371,6 +405,7 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
   auto read_np = [&](int buf, int kk, int q, uint32_t l0, uint32_t l4, auto nl)
       __attribute__((always_inline)) {
     static_assert(PF || KB == 128, "fragment addressing");
+    if constexpr (!B4) {
     constexpr int NL = decltype(nl)::value;
     if (q < FM ? q >= NL : NL == 0) return;
     const uint8_t* st = lds + buf * SL::SIZE;
@@ -388,6 +423,7 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
       else { bfr[0][q - FM] = v; sb[0][q - FM] = sc; }
     } else {
       read(buf, kk, q, 0, nl);
+    }
     }
   };
   const uint32_t l0_lane = (uint32_t)(lr * KB + ((lg ^ ((lr >> 1) & 7)) << 4)), l4_lane = (uint32_t)lr * 4;
@@ -407,7 +443,7 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
         if (i < NL) {
           if constexpr (!MX)
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[0][i], bfr[0][j], acc[i][j], 0, 0, 0);
-          else
+          else if constexpr (!B4)
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                 af[0][i], bfr[0][j], acc[i][j], 0, 0, 0, sa[0][i], 0, sb[0][j]);
         }

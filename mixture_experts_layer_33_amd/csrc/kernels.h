@@ -94,6 +94,21 @@ hipError_t launch_decode(const void* x, const float* w_r, const float* b_r, cons
                          int f, int fs, void* y, int32_t* topk_idx, float* topk_gate, void* ws,
                          hipStream_t st);
 
+// MXFP4: quantisation of a bf16 matrix along its rows, the product of bf16 rows, the layer for a few tokens
+hipError_t launch_quantize_mxfp4(const void* src, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
+                                 hipStream_t st);
+size_t matmul_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_matmul_mxfp4(const void* x, const uint8_t* w, const uint8_t* w_scale, int64_t M, int64_t N, int64_t K,
+                               bool f32_out, void* out, void* ws, hipStream_t st);
+struct Mx4Weights {
+  const uint8_t *gate, *up, *down, *s_gate, *s_up, *s_down;
+};
+size_t decode_mxfp4_workspace_bytes(int T, int d, int E, int k, int f, int fs);
+hipError_t launch_decode_mxfp4(const void* x, const float* w_r, const float* b_r, const float* balance,
+                               const ScoreRule& rule, const Mx4Weights& w, const Mx4Weights& shared, int T, int d, int E,
+                               int k, int f, int fs, void* y, int32_t* topk_idx, float* topk_gate, void* ws,
+                               hipStream_t st);
+
 // the whole forward in one cooperative launch (bf16)
 size_t fused_workspace_bytes(int64_t T, int64_t C, int d, int E, int f);
 hipError_t launch_forward_fused(const void* x, const float* w_r, const float* b_r,
