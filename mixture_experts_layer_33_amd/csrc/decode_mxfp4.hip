@@ -4,12 +4,13 @@
 //   h_tj = g_tj silu(W_gate[e] x_t) * (W_up[e] x_t)   (e: the j-th expert of token t; the shared expert's gate is 1)
 //   y_t  = sum_j W_down[e_tj] h_tj + W_s_down h_ts
 //
-// Every used expert's weights are read once, whatever the number of tokens that chose it: the tokens are the 16
-// columns of the MFMA's second operand.  h is formed in fp32 and kept as two bf16 parts, hi = bf16(h) and
-// lo = bf16(h - hi) (2^-17 of h is left out; y's own rounding is 2^-9).  Up to eight tokens the two parts are
-// columns t and t + 8 of one product, above that two products.
+// Every used expert's weights are read once, whatever the number of tokens that chose it (mx4.h: up to eight tokens are
+// columns of one product).  h is formed in fp32 and kept as two bf16 parts, hi = bf16(h) and lo = bf16(h - hi)
+// (2^-17 of h is left out; y's own rounding is 2^-9).
 #include <algorithm>
+#include <type_traits>
 
+#include "fp8_tile.h"
 #include "kernels.h"
 #include "mx4.h"
 
@@ -31,12 +32,24 @@ struct D4Args {
   bf16_t* y;
 };
 
-// The experts that the tokens chose, ascending, and which token has which of them as its how-manieth.
+// What the tokens chose: the experts, ascending (gate and up read each one's weights once for all tokens).
 struct D4List {
   uint32_t bits[32];                      // E <= 1024
+  int32_t below[32];                      // bits in the words before
   int32_t expert[D4_PAIRS];
-  uint8_t slot[D4_PAIRS][D4_TMAX];        // [place in the list][token]: j + 1, 0: not chosen
+  float gate[D4_PAIRS];                   // [token, j]
+  __attribute__((aligned(16))) uint8_t slot[D4_PAIRS][D4_TMAX];   // [place in the list][token]: j + 1, 0: not chosen
   int32_t U;
+};
+// ... and, for the down product, entries of an expert (the shared one, E, last) with up to four of its tokens, the columns of
+// one product: an expert of more tokens has several.  Up to four tokens in all a column is a token's own (-1: not chosen).
+constexpr int D4_COLS = 4;
+constexpr int D4_ENTRIES = D4_PAIRS + D4_TMAX / D4_COLS;
+struct D4Entries {
+  int32_t n, routed;
+  int16_t before[D4_PAIRS];               // entries of the experts before
+  int16_t expert[D4_ENTRIES];
+  int16_t row[D4_ENTRIES][D4_COLS];       // rows of h (t k + j; in the shared expert's part: t), -1: none
 };
 
 __device__ __forceinline__ void d4_list(const D4Args& p, D4List& L) {
@@ -47,208 +60,416 @@ __device__ __forceinline__ void d4_list(const D4Args& p, D4List& L) {
   for (int q = tid; q < n; q += blockDim.x) {
     const int e = p.topk_idx[q];
     atomicOr(&L.bits[e >> 5], 1u << (e & 31));
+    L.gate[q] = p.topk_gate[q];
+  }
+  __syncthreads();
+  if (tid < 64) {
+    const int own = tid < 32 ? __popc(L.bits[tid & 31]) : 0, incl = lanes_scan(own);
+    if (tid < 32) L.below[tid] = incl - own;
+    if (tid == 31) L.U = incl;
   }
   __syncthreads();
   for (int q = tid; q < n; q += blockDim.x) {
-    const int e = p.topk_idx[q];
-    int at = __popc(L.bits[e >> 5] & ((1u << (e & 31)) - 1u));
-    for (int w = 0; w < (e >> 5); ++w) at += __popc(L.bits[w]);
+    const int e = p.topk_idx[q], at = L.below[e >> 5] + __popc(L.bits[e >> 5] & ((1u << (e & 31)) - 1u));
     L.expert[at] = e;
     L.slot[at][q / p.k] = (uint8_t)(q % p.k + 1);
   }
-  if (tid == 0) {
-    int u = 0;
-    for (int w = 0; w < 32; ++w) u += __popc(L.bits[w]);
-    L.U = u;
+  __syncthreads();
+}
+
+__device__ __forceinline__ void d4_entries(const D4Args& p, const D4List& L, D4Entries& N) {
+  // chosen by which tokens: the slots that are not 0 in a place's 16 bytes
+  auto chosen = [&](int u) {
+    const u32x4 s = *(const u32x4*)L.slot[u];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m |= ((s[i / 4] >> (8 * (i % 4))) & 0xffu) ? 1u << i : 0u;
+    return m;
+  };
+  if (threadIdx.x < 64) {   // entries of the experts before each one: a scan, 64 experts at a time
+    int sum = 0;
+    for (int u0 = 0; u0 < L.U; u0 += 64) {
+      const int u = u0 + (int)threadIdx.x;
+      const int own = u < L.U ? (__popc(chosen(u)) + D4_COLS - 1) / D4_COLS : 0, incl = lanes_scan(own);
+      if (u < L.U) N.before[u] = (int16_t)(sum + incl - own);
+      sum += __builtin_amdgcn_readlane(incl, 63);
+    }
+    if (threadIdx.x == 0) N.routed = sum;
+  }
+  __syncthreads();
+  for (int u = threadIdx.x; u <= L.U; u += blockDim.x) {
+    const bool shared = u == L.U;
+    const int at = shared ? N.routed : N.before[u];
+    uint32_t m = !shared ? chosen(u) : p.fs > 0 ? (1u << p.T) - 1u : 0u;
+    const int parts = (__popc(m) + D4_COLS - 1) / D4_COLS;
+    for (int r = 0; r < parts; ++r) {
+      N.expert[at + r] = (int16_t)(shared ? p.E : L.expert[u]);
+      for (int i = 0; i < D4_COLS; ++i) {
+        int t = __ffs(m) - 1;             // -1: none left
+        if (p.T > D4_COLS) m &= m - 1;
+        else t = (m >> i) & 1u ? i : -1;
+        N.row[at + r][i] = (int16_t)(t < 0 || shared ? t : t * p.k + L.slot[u][t] - 1);
+      }
+    }
+    if (shared) N.n = at + parts;
   }
   __syncthreads();
 }
 
 // ------------------------------------------------------------------ gate and up
-// A unit is eight columns of f of one expert: an MFMA tile of their eight W_gate rows over their eight W_up rows.  The
-// workgroup's wavefronts split d and keep their part of the tokens in registers over all units.
-template <int PPW>
-__global__ __launch_bounds__(512) void d4_up_kernel(D4Args p) {
-  __shared__ D4List L;
-  __shared__ __attribute__((aligned(16))) float part[2][8][256];
+// A unit is eight columns of f of one expert: their eight W_gate rows and eight W_up rows.  The workgroup's NW wavefronts
+// split d (wavefront w has pairs w, w + NW, ...), keep their part of the tokens in registers over all units, and join
+// their sums through LDS in a fixed order, a group of units at a time.  D units are in flight: a pair's registers are
+// requested again, for the unit D further on, as soon as the pair is multiplied.  No branch stands between (a load that a branch
+// may skip makes every later wait a wait for all): past the last unit, and where d ends inside a pair, the addresses
+// lie outside their buffers, which costs no memory access, and x is zero.
+template <int TS>
+struct D4Part {                          // [half][gate, up][token][column]
+  static constexpr int GROUP = 4 / TS, SIZE = TS * 256;
+  float v[2 * GROUP][8][SIZE];
+};
+template <int PPW, int TS, int D>        // TS: sets of eight tokens
+__device__ __forceinline__ void d4_up(const D4Args& p, const D4List& L, D4Part<TS>& part) {
+  constexpr int GROUP = D4Part<TS>::GROUP;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), NW = blockDim.x >> 6;
-  const int g = lane >> 4, col = lane & 15;
+  const int g = lane >> 4, col = lane & 15, chunk = lane >> 3, row = lane & 7, P = (p.d + 255) / 256;
   const uint32_t rowb = (uint32_t)p.d / 2;
-  bf16x8 x[PPW][8];
+  bf16x8 x[PPW][TS][4];
 #pragma unroll
-  for (int i = 0; i < PPW; ++i) {
-    const int k = (i * NW + wave) * 256;
-    const bool in = k + 64 * g < p.d;
-    const bf16_t* xr = p.x + (int64_t)min(col, p.T - 1) * p.d + (in ? k + 64 * g : 0);
+  for (int i = 0; i < PPW; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const u32x4 v = *(const u32x4*)(xr + 8 * j);
-      x[i][j] = __builtin_bit_cast(bf16x8, in ? v : u32x4{0, 0, 0, 0});
+    for (int s = 0; s < TS; ++s) {
+      const int k = (i * NW + wave) * 256 + 64 * g + 32 * (col >> 3);
+      const bool in = k < p.d;
+      const bf16_t* xr = p.x + (int64_t)min(8 * s + (col & 7), p.T - 1) * p.d + (in ? k : 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const u32x4 v = *(const u32x4*)(xr + 8 * j);
+        x[i][s][j] = __builtin_bit_cast(bf16x8, in ? v : u32x4{0, 0, 0, 0});
+      }
     }
-  }
-  d4_list(p, L);
   // this workgroup's units: a share of the shared expert's, then of the routed ones
   const int U = L.U, per = p.f / 8, su = p.fs / 8, ru = U * per, G = gridDim.x, b = blockIdx.x;
   const int s0 = (int)((int64_t)su * b / G), s1 = (int)((int64_t)su * (b + 1) / G);
   const int r0 = (int)((int64_t)ru * b / G), r1 = (int)((int64_t)ru * (b + 1) / G);
   const int ns = s1 - s0, steps = ns + r1 - r0;
-  W4Pair w[2][PPW];
-  auto load = [&](int step, auto set) __attribute__((always_inline)) {
+  // the place of the unit whose loads come next
+  int n = -1, at = 0, i0 = 0;
+  __amdgpu_buffer_rsrc_t gr, ur, gs, us;
+  uint32_t from = 0, srows = 0, off = OUTSIDE, last_off = OUTSIDE;
+  const int last = (PPW - 1) * NW + wave;   // its last pair, which d may cut in half or leave out
+  const bool cut = last * 128 + chunk * 16 >= (int)rowb;
+  auto next = [&]() __attribute__((always_inline)) {
+    ++n;
+    const bool shared = n < ns, live = n < steps;
+    if (shared || n == ns) {
+      i0 = (shared ? s0 + n : r0 % per) * 8;
+      at = shared ? 0 : r0 / per;
+    } else {
+      i0 += 8;
+      if (i0 == p.f) {
+        i0 = 0;
+        ++at;
+      }
+    }
+    const int e = __builtin_amdgcn_readfirstlane(shared ? 0 : L.expert[min(at, U - 1)]), F = shared ? p.fs : p.f;
+    const uint32_t size = (uint32_t)F * rowb;
+    gr = buffer_of(either(shared, p.ws_gate, p.w_gate) + (int64_t)e * size, size);
+    ur = buffer_of(either(shared, p.ws_up, p.w_up) + (int64_t)e * size, size);
+    from = live ? i0 * rowb : 0;
+    off = live ? row * rowb + chunk * 16 : OUTSIDE;
+    last_off = cut ? OUTSIDE : off;
+    srows = (uint32_t)(shared ? p.fs : p.E * p.f) * 4;
+    const uint32_t sfrom = (uint32_t)(e * F + (live ? i0 : 0)) * 4, sbytes = (uint32_t)(p.d / 128) * srows - sfrom;
+    gs = buffer_of(either(shared, p.ss_gate, p.s_gate) + sfrom, sbytes);
+    us = buffer_of(either(shared, p.ss_up, p.s_up) + sfrom, sbytes);
+  };
+  W4Pair w[D][PPW];
+  auto load = [&](W4Pair& q, int i) __attribute__((always_inline)) {
+    const uint32_t pair = i * NW + wave, so = min(pair, (uint32_t)P - 1) * 2 * srows;
+    const uint32_t sl = (i == PPW - 1 && cut ? 0 : (chunk >> 2) * srows) + row * 4;
+    q.a = load_b128_nt(gr, i == PPW - 1 ? last_off : off, from + pair * 128);
+    q.b = load_b128_nt(ur, i == PPW - 1 ? last_off : off, from + pair * 128);
+    q.sa = load_b32(gs, sl, so);
+    q.sb = load_b32(us, sl, so);
+  };
+  // unit m of the workgroup, whose codes are in the set; the set takes the unit D further on
+  auto step = [&](int m, auto set) __attribute__((always_inline)) {
     constexpr int S = decltype(set)::value;
-    const bool shared = step < ns;
-    const int unit = shared ? s0 + step : r0 + step - ns;
-    const int at = shared ? 0 : unit / per, i0 = (shared ? unit : unit % per) * 8;
-    const int e = __builtin_amdgcn_readfirstlane(shared ? 0 : L.expert[at]), F = shared ? p.fs : p.f;
-    const uint32_t bytes = (uint32_t)F * rowb;
-    const __amdgpu_buffer_rsrc_t gr = buffer_of((shared ? p.ws_gate : p.w_gate) + (int64_t)e * bytes, bytes);
-    const __amdgpu_buffer_rsrc_t ur = buffer_of((shared ? p.ws_up : p.w_up) + (int64_t)e * bytes, bytes);
-    const int64_t rows = shared ? p.fs : (int64_t)p.E * p.f;
-    const uint8_t* sc = col < 8 ? (shared ? p.ss_gate : p.s_gate) : (shared ? p.ss_up : p.s_up);
-    const uint8_t* sr = sc + ((int64_t)e * F + i0 + (col & 7)) * 4;
+    f32x4 ag[TS] = {}, au[TS] = {};
+    next();
 #pragma unroll
     for (int i = 0; i < PPW; ++i) {
-      const int pair = i * NW + wave;
-      const uint32_t off = (uint32_t)pair * 128 + (lane >> 3) * 16;
-      const uint32_t o = off < rowb ? (uint32_t)(i0 + (lane & 7)) * rowb + off : OUTSIDE;
-      w[S][i].a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(gr, o, 0, NT_LOAD));
-      w[S][i].b = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ur, o, 0, NT_LOAD));
-      const int kb = min(pair * 2 + (g >> 1), p.d / 128 - 1);
-      w[S][i].s = *(const uint32_t*)(sr + kb * rows * 4);
-    }
-  };
-  auto consume = [&](int step, auto set) __attribute__((always_inline)) {
-    constexpr int S = decltype(set)::value;
-    f32x4 acc0{}, acc1{};
+      const float fa = chunk_scale(w[S][i].sa), fb = chunk_scale(w[S][i].sb);
 #pragma unroll
-    for (int i = 0; i < PPW; ++i) mul_pair(rows_of(w[S][i]), x[i], acc0, acc1);
-    float(*to)[256] = part[S];
-    *(f32x4*)&to[wave][col * 16 + 4 * g] = acc0 + acc1;
-    lds_barrier();
-    for (int o8 = tid; o8 < 8 * p.T; o8 += blockDim.x) {
-      const bool shared = step < ns;
-      const int unit = shared ? s0 + step : r0 + step - ns;
-      const int at = shared ? 0 : unit / per, i = (shared ? unit : unit % per) * 8 + (o8 & 7), t = o8 >> 3;
-      const int j = shared ? 1 : (int)L.slot[at][t];
-      if (j > 0) {
-        const int q = t * 16 + (o8 & 7);
-        float a = to[0][q], u = to[0][q + 8];
-        for (int v = 1; v < NW; ++v) {
-          a += to[v][q];
-          u += to[v][q + 8];
+      for (int j = 0; j < 4; ++j) {
+        const bf16x8 a = widen4(w[S][i].a[j], fa), u = widen4(w[S][i].b[j], fb);
+#pragma unroll
+        for (int s = 0; s < TS; ++s) {
+          ag[s] = mfma16(a, x[i][s][j], ag[s]);
+          au[s] = mfma16(u, x[i][s][j], au[s]);
         }
-        float h = silu(a) * u;
-        const int64_t n = (int64_t)p.T * p.k * p.f;
-        if (!shared) h *= p.topk_gate[t * p.k + j - 1];
-        const bf16_t hi = f2bf(h), lo = f2bf(fabsf(h) < 3.39e38f ? h - bf2f(hi) : 0.f);   // an infinite hi has no rest
-        bf16_t* o = shared ? p.h + 2 * n + (int64_t)t * p.fs + i : p.h + (int64_t)(t * p.k + j - 1) * p.f + i;
-        o[0] = hi;
-        o[shared ? (int64_t)p.T * p.fs : n] = lo;
+      }
+      load(w[S][i], i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (holds_half()) {
+#pragma unroll
+      for (int s = 0; s < TS; ++s) {
+        float* to = part.v[m % (2 * GROUP)][wave] + s * 256 + (col >> 3) * 128 + (col & 7) * 8 + 4 * (g & 1);
+        *(f32x4*)to = ag[s];
+        *(f32x4*)(to + 64) = au[s];
       }
     }
   };
-  using A = std::integral_constant<int, 0>;
-  using B = std::integral_constant<int, 1>;
-  if (steps > 0) load(0, A{});
-  for (int s = 0; s < steps; s += 2) {
-    if (s + 1 < steps) load(s + 1, B{});
-    consume(s, A{});
-    if (s + 1 >= steps) break;
-    if (s + 2 < steps) load(s + 2, A{});
-    consume(s + 1, B{});
+  // h of units m0 .. m0 + count - 1
+  auto flush = [&](int m0, int count) __attribute__((always_inline)) {
+    lds_barrier();
+    const int turn = wave + m0 / GROUP % NW, first = (turn >= NW ? turn - NW : turn) * 64 + lane;
+    for (int q = first; q < 8 * GROUP * p.T; q += blockDim.x) {
+      const int m = q / 8 % GROUP, t = q / (8 * GROUP);
+      if (m >= count) continue;
+      const bool shared = m0 + m < ns;
+      const int unit = shared ? s0 + m0 + m : r0 + m0 + m - ns;
+      const int place = shared ? 0 : unit / per, i = (shared ? unit : unit % per) * 8 + q % 8;
+      const int j = shared ? 1 : (int)L.slot[place][t];
+      if (j == 0) continue;
+      const float(*sums)[D4Part<TS>::SIZE] = part.v[(m0 + m) % (2 * GROUP)];
+      const int c = (t >> 3) * 256 + (t & 7) * 8 + q % 8;
+      float a = 0.f, u = 0.f;
+      for (int v = 0; v < NW; ++v) {
+        a += sums[v][c] + sums[v][c + 128];
+        u += sums[v][c + 64] + sums[v][c + 192];
+      }
+      float h = silu(a) * u;
+      if (!shared) h *= L.gate[t * p.k + j - 1];
+      const bf16_t hi = f2bf(h), lo = f2bf(fabsf(h) < 3.39e38f ? h - bf2f(hi) : 0.f);   // an infinite hi has no rest
+      const int64_t all = (int64_t)p.T * p.k * p.f;
+      bf16_t* o = shared ? p.h + 2 * all + (int64_t)t * p.fs + i : p.h + (int64_t)(t * p.k + j - 1) * p.f + i;
+      o[0] = hi;
+      o[shared ? (int64_t)p.T * p.fs : all] = lo;
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < D; ++s) {
+    next();
+#pragma unroll
+    for (int i = 0; i < PPW; ++i) load(w[s][i], i);
+  }
+  for (int m = 0; m < steps; m += D) {
+    unrolled<D>([&](auto s) __attribute__((always_inline)) {
+      constexpr int S = decltype(s)::value;
+      step(m + S, s);
+      const int done = m + S + 1;
+      if (done <= steps && (done % GROUP == 0 || done == steps)) {
+        const int m0 = (done - 1) / GROUP * GROUP;
+        flush(m0, done - m0);
+      }
+    });
   }
 }
 
-// ------------------------------------------------------------------ down
-// A workgroup owns RW <= 16 NT output rows.  The columns of all used experts (then the shared one's) are one long sum, cut into
-// pairs of 256 that the wavefronts take in turn; a token that did not choose an expert reads zeros.
-template <int NT, bool MANY>   // MANY: more than eight tokens
-__global__ __launch_bounds__(512) void d4_down_kernel(D4Args p, int RW) {
+template <int PPW, int TS, int D>
+__global__ __launch_bounds__(512) void d4_up_kernel(D4Args p) {
   __shared__ D4List L;
-  __shared__ __attribute__((aligned(16))) float part[NT][8][256];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), NW = blockDim.x >> 6;
-  const int g = lane >> 4, col = lane & 15, t = MANY ? col : col & 7;
+  __shared__ __attribute__((aligned(16))) D4Part<TS> part;
   d4_list(p, L);
-  const int U = L.U, per = (p.f + 255) / 256, pers = (p.fs + 255) / 256, steps = U * per + pers;
-  const int64_t n = (int64_t)p.T * p.k * p.f, ns = (int64_t)p.T * p.fs;
-  const __amdgpu_buffer_rsrc_t hr = buffer_of(p.h, (uint32_t)(4 * (n + ns)));
-  constexpr int PL = MANY ? 2 : 1;   // parts of h a lane holds
+  d4_up<PPW, TS, D>(p, L, part);
+}
+
+// ------------------------------------------------------------------ down
+// A workgroup owns `rows` <= 16 NT output rows from o0 on.  The columns of all entries are cut into runs of up to `run` pairs,
+// which the wavefronts take in turn, D pairs in flight.  A run of four starts at another of its pairs from workgroup to
+// workgroup: all of the chip would read the same 128 bytes of every 1024 at a time.
+//
+// A pair's h (up to four tokens, hi and lo of 256 columns: 1 KB a token) comes by global -> LDS copies of one
+// instruction a token; read straight into the MFMA's layout it took eight 16-byte loads a lane, nearly all of them of
+// columns without a token, at 16 clocks each (decode of 8 tokens, this kernel: 103 us, 82 with no h at all).  Columns
+// c and c + 4 of a chunk are hi and lo of token c: one MFMA for both.  The copies are issued before the pair's weights,
+// so a wait that leaves no more than the weights of D pairs outstanding is past them.
+//
+// At the end, and with more than four tokens when the entry changes, the sums of the columns are added to the
+// wavefront's sums of all tokens in LDS, [NW][half][16][16 NT].
+template <int NT, int D>
+struct D4Down {
+  u32x4 h[8][D][D4_COLS][64];            // [wavefront][in flight][column][hi, lo: 32 pieces of eight columns each]
+  float y[8][2][D4_TMAX][16 * NT];
+};
+template <int NT, int D>
+__device__ __forceinline__ void d4_down(const D4Args& p, const D4Entries& N, D4Down<NT, D>& m, int o0, int rows) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), NW = blockDim.x >> 6;
+  const int g = lane >> 4, col = lane & 15, chunk = lane >> 3, row = lane & 7;
+  for (int i = tid; i < NW * 2 * D4_TMAX * 16 * NT; i += blockDim.x) (&m.y[0][0][0][0])[i] = 0.f;
+  const int per = (p.f + 255) / 256, pers = (p.fs + 255) / 256, run = p.T > D4_COLS ? 4 : 1;
+  const int entries = __builtin_amdgcn_readfirstlane(N.n), routed = __builtin_amdgcn_readfirstlane(N.routed);
+  const int runs = (per + run - 1) / run, runss = (pers + run - 1) / run, all = routed * runs + (entries - routed) * runss;
+  const int64_t nh = (int64_t)p.T * p.k * p.f, nsh = (int64_t)p.T * p.fs;
+  // pair `i` of run number `n`, `length` long, of an entry
+  struct Place {
+    int n, i, entry, from, length;
+  };
+  auto set = [&](Place& at) __attribute__((always_inline)) {
+    const bool shared = at.n >= routed * runs;
+    const int q = shared ? at.n - routed * runs : at.n, of = shared ? runss : runs;
+    const int en = q / of, r = q - en * of;
+    at.entry = min(shared ? routed + en : en, entries - 1);
+    at.from = r * run;
+    at.length = min(run, (shared ? pers : per) - at.from);
+    at.i = 0;
+  };
+  auto advance = [&](Place& at) __attribute__((always_inline)) {   // whether that is another run
+    if (++at.i < at.length) return false;
+    at.n += NW;
+    set(at);
+    return true;
+  };
+  const int turned = blockIdx.x & 3;
+  int F = 0;
+  Place next{wave, 0, 0, 0, 0};    // whose loads come next
+  set(next);
+  __amdgpu_buffer_rsrc_t wr, sr;
+  const bf16_t* hbase = nullptr;
+  int hrow[D4_COLS];
+  uint32_t plane = 0, rowb = 0, srows = 0, lane_off[2 * NT];
+  auto enter = [&]() __attribute__((always_inline)) {   // next.entry
+    const int at = next.entry, ex = __builtin_amdgcn_readfirstlane((int)N.expert[at]);
+    const bool shared = ex == p.E;
+    const int e = shared ? 0 : ex;
+    F = shared ? p.fs : p.f;
+    rowb = (uint32_t)F / 2;
+    const uint32_t bytes = (uint32_t)p.d * rowb;
+    wr = buffer_of(either(shared, p.ws_down, p.w_down) + (int64_t)e * bytes, bytes);
+    srows = (uint32_t)(shared ? p.d : p.E * p.d) * 4;
+    const uint32_t sfrom = (uint32_t)(e * p.d + o0) * 4;
+    sr = buffer_of(either(shared, p.ss_down, p.s_down) + sfrom, (uint32_t)(F / 128) * srows - sfrom);
+#pragma unroll
+    for (int r = 0; r < 2 * NT; ++r) lane_off[r] = 8 * r + row < rows ? (uint32_t)(o0 + 8 * r + row) * rowb + chunk * 16 : OUTSIDE;
+    const uint2 rw = *(const uint2*)N.row[at];
+#pragma unroll
+    for (int c = 0; c < D4_COLS; ++c)
+      hrow[c] = (int)(int16_t)(__builtin_amdgcn_readfirstlane((int)(c < 2 ? rw.x : rw.y)) >> (16 * (c & 1)));
+    hbase = p.h + (shared ? 2 * nh : 0);
+    plane = (uint32_t)(2 * (shared ? nsh : nh));
+  };
+  enter();
   struct Step {
     W4Pair w[NT];
-    u32x4 h[PL][8];
   };
+  auto load = [&](Step& s, int slot) __attribute__((always_inline)) {
+    const bool live = next.n < all;
+    const int pair = live ? next.from + (next.length == 4 ? (next.i + turned) & 3 : next.i) : 0;
+    if (live) {
+      // 16 bytes a lane: lanes 0-31 hi, 32-63 lo; where F ends inside the pair its first half again (the codes are zeros there)
+      const uint32_t at = ((uint32_t)lane & 31) * 8 + pair * 256 < (uint32_t)F ? (lane & 31) * 16 : (lane & 15) * 16;
+      const uint32_t off = (lane < 32 ? 0 : plane) + at;
+#pragma unroll
+      for (int c = 0; c < D4_COLS; ++c) {
+        u32x4* to = m.h[wave][slot][c];
+        if (hrow[c] >= 0)
+          dma16(hbase + (int64_t)hrow[c] * F + pair * 256, off, __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to));
+        else if (p.T <= D4_COLS && c < p.T)
+          to[lane] = u32x4{0, 0, 0, 0};
+      }
+    }
+    const uint32_t so = pair * 128, ss = pair * 2 * srows;
+    const uint32_t sl = (pair * 2 + (chunk >> 2) < F / 128 ? (chunk >> 2) * srows : 0) + row * 4;
+    const bool in = live && so + chunk * 16 < rowb;
+#pragma unroll
+    for (int r = 0; r < NT; ++r) {
+      s.w[r].a = load_b128_nt(wr, in ? lane_off[2 * r] + so : OUTSIDE, 0);
+      s.w[r].b = load_b128_nt(wr, in ? lane_off[2 * r + 1] + so : OUTSIDE, 0);
+      s.w[r].sa = load_b32(sr, 8 * (2 * r) + row < rows ? sl + 64 * r : 0, ss);
+      s.w[r].sb = load_b32(sr, 8 * (2 * r + 1) + row < rows ? sl + 64 * r + 32 : 0, ss);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (advance(next) && next.n < all) enter();
+  };
+  f32x4 acc[2 * NT];
+#pragma unroll
+  for (int r = 0; r < 2 * NT; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+  Place now{wave, 0, 0, 0, 0};     // which is multiplied next
+  set(now);
+  auto flush = [&](int entry) __attribute__((always_inline)) {
+    const int ex = (int)N.expert[entry], hr = N.row[entry][col & 3];
+    const int t = p.T <= D4_COLS ? ((col & 3) < p.T ? col & 3 : -1) : ex == p.E ? hr : hr >= 0 ? hr / p.k : -1;
+    const bool mine = holds_half() && (col & 4) == 0 && t >= 0;
+    float* to = m.y[wave][col >> 3][max(t, 0)] + 4 * (g & 1);
+#pragma unroll
+    for (int r = 0; r < 2 * NT; ++r) {
+      f32x4 v = acc[r];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)   // hi's sum and lo's, four lanes on
+        v[i] += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[i]), 0x104, 0xf, 0xf, true));
+      if (mine) *(f32x4*)(to + 8 * r) = *(f32x4*)(to + 8 * r) + v;
+      acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  };
+  auto consume = [&](Step& s, int slot) __attribute__((always_inline)) {
+    wait_vm<4 * NT * D>();
+    __builtin_amdgcn_sched_barrier(0);
+    const u32x4* from = m.h[wave][slot][col & 3] + ((col >> 2) & 1) * 32 + 8 * g + 4 * (col >> 3);
+    bf16x8 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __builtin_bit_cast(bf16x8, from[i]);
+#pragma unroll
+    for (int r = 0; r < NT; ++r) {
+      const float fa = chunk_scale(s.w[r].sa), fb = chunk_scale(s.w[r].sb);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[2 * r] = mfma16(widen4(s.w[r].a[i], fa), h[i], acc[2 * r]);
+        acc[2 * r + 1] = mfma16(widen4(s.w[r].b[i], fb), h[i], acc[2 * r + 1]);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (now.n >= all) return;
+    const int was = now.entry;
+    if (advance(now) && (p.T > D4_COLS || now.n >= all)) flush(was);
+  };
+  __syncthreads();   // the zeros
+  {
+    Step s[D];
+#pragma unroll
+    for (int i = 0; i < D; ++i) load(s[i], i);
+    while (now.n < all) {
+#pragma unroll
+      for (int i = 0; i < D; ++i) {
+        consume(s[i], i);
+        load(s[i], i);
+      }
+    }
+  }
+  wait_vm<0>();      // no copy outlives the array
+  __syncthreads();
+  for (int q = tid; q < 16 * NT * p.T; q += blockDim.x) {
+    const int r = q % (16 * NT), t = q / (16 * NT);
+    if (r >= rows) continue;
+    float sum = 0.f;
+    for (int v = 0; v < NW; ++v) sum += m.y[v][0][t][r] + m.y[v][1][t][r];
+    p.y[(int64_t)t * p.d + o0 + r] = f2bf(sum);
+  }
+}
+
+template <int NT, int D>
+__global__ __launch_bounds__(512) void d4_down_kernel(D4Args p, int RW) {
+  __shared__ D4List L;
+  __shared__ D4Entries N;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  d4_list(p, L);
+  d4_entries(p, L, N);
   for (int o0 = blockIdx.x * RW; o0 < p.d; o0 += gridDim.x * RW) {
-    const int rows = min(RW, p.d - o0);
-    auto load = [&](int step, Step& s) __attribute__((always_inline)) {
-      const bool shared = step >= U * per;
-      const int at = shared ? 0 : step / per, pair = shared ? step - U * per : step % per;
-      const int e = __builtin_amdgcn_readfirstlane(shared ? 0 : L.expert[at]), F = shared ? p.fs : p.f;
-      const uint32_t rowb = (uint32_t)F / 2, bytes = (uint32_t)p.d * rowb;
-      const __amdgpu_buffer_rsrc_t wr = buffer_of((shared ? p.ws_down : p.w_down) + (int64_t)e * bytes, bytes);
-      const uint32_t off = (uint32_t)pair * 128 + (lane >> 3) * 16;
-      const int kb = min(pair * 2 + (g >> 1), F / 128 - 1);
-      const uint8_t* sr = (shared ? p.ss_down : p.s_down) + ((int64_t)kb * (shared ? p.d : (int64_t)p.E * p.d) + (int64_t)e * p.d) * 4;
-#pragma unroll
-      for (int r = 0; r < NT; ++r) {
-        const int ra = 16 * r + (lane & 7), rb = ra + 8;
-        s.w[r].a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                 wr, ra < rows && off < rowb ? (uint32_t)(o0 + ra) * rowb + off : OUTSIDE, 0, NT_LOAD));
-        s.w[r].b = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                 wr, rb < rows && off < rowb ? (uint32_t)(o0 + rb) * rowb + off : OUTSIDE, 0, NT_LOAD));
-        s.w[r].s = *(const uint32_t*)(sr + (int64_t)min(o0 + 16 * r + col, p.d - 1) * 4);
-      }
-      const int j = t >= p.T ? 0 : shared ? 1 : (int)L.slot[at][t], k0 = pair * 256 + 64 * g;
-      const int64_t row = shared ? 2 * n + (int64_t)t * p.fs : (int64_t)(t * p.k + j - 1) * p.f;
-#pragma unroll
-      for (int q = 0; q < PL; ++q) {
-        const int64_t plane = (MANY ? q : col >> 3) * (shared ? ns : n);
-        const uint32_t o = j > 0 && k0 < F ? (uint32_t)(2 * (plane + row + k0)) : OUTSIDE;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          s.h[q][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(hr, o == OUTSIDE ? o : o + 16 * i, 0, 0));
-      }
-    };
-    f32x4 acc[NT][2];
-#pragma unroll
-    for (int r = 0; r < NT; ++r) acc[r][0] = acc[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto consume = [&](const Step& s) __attribute__((always_inline)) {
-#pragma unroll
-      for (int r = 0; r < NT; ++r) {
-        const W4Rows w = rows_of(s.w[r]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bf16x8 wp = widen4(w.p[i], w.sp), wq = widen4(w.q[i], w.sq);
-#pragma unroll
-          for (int q = 0; q < PL; ++q) {
-            acc[r][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wp, __builtin_bit_cast(bf16x8, s.h[q][i]), acc[r][0], 0, 0, 0);
-            acc[r][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wq, __builtin_bit_cast(bf16x8, s.h[q][4 + i]), acc[r][1], 0, 0, 0);
-          }
-        }
-      }
-    };
-    Step sa, sb;
-    if (wave < steps) load(wave, sa);
-    for (int s = wave; s < steps; s += 2 * NW) {
-      if (s + NW < steps) load(s + NW, sb);
-      consume(sa);
-      if (s + NW >= steps) break;
-      if (s + 2 * NW < steps) load(s + 2 * NW, sa);
-      consume(sb);
-    }
-#pragma unroll
-    for (int r = 0; r < NT; ++r) *(f32x4*)&part[r][wave][col * 16 + 4 * g] = acc[r][0] + acc[r][1];
-    __syncthreads();
-    for (int q = tid; q < 16 * NT * p.T; q += blockDim.x) {
-      const int r = q % (16 * NT), tok = q / (16 * NT);
-      if (r < rows) {
-        const float(*from)[256] = part[r / 16];
-        const int at = tok * 16 + r % 16;
-        float sum = 0.f;
-        for (int v = 0; v < NW; ++v) sum += MANY ? from[v][at] : from[v][at] + from[v][at + 128];
-        p.y[(int64_t)tok * p.d + o0 + r] = f2bf(sum);
-      }
-    }
+    d4_down<NT, D>(p, N, *(D4Down<NT, D>*)lds, o0, min(RW, p.d - o0));
     __syncthreads();
   }
+}
+
+template <int NT, int D>
+static hipError_t run_down(const D4Args& a, int RW, int grid, hipStream_t st) {
+  auto kern = d4_down_kernel<NT, D>;
+  const size_t lds = sizeof(D4Down<NT, D>);
+  const hipError_t err = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (err != hipSuccess) return err;
+  kern<<<grid, 512, lds, st>>>(a, RW);
+  return hipGetLastError();
 }
 
 // Workspace: the router's logit planes | expert counts [E] | h [2][T k f] | [2][T fs].
@@ -275,23 +496,19 @@ hipError_t launch_decode_mxfp4(const void* x, const float* w_r, const float* b_r
                  shared.s_gate, shared.s_up, shared.s_down, T, d, E, k, f, fs, topk_idx, topk_gate,
                  (bf16_t*)(base + d4_route_bytes(T, E, d) + 4096), (bf16_t*)y};
   const int P = (d + 255) / 256, nw = std::min(8, P), ppw = (P + nw - 1) / nw;
+#define UP(N)                                                               \
+  case N:                                                                   \
+    if (T > 8) d4_up_kernel<N, 2, N <= 2 ? 4 : 2><<<ncu, 64 * nw, 0, st>>>(a);   \
+    else d4_up_kernel<N, 1, N <= 2 ? 4 : 3><<<ncu, 64 * nw, 0, st>>>(a);         \
+    break;
   switch (ppw) {
-    case 1: d4_up_kernel<1><<<ncu, 64 * nw, 0, st>>>(a); break;
-    case 2: d4_up_kernel<2><<<ncu, 64 * nw, 0, st>>>(a); break;
-    case 3: d4_up_kernel<3><<<ncu, 64 * nw, 0, st>>>(a); break;
-    case 4: d4_up_kernel<4><<<ncu, 64 * nw, 0, st>>>(a); break;
+    UP(1) UP(2) UP(3) UP(4)
     default: return hipErrorInvalidValue;
   }
+#undef UP
   if ((err = hipGetLastError()) != hipSuccess) return err;
   const int RW = std::min(D4_ROWS, std::max(8, (d + ncu - 1) / ncu)), g2 = (d + RW - 1) / RW;
-  if (RW <= 16) {
-    if (T > 8) d4_down_kernel<1, true><<<g2, 512, 0, st>>>(a, RW);
-    else d4_down_kernel<1, false><<<g2, 512, 0, st>>>(a, RW);
-  } else {
-    if (T > 8) d4_down_kernel<2, true><<<g2, 512, 0, st>>>(a, RW);
-    else d4_down_kernel<2, false><<<g2, 512, 0, st>>>(a, RW);
-  }
-  return hipGetLastError();
+  return RW <= 16 ? run_down<1, 4>(a, RW, g2, st) : run_down<2, 3>(a, RW, g2, st);
 }
 
 }  // namespace moe

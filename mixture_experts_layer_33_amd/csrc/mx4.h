@@ -2,18 +2,23 @@
 // MX scale layout [cols / 128][rows][4]) as operands of the bf16 MFMA: the loads and the widening that the
 // weight-stream kernels share.
 //
-// A wavefront takes 16 weight rows x 256 columns (a "pair" of 128-column groups) per step: two 16-byte loads a lane,
-// in which eight lanes cover the 128 contiguous bytes of one row (a request for half a 128-byte line moves the
-// whole of it).  The first load holds rows 0-7, the second rows 8-15; lane l has row l & 7, 16-byte chunk l >> 3,
-// and a chunk is one scale block of 32 columns.  The MFMA wants row l & 15 in every lane: lanes 8 apart trade halves
-// (a DPP move of eight lanes within a row of 16), after which a lane holds chunks 2g and 2g + 1 of its row (g = l >> 4).
-// Which columns a lane group holds is free as long as the tokens' operand agrees, so x is read in that
-// order: columns 64 g .. 64 g + 63 of the pair.
+// A wavefront takes 16 weight rows x 256 columns (a "pair" of 128-column groups) per step, in two 16-byte loads a lane of
+// eight rows each: eight lanes cover the 128 contiguous bytes of one row (a request for half a 128-byte line moves
+// the whole of it).  Lane l holds row l & 7, 16-byte chunk l >> 3, and a chunk is one scale block of 32 columns.
+//
+// The 16x16x32 MFMA reads lane l as row l & 15 of its first operand, columns of lane group g = l >> 4.  So rows 0-7 of the
+// operand are the eight weight rows with chunk 2g, and rows 8-15 the same weight rows with chunk 2g + 1.  The second
+// operand's columns are split alike: column c < 8 is token c's chunk 2g, column c + 8 its chunk 2g + 1.  Of the 16 x 16
+// results those with row < 8 and column < 8 or with both >= 8 are sums of the product, in two halves to be added; the
+// others mix a chunk with another's token and are dropped.  No lane moves a value to another, a token takes half the registers
+// that an operand of 16 tokens would, and up to eight tokens the MFMAs are as many as without the split.
 //
 // The codes widen to bf16 by gfx950's v_cvt_scalef32_pk_bf16_fp4 (two codes and the block's scale in one instruction at the
 // full VALU rate; checked for every byte, byte place and scale from 2^-127 up: code value x 2^(byte - 127), NaN for byte
 // 255).  E2M1 x 2^X is exact in bf16, products and sums are the bf16 MFMA's in fp32.
 #pragma once
+
+#include <type_traits>
 
 #include "common.h"
 
@@ -22,19 +27,36 @@ namespace moe {
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr uint32_t RSRC_WORD3 = 0x00027000;   // raw buffer, 32-bit data
-constexpr uint32_t OUTSIDE = 0xfffffff0u;      // an offset past every buffer: the load returns zeros
+constexpr uint32_t OUTSIDE = 0x80000000u;      // an offset past every buffer (they are below 2 GiB): the load returns zeros
 constexpr int NT_LOAD = 2;                     // cache policy of a buffer load: non-temporal
 
+// (offset: per lane, `at`: of the wavefront, which has to be at most the buffer's size)
+__device__ __forceinline__ u32x4 load_b128(__amdgpu_buffer_rsrc_t r, uint32_t offset, uint32_t at) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)offset, (int)at, 0));
+}
+__device__ __forceinline__ u32x4 load_b128_nt(__amdgpu_buffer_rsrc_t r, uint32_t offset, uint32_t at) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)offset, (int)at, NT_LOAD));
+}
+__device__ __forceinline__ uint32_t load_b32(__amdgpu_buffer_rsrc_t r, uint32_t offset, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b32(r, (int)offset, (int)at, 0);
+}
+// One of two addresses that are the same in the whole wavefront.  Both are scalar registers by then: a choice between kernel
+// arguments may otherwise become a load from a chosen place of the argument block, address and buffer per lane.
+__device__ __forceinline__ const uint8_t* either(bool first, const uint8_t* a, const uint8_t* b) {
+  uint64_t u = (uint64_t)a, v = (uint64_t)b;
+  asm("" : "+s"(u), "+s"(v));
+  return (const uint8_t*)(first ? u : v);
+}
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)bytes, (int)RSRC_WORD3);
 }
 
 struct W4Pair {
-  u32x4 a, b;      // rows 0-7, rows 8-15
-  uint32_t s;      // the four scale bytes of row l & 15, columns 128 (g / 2) .. of the pair
+  u32x4 a, b;          // two times eight rows
+  uint32_t sa, sb;     // the four scale bytes of the row's 128 columns in which the chunk lies
 };
 
-// Four dwords of codes of one row and block -> acc += W x over the block's 32 columns of each lane group.
+// Eight codes of one row and block as bf16.
 __device__ __forceinline__ bf16x8 widen4(uint32_t codes, float scale) {
   const bf16x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
   const bf16x2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1);
@@ -43,31 +65,25 @@ __device__ __forceinline__ bf16x8 widen4(uint32_t codes, float scale) {
   return bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// The pair's halves traded between lanes 8 apart: p, q hold chunks 2g, 2g + 1 of row l & 15; sp, sq their scales.
-struct W4Rows {
-  u32x4 p, q;
-  float sp, sq;
-};
-__device__ __forceinline__ W4Rows rows_of(const W4Pair& w) {
-  W4Rows r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // row_ror:8 hands lane i the value of lane i ^ 8 of its row of 16; only the banks named are written
-    r.p[i] = (uint32_t)__builtin_amdgcn_update_dpp((int)w.a[i], (int)w.b[i], 0x128, 0xf, 0xc, false);
-    r.q[i] = (uint32_t)__builtin_amdgcn_update_dpp((int)w.b[i], (int)w.a[i], 0x128, 0xf, 0x3, false);
-  }
-  const uint32_t s = w.s >> (threadIdx.x & 16);   // bytes 2 (g & 1), 2 (g & 1) + 1
-  r.sp = __uint_as_float((s & 0xffu) << 23);
-  r.sq = __uint_as_float((s & 0xff00u) << 15);
-  return r;
+// The scale of this lane's chunk, from the word that holds it, as the conversion takes it.
+__device__ __forceinline__ float chunk_scale(uint32_t word) {
+  const int c = (threadIdx.x >> 3) & 3;
+  return __uint_as_float(__builtin_amdgcn_ubfe(word, 8 * c, 8) << 23);
 }
 
-// acc0, acc1 += W x over the pair's 256 columns; x[i]: columns 64 g + 8 i .. + 7 of token l & 15.
-__device__ __forceinline__ void mul_pair(const W4Rows& r, const bf16x8 (&x)[8], f32x4& acc0, f32x4& acc1) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    acc0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen4(r.p[i], r.sp), x[i], acc0, 0, 0, 0);
-    acc1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen4(r.q[i], r.sq), x[4 + i], acc1, 0, 0, 0);
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// This lane's results (rows 4 (g & 1) .. + 3 of the eight, token l & 7) are one of the two halves; else they are dropped.
+__device__ __forceinline__ bool holds_half() { return ((threadIdx.x >> 5) & 1) == ((threadIdx.x >> 3) & 1); }
+
+// f(0), ..., f(N - 1) with constant arguments.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unrolled(F f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    unrolled<N, I + 1>(f);
   }
 }
 

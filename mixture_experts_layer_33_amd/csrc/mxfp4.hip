@@ -1,5 +1,6 @@
 // MXFP4 weights: their quantisation, and the product of bf16 rows with them.
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "mx4.h"
@@ -58,10 +59,11 @@ hipError_t launch_quantize_mxfp4(const void* src, int64_t rows, int64_t cols, ui
 }
 
 // ------------------------------------------------------------------ product, few rows
-// out[m][n] = sum_k x[m][k] W[n][k] for up to 16 rows of x: a weight stream.  A unit is 16 weight rows; a workgroup's
-// wavefronts split its columns (wavefront w takes pairs w, w + NW, ...: together they read whole rows), keep
-// their part of x in registers over all units of the workgroup, and join their 16 x 16 sums through LDS in a
-// fixed order.  The next unit's codes are requested before a unit is multiplied.
+// out[m][n] = sum_k x[m][k] W[n][k] for up to 16 rows of x: a weight stream (mx4.h).  A unit is 16 weight rows; a
+// workgroup's NW wavefronts split its columns (wavefront w takes pairs w, w + NW, ...: together they read whole rows),
+// keep their part of x in registers over all units of the workgroup (rows longer than NW PPW pairs: read again for every
+// chunk of them), and join their sums through LDS in a fixed order.  D chunks of codes are in flight, without a branch
+// between their requests: what lies past the end has addresses outside its buffer.
 struct Mx4Args {
   const bf16_t* x;
   const uint8_t* w;
@@ -71,93 +73,125 @@ struct Mx4Args {
   void* out;
 };
 
-template <int PPW, bool F32OUT>   // PPW: pairs a wavefront holds (x: 32 registers each)
+template <int PPW, int TS, int D, bool F32OUT>   // PPW: pairs a wavefront holds; TS: sets of eight rows of x
 __global__ __launch_bounds__(512) void mx4_vec_kernel(Mx4Args p, int units) {
-  __shared__ __attribute__((aligned(16))) float part[2][8][256];
+  __shared__ __attribute__((aligned(16))) float part[2][8][TS * 256];   // [half][first, second eight rows][row of x][row of W]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), NW = blockDim.x >> 6;
-  const int g = lane >> 4, col = lane & 15, P = (p.K + 255) / 256;
+  const int g = lane >> 4, col = lane & 15, chunk = lane >> 3, row = lane & 7, P = (p.K + 255) / 256;
   const int64_t m0 = (int64_t)blockIdx.y * 16;
   const int M = (int)min(p.M - m0, (int64_t)16);
   const int chunks = (P + NW * PPW - 1) / (NW * PPW);
-  const uint32_t rowb = (uint32_t)p.K / 2;
-  const __amdgpu_buffer_rsrc_t wr = buffer_of(p.w, (uint32_t)p.N * rowb);
-  const bf16_t* xrow = p.x + (m0 + min(col, M - 1)) * p.K + 64 * g;
-  bf16x8 x[PPW][8];
-  auto load_x = [&](int chunk) __attribute__((always_inline)) {
+  const uint32_t rowb = (uint32_t)p.K / 2, srows = (uint32_t)p.N * 4;
+  const __amdgpu_buffer_rsrc_t wr = buffer_of(p.w, (uint32_t)p.N * rowb), sr = buffer_of(p.s, (uint32_t)(p.K / 128) * srows);
+  bf16x8 x[PPW][TS][4];
+  auto load_x = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < PPW; ++i) {
-      const int k = ((chunk * PPW + i) * NW + wave) * 256;
-      const bool in = k + 64 * g < p.K;
+    for (int i = 0; i < PPW; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const u32x4 v = *(const u32x4*)(xrow + (in ? k + 8 * j : -64 * g));
-        x[i][j] = __builtin_bit_cast(bf16x8, in ? v : u32x4{0, 0, 0, 0});
+      for (int s = 0; s < TS; ++s) {
+        const int k = ((c * PPW + i) * NW + wave) * 256 + 64 * g + 32 * (col >> 3);
+        const bool in = k < p.K;
+        const bf16_t* xr = p.x + (m0 + min(8 * s + (col & 7), M - 1)) * p.K + (in ? k : 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const u32x4 v = *(const u32x4*)(xr + 8 * j);
+          x[i][s][j] = __builtin_bit_cast(bf16x8, in ? v : u32x4{0, 0, 0, 0});
+        }
       }
-    }
   };
   const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
   const int steps = (u1 - u0) * chunks;
-  W4Pair w[2][PPW];
-  auto load = [&](int step, auto set) __attribute__((always_inline)) {
+  W4Pair w[D][PPW];
+  int n = -1, unit = u0, c = -1;            // the step whose loads come next
+  uint32_t oa = OUTSIDE, ob = OUTSIDE, sa = 0, sb = 0;
+  auto next = [&]() __attribute__((always_inline)) {
+    ++n;
+    if (++c == chunks) {
+      c = 0;
+      ++unit;
+    }
+    const int ra = unit * 16 + row, rb = ra + 8;
+    oa = n < steps && ra < p.N ? ra * rowb + chunk * 16 : OUTSIDE;
+    ob = n < steps && rb < p.N ? rb * rowb + chunk * 16 : OUTSIDE;
+    sa = min(ra, p.N - 1) * 4;
+    sb = min(rb, p.N - 1) * 4;
+  };
+  auto load = [&](W4Pair& q, int i) __attribute__((always_inline)) {
+    const uint32_t pair = (c * PPW + i) * NW + wave;
+    const bool in = pair * 128 + chunk * 16 < rowb;
+    const uint32_t kb = in ? pair * 2 + (chunk >> 2) : 0;
+    q.a = load_b128_nt(wr, in ? oa + pair * 128 : OUTSIDE, 0);
+    q.b = load_b128_nt(wr, in ? ob + pair * 128 : OUTSIDE, 0);
+    q.sa = load_b32(sr, kb * srows + sa, 0);
+    q.sb = load_b32(sr, kb * srows + sb, 0);
+  };
+  f32x4 aa[TS], ab[TS];
+  auto step = [&](int m, auto set) __attribute__((always_inline)) {
     constexpr int S = decltype(set)::value;
-    const int n0 = (u0 + step / chunks) * 16, chunk = step % chunks;
-    const int ra = n0 + (lane & 7), rb = ra + 8, rs = min(n0 + col, p.N - 1);
+    const int mu = m / chunks, mc = m % chunks;
+    if (chunks > 1) load_x(mc);
+    if (mc == 0) {
+#pragma unroll
+      for (int s = 0; s < TS; ++s) aa[s] = ab[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    next();
 #pragma unroll
     for (int i = 0; i < PPW; ++i) {
-      const int pair = (chunk * PPW + i) * NW + wave;
-      const uint32_t at = (uint32_t)pair * 128 + (lane >> 3) * 16;
-      const bool in = at < rowb;
-      w[S][i].a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                wr, in && ra < p.N ? (uint32_t)ra * rowb + at : OUTSIDE, 0, NT_LOAD));
-      w[S][i].b = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                wr, in && rb < p.N ? (uint32_t)rb * rowb + at : OUTSIDE, 0, NT_LOAD));
-      const int kb = min(pair * 2 + (g >> 1), p.K / 128 - 1);
-      w[S][i].s = *(const uint32_t*)(p.s + ((int64_t)kb * p.N + rs) * 4);
-    }
-  };
-  f32x4 acc0{}, acc1{};
-  auto consume = [&](int step, auto set) __attribute__((always_inline)) {
-    constexpr int S = decltype(set)::value;
-    const int unit = step / chunks, chunk = step % chunks;
-    if (chunks > 1) load_x(chunk);
-    if (chunk == 0) acc0 = acc1 = f32x4{0.f, 0.f, 0.f, 0.f};
+      const float fa = chunk_scale(w[S][i].sa), fb = chunk_scale(w[S][i].sb);
 #pragma unroll
-    for (int i = 0; i < PPW; ++i) mul_pair(rows_of(w[S][i]), x[i], acc0, acc1);
-    if (chunk != chunks - 1) return;
-    float(*to)[256] = part[unit & 1];
-    *(f32x4*)&to[wave][col * 16 + 4 * g] = acc0 + acc1;   // rows 4 g .. 4 g + 3 of token col
-    lds_barrier();
-    const int n0 = (u0 + unit) * 16;
-    for (int q = tid; q < 16 * M; q += blockDim.x) {
-      float sum = to[0][q];
-      for (int v = 1; v < NW; ++v) sum += to[v][q];
-      const int n = n0 + (q & 15);
-      if (n < p.N) {
-        const int64_t o = (m0 + (q >> 4)) * p.N + n;
-        if (F32OUT) ((float*)p.out)[o] = sum;
-        else ((bf16_t*)p.out)[o] = f2bf(sum);
+      for (int j = 0; j < 4; ++j) {
+        const bf16x8 a = widen4(w[S][i].a[j], fa), b = widen4(w[S][i].b[j], fb);
+#pragma unroll
+        for (int s = 0; s < TS; ++s) {
+          aa[s] = mfma16(a, x[i][s][j], aa[s]);
+          ab[s] = mfma16(b, x[i][s][j], ab[s]);
+        }
+      }
+      load(w[S][i], i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (mc != chunks - 1 || m >= steps) return;
+    if (holds_half()) {
+#pragma unroll
+      for (int s = 0; s < TS; ++s) {
+        float* to = part[mu & 1][wave] + s * 256 + (col >> 3) * 128 + (col & 7) * 8 + 4 * (g & 1);
+        *(f32x4*)to = aa[s];
+        *(f32x4*)(to + 64) = ab[s];
       }
     }
+    lds_barrier();
+    for (int q = tid; q < 16 * M; q += blockDim.x) {
+      const int r = q & 15, t = q >> 4, o = (u0 + mu) * 16 + r;
+      if (o >= p.N) continue;
+      const int at = (t >> 3) * 256 + (r >> 3) * 64 + (t & 7) * 8 + (r & 7);
+      float sum = 0.f;
+      for (int v = 0; v < NW; ++v) sum += part[mu & 1][v][at] + part[mu & 1][v][at + 128];
+      if (F32OUT) ((float*)p.out)[(m0 + t) * p.N + o] = sum;
+      else ((bf16_t*)p.out)[(m0 + t) * p.N + o] = f2bf(sum);
+    }
   };
-  using A = std::integral_constant<int, 0>;
-  using B = std::integral_constant<int, 1>;
-  if (steps > 0) load(0, A{});
-  if (chunks == 1) load_x(0);
-  for (int s = 0; s < steps; s += 2) {
-    if (s + 1 < steps) load(s + 1, B{});
-    consume(s, A{});
-    if (s + 1 >= steps) break;
-    if (s + 2 < steps) load(s + 2, A{});
-    consume(s + 1, B{});
+#pragma unroll
+  for (int s = 0; s < D; ++s) {
+    next();
+#pragma unroll
+    for (int i = 0; i < PPW; ++i) load(w[s][i], i);
   }
+  if (chunks == 1) load_x(0);
+  for (int m = 0; m < steps; m += D) unrolled<D>([&](auto s) __attribute__((always_inline)) { step(m + decltype(s)::value, s); });
 }
 
 size_t matmul_mxfp4_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 
 template <int PPW>
 static void run_vec(const Mx4Args& a, bool f32_out, dim3 grid, int units, int nw, hipStream_t st) {
-  if (f32_out) mx4_vec_kernel<PPW, true><<<grid, 64 * nw, 0, st>>>(a, units);
-  else mx4_vec_kernel<PPW, false><<<grid, 64 * nw, 0, st>>>(a, units);
+  constexpr int D = 2;
+  if (a.M > 8) {
+    if (f32_out) mx4_vec_kernel<PPW, 2, D, true><<<grid, 64 * nw, 0, st>>>(a, units);
+    else mx4_vec_kernel<PPW, 2, D, false><<<grid, 64 * nw, 0, st>>>(a, units);
+  } else {
+    if (f32_out) mx4_vec_kernel<PPW, 1, D, true><<<grid, 64 * nw, 0, st>>>(a, units);
+    else mx4_vec_kernel<PPW, 1, D, false><<<grid, 64 * nw, 0, st>>>(a, units);
+  }
 }
 
 hipError_t launch_matmul_mxfp4(const void* x, const uint8_t* w, const uint8_t* w_scale, int64_t M, int64_t N, int64_t K,
