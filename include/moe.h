@@ -569,7 +569,7 @@ size_t moe_matmul_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * toolnavs.com warp-decode page, for this weight format and with moe_route_scored's rules):
  *   S_t, g_t by `router` (as moe_route_scored);  y_t = sum_j g_tj E_{S_tj}(x_t) + E_shared(x_t),
  * x in bf16 as it is (no 8-bit rows), products exact, sums in fp32; the inner h, times its gate, is held to 2^-16 of
- * its value; y is rounded once.  topk_idx and topk_gate are bit for bit moe_route_scored's.
+ * its value; y is rounded once.  The logits are moe_route_scored's, summed in another order.
  * In:  x [T,d] bf16, T = shape->tokens in 1..16; w_router [E,d] f32, b_router and balance [E] f32 or NULL;
  *      w_gate, w_up [E,f,d/2] and w_down [E,d,f/2] codes, w_gate_scale and w_up_scale [d/128][E*f][4],
  *      w_down_scale [f/128][E*d][4]; the shared expert's ws_gate, ws_up [fs,d/2], ws_down [d,fs/2] and scales

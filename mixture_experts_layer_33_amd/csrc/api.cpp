@@ -102,8 +102,8 @@ size_t moe_workspace_bytes(const moe_shape* s, int op) {
     case MOE_OP_DECODE:
       if (s->dtype == MOE_MXFP4)
         return decode_mxfp4_shape(s) ? 0
-                                     : align256(moe::decode_mxfp4_workspace_bytes((int)T, s->hidden, s->experts, s->top_k,
-                                                                                  s->ffn, s->shared_ffn));
+                                     : align256(moe::decode_mxfp4_workspace_bytes((int)T, s->experts, s->top_k, s->ffn,
+                                                                                  s->shared_ffn));
       return align256(moe::decode_workspace_bytes((int)T, s->experts, s->top_k, s->ffn,
                                                   s->shared_ffn));
     case MOE_OP_FORWARD:

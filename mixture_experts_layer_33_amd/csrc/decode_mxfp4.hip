@@ -13,6 +13,7 @@
 #include "fp8_tile.h"
 #include "kernels.h"
 #include "mx4.h"
+#include "score_body.h"
 
 namespace moe {
 
@@ -26,14 +27,19 @@ struct D4Args {
   const uint8_t *w_gate, *w_up, *w_down, *s_gate, *s_up, *s_down;        // codes and scale bytes of the expert stacks
   const uint8_t *ws_gate, *ws_up, *ws_down, *ss_gate, *ss_up, *ss_down;   // the shared expert's
   int T, d, E, k, f, fs;
-  const int32_t* topk_idx;
-  const float* topk_gate;
+  const float *w_r, *b_r, *balance;
+  ScoreRule rule;
+  int run;         // group_run of the experts' groups, for the lanes' experts in the choice
+  float* planes;   // [D4_KS][T][E] partial logits
+  int32_t* topk_idx;
+  float* topk_gate;
   bf16_t* h;       // [2][T k][f] (hi, lo), then the shared expert's [2][T][fs]
   bf16_t* y;
 };
 
 // What the tokens chose: the experts, ascending (gate and up read each one's weights once for all tokens).
 struct D4List {
+  int32_t id[D4_PAIRS];                   // [token, j]
   uint32_t bits[32];                      // E <= 1024
   int32_t below[32];                      // bits in the words before
   int32_t expert[D4_PAIRS];
@@ -52,16 +58,13 @@ struct D4Entries {
   int16_t row[D4_ENTRIES][D4_COLS];       // rows of h (t k + j; in the shared expert's part: t), -1: none
 };
 
-__device__ __forceinline__ void d4_list(const D4Args& p, D4List& L) {
+__device__ __forceinline__ void d4_clear(D4List& L) {   // before the barrier before d4_list
+  for (int i = threadIdx.x; i < D4_PAIRS * D4_TMAX / 4; i += blockDim.x) ((uint32_t*)L.slot)[i] = 0u;
+  if (threadIdx.x < 32) L.bits[threadIdx.x] = 0u;
+}
+__device__ __forceinline__ void d4_list(const D4Args& p, D4List& L) {   // L.id is known
   const int tid = threadIdx.x, n = p.T * p.k;
-  if (tid < 32) L.bits[tid] = 0u;
-  for (int i = tid; i < D4_PAIRS * D4_TMAX / 4; i += blockDim.x) ((uint32_t*)L.slot)[i] = 0u;
-  __syncthreads();
-  for (int q = tid; q < n; q += blockDim.x) {
-    const int e = p.topk_idx[q];
-    atomicOr(&L.bits[e >> 5], 1u << (e & 31));
-    L.gate[q] = p.topk_gate[q];
-  }
+  for (int q = tid; q < n; q += blockDim.x) atomicOr(&L.bits[L.id[q] >> 5], 1u << (L.id[q] & 31));
   __syncthreads();
   if (tid < 64) {
     const int own = tid < 32 ? __popc(L.bits[tid & 31]) : 0, incl = lanes_scan(own);
@@ -70,7 +73,7 @@ __device__ __forceinline__ void d4_list(const D4Args& p, D4List& L) {
   }
   __syncthreads();
   for (int q = tid; q < n; q += blockDim.x) {
-    const int e = p.topk_idx[q], at = L.below[e >> 5] + __popc(L.bits[e >> 5] & ((1u << (e & 31)) - 1u));
+    const int e = L.id[q], at = L.below[e >> 5] + __popc(L.bits[e >> 5] & ((1u << (e & 31)) - 1u));
     L.expert[at] = e;
     L.slot[at][q / p.k] = (uint8_t)(q % p.k + 1);
   }
@@ -128,8 +131,8 @@ struct D4Part {                          // [half][gate, up][token][column]
   static constexpr int GROUP = 4 / TS, SIZE = TS * 256;
   float v[2 * GROUP][8][SIZE];
 };
-template <int PPW, int TS, int D>        // TS: sets of eight tokens
-__device__ __forceinline__ void d4_up(const D4Args& p, const D4List& L, D4Part<TS>& part) {
+template <int PPW, int TS, int D, typename Route>        // TS: sets of eight tokens; `route` makes the list
+__device__ __forceinline__ void d4_up(const D4Args& p, const D4List& L, D4Part<TS>& part, Route route) {
   constexpr int GROUP = D4Part<TS>::GROUP;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), NW = blockDim.x >> 6;
   const int g = lane >> 4, col = lane & 15, chunk = lane >> 3, row = lane & 7, P = (p.d + 255) / 256;
@@ -148,6 +151,7 @@ __device__ __forceinline__ void d4_up(const D4Args& p, const D4List& L, D4Part<T
         x[i][s][j] = __builtin_bit_cast(bf16x8, in ? v : u32x4{0, 0, 0, 0});
       }
     }
+  route();
   // this workgroup's units: a share of the shared expert's, then of the routed ones
   const int U = L.U, per = p.f / 8, su = p.fs / 8, ru = U * per, G = gridDim.x, b = blockIdx.x;
   const int s0 = (int)((int64_t)su * b / G), s1 = (int)((int64_t)su * (b + 1) / G);
@@ -269,12 +273,135 @@ __device__ __forceinline__ void d4_up(const D4Args& p, const D4List& L, D4Part<T
   }
 }
 
-template <int PPW, int TS, int D>
+// ------------------------------------------------------------------ router
+// Partial logits of W_r (fp32) and the tokens: K split z of two expert rows by a wavefront, in plain fp32.
+// What bounds it is latency: a workgroup requests its rows of W_r at once, then brings the tokens' part into LDS.
+constexpr int D4_KS = 8, D4_SLICE = 1024 + 64;   // d <= 8192 in 8 splits of whole 64
+__global__ __launch_bounds__(256) void d4_logits_kernel(D4Args p) {
+  __shared__ __attribute__((aligned(16))) bf16_t xs[D4_TMAX * D4_SLICE];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int z = blockIdx.x % D4_KS, e0 = ((int)(blockIdx.x / D4_KS) * 4 + wave) * 2, KA = p.d / 64;
+  const int i0 = KA * z / D4_KS * 64, n = KA * (z + 1) / D4_KS * 64 - i0;
+  constexpr int IT = (D4_SLICE + 255) / 256;
+  f32x4 w[2][IT];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int q = 0; q < IT; ++q) {
+      const int i = q * 256 + lane * 4;
+      w[r][q] = i < n ? __builtin_nontemporal_load((const f32x4*)(p.w_r + (int64_t)min(e0 + r, p.E - 1) * p.d + i0 + i)) : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  for (int v = tid; v < p.T * (n / 8); v += 256) {
+    const int t = v / (n / 8), i = v % (n / 8) * 8;
+    *(u32x4*)(xs + t * D4_SLICE + i) = *(const u32x4*)(p.x + (int64_t)t * p.d + i0 + i);
+  }
+  __syncthreads();
+  float mine = 0.f;      // lane 16 r + t: expert e0 + r, token t
+  for (int t0 = 0; t0 < p.T; t0 += 4) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int t = min(t0 + u, p.T - 1);
+      float a[2] = {0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < IT; ++q) {
+        const int i = min(q * 256 + lane * 4, max(n - 4, 0));   // past the slice w is zero
+        const u32x2 v = n > 0 ? *(const u32x2*)(xs + t * D4_SLICE + i) : u32x2{0, 0};
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (q * 256 + lane * 4 >= n) continue;   // not 0 times a token's infinity
+          a[r] = fmaf(w[r][q][0], lo_bf(v[0]), a[r]);
+          a[r] = fmaf(w[r][q][1], hi_bf(v[0]), a[r]);
+          a[r] = fmaf(w[r][q][2], lo_bf(v[1]), a[r]);
+          a[r] = fmaf(w[r][q][3], hi_bf(v[1]), a[r]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float sum = lanes_sum<1>(a[r]);
+        if (lane == 16 * r + t) mine = sum;
+      }
+    }
+  }
+  const int e = e0 + (lane >> 4), t = lane & 15;
+  if (lane < 32 && t < p.T && e < p.E) p.planes[((int64_t)z * p.T + t) * p.E + e] = mine;
+}
+
+// One token's choice by this wavefront into the list (and, by workgroup 0, to the caller).
+template <int VPL, int Z>
+__device__ __forceinline__ void d4_choose(const D4Args& p, D4List& L, float* row, int t, const float (&v)[Z][VPL],
+                                          const float (&bias)[VPL], const float (&bal)[VPL]) {
+  const int lane = threadIdx.x & 63, e0 = lane * VPL;
+  float l[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    l[i] = v[0][i];
+#pragma unroll
+    for (int z = 1; z < Z; ++z) l[i] += v[z][i];
+    if (p.b_r) l[i] += bias[i];
+    if (e0 + i >= p.E) l[i] = -INFINITY;
+    row[e0 + i] = l[i];
+  }
+  int choice, rank;
+  float gate;
+  select_row<VPL>(p.rule, p.balance != nullptr, p.E, p.k, p.run, l, bal, row, choice, rank, gate);
+  if (lane < p.k) {
+    L.id[t * p.k + rank] = choice;
+    L.gate[t * p.k + rank] = gate;
+    if (blockIdx.x == 0) {
+      p.topk_idx[t * p.k + rank] = choice;
+      p.topk_gate[t * p.k + rank] = gate;
+    }
+  }
+}
+template <int VPL, int Z>
+__device__ __forceinline__ void d4_planes(const D4Args& p, int t, int z0, float (&v)[Z][VPL], float (&bias)[VPL], float (&bal)[VPL]) {
+  auto read = [&](auto vec) __attribute__((always_inline)) {
+    constexpr bool VEC = decltype(vec)::value;
+#pragma unroll
+    for (int z = 0; z < Z; ++z) lane_row<VEC>(p.planes + ((int64_t)(z0 + z) * p.T + t) * p.E, p.E, v[z]);
+    lane_row<VEC>(p.b_r ? p.b_r : p.planes, p.E, bias);
+    lane_row<VEC>(p.balance ? p.balance : p.planes, p.E, bal);
+  };
+  if (p.E % 4 == 0) read(std::true_type{});
+  else read(std::false_type{});
+}
+
+// VPL: experts a lane looks at in the choice.
+template <int PPW, int TS, int D, int VPL>
 __global__ __launch_bounds__(512) void d4_up_kernel(D4Args p) {
   __shared__ D4List L;
   __shared__ __attribute__((aligned(16))) D4Part<TS> part;
-  d4_list(p, L);
-  d4_up<PPW, TS, D>(p, L, part);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), NW = blockDim.x >> 6;
+  float* row = &part.v[0][0][0] + wave * 64 * VPL;      // the choice's, before gate and up
+  d4_clear(L);
+  if constexpr (VPL == 4) {
+    // the logits are requested before the tokens: waits are in the order of requests
+    float v[D4_KS][VPL], bias[VPL], bal[VPL];
+    d4_planes<VPL, D4_KS>(p, min(wave, p.T - 1), 0, v, bias, bal);
+    d4_up<PPW, TS, D>(p, L, part, [&]() __attribute__((always_inline)) {
+      for (int t = wave; t < p.T; t += NW) {
+        if (t > wave) d4_planes<VPL, D4_KS>(p, t, 0, v, bias, bal);
+        d4_choose<VPL, D4_KS>(p, L, row, t, v, bias, bal);
+      }
+      __syncthreads();
+      d4_list(p, L);
+    });
+  } else {      // wide rows: their registers and the tokens' one after another
+    for (int t = wave; t < p.T; t += NW) {
+      float v[2][VPL], w[4][VPL], bias[VPL], bal[VPL];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {      // four planes at a time: eight spill
+        d4_planes<VPL, 4>(p, t, 4 * q, w, bias, bal);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) v[q][i] = w[0][i] + w[1][i] + (w[2][i] + w[3][i]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      d4_choose<VPL, 2>(p, L, row, t, v, bias, bal);
+    }
+    __syncthreads();
+    d4_list(p, L);
+    d4_up<PPW, TS, D>(p, L, part, []() {});
+  }
 }
 
 // ------------------------------------------------------------------ down
@@ -366,7 +493,7 @@ __device__ __forceinline__ void d4_down(const D4Args& p, const D4Entries& N, D4D
       for (int c = 0; c < D4_COLS; ++c) {
         u32x4* to = m.h[wave][slot][c];
         if (hrow[c] >= 0)
-          dma16(hbase + (int64_t)hrow[c] * F + pair * 256, off, __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to));
+          copy16(hbase + (int64_t)hrow[c] * F + pair * 256, off, __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to));
         else if (p.T <= D4_COLS && c < p.T)
           to[lane] = u32x4{0, 0, 0, 0};
       }
@@ -454,6 +581,9 @@ __global__ __launch_bounds__(512) void d4_down_kernel(D4Args p, int RW) {
   __shared__ D4List L;
   __shared__ D4Entries N;
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  d4_clear(L);
+  for (int q = threadIdx.x; q < p.T * p.k; q += blockDim.x) L.id[q] = p.topk_idx[q];
+  __syncthreads();
   d4_list(p, L);
   d4_entries(p, L, N);
   for (int o0 = blockIdx.x * RW; o0 < p.d; o0 += gridDim.x * RW) {
@@ -472,13 +602,19 @@ static hipError_t run_down(const D4Args& a, int RW, int grid, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Workspace: the router's logit planes | expert counts [E] | h [2][T k f] | [2][T fs].
-static size_t d4_route_bytes(int T, int E, int d) {
-  const size_t b = std::max(route_workspace_bytes(T, E, d), route_scored_workspace_bytes(T, E, d));
-  return (b + 255) & ~(size_t)255;
+// Workspace: partial logits [D4_KS][T][E] | h [2][T k][f] | [2][T fs].
+static size_t d4_planes_bytes(int T, int E) { return ((size_t)D4_KS * T * E * sizeof(float) + 255) & ~(size_t)255; }
+size_t decode_mxfp4_workspace_bytes(int T, int E, int k, int f, int fs) {
+  return d4_planes_bytes(T, E) + 4 * ((size_t)T * k * f + (size_t)T * fs);
 }
-size_t decode_mxfp4_workspace_bytes(int T, int d, int E, int k, int f, int fs) {
-  return d4_route_bytes(T, E, d) + 4096 + 4 * ((size_t)T * k * f + (size_t)T * fs);
+
+template <int PPW, int TS>
+static hipError_t run_up(const D4Args& a, int grid, int nw, hipStream_t st) {
+  constexpr int D = PPW <= 2 ? 4 : TS == 1 ? 3 : 2;
+  if (a.E > 512) d4_up_kernel<PPW, TS, D, 16><<<grid, 64 * nw, 0, st>>>(a);
+  else if (a.E > 256) d4_up_kernel<PPW, TS, D, 8><<<grid, 64 * nw, 0, st>>>(a);
+  else d4_up_kernel<PPW, TS, D, 4><<<grid, 64 * nw, 0, st>>>(a);
+  return hipGetLastError();
 }
 
 hipError_t launch_decode_mxfp4(const void* x, const float* w_r, const float* b_r, const float* balance, const ScoreRule& rule,
@@ -489,24 +625,20 @@ hipError_t launch_decode_mxfp4(const void* x, const float* w_r, const float* b_r
   if (err != hipSuccess) return err;
   if ((err = hipDeviceGetAttribute(&ncu, hipDeviceAttributeMultiprocessorCount, dev)) != hipSuccess) return err;
   uint8_t* base = (uint8_t*)ws;
-  int32_t* count = (int32_t*)(base + d4_route_bytes(T, E, d));
-  err = launch_route_scored(x, false, w_r, b_r, balance, rule, T, d, E, k, (float*)base, topk_idx, topk_gate, count, nullptr, st);
-  if (err != hipSuccess) return err;
   const D4Args a{(const bf16_t*)x, w.gate, w.up, w.down, w.s_gate, w.s_up, w.s_down, shared.gate, shared.up, shared.down,
-                 shared.s_gate, shared.s_up, shared.s_down, T, d, E, k, f, fs, topk_idx, topk_gate,
-                 (bf16_t*)(base + d4_route_bytes(T, E, d) + 4096), (bf16_t*)y};
-  const int P = (d + 255) / 256, nw = std::min(8, P), ppw = (P + nw - 1) / nw;
-#define UP(N)                                                               \
-  case N:                                                                   \
-    if (T > 8) d4_up_kernel<N, 2, N <= 2 ? 4 : 2><<<ncu, 64 * nw, 0, st>>>(a);   \
-    else d4_up_kernel<N, 1, N <= 2 ? 4 : 3><<<ncu, 64 * nw, 0, st>>>(a);         \
-    break;
-  switch (ppw) {
-    UP(1) UP(2) UP(3) UP(4)
-    default: return hipErrorInvalidValue;
-  }
-#undef UP
+                 shared.s_gate, shared.s_up, shared.s_down, T, d, E, k, f, fs, w_r, b_r, balance, rule,
+                 group_run(E / rule.groups, E <= 256 ? 4 : E <= 512 ? 8 : 16), (float*)base, topk_idx, topk_gate,
+                 (bf16_t*)(base + d4_planes_bytes(T, E)), (bf16_t*)y};
+  d4_logits_kernel<<<(E + 7) / 8 * D4_KS, 256, 0, st>>>(a);
   if ((err = hipGetLastError()) != hipSuccess) return err;
+  const int P = (d + 255) / 256, nw = std::min(8, P), ppw = (P + nw - 1) / nw;
+  switch (ppw) {
+    case 1: err = T > 8 ? run_up<1, 2>(a, ncu, nw, st) : run_up<1, 1>(a, ncu, nw, st); break;
+    case 2: err = T > 8 ? run_up<2, 2>(a, ncu, nw, st) : run_up<2, 1>(a, ncu, nw, st); break;
+    case 3: err = T > 8 ? run_up<3, 2>(a, ncu, nw, st) : run_up<3, 1>(a, ncu, nw, st); break;
+    default: err = T > 8 ? run_up<4, 2>(a, ncu, nw, st) : run_up<4, 1>(a, ncu, nw, st);
+  }
+  if (err != hipSuccess) return err;
   const int RW = std::min(D4_ROWS, std::max(8, (d + ncu - 1) / ncu)), g2 = (d + RW - 1) / RW;
   return RW <= 16 ? run_down<1, 4>(a, RW, g2, st) : run_down<2, 3>(a, RW, g2, st);
 }

@@ -103,7 +103,7 @@ hipError_t launch_matmul_mxfp4(const void* x, const uint8_t* w, const uint8_t* w
 struct Mx4Weights {
   const uint8_t *gate, *up, *down, *s_gate, *s_up, *s_down;
 };
-size_t decode_mxfp4_workspace_bytes(int T, int d, int E, int k, int f, int fs);
+size_t decode_mxfp4_workspace_bytes(int T, int E, int k, int f, int fs);
 hipError_t launch_decode_mxfp4(const void* x, const float* w_r, const float* b_r, const float* balance,
                                const ScoreRule& rule, const Mx4Weights& w, const Mx4Weights& shared, int T, int d, int E,
                                int k, int f, int fs, void* y, int32_t* topk_idx, float* topk_gate, void* ws,

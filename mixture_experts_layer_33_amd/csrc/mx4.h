@@ -30,7 +30,7 @@ constexpr uint32_t RSRC_WORD3 = 0x00027000;   // raw buffer, 32-bit data
 constexpr uint32_t OUTSIDE = 0x80000000u;      // an offset past every buffer (they are below 2 GiB): the load returns zeros
 constexpr int NT_LOAD = 2;                     // cache policy of a buffer load: non-temporal
 
-// (offset: per lane, `at`: of the wavefront, which has to be at most the buffer's size)
+// (offset: per lane; `at`: of the wavefront, at most the buffer's size: beyond it nothing counts as outside)
 __device__ __forceinline__ u32x4 load_b128(__amdgpu_buffer_rsrc_t r, uint32_t offset, uint32_t at) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)offset, (int)at, 0));
 }
@@ -85,6 +85,14 @@ __device__ __forceinline__ void unrolled(F f) {
     f(std::integral_constant<int, I>{});
     unrolled<N, I + 1>(f);
   }
+}
+
+// Global -> LDS copy of 16 bytes a lane, to `lds` + 16 lane, that the compiler does not wait for (as gemm_body.h's).  The compiler
+// does not look into the asm: five wait states between a vector instruction that writes the address's scalar
+// registers and the copy that reads them, and one behind m0, are written out.
+__device__ __forceinline__ void copy16(const void* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %1"
+               ::"v"(offset), "s"(base), "s"(lds) : "memory", "m0");
 }
 
 // A barrier that publishes LDS only: loads into registers stay in flight (a full barrier may wait for them).
