@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["api.cpp", "route.hip", "dispatch.hip", "gemm.hip", "combine.hip", "decode.hip",
            "backward.hip", "mxq.hip", "fused.hip", "norm.hip", "score.hip", "fp8.hip", "mxfp4.hip",
-           "decode_mxfp4.hip"]
+           "decode_mxfp4.hip", "mxfp4_tile.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -98,6 +98,9 @@ hipError_t launch_decode(const void* x, const float* w_r, const float* b_r, cons
 hipError_t launch_quantize_mxfp4(const void* src, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
                                  hipStream_t st);
 size_t matmul_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+size_t mx4_tile_workspace_bytes(int64_t M, int64_t N, int64_t K);   // more than a few rows
+hipError_t launch_mx4_tiles(const void* x, const uint8_t* w, const uint8_t* w_scale, int64_t M, int64_t N, int64_t K,
+                            bool f32_out, void* out, void* ws, hipStream_t st);
 hipError_t launch_matmul_mxfp4(const void* x, const uint8_t* w, const uint8_t* w_scale, int64_t M, int64_t N, int64_t K,
                                bool f32_out, void* out, void* ws, hipStream_t st);
 struct Mx4Weights {

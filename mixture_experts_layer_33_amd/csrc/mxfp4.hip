@@ -180,7 +180,11 @@ __global__ __launch_bounds__(512) void mx4_vec_kernel(Mx4Args p, int units) {
   for (int m = 0; m < steps; m += D) unrolled<D>([&](auto s) __attribute__((always_inline)) { step(m + decltype(s)::value, s); });
 }
 
-size_t matmul_mxfp4_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+// Up to 16 rows the product is the stream of W; more (mxfp4_tile.hip) are tiles, as long as a tile's offsets fit 32 bits.
+static bool few_rows(int64_t M, int64_t K) { return M <= 16 || K >= (int64_t)1 << 23; }
+size_t matmul_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return few_rows(M, K) ? 0 : mx4_tile_workspace_bytes(M, N, K);
+}
 
 template <int PPW>
 static void run_vec(const Mx4Args& a, bool f32_out, dim3 grid, int units, int nw, hipStream_t st) {
@@ -195,7 +199,8 @@ static void run_vec(const Mx4Args& a, bool f32_out, dim3 grid, int units, int nw
 }
 
 hipError_t launch_matmul_mxfp4(const void* x, const uint8_t* w, const uint8_t* w_scale, int64_t M, int64_t N, int64_t K,
-                               bool f32_out, void* out, void*, hipStream_t st) {
+                               bool f32_out, void* out, void* ws, hipStream_t st) {
+  if (!few_rows(M, K)) return launch_mx4_tiles(x, w, w_scale, M, N, K, f32_out, out, ws, st);
   const Mx4Args a{(const bf16_t*)x, w, w_scale, M, (int)N, (int)K, out};
   const int units = (int)((N + 15) / 16), P = (int)((K + 255) / 256), nw = std::min(8, P);
   const int ppw = std::min(4, (P + nw - 1) / nw);

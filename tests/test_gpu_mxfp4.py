@@ -120,7 +120,7 @@ def check_product(out, x, W):
 SIZES = [(1, 1, 128), (1, 16, 256), (1, 7168, 512), (2, 40, 384), (3, 129, 640), (5, 1000, 2048), (8, 256, 1024), (9, 4100, 1152), (15, 72, 128),
          (16, 131, 7168), (2, 50, 8192), (1, 33, 8320), (7, 100, 12288), (17, 264, 640), (31, 512, 256), (33, 130, 128), (48, 2048, 1408), (64, 384, 384),
          (65, 128, 256), (100, 77, 512), (127, 256, 128), (128, 128, 256), (129, 257, 384), (200, 640, 1152), (255, 255, 128), (257, 1032, 256),
-         (512, 512, 512), (700, 4168, 640), (1000, 128, 2048), (1536, 1544, 256)]
+         (512, 512, 512), (700, 4168, 640), (1000, 128, 2048), (1536, 1544, 256), (2045, 4100, 256), (40, 1001, 7168), (61, 8, 4096), (300, 300, 4224)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
