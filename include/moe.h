@@ -554,7 +554,7 @@ int moe_quantize_mxfp4(const void* src_bf16, int64_t rows, int64_t cols, uint8_t
  * products exact, sums in fp32, one rounding.  out may not overlap an input.  A scale byte of 252 or more gives
  * values past bf16's range, which count as infinite (255: NaN).
  * In:  x [M,K] bf16; w [N,K/2] codes, w_scale [K/128][N][4] (moe_quantize_mxfp4).  K % 128 == 0; M K and
- *      N K < 2^32, M N < 2^38.
+ *      N K < 2^32, M N < 2^38, K < 2^23.
  * Out: out [M,N]: out_dtype MOE_BF16 or MOE_F32 (MOE_ERR_DTYPE otherwise).
  * M = 0 or N = 0: nothing is written.
  * workspace: moe_matmul_mxfp4_workspace_bytes(M, N, K) bytes (NULL if that is 0).  x and w are aligned to 16

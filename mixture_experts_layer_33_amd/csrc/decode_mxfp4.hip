@@ -131,27 +131,37 @@ struct D4Part {                          // [half][gate, up][token][column]
   static constexpr int GROUP = 4 / TS, SIZE = TS * 256;
   float v[2 * GROUP][8][SIZE];
 };
-template <int PPW, int TS, int D, typename Route>        // TS: sets of eight tokens; `route` makes the list
-__device__ __forceinline__ void d4_up(const D4Args& p, const D4List& L, D4Part<TS>& part, Route route) {
+// `lds`: the tokens' blocks first, then the sums.
+template <int PPW, int TS>
+constexpr int D4_UP_LDS = (PPW * TS < 4 ? PPW * TS : 4) * 8 * XBLOCK > (int)sizeof(D4Part<TS>) ? (PPW * TS < 4 ? PPW * TS : 4) * 8 * XBLOCK
+                                                                                              : (int)sizeof(D4Part<TS>);
+template <int PPW, int TS, int D>        // TS: sets of eight tokens
+__device__ __forceinline__ void d4_up(const D4Args& p, D4List& L, uint8_t* stage) {
+  D4Part<TS>& part = *(D4Part<TS>*)stage;
   constexpr int GROUP = D4Part<TS>::GROUP;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), NW = blockDim.x >> 6;
   const int g = lane >> 4, col = lane & 15, chunk = lane >> 3, row = lane & 7, P = (p.d + 255) / 256;
   const uint32_t rowb = (uint32_t)p.d / 2;
   bf16x8 x[PPW][TS][4];
+  constexpr int BLOCKS = PPW * TS < 4 ? PPW * TS : 4;     // of x on their way at a time (the first ones while the list is made)
 #pragma unroll
-  for (int i = 0; i < PPW; ++i)
+  for (int b0 = 0; b0 < PPW * TS; b0 += BLOCKS) {
 #pragma unroll
-    for (int s = 0; s < TS; ++s) {
-      const int k = (i * NW + wave) * 256 + 64 * g + 32 * (col >> 3);
-      const bool in = k < p.d;
-      const bf16_t* xr = p.x + (int64_t)min(8 * s + (col & 7), p.T - 1) * p.d + (in ? k : 0);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const u32x4 v = *(const u32x4*)(xr + 8 * j);
-        x[i][s][j] = __builtin_bit_cast(bf16x8, in ? v : u32x4{0, 0, 0, 0});
-      }
+    for (int b = 0; b < BLOCKS; ++b) {
+      if (b0 + b >= PPW * TS) break;
+      const int k = ((b0 + b) / TS * NW + wave) * 256, at = k < p.d ? k : 0, r0 = min((b0 + b) % TS * 8, p.T - 1);
+      x_copy(p.x + (int64_t)r0 * p.d + at, p.T - 1 - r0, (uint32_t)p.d, p.d - at,
+             (uint32_t)(uintptr_t)(stage + (wave * BLOCKS + b) * XBLOCK));
     }
-  route();
+    if (b0 == 0) d4_list(p, L);
+    wait_all();
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b)
+      if (b0 + b < PPW * TS)
+        x_read(stage + (wave * BLOCKS + b) * XBLOCK, ((b0 + b) / TS * NW + wave) * 256 + 64 * g + 32 * (col >> 3) < p.d,
+               x[(b0 + b) / TS][(b0 + b) % TS]);
+    lds_barrier();      // read: the next blocks, or the sums, may come
+  }
   // this workgroup's units: a share of the shared expert's, then of the routed ones
   const int U = L.U, per = p.f / 8, su = p.fs / 8, ru = U * per, G = gridDim.x, b = blockIdx.x;
   const int s0 = (int)((int64_t)su * b / G), s1 = (int)((int64_t)su * (b + 1) / G);
@@ -370,38 +380,29 @@ __device__ __forceinline__ void d4_planes(const D4Args& p, int t, int z0, float 
 template <int PPW, int TS, int D, int VPL>
 __global__ __launch_bounds__(512) void d4_up_kernel(D4Args p) {
   __shared__ D4List L;
-  __shared__ __attribute__((aligned(16))) D4Part<TS> part;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[D4_UP_LDS<PPW, TS>];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), NW = blockDim.x >> 6;
-  float* row = &part.v[0][0][0] + wave * 64 * VPL;      // the choice's, before gate and up
+  float* row = (float*)lds + wave * 64 * VPL;      // the choice's, before anything else
+  constexpr int Z = VPL == 4 ? D4_KS : 4;          // planes in flight: eight of a wide row spill
+  float v[Z][VPL], bias[VPL], bal[VPL];
+  d4_planes<VPL, Z>(p, min(wave, p.T - 1), 0, v, bias, bal);
   d4_clear(L);
-  if constexpr (VPL == 4) {
-    // the logits are requested before the tokens: waits are in the order of requests
-    float v[D4_KS][VPL], bias[VPL], bal[VPL];
-    d4_planes<VPL, D4_KS>(p, min(wave, p.T - 1), 0, v, bias, bal);
-    d4_up<PPW, TS, D>(p, L, part, [&]() __attribute__((always_inline)) {
-      for (int t = wave; t < p.T; t += NW) {
-        if (t > wave) d4_planes<VPL, D4_KS>(p, t, 0, v, bias, bal);
-        d4_choose<VPL, D4_KS>(p, L, row, t, v, bias, bal);
-      }
-      __syncthreads();
-      d4_list(p, L);
-    });
-  } else {      // wide rows: their registers and the tokens' one after another
-    for (int t = wave; t < p.T; t += NW) {
-      float v[2][VPL], w[4][VPL], bias[VPL], bal[VPL];
+  for (int t = wave; t < p.T; t += NW) {
+    if (t > wave) d4_planes<VPL, Z>(p, t, 0, v, bias, bal);
+    float l[1][VPL];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {      // four planes at a time: eight spill
-        d4_planes<VPL, 4>(p, t, 4 * q, w, bias, bal);
+    for (int z0 = 0; z0 < D4_KS; z0 += Z) {
+      if (z0 > 0) d4_planes<VPL, Z>(p, t, z0, v, bias, bal);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) v[q][i] = w[0][i] + w[1][i] + (w[2][i] + w[3][i]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      d4_choose<VPL, 2>(p, L, row, t, v, bias, bal);
+      for (int i = 0; i < VPL; ++i)
+#pragma unroll
+        for (int z = 0; z < Z; ++z) l[0][i] = z0 + z == 0 ? v[0][i] : l[0][i] + v[z][i];
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __syncthreads();
-    d4_list(p, L);
-    d4_up<PPW, TS, D>(p, L, part, []() {});
+    d4_choose<VPL, 1>(p, L, row, t, l, bias, bal);
   }
+  __syncthreads();
+  d4_up<PPW, TS, D>(p, L, lds);
 }
 
 // ------------------------------------------------------------------ down

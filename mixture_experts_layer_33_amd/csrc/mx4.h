@@ -95,6 +95,31 @@ __device__ __forceinline__ void copy16(const void* base, uint32_t offset, uint32
                ::"v"(offset), "s"(base), "s"(lds) : "memory", "m0");
 }
 
+// Waits for all copies (and loads) of this wavefront.
+__device__ __forceinline__ void wait_all() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Eight rows of x of one pair as second operands.  A lane's part is 64 contiguous bytes of a row: read straight into registers
+// each of the four 16-byte loads touches 64 pieces of 64 bytes, so the block (4 KB) goes through LDS in
+// four copies of whole 128-byte lines: copy i has chunks 2i and 2i + 1 of each row, 16-byte pieces exchanged among themselves
+// so that 16 lanes read from all banks.
+constexpr int XBLOCK = 4096;
+// `base`: the first row at the pair's first column, `left` >= 128 columns from there on (a multiple of 128), `lds`: the block.
+__device__ __forceinline__ void x_copy(const bf16_t* base, int last_row, uint32_t K, int left, uint32_t lds) {
+  const int lane = threadIdx.x & 63, r = lane >> 3, piece = (lane & 7) ^ ((r >> 1) & 3);
+  const uint32_t at = (uint32_t)min(r, last_row) * K * 2 + piece * 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) copy16(base, at + (left > 128 || i < 2 ? i : i - 2) * 128, __builtin_amdgcn_readfirstlane(lds + i * 1024));
+}
+// `in`: the pair has this lane's chunk.
+__device__ __forceinline__ void x_read(const uint8_t* block, bool in, bf16x8 (&x)[4]) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15, r = col & 7;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const u32x4 v = *(const u32x4*)(block + g * 1024 + r * 128 + ((((col >> 3) * 4 + j) ^ ((r >> 1) & 3)) << 4));
+    x[j] = __builtin_bit_cast(bf16x8, in ? v : u32x4{0, 0, 0, 0});
+  }
+}
+
 // A barrier that publishes LDS only: loads into registers stay in flight (a full barrier may wait for them).
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");

@@ -76,28 +76,40 @@ struct Mx4Args {
 template <int PPW, int TS, int D, bool F32OUT>   // PPW: pairs a wavefront holds; TS: sets of eight rows of x
 __global__ __launch_bounds__(512) void mx4_vec_kernel(Mx4Args p, int units) {
   __shared__ __attribute__((aligned(16))) float part[2][8][TS * 256];   // [half][first, second eight rows][row of x][row of W]
+  constexpr int BLOCKS = PPW * TS < 4 ? PPW * TS : 4;     // of x on their way at a time
+  __shared__ __attribute__((aligned(1024))) uint8_t stage[8][BLOCKS][XBLOCK];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), NW = blockDim.x >> 6;
   const int g = lane >> 4, col = lane & 15, chunk = lane >> 3, row = lane & 7, P = (p.K + 255) / 256;
-  const int64_t m0 = (int64_t)blockIdx.y * 16;
-  const int M = (int)min(p.M - m0, (int64_t)16);
+  const int M = (int)p.M;
   const int chunks = (P + NW * PPW - 1) / (NW * PPW);
   const uint32_t rowb = (uint32_t)p.K / 2, srows = (uint32_t)p.N * 4;
   const __amdgpu_buffer_rsrc_t wr = buffer_of(p.w, (uint32_t)p.N * rowb), sr = buffer_of(p.s, (uint32_t)(p.K / 128) * srows);
   bf16x8 x[PPW][TS][4];
-  auto load_x = [&](int c) __attribute__((always_inline)) {
+  auto first_column = [&](int c, int i) __attribute__((always_inline)) { return ((c * PPW + i) * NW + wave) * 256; };
+  auto copy_x = [&](int c, int b0) __attribute__((always_inline)) {     // blocks b0 .. b0 + BLOCKS - 1: (pair, set)
 #pragma unroll
-    for (int i = 0; i < PPW; ++i)
+    for (int b = 0; b < BLOCKS; ++b) {
+      if (b0 + b >= PPW * TS) break;
+      const int k = first_column(c, (b0 + b) / TS), s = (b0 + b) % TS, at = k < p.K ? k : 0, r0 = min(8 * s, M - 1);
+      x_copy(p.x + (int64_t)r0 * p.K + at, M - 1 - r0, (uint32_t)p.K, p.K - at, (uint32_t)(uintptr_t)stage[wave][b]);
+    }
+  };
+  auto read_x = [&](int c, int b0) __attribute__((always_inline)) {
 #pragma unroll
-      for (int s = 0; s < TS; ++s) {
-        const int k = ((c * PPW + i) * NW + wave) * 256 + 64 * g + 32 * (col >> 3);
-        const bool in = k < p.K;
-        const bf16_t* xr = p.x + (m0 + min(8 * s + (col & 7), M - 1)) * p.K + (in ? k : 0);
+    for (int b = 0; b < BLOCKS; ++b)
+      if (b0 + b < PPW * TS)
+        x_read(stage[wave][b], first_column(c, (b0 + b) / TS) + 64 * g + 32 * (col >> 3) < p.K,
+               x[(b0 + b) / TS][(b0 + b) % TS]);
+  };
+  auto rest_of_x = [&](int c) __attribute__((always_inline)) {          // the first blocks are copied
+    read_x(c, 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const u32x4 v = *(const u32x4*)(xr + 8 * j);
-          x[i][s][j] = __builtin_bit_cast(bf16x8, in ? v : u32x4{0, 0, 0, 0});
-        }
-      }
+    for (int b0 = BLOCKS; b0 < PPW * TS; b0 += BLOCKS) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");                // the blocks before are read
+      copy_x(c, b0);
+      wait_all();
+      read_x(c, b0);
+    }
   };
   const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
   const int steps = (u1 - u0) * chunks;
@@ -129,7 +141,12 @@ __global__ __launch_bounds__(512) void mx4_vec_kernel(Mx4Args p, int units) {
   auto step = [&](int m, auto set) __attribute__((always_inline)) {
     constexpr int S = decltype(set)::value;
     const int mu = m / chunks, mc = m % chunks;
-    if (chunks > 1) load_x(mc);
+    if (chunks > 1) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      copy_x(mc, 0);
+      wait_all();
+      rest_of_x(mc);
+    }
     if (mc == 0) {
 #pragma unroll
       for (int s = 0; s < TS; ++s) aa[s] = ab[s] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -166,29 +183,30 @@ __global__ __launch_bounds__(512) void mx4_vec_kernel(Mx4Args p, int units) {
       const int at = (t >> 3) * 256 + (r >> 3) * 64 + (t & 7) * 8 + (r & 7);
       float sum = 0.f;
       for (int v = 0; v < NW; ++v) sum += part[mu & 1][v][at] + part[mu & 1][v][at + 128];
-      if (F32OUT) ((float*)p.out)[(m0 + t) * p.N + o] = sum;
-      else ((bf16_t*)p.out)[(m0 + t) * p.N + o] = f2bf(sum);
+      if (F32OUT) ((float*)p.out)[(int64_t)t * p.N + o] = sum;
+      else ((bf16_t*)p.out)[(int64_t)t * p.N + o] = f2bf(sum);
     }
   };
+  copy_x(0, 0);
 #pragma unroll
   for (int s = 0; s < D; ++s) {
     next();
 #pragma unroll
     for (int i = 0; i < PPW; ++i) load(w[s][i], i);
   }
-  if (chunks == 1) load_x(0);
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * D * PPW) : "memory");    // the copies: only the loads are behind them
+  if (chunks == 1) rest_of_x(0);
   for (int m = 0; m < steps; m += D) unrolled<D>([&](auto s) __attribute__((always_inline)) { step(m + decltype(s)::value, s); });
 }
 
-// Up to 16 rows the product is the stream of W; more (mxfp4_tile.hip) are tiles, as long as a tile's offsets fit 32 bits.
-static bool few_rows(int64_t M, int64_t K) { return M <= 16 || K >= (int64_t)1 << 23; }
-size_t matmul_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return few_rows(M, K) ? 0 : mx4_tile_workspace_bytes(M, N, K);
-}
+// Up to 16 rows the product is a stream of W; more are tiles (mxfp4_tile.hip).
+static bool few_rows(int64_t M) { return M <= 16; }
+size_t matmul_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) { return few_rows(M) ? 0 : mx4_tile_workspace_bytes(M, N, K); }
 
 template <int PPW>
 static void run_vec(const Mx4Args& a, bool f32_out, dim3 grid, int units, int nw, hipStream_t st) {
-  constexpr int D = 2;
+  constexpr int D = 1;      // most workgroups have one unit: two in flight cost 0.3 to 2 us more (requests past the end), 1 x 7168 x 2048: 5.3 and 5.6
   if (a.M > 8) {
     if (f32_out) mx4_vec_kernel<PPW, 2, D, true><<<grid, 64 * nw, 0, st>>>(a, units);
     else mx4_vec_kernel<PPW, 2, D, false><<<grid, 64 * nw, 0, st>>>(a, units);
@@ -200,26 +218,18 @@ static void run_vec(const Mx4Args& a, bool f32_out, dim3 grid, int units, int nw
 
 hipError_t launch_matmul_mxfp4(const void* x, const uint8_t* w, const uint8_t* w_scale, int64_t M, int64_t N, int64_t K,
                                bool f32_out, void* out, void* ws, hipStream_t st) {
-  if (!few_rows(M, K)) return launch_mx4_tiles(x, w, w_scale, M, N, K, f32_out, out, ws, st);
+  if (!few_rows(M)) return launch_mx4_tiles(x, w, w_scale, M, N, K, f32_out, out, ws, st);
   const Mx4Args a{(const bf16_t*)x, w, w_scale, M, (int)N, (int)K, out};
   const int units = (int)((N + 15) / 16), P = (int)((K + 255) / 256), nw = std::min(8, P);
   const int ppw = std::min(4, (P + nw - 1) / nw);
-  for (int64_t m = 0; m < M; m += 16 * 65535) {   // grid.y
-    Mx4Args b = a;
-    b.x += m * K;
-    b.out = (uint8_t*)out + m * N * (f32_out ? 4 : 2);
-    b.M = std::min<int64_t>(M - m, 16 * 65535);
-    const dim3 grid((unsigned)std::min(units, 256), (unsigned)((b.M + 15) / 16));
-    switch (ppw) {
-      case 1: run_vec<1>(b, f32_out, grid, units, nw, st); break;
-      case 2: run_vec<2>(b, f32_out, grid, units, nw, st); break;
-      case 3: run_vec<3>(b, f32_out, grid, units, nw, st); break;
-      default: run_vec<4>(b, f32_out, grid, units, nw, st); break;
-    }
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
+  const dim3 grid((unsigned)std::min(units, 256));
+  switch (ppw) {
+    case 1: run_vec<1>(a, f32_out, grid, units, nw, st); break;
+    case 2: run_vec<2>(a, f32_out, grid, units, nw, st); break;
+    case 3: run_vec<3>(a, f32_out, grid, units, nw, st); break;
+    default: run_vec<4>(a, f32_out, grid, units, nw, st);
   }
-  return hipSuccess;
+  return hipGetLastError();
 }
 
 }  // namespace moe

@@ -44,7 +44,7 @@ def test_quantiser_refusals():
 def test_matmul_refusals():
     def mm(M=16, N=256, K=256, ty=_lib.MOE_BF16, x=FAKE, w=FAKE, s=FAKE, out=FAKE, ws=FAKE, n=1 << 40):
         return L().moe_matmul_mxfp4(x, w, s, M, N, K, ty, out, ws, n, None)
-    for bad in (dict(K=192), dict(K=0), dict(M=-1), dict(N=-1), dict(M=1 << 25), dict(N=1 << 25), dict(M=1 << 31), dict(M=1 << 22, N=1 << 22, K=128)):
+    for bad in (dict(K=192), dict(K=0), dict(M=-1), dict(N=-1), dict(M=1 << 25), dict(N=1 << 25), dict(M=1 << 31), dict(M=1 << 22, N=1 << 22, K=128), dict(M=1, N=1, K=1 << 23)):
         assert mm(**bad) == SHAPE, bad
     assert mm(ty=_lib.MOE_MXFP4) == DTYPE
     for bad in (dict(x=None), dict(w=None), dict(s=None), dict(out=None)):
