@@ -514,9 +514,9 @@ __device__ __forceinline__ void gg_mfma_body(const GemmArgs p, int vb, uint8_t* 
   }
   };
   for (int s = 0; s < S - 1 && s < KT; ++s) issue(s);
-  static_assert(FM == 2, "three loop forms: 2, 1 or 0 live A fragments");
+  static_assert(FM <= 2, "three loop forms: 2, 1 or 0 live A fragments");
   if (nlive == FM) kloop(std::integral_constant<int, FM>{});
-  else if (nlive == 1) kloop(std::integral_constant<int, 1>{});
+  else if (FM == 2 && nlive == 1) kloop(std::integral_constant<int, 1>{});
   else kloop(std::integral_constant<int, 0>{});
   __syncthreads();
 

@@ -384,6 +384,8 @@ EXPERTS = {
     "many_rows": dict(T=700, d=384, E=2, k=2, f=256),      # 256-row tiles
     "one_expert": dict(T=513, d=256, E=1, k=1, f=384),
     "empty_experts": dict(T=4, d=256, E=64, k=2, f=128),
+    "whole_lines": dict(T=190, d=512, E=2, k=1, f=768, crowd=1),
+    "long_rows": dict(T=90, d=2048, E=3, k=2, f=1280),
 }
 
 
