@@ -36,23 +36,28 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-template <int BM, int BN, int WM, int WN, int S>
+// G groups of WM x WN wavefronts have a part of K each, with a ring of its own, and join their sums in LDS.
+template <int BM, int BN, int WM, int WN, int S, int G>
 struct Tile4 {
   static constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
-  static constexpr int NA = BM / 8 / NW, NB = BN >= 32 * NW ? BN / 32 / NW : 1, NS = BN >= 64 * NW ? BN / 64 / NW : 1;
-  static constexpr int L = NA + NB + NS;           // copies of a wavefront per stage (where there are fewer pieces, repeated ones)
+  static constexpr int PA = BM / 8, PB = BN / 32, PS = BN / 64;   // a stage's copies: x, codes, scales
+  static constexpr int L = (PA + PB + PS + NW - 1) / NW;          // of one wavefront (past the last piece: that once more)
   static constexpr int A = 0, B = BM * 128, SC = B + BN * 32, STAGE = SC + BN * 4;
-  static constexpr int RING = S * STAGE, EPI = NW * 32 * (WTN * 4 + 16), LDS = RING > EPI ? RING : EPI;
+  static constexpr int RING = S * STAGE, RS = BN * 4 + 16;
+  static constexpr int EPI = G == 1 ? NW * 32 * (WTN * 4 + 16) : G * BM * RS, LDS = G * RING > EPI ? G * RING : EPI;
 };
 
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef u32x2 __attribute__((aligned(2))) u32x2_any;
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
 
-template <int BM, int BN, int WM, int WN, int S, bool F32OUT>
-__global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(TileArgs p) {
-  using T = Tile4<BM, BN, WM, WN, S>;
+template <int BM, int BN, int WM, int WN, int S, int G, bool F32OUT>
+__global__ __launch_bounds__(64 * WM * WN * G) void mx4_tile_kernel(TileArgs p) {
+  using T = Tile4<BM, BN, WM, WN, S, G>;
   constexpr int NW = T::NW, FM = T::FM, FN = T::FN;
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, all_waves = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = all_waves / NW, wave = all_waves % NW;
   const int lr = lane & 31, half = lane >> 5, wm = wave / WN, wn = wave % WN;
   // XCD b % 8 takes one run of the tiles, in groups of four rows of tiles: tiles that run together share x and W in its L2
   const int mt = (int)((p.M + BM - 1) / BM), nt = (p.N + BN - 1) / BN, all = mt * nt * p.splits, per = (all + 7) / 8;
@@ -62,34 +67,35 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(TileArgs p) {
   const int nb = tg / gs, mb = grp * 4 + tg - nb * gs;
   const int64_t m0 = (int64_t)mb * BM;
   const int n0 = nb * BN, rows = (int)min((int64_t)BM, p.M - m0), cols = min(BN, p.N - n0);
-  const int KA = p.K / 128, k0 = (int)((int64_t)KA * z / p.splits) * 2, steps = (int)((int64_t)KA * (z + 1) / p.splits) * 2 - k0;
-  const uint32_t rowb = (uint32_t)p.K / 2, lds0 = (uint32_t)(uintptr_t)lds;
+  const int KA = p.K / 128, parts = p.splits * G, part = z * G + group;
+  const int k0 = (int)((int64_t)KA * part / parts) * 2, steps = (int)((int64_t)KA * (part + 1) / parts) * 2 - k0;
+  const int rounds = (KA + parts - 1) / parts * 2;      // the most steps of a part
+  uint8_t* const ring = lds + group * T::RING;
+  const uint32_t rowb = (uint32_t)p.K / 2, lds0 = (uint32_t)(uintptr_t)ring;
   const uint8_t* xb = (const uint8_t*)(p.x + m0 * p.K) + (size_t)k0 * 128;
   const uint8_t* wb = p.w + (size_t)n0 * rowb + (size_t)k0 * 32;
   const uint8_t* sb = p.s + ((size_t)(k0 / 2) * p.N + n0) * 4;
   // 16-byte chunks of a row are swapped among themselves so that 16 lanes that read one chunk of 16 rows hit all banks
-  uint32_t a_off[T::NA], b_off[T::NB], s_off[T::NS];
+  uint32_t off[T::L];
 #pragma unroll
-  for (int i = 0; i < T::NA; ++i) {
-    const int r = (NW * i + wave) * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
-    a_off[i] = (uint32_t)min(r, rows - 1) * (uint32_t)p.K * 2 + c * 16;
+  for (int c = 0; c < T::L; ++c) {
+    const int q = min(NW * c + wave, T::PA + T::PB + T::PS - 1);
+    if (q < T::PA) {
+      const int r = q * 8 + (lane >> 3), k = (lane & 7) ^ ((r >> 1) & 7);
+      off[c] = (uint32_t)min(r, rows - 1) * (uint32_t)p.K * 2 + k * 16;
+    } else if (q < T::PA + T::PB) {
+      const int r = (q - T::PA) * 32 + (lane >> 1), k = (lane & 1) ^ ((r >> 3) & 1);
+      off[c] = (uint32_t)min(r, cols - 1) * rowb + k * 16;
+    } else {
+      off[c] = (uint32_t)min((q - T::PA - T::PB) * 64 + lane, cols - 1) * 4;
+    }
   }
-#pragma unroll
-  for (int i = 0; i < T::NB; ++i) {
-    const int r = (NW * i + wave) % (BN / 32) * 32 + (lane >> 1), c = (lane & 1) ^ ((r >> 3) & 1);
-    b_off[i] = (uint32_t)min(r, cols - 1) * rowb + c * 16;
-  }
-#pragma unroll
-  for (int i = 0; i < T::NS; ++i) s_off[i] = (uint32_t)min((NW * i + wave) % (BN / 64) * 64 + lane, cols - 1) * 4;
   auto copy = [&](int i, int c) __attribute__((always_inline)) {   // copy c of step i
     const uint32_t st = lds0 + (uint32_t)(i % S) * T::STAGE;
-    if (c < T::NA) copy16(xb + (size_t)i * 128, a_off[c], __builtin_amdgcn_readfirstlane(st + T::A + (NW * c + wave) * 1024));
-    else if (c < T::NA + T::NB)
-      copy16(wb + (size_t)i * 32, b_off[c - T::NA],
-             __builtin_amdgcn_readfirstlane(st + T::B + (NW * (c - T::NA) + wave) % (BN / 32) * 1024));
-    else
-      copy4(sb + (size_t)(i / 2) * p.N * 4, s_off[c - T::NA - T::NB],
-            __builtin_amdgcn_readfirstlane(st + T::SC + (NW * (c - T::NA - T::NB) + wave) % (BN / 64) * 256));
+    const int q = min(NW * c + wave, T::PA + T::PB + T::PS - 1);
+    if (q < T::PA) copy16(xb + (size_t)i * 128, off[c], __builtin_amdgcn_readfirstlane(st + T::A + q * 1024));
+    else if (q < T::PA + T::PB) copy16(wb + (size_t)i * 32, off[c], __builtin_amdgcn_readfirstlane(st + T::B + (q - T::PA) * 1024));
+    else copy4(sb + (size_t)(i / 2) * p.N * 4, off[c], __builtin_amdgcn_readfirstlane(st + T::SC + (q - T::PA - T::PB) * 256));
   };
   f32x16 acc[FM][FN];
 #pragma unroll
@@ -111,11 +117,12 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(TileArgs p) {
     if (i < steps)
 #pragma unroll
       for (int c = 0; c < T::L; ++c) copy(i, c);
-  for (int i = 0; i < steps; ++i) {
+  for (int i = 0; i < rounds; ++i) {
     if (steps - 1 - i >= S - 2) wait_copies<(S - 2) * T::L>();   // step i's have landed
     else wait_copies<0>();
     lds_barrier();     // for all wavefronts; and the stage before is read
-    const uint8_t* st = lds + (i % S) * T::STAGE;
+    if (i >= steps) continue;
+    const uint8_t* st = ring + (i % S) * T::STAGE;
 #pragma unroll
     for (int n = 0; n < FN; ++n) {
       const int r = wn * T::WTN + n * 32 + lr;
@@ -150,6 +157,41 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(TileArgs p) {
       for (int q = FM * FN; q < FM; ++q)
         if (j < 3) read_a(st, j + 1, q, (j + 1) & 1);
     }
+  }
+  if constexpr (G > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < FM; ++q)
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const f32x16& a = acc[q][n];
+          *(f32x4*)(lds + (group * BM + wm * T::WTM + q * 32 + lr) * T::RS + (wn * T::WTN + n * 32 + 8 * v + 4 * half) * 4) =
+              f32x4{a[4 * v], a[4 * v + 1], a[4 * v + 2], a[4 * v + 3]};
+        }
+    __syncthreads();
+    for (int k = tid; k < BM * BN / 4; k += 64 * NW * G) {
+      const int row = k / (BN / 4), col = k % (BN / 4) * 4;
+      if (row >= rows || col >= cols) continue;
+      f32x4 sum = *(const f32x4*)(lds + row * T::RS + col * 4);
+#pragma unroll
+      for (int g = 1; g < G; ++g) sum += *(const f32x4*)(lds + (g * BM + row) * T::RS + col * 4);
+      const int64_t at = (m0 + row) * p.N + n0 + col;
+      if constexpr (F32OUT) {
+        float* o = (float*)p.out + z * p.plane + at;
+        if (col + 4 <= cols) *(f32x4_any*)o = sum;
+        else
+          for (int b = 0; b < cols - col; ++b) o[b] = sum[b];
+      } else {
+        bf16_t* o = (bf16_t*)p.out + at;
+        if (col + 4 <= cols)
+          *(u32x2_any*)o = u32x2{(uint32_t)f2bf(sum[0]) | (uint32_t)f2bf(sum[1]) << 16, (uint32_t)f2bf(sum[2]) | (uint32_t)f2bf(sum[3]) << 16};
+        else
+          for (int b = 0; b < cols - col; ++b) o[b] = f2bf(sum[b]);
+      }
+    }
+    return;
   }
   // 32 rows of x at a time through this wavefront's part of LDS, so that a store covers whole pieces of a row
   constexpr int EB = F32OUT ? 4 : 2, RS = T::WTN * EB + 16, CPR = T::WTN * EB / 16;
@@ -201,29 +243,45 @@ __global__ __launch_bounds__(256) void mx4_join_kernel(const float* planes, int6
     }
 }
 
+// The tile shape and the splits of K.  A round of 256 workgroups takes K / splits times its shape's nanoseconds a column
+// (measured with about 256 tiles), and splits add a launch and the traffic of their sums; the least is taken.  Measured, us:
+// 61 x 4168 x 7168 64 x 64 in 3 splits 14.6, in one 23.5, 32 x 64 in 3 15.7; 32 x 4096 x 7168 32 x 64 in 4 splits 11.5, 64 x 64 in 4
+// 13.0; 512 x 4096 x 4096 64 x 128 23.5, 64 x 64 32.9, 128 x 128 29.3; 1024 x 4096 x 4096 128 x 128 34.7, 128 x 256 50.9;
+// 1024 x 7168 x 2048 128 x 256 31.6, 128 x 128 36.5, 256 x 256 45.3; 2045 x 7168 x 4096 256 x 256 100.6, 128 x 256 105.8.
 struct TilePlan {
-  int kind, splits;     // 0: 64 x 64, 1: 128 x 128, 2: 256 x 256
+  int kind, splits;
   int64_t tiles;
 };
 static TilePlan tile_plan(int64_t M, int64_t N, int64_t K) {
-  auto tiles = [&](int64_t b) { return ((M + b - 1) / b) * ((N + b - 1) / b); };
-  if (tiles(256) >= 128) return {2, 1, tiles(256)};
-  if (tiles(128) >= 128) return {1, 1, tiles(128)};
-  const int64_t n = tiles(64);
-  return {0, (int)std::max<int64_t>(1, std::min<int64_t>(K / 512, 320 / n)), n};
+  constexpr struct { int bm, bn, groups; double ns; } shapes[] = {{32, 64, 4, 2.1},   {64, 64, 4, 3.5},    {64, 128, 2, 5.0},
+                                                                   {128, 128, 2, 7.6}, {128, 256, 1, 12.8}, {256, 256, 1, 23.5}};
+  TilePlan best{0, 1, 0};
+  double least = 0;
+  for (int k = 0; k < 6; ++k) {
+    const int64_t tiles = (M + shapes[k].bm - 1) / shapes[k].bm * ((N + shapes[k].bn - 1) / shapes[k].bn);
+    for (int s = 1; s <= 16 && (s == 1 || K >= 128 * (int64_t)s * shapes[k].groups); ++s) {
+      const double join = s == 1 ? 0 : 2600 + (double)M * N * s * 8 / 2400;      // ns
+      const double t = (double)((tiles * s + 255) / 256) * K / s * shapes[k].ns + join;
+      if (best.tiles == 0 || t < least) {
+        best = {k, s, tiles};
+        least = t;
+      }
+    }
+  }
+  return best;
 }
 size_t mx4_tile_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   const TilePlan t = tile_plan(M, N, K);
   return t.splits == 1 ? 0 : (size_t)t.splits * ((M * N + 3) / 4 * 4) * sizeof(float);
 }
 
-template <int BM, int BN, int WM, int WN, int S>
+template <int BM, int BN, int WM, int WN, int S, int G>
 static hipError_t run_tiles(const TileArgs& a, bool f32, int64_t tiles, hipStream_t st) {
-  using T = Tile4<BM, BN, WM, WN, S>;
-  auto kern = f32 ? mx4_tile_kernel<BM, BN, WM, WN, S, true> : mx4_tile_kernel<BM, BN, WM, WN, S, false>;
+  using T = Tile4<BM, BN, WM, WN, S, G>;
+  auto kern = f32 ? mx4_tile_kernel<BM, BN, WM, WN, S, G, true> : mx4_tile_kernel<BM, BN, WM, WN, S, G, false>;
   const hipError_t err = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
   if (err != hipSuccess) return err;
-  kern<<<(unsigned)((tiles * a.splits + 7) / 8 * 8), 64 * T::NW, T::LDS, st>>>(a);
+  kern<<<(unsigned)((tiles * a.splits + 7) / 8 * 8), 64 * T::NW * G, T::LDS, st>>>(a);
   return hipGetLastError();
 }
 
@@ -235,9 +293,14 @@ hipError_t launch_mx4_tiles(const void* x, const uint8_t* w, const uint8_t* w_sc
   const TileArgs a{(const bf16_t*)x, w, w_scale, M, (int)N, (int)K, join ? ws : out, t.splits, plane};
   const bool f32 = join || f32_out;
   hipError_t err;
-  if (t.kind == 2) err = run_tiles<256, 256, 2, 4, 3>(a, f32, t.tiles, st);
-  else if (t.kind == 1) err = run_tiles<128, 128, 2, 2, 3>(a, f32, t.tiles, st);
-  else err = run_tiles<64, 64, 2, 2, 6>(a, f32, t.tiles, st);
+  switch (t.kind) {
+    case 0: err = run_tiles<32, 64, 1, 2, 3, 4>(a, f32, t.tiles, st); break;
+    case 1: err = run_tiles<64, 64, 2, 2, 3, 4>(a, f32, t.tiles, st); break;
+    case 2: err = run_tiles<64, 128, 2, 2, 3, 2>(a, f32, t.tiles, st); break;
+    case 3: err = run_tiles<128, 128, 2, 2, 3, 2>(a, f32, t.tiles, st); break;
+    case 4: err = run_tiles<128, 256, 2, 4, 3, 1>(a, f32, t.tiles, st); break;
+    default: err = run_tiles<256, 256, 2, 4, 3, 1>(a, f32, t.tiles, st);
+  }
   if (err != hipSuccess || !join) return err;
   const unsigned grid = (unsigned)((M * N + 1023) / 1024);
   if (f32_out) mx4_join_kernel<true><<<grid, 256, 0, st>>>((const float*)ws, plane, t.splits, M * N, out);
