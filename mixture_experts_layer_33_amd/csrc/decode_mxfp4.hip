@@ -31,6 +31,7 @@ struct D4Args {
   ScoreRule rule;
   int run;         // group_run of the experts' groups, for the lanes' experts in the choice
   float* planes;   // [D4_KS][T][E] partial logits
+  struct D4Entries* entries;   // of the down product
   int32_t* topk_idx;
   float* topk_gate;
   bf16_t* h;       // [2][T k][f] (hi, lo), then the shared expert's [2][T][fs]
@@ -51,7 +52,7 @@ struct D4List {
 // one product: an expert of more tokens has several.  Up to four tokens in all a column is a token's own (-1: not chosen).
 constexpr int D4_COLS = 4;
 constexpr int D4_ENTRIES = D4_PAIRS + D4_TMAX / D4_COLS;
-struct D4Entries {
+struct __attribute__((aligned(16))) D4Entries {
   int32_t n, routed;
   int16_t before[D4_PAIRS];               // entries of the experts before
   int16_t expert[D4_ENTRIES];
@@ -99,7 +100,7 @@ __device__ __forceinline__ void d4_entries(const D4Args& p, const D4List& L, D4E
     }
     if (threadIdx.x == 0) N.routed = sum;
   }
-  __syncthreads();
+  lds_barrier();
   for (int u = threadIdx.x; u <= L.U; u += blockDim.x) {
     const bool shared = u == L.U;
     const int at = shared ? N.routed : N.before[u];
@@ -116,7 +117,7 @@ __device__ __forceinline__ void d4_entries(const D4Args& p, const D4List& L, D4E
     }
     if (shared) N.n = at + parts;
   }
-  __syncthreads();
+  lds_barrier();
 }
 
 // ------------------------------------------------------------------ gate and up
@@ -136,7 +137,7 @@ template <int PPW, int TS>
 constexpr int D4_UP_LDS = (PPW * TS < 4 ? PPW * TS : 4) * 8 * XBLOCK > (int)sizeof(D4Part<TS>) ? (PPW * TS < 4 ? PPW * TS : 4) * 8 * XBLOCK
                                                                                               : (int)sizeof(D4Part<TS>);
 template <int PPW, int TS, int D>        // TS: sets of eight tokens
-__device__ __forceinline__ void d4_up(const D4Args& p, D4List& L, uint8_t* stage) {
+__device__ __forceinline__ void d4_up(const D4Args& p, D4List& L, D4Entries& N, uint8_t* stage) {
   D4Part<TS>& part = *(D4Part<TS>*)stage;
   constexpr int GROUP = D4Part<TS>::GROUP;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), NW = blockDim.x >> 6;
@@ -270,6 +271,10 @@ __device__ __forceinline__ void d4_up(const D4Args& p, D4List& L, uint8_t* stage
 #pragma unroll
     for (int i = 0; i < PPW; ++i) load(w[s][i], i);
   }
+  if (b == 0) {       // while the first weights come: the entries, for every workgroup of the down product
+    d4_entries(p, L, N);
+    for (int i = tid; i < (int)(sizeof(D4Entries) / 16); i += blockDim.x) ((u32x4*)p.entries)[i] = ((const u32x4*)&N)[i];
+  }
   for (int m = 0; m < steps; m += D) {
     unrolled<D>([&](auto s) __attribute__((always_inline)) {
       constexpr int S = decltype(s)::value;
@@ -314,6 +319,7 @@ __global__ __launch_bounds__(256) void d4_logits_kernel(D4Args p) {
       float a[2] = {0.f, 0.f};
 #pragma unroll
       for (int q = 0; q < IT; ++q) {
+        if (q * 256 >= n) break;
         const int i = min(q * 256 + lane * 4, max(n - 4, 0));   // past the slice w is zero
         const u32x2 v = n > 0 ? *(const u32x2*)(xs + t * D4_SLICE + i) : u32x2{0, 0};
 #pragma unroll
@@ -380,6 +386,7 @@ __device__ __forceinline__ void d4_planes(const D4Args& p, int t, int z0, float 
 template <int PPW, int TS, int D, int VPL>
 __global__ __launch_bounds__(512) void d4_up_kernel(D4Args p) {
   __shared__ D4List L;
+  __shared__ D4Entries N;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[D4_UP_LDS<PPW, TS>];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), NW = blockDim.x >> 6;
   float* row = (float*)lds + wave * 64 * VPL;      // the choice's, before anything else
@@ -402,7 +409,7 @@ __global__ __launch_bounds__(512) void d4_up_kernel(D4Args p) {
     d4_choose<VPL, 1>(p, L, row, t, l, bias, bal);
   }
   __syncthreads();
-  d4_up<PPW, TS, D>(p, L, lds);
+  d4_up<PPW, TS, D>(p, L, N, lds);
 }
 
 // ------------------------------------------------------------------ down
@@ -579,14 +586,10 @@ __device__ __forceinline__ void d4_down(const D4Args& p, const D4Entries& N, D4D
 
 template <int NT, int D>
 __global__ __launch_bounds__(512) void d4_down_kernel(D4Args p, int RW) {
-  __shared__ D4List L;
   __shared__ D4Entries N;
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  d4_clear(L);
-  for (int q = threadIdx.x; q < p.T * p.k; q += blockDim.x) L.id[q] = p.topk_idx[q];
+  for (int i = threadIdx.x; i < (int)(sizeof(D4Entries) / 16); i += blockDim.x) ((u32x4*)&N)[i] = ((const u32x4*)p.entries)[i];
   __syncthreads();
-  d4_list(p, L);
-  d4_entries(p, L, N);
   for (int o0 = blockIdx.x * RW; o0 < p.d; o0 += gridDim.x * RW) {
     d4_down<NT, D>(p, N, *(D4Down<NT, D>*)lds, o0, min(RW, p.d - o0));
     __syncthreads();
@@ -603,10 +606,11 @@ static hipError_t run_down(const D4Args& a, int RW, int grid, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Workspace: partial logits [D4_KS][T][E] | h [2][T k][f] | [2][T fs].
+// Workspace: partial logits [D4_KS][T][E] | entries | h [2][T k][f] | [2][T fs].
 static size_t d4_planes_bytes(int T, int E) { return ((size_t)D4_KS * T * E * sizeof(float) + 255) & ~(size_t)255; }
+constexpr size_t D4_ENTRY_BYTES = (sizeof(D4Entries) + 255) & ~(size_t)255;
 size_t decode_mxfp4_workspace_bytes(int T, int E, int k, int f, int fs) {
-  return d4_planes_bytes(T, E) + 4 * ((size_t)T * k * f + (size_t)T * fs);
+  return d4_planes_bytes(T, E) + D4_ENTRY_BYTES + 4 * ((size_t)T * k * f + (size_t)T * fs);
 }
 
 template <int PPW, int TS>
@@ -628,8 +632,8 @@ hipError_t launch_decode_mxfp4(const void* x, const float* w_r, const float* b_r
   uint8_t* base = (uint8_t*)ws;
   const D4Args a{(const bf16_t*)x, w.gate, w.up, w.down, w.s_gate, w.s_up, w.s_down, shared.gate, shared.up, shared.down,
                  shared.s_gate, shared.s_up, shared.s_down, T, d, E, k, f, fs, w_r, b_r, balance, rule,
-                 group_run(E / rule.groups, E <= 256 ? 4 : E <= 512 ? 8 : 16), (float*)base, topk_idx, topk_gate,
-                 (bf16_t*)(base + d4_planes_bytes(T, E)), (bf16_t*)y};
+                 group_run(E / rule.groups, E <= 256 ? 4 : E <= 512 ? 8 : 16), (float*)base, (D4Entries*)(base + d4_planes_bytes(T, E)),
+                 topk_idx, topk_gate, (bf16_t*)(base + d4_planes_bytes(T, E) + D4_ENTRY_BYTES), (bf16_t*)y};
   d4_logits_kernel<<<(E + 7) / 8 * D4_KS, 256, 0, st>>>(a);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   const int P = (d + 255) / 256, nw = std::min(8, P), ppw = (P + nw - 1) / nw;
