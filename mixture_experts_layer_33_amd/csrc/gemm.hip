@@ -83,10 +83,11 @@ static hipError_t run_mfma(const GemmArgs& a, int max_tiles, hipStream_t st) {
   return hipGetLastError();
 }
 
-// MXFP4 weights, tiles of up to 128 rows, K a multiple of 256: whole 128-byte lines of the codes a copy (KB = 256; with half
-// lines of KB = 128 each line was fetched twice: 64 rows of each of 256 experts, 7168 x 2048, gate and up | down
-// 1054 | 667 us, with whole lines 943 | 507).  What bounds it is how many bytes of W are on their way: a tile of up to
-// 64 rows (the last, or only one of an expert) has room for a third stage beside half as many rows of A.
+// MXFP4 weights, tiles of up to 128 rows, K a multiple of 256: a copy takes whole 128-byte lines of the codes (KB = 256; other K
+// go in half lines, KB = 128 in four stages.  64 rows on average of each of 256 experts, 7168 x 2048, gate/up | down: half
+// lines 1054 | 667 us, whole ones 943 | 507).  What bounds it then is how many bytes of W are on their way: 32 KB a
+// workgroup beside 128 rows of A in two stages.  A tile of up to 64 rows (the last, or only one of an expert) has room for a third
+// stage: gate/up of the same experts with 32 | 64 | 72 | 128 rows each 633 | 740 | 875 | 999 us, 6.4 | 5.6 | 4.7 | 4.2 TB/s.
 template <bool SWIGLU, int POL>
 __global__ __launch_bounds__(512) void gg_w4_kernel(GemmArgs p) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
