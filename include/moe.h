@@ -577,7 +577,8 @@ size_t moe_matmul_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *      infinity or NaN may reach every token of the call.
  * Out: y [T,d] bf16; topk_idx [T,k] int32, ascending; topk_gate [T,k] f32.
  * No output may overlap an input or another output.
- * MOE_MXFP4 only; top_k <= 16, d <= 8192, f and fs <= 65536, fs a multiple of 128 (MOE_ERR_SHAPE otherwise).
+ * MOE_MXFP4 only; top_k <= 16, d <= 8192, f and fs <= 65536, fs a multiple of 128, E f d < 2^36 (MOE_ERR_SHAPE
+ * otherwise).
  * workspace: moe_workspace_bytes(shape, MOE_OP_DECODE) bytes (no initial contents needed).  x, w_router, weights and
  * workspace are aligned to 16 bytes, y to 2, everything else to 4 (MOE_ERR_ALIGN).
  */

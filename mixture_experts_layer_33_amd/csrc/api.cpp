@@ -75,11 +75,13 @@ int check_shape(const moe_shape* s) {
 int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 // What moe_decode_mxfp4 takes of a shape that check_shape has passed: a wavefront's part of a token is registers (d), the
-// expert list 16 x 16 entries, and a shared expert's matrix is addressed with 32-bit offsets like a routed one's.
+// expert list 16 x 16 entries, a shared expert's matrix is addressed with 32-bit offsets like a routed one's, and so is the
+// whole stack's array of scale bytes (E f d / 32, below 2 GiB).
 int decode_mxfp4_shape(const moe_shape* s) {
   if (s->tokens < 1 || s->tokens > 16 || s->top_k > 16 || s->hidden > 8192 || s->ffn > 65536 || s->shared_ffn > 65536 ||
       s->shared_ffn % 128)
     return MOE_ERR_SHAPE;
+  if ((int64_t)s->hidden * s->ffn >= ((int64_t)1 << 36) / s->experts) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 

@@ -173,6 +173,59 @@ def test_matmul_of_nothing():
     moe.moe_matmul_mxfp4(torch.zeros(3, 256, dtype=BF, device=DEV), w[:0], s[:, :0].contiguous(), torch.empty(3, 0, dtype=F32, device=DEV))
 
 
+def test_matmul_of_many_bytes():
+    """Codes, rows and outputs whose offsets pass 2^31 and 2^32: the last ones are as right as the first."""
+    print("\n[case] matmul_mxfp4 large", flush=True)
+    g = gen(6)
+    N, K = 262128, 16256                       # 2.1 GB of codes
+    w, s = torch.zeros(N, K // 2, dtype=U8, device=DEV), torch.full((K // 128, N, 4), 127, dtype=U8, device=DEV)
+    at = torch.tensor([0, 1, N // 2, N - 9, N - 2, N - 1], device=DEV)
+    part, ps, W = weights(g, len(at), K)
+    w[at], s[:, at] = part, ps
+    for M in (1, 11, 20):
+        x = randn(g, M, K, dtype=BF)
+        out = matmul(x, w, s, F32)
+        check_product(out[:, at], x, W)
+        rest = torch.ones(N, dtype=torch.bool, device=DEV)
+        rest[at] = False
+        assert bool((out[:, rest] == 0).all())
+    del w, s, out, rest
+    M, K, N = 250007, 16384, 24                # 8.2 GB of rows
+    x = torch.zeros(M, K, dtype=BF, device=DEV)
+    at = torch.tensor([0, 127, M // 2, M - 3, M - 1], device=DEV)
+    x[at] = randn(g, len(at), K, dtype=BF)
+    w, s, W = weights(g, N, K)
+    out = matmul(x, w, s, F32)
+    check_product(out[at], x[at], W)
+    out[at] = 0
+    assert bool((out == 0).all())
+
+
+def test_matmul_side_stream_and_graph():
+    print("\n[case] matmul_mxfp4 graph", flush=True)
+    for M, N, K in ((2, 512, 1024), (12, 512, 9216), (40, 520, 4096), (300, 520, 512), (2100, 1024, 256)):
+        g = gen(M)
+        x = randn(g, M, K, dtype=BF)
+        w, s, _ = weights(g, N, K)
+        want = matmul(x, w, s, BF)
+        ws = moe.matmul_mxfp4_workspace(M, N, K, DEV)
+        out = torch.zeros_like(want)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        moe.moe_matmul_mxfp4(x, w, s, out, ws, stream=side)
+        side.synchronize()
+        assert same_bits(out, want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.moe_matmul_mxfp4(x, w, s, out, ws)
+        for _ in range(4):
+            x.mul_(-1.5)
+            graph.replay()
+            torch.cuda.synchronize()
+            got = out.clone()
+            assert same_bits(got, matmul(x, w, s, BF))
+
+
 # ----------------------------------------------------------------------------- the layer for a few tokens
 class Decode:
     def __init__(self, T, d, E, k, f, fs=0, seed=0, bias=False, balance=False, **rule):
@@ -308,6 +361,40 @@ def test_decode_tokens_are_independent():
         assert bool(torch.isnan(y[2]).all())
 
 
+def test_decode_in_graphs_that_share_a_workspace():
+    """Two captured calls of different shapes with one workspace, replayed in turn, and calls on two streams with a workspace each."""
+    print("\n[case] decode_mxfp4 graphs", flush=True)
+    cases = [Decode(T=3, d=640, E=24, k=3, f=256, fs=128, seed=80), Decode(T=12, d=384, E=300, k=4, f=128, seed=81)]
+    big = torch.full((max(c.ws.numel() for c in cases),), 0x5A, dtype=U8, device=DEV)
+    graphs = []
+    for c in cases:
+        c.run(ws=big)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            c.run(ws=big)
+        graphs.append(graph)
+    for i in range(3):
+        for c, graph in zip(cases, graphs):
+            c.x.copy_(randn(gen(90 + i), *c.x.shape, dtype=BF))
+            graph.replay()
+            torch.cuda.synchronize()
+            got = [t.clone() for t in c.out]
+            eager = tuple(torch.empty_like(t) for t in c.out)
+            c.run(out=eager)
+            torch.cuda.synchronize()
+            assert all(same_bits(a, b) for a, b in zip(got, eager))
+    want = [[t.clone() for t in c.run()] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, stream in zip(cases, streams):
+            c.run(stream=stream)
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        assert all(same_bits(a, b) for a, b in zip(c.out, w))
+
+
 def test_decode_experts_that_are_taken_out():
     """A bias of -inf takes experts out; a token that keeps none has gates 0 and the shared expert's output alone."""
     print("\n[case] decode_mxfp4 -inf", flush=True)
@@ -431,6 +518,21 @@ def test_experts_are_the_mxfp8_layers(name):
     torch.cuda.synchronize()
     print("  bits equal:", same_bits(y, y8), flush=True)
     assert np.linalg.norm(host(y) - host(y8)) <= 2.0 ** -7 * np.linalg.norm(host(y8))
+
+
+def test_experts_in_a_graph():
+    print("\n[case] expert_ffn mxfp4 graph", flush=True)
+    c = Experts(**EXPERTS["long_rows"], seed=5)
+    want = c.run()[3].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = c.run()[3]
+    for _ in range(3):
+        y.fill_(1)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same_bits(y, want)
 
 
 def test_layer_serves_a_prompt_and_then_tokens():

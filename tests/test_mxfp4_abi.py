@@ -74,7 +74,8 @@ def test_decode_refusals():
         assert decode(shape(ty)) == DTYPE
     assert decode(None) == NULL and decode(s, None) == NULL
     assert decode(s, _lib.MoeRouter(2, 4, 2, 2, 1, 2.5)) == SHAPE
-    for bad in (dict(T=0), dict(T=17), dict(k=17, E=64), dict(d=8320), dict(f=65664), dict(fs=64), dict(fs=65664), dict(fs=-128)):
+    for bad in (dict(T=0), dict(T=17), dict(k=17, E=64), dict(d=8320), dict(f=65664), dict(fs=64), dict(fs=65664), dict(fs=-128),
+                dict(E=512, f=16384, d=8192), dict(E=1024, k=4, f=8192, d=8192)):      # scale bytes of 2 GiB
         assert decode(shape(**bad)) == SHAPE, bad
         assert moe.workspace_bytes(shape(**bad), moe.OP_DECODE) == 0
     for a in NAMES:
