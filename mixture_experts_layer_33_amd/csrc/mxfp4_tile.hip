@@ -9,6 +9,10 @@
 // that both share.  Lane half h takes scale block h of a step's two, four MFMAs j with the block's columns 8j .. 8j + 7:
 // a lane's codes of a step are one 16-byte read, under one scale.  W's rows are the first operand, so that a lane
 // holds four neighbouring outputs of one row of x.
+//
+// 2045 x 7168 x 4096 takes 94 us, 1.28 PFLOP/s, in 224 tiles of 256 x 256 (bound by the MFMAs at the clock they run at and by
+// 32 tiles too few for the chip); the library's product of bf16 weights, four times the bytes, takes 97.  61 x 4168 x 7168: 13 us, of
+// which the sums of three splits are 2: a tile's copies land 1 us after they are asked for, two steps ahead.
 #include <algorithm>
 
 #include "kernels.h"
