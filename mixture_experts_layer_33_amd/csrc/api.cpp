@@ -81,7 +81,7 @@ int decode_mxfp4_shape(const moe_shape* s) {
   if (s->tokens < 1 || s->tokens > 16 || s->top_k > 16 || s->hidden > 8192 || s->ffn > 65536 || s->shared_ffn > 65536 ||
       s->shared_ffn % 128)
     return MOE_ERR_SHAPE;
-  if ((int64_t)s->hidden * s->ffn >= ((int64_t)1 << 36) / s->experts) return MOE_ERR_SHAPE;
+  if ((int64_t)s->hidden * s->ffn * s->experts >= (int64_t)1 << 36) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 
