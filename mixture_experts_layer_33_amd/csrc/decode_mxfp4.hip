@@ -71,6 +71,15 @@ __device__ __forceinline__ void d4_clear(D4List& L) {   // before the barrier be
 }
 __device__ __forceinline__ void d4_list(const D4Args& p, D4List& L) {   // L.id is known
   const int tid = threadIdx.x, n = p.T * p.k;
+  if (p.T == 1) {       // one token's choice is ascending and distinct: it is the list (gate and up 35.9 -> 35.2 us)
+    if (tid < n) {
+      L.expert[tid] = L.id[tid];
+      L.slot[tid][0] = (uint8_t)(tid + 1);
+    }
+    if (tid == 0) L.U = n;
+    __syncthreads();
+    return;
+  }
   for (int q = tid; q < n; q += blockDim.x) atomicOr(&L.bits[L.id[q] >> 5], 1u << (L.id[q] & 31));
   __syncthreads();
   if (tid < 64) {
