@@ -679,8 +679,7 @@ int moe_quantize_fp8(const void* src_bf16, int64_t rows, int64_t cols, int row_b
 namespace {
 int check_matmul_fp8(int64_t M, int64_t N, int64_t K) {
   const int64_t top = ((int64_t)1 << 31) - 1;
-  if (M < 0 || N < 0 || K <= 0 || K % 128 || M > top || N > top) return MOE_ERR_SHAPE;
-  if (K >= (int64_t)1 << 23) return MOE_ERR_SHAPE;      // 32-bit offsets within a tile of 256 rows
+  if (M < 0 || N < 0 || K <= 0 || K % 128 || M > top || N > top || K > top) return MOE_ERR_SHAPE;
   if (M * K >= ((int64_t)1 << 32) || N * K >= ((int64_t)1 << 32) || M * N >= (int64_t)1 << 38)
     return MOE_ERR_SHAPE;
   return MOE_OK;
