@@ -40,8 +40,10 @@ struct SelectArgs {
 // one lane read (8 of 256 experts in 8 groups, 2,048 tokens: 8 us; 30 with strided ownership, plane
 // after plane, and two butterflies a round).  Past four keys a lane the sort costs more than looking
 // through them each round (512 experts, 8,192 tokens: 26 us sorted, 18 not).
+// Sixteen keys a lane and one plane sit at the border of 128 registers, above which a SIMD holds three wavefronts and not four:
+// the bound says which (32,768 tokens, d 1024: 1,024 experts 298 -> 292 us a call, 600 experts 210 -> 204).
 template <int VPL, int PB>   // PB: planes in flight after the first
-__global__ __launch_bounds__(256) void score_select_kernel(SelectArgs p, int run) {
+__global__ __launch_bounds__(256, VPL == 16 && PB == 1 ? 4 : 1) void score_select_kernel(SelectArgs p, int run) {
   __shared__ int chosen[4 * 32];
   __shared__ __attribute__((aligned(16))) float rows[4][64 * VPL];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
