@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "decode_runs.h"
 #include "fp8_tile.h"
 #include "kernels.h"
 #include "mx4.h"
@@ -450,33 +451,15 @@ __device__ __forceinline__ void d4_down(const D4Args& p, const D4Entries& N, D4D
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), NW = blockDim.x >> 6;
   const int g = lane >> 4, col = lane & 15, chunk = lane >> 3, row = lane & 7;
   for (int i = tid; i < NW * 2 * D4_TMAX * 16 * NT; i += blockDim.x) (&m.y[0][0][0][0])[i] = 0.f;
-  const int per = (p.f + 255) / 256, pers = (p.fs + 255) / 256, run = p.T > D4_COLS ? 4 : 1;
-  const int entries = __builtin_amdgcn_readfirstlane(N.n), routed = __builtin_amdgcn_readfirstlane(N.routed);
-  const int runs = (per + run - 1) / run, runss = (pers + run - 1) / run, all = routed * runs + (entries - routed) * runss;
+  const D4Runs runs = d4_runs(__builtin_amdgcn_readfirstlane(N.routed), __builtin_amdgcn_readfirstlane(N.n), (p.f + 255) / 256,
+                              (p.fs + 255) / 256, p.T > D4_COLS ? 4 : 1);
+  const int all = runs.all;
   const int64_t nh = (int64_t)p.T * p.k * p.f, nsh = (int64_t)p.T * p.fs;
-  // pair `i` of run number `n`, `length` long, of an entry
-  struct Place {
-    int n, i, entry, from, length;
-  };
-  auto set = [&](Place& at) __attribute__((always_inline)) {
-    const bool shared = at.n >= routed * runs;
-    const int q = shared ? at.n - routed * runs : at.n, of = shared ? runss : runs;
-    const int en = q / of, r = q - en * of;
-    at.entry = min(shared ? routed + en : en, entries - 1);
-    at.from = r * run;
-    at.length = min(run, (shared ? pers : per) - at.from);
-    at.i = 0;
-  };
-  auto advance = [&](Place& at) __attribute__((always_inline)) {   // whether that is another run
-    if (++at.i < at.length) return false;
-    at.n += NW;
-    set(at);
-    return true;
-  };
+  auto advance = [&](D4Place& at) __attribute__((always_inline)) { return d4_advance(runs, NW, at); };
   const int turned = blockIdx.x & 3;
   int F = 0;
-  Place next{wave, 0, 0, 0, 0};    // whose loads come next
-  set(next);
+  D4Place next{wave, 0, 0, 0, 0};    // whose loads come next
+  d4_set(runs, next);
   __amdgpu_buffer_rsrc_t wr, sr;
   const bf16_t* hbase = nullptr;
   int hrow[D4_COLS];
@@ -537,8 +520,8 @@ __device__ __forceinline__ void d4_down(const D4Args& p, const D4Entries& N, D4D
   f32x4 acc[2 * NT];
 #pragma unroll
   for (int r = 0; r < 2 * NT; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
-  Place now{wave, 0, 0, 0, 0};     // which is multiplied next
-  set(now);
+  D4Place now{wave, 0, 0, 0, 0};     // which is multiplied next
+  d4_set(runs, now);
   auto flush = [&](int entry) __attribute__((always_inline)) {
     const int ex = (int)N.expert[entry], hr = N.row[entry][col & 3];
     const int t = p.T <= D4_COLS ? ((col & 3) < p.T ? col & 3 : -1) : ex == p.E ? hr : hr >= 0 ? hr / p.k : -1;
