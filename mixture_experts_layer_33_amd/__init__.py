@@ -508,7 +508,8 @@ class Layer:
     """Buffers of one layer shape, and the forward / backward / decode as chained C calls.
 
     Expert weights are passed per call; for MXFP8 pass their MX codes and scales, for FP8 those of
-    quantize_fp8, for MXFP4 those of quantize_mxfp4.  With a `router` (make_router) the layer routes by moe_route_scored.
+    quantize_fp8, for MXFP4 those of quantize_mxfp4 (no backward: ValueError).  With a `router` (make_router) the layer
+    routes by moe_route_scored.
 
     The layer remembers the rule of the last call that routed (route, forward, forward_fused, decode), and a
     backward of other gates raises ValueError.  A replayed graph's forward is not seen: capture the backward with
@@ -551,6 +552,10 @@ class Layer:
             if r.score != SCORE_SOFTMAX or not r.renormalise or r.scale != 1.0:
                 raise ValueError(f"{fn}: the tokens were routed by a router whose gates have another gradient than moe_route's "
                                  "(renormalised softmax, scale 1)")
+
+    def _no_mxfp4(self, fn):
+        if self.shape.dtype == MOE_MXFP4:
+            raise ValueError(f"{fn}: an MXFP4 layer has no backward")
 
     def route(self, x, w_router, b_router=None, router=None, balance=None):
         s = self.shape
@@ -614,6 +619,8 @@ class Layer:
 
     def expert_ffn(self, ring_x, ring_x_scale, expert_offset, head, w_gate, w_up, w_down,
                    scales=(None, None, None), save_au=False, events=None):
+        if save_au:
+            self._no_mxfp4("expert_ffn(save_au=True)")
         s = self.shape
         ydt = torch.float32 if s.dtype == MOE_F32 else torch.bfloat16
         ring_y = self._buf("ring_y", (s.capacity, s.hidden), ydt)
@@ -637,6 +644,8 @@ class Layer:
                 head=0, save_au=False, events=None, router=None, balance=None, x8=None, x8_scale=None):
         """x8 and x8_scale: the 8-bit rows of x for the experts (add_rmsnorm), instead of
         quantising x in the dispatch."""
+        if save_au:
+            self._no_mxfp4("forward(save_au=True)")
         idx, gate, cnt = self.route(x, w_router, b_router, router, balance)
         ring, rsc, off, cs, sc = self.dispatch(x if x8 is None else x8, idx, head, x8_scale)
         ring_y, au = self.expert_ffn(ring, rsc, off, head, w_gate, w_up, w_down, scales, save_au,
@@ -694,6 +703,7 @@ class Layer:
         """The MXFP8 layer's gradients after forward(..., save_au=True) with the same buffers.  Its router part is
         that of moe_route's gates: after a forward with another router (sigmoid or plain softmax scores, a scale) it
         raises ValueError."""
+        self._no_mxfp4("backward_mx")
         self._check_rule("backward_mx")
         s = self.shape
         b = self.bufs
@@ -713,6 +723,7 @@ class Layer:
         and the bias's gradient is left in bufs["db_router"]).  After an FP8 forward the weights
         are the bf16 ones: the tokens are dispatched again in bf16, and the forward's rounding to
         8 bits counts as the identity."""
+        self._no_mxfp4("backward")
         self._check_rule("backward", router)
         s = self.shape
         b = self.bufs
