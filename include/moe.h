@@ -551,8 +551,8 @@ int moe_quantize_mxfp4(const void* src_bf16, int64_t rows, int64_t cols, uint8_t
 /*
  * moe_matmul_mxfp4: out = X W^T of bf16 rows and an MXFP4 matrix in nn.Linear layout,
  *   out[m,n] = sum_b 2^(w_scale[n,b] - 127) sum_{i in block b of 32} x[m,i] w[n,i],
- * products exact, sums in fp32, one rounding.  out may not overlap an input.  A scale byte of 252 or more gives
- * values past bf16's range, which count as infinite (255: NaN).
+ * products exact, sums in fp32, one rounding.  out may not overlap an input.  Weights past bf16's
+ * range, 2^128 and above, count as infinite: some of those under a scale byte of 253 or 254 (255: NaN).
  * In:  x [M,K] bf16; w [N,K/2] codes, w_scale [K/128][N][4] (moe_quantize_mxfp4).  K % 128 == 0; M K and
  *      N K < 2^32, M N < 2^38, K < 2^23.
  * Out: out [M,N]: out_dtype MOE_BF16 or MOE_F32 (MOE_ERR_DTYPE otherwise).
@@ -569,11 +569,12 @@ size_t moe_matmul_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * toolnavs.com warp-decode page, for this weight format and with moe_route_scored's rules):
  *   S_t, g_t by `router` (as moe_route_scored);  y_t = sum_j g_tj E_{S_tj}(x_t) + E_shared(x_t),
  * x in bf16 as it is (no 8-bit rows), products exact, sums in fp32; the inner h, times its gate, is held to 2^-16 of
- * its value; y is rounded once.  The logits are moe_route_scored's, summed in another order.
+ * its value (below 2^-117 to 2^-133, bf16's smallest step); y is rounded once.  The logits are moe_route_scored's, summed in another order.
  * In:  x [T,d] bf16, T = shape->tokens in 1..16; w_router [E,d] f32, b_router and balance [E] f32 or NULL;
  *      w_gate, w_up [E,f,d/2] and w_down [E,d,f/2] codes, w_gate_scale and w_up_scale [d/128][E*f][4],
  *      w_down_scale [f/128][E*d][4]; the shared expert's ws_gate, ws_up [fs,d/2], ws_down [d,fs/2] and scales
- *      likewise, read only when fs = shape->shared_ffn > 0.  Weights are finite (scale bytes up to 251): an expert's
+ *      likewise, read only when fs = shape->shared_ffn > 0.  Weights are finite (scale bytes up to 252, the largest
+ *      that moe_quantize_mxfp4 writes for finite values): an expert's
  *      infinity or NaN may reach every token of the call.
  * Out: y [T,d] bf16; topk_idx [T,k] int32, ascending; topk_gate [T,k] f32.
  * No output may overlap an input or another output.

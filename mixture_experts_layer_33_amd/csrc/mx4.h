@@ -14,8 +14,9 @@
 // that an operand of 16 tokens would, and up to eight tokens the MFMAs are as many as without the split.
 //
 // The codes widen to bf16 by gfx950's v_cvt_scalef32_pk_bf16_fp4 (two codes and the block's scale in one instruction at the
-// full VALU rate; checked for every byte, byte place and scale from 2^-127 up: code value x 2^(byte - 127), NaN for byte
-// 255).  E2M1 x 2^X is exact in bf16, products and sums are the bf16 MFMA's in fp32.
+// full VALU rate; checked for every byte, byte place and scale from 2^-127 up: code value x 2^(byte - 127), infinite from
+// 2^128 on, NaN for byte 255).  E2M1 x 2^X is exact in bf16, whose subnormal values the bf16 MFMA takes as they are; products
+// and sums are the MFMA's in fp32.
 #pragma once
 
 #include <type_traits>
