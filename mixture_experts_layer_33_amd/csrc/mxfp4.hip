@@ -59,10 +59,10 @@ hipError_t launch_quantize_mxfp4(const void* src, int64_t rows, int64_t cols, ui
 }
 
 // ------------------------------------------------------------------ product, few rows
-// out[m][n] = sum_k x[m][k] W[n][k] for up to 16 rows of x: a weight stream (mx4.h).  A unit is 16 weight rows; a
+// out[m][n] = sum_k x[m][k] W[n][k] for few rows of x (few_rows): a weight stream (mx4.h).  A unit is 16 weight rows; a
 // workgroup's NW wavefronts split its columns (wavefront w takes pairs w, w + NW, ...: together they read whole rows),
-// keep their part of x in registers over all units of the workgroup (rows longer than NW PPW pairs: read again for every
-// chunk of them), and join their sums through LDS in a fixed order.  D chunks of codes are in flight, without a branch
+// keep their part of x in registers over all units of the workgroup (rows longer than NW PPW pairs, of up to eight tokens: read
+// again for every chunk of them), and join their sums through LDS in a fixed order.  D chunks of codes are in flight, without a branch
 // between their requests: what lies past the end has addresses outside its buffer.
 // What bounds it is latency, of the launch, the first codes and x.  1 x 7168 x 2048 4.6 us (1.7 TB/s), 8 x 4096 x 7168 7.2 (2.2
 // TB/s; 9.9 with x read straight into the operand's layout), 12 x 16384 x 8192 21.5 (3.3 TB/s).  Tiles (mxfp4_tile.hip) take 7.0, 10.6
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(512) void mx4_vec_kernel(Mx4Args p, int units) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), NW = blockDim.x >> 6;
   const int g = lane >> 4, col = lane & 15, chunk = lane >> 3, row = lane & 7, P = (p.K + 255) / 256;
   const int M = (int)p.M;
-  const int chunks = (P + NW * PPW - 1) / (NW * PPW);
+  const int chunks = TS == 1 ? (P + NW * PPW - 1) / (NW * PPW) : 1;
   const uint32_t rowb = (uint32_t)p.K / 2, srows = (uint32_t)p.N * 4;
   const __amdgpu_buffer_rsrc_t wr = buffer_of(p.w, (uint32_t)p.N * rowb), sr = buffer_of(p.s, (uint32_t)(p.K / 128) * srows);
   bf16x8 x[PPW][TS][4];
@@ -203,9 +203,14 @@ __global__ __launch_bounds__(512) void mx4_vec_kernel(Mx4Args p, int units) {
   for (int m = 0; m < steps; m += D) unrolled<D>([&](auto s) __attribute__((always_inline)) { step(m + decltype(s)::value, s); });
 }
 
-// Up to 16 rows the product is a stream of W; more are tiles (mxfp4_tile.hip).
-static bool few_rows(int64_t M) { return M <= 16; }
-size_t matmul_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) { return few_rows(M) ? 0 : mx4_tile_workspace_bytes(M, N, K); }
+// Up to 8 rows the product is a stream of W, and up to 16 while all of x stays in registers; more are tiles (mxfp4_tile.hip).
+// Stream | tiles, us: 8 x 4096 x 12288 13.5 | 15.1, 8 x 8192 x 28672 39.8 | 43.5; 16 x 512 x 1024 3.6 | 5.2, 12 x 2048 x 4096 5.9 | 8.7,
+// 16 x 7168 x 8192 14.2 | 16.7, 9 x 4096 x 8192 10.6 | 11.7; longer rows, read again for every unit: 16 x 512 x 9216 14.5 | 9.7,
+// 12 x 7168 x 9216 24.6 | 18.2, 16 x 4096 x 12288 17.1 | 15.3, 16 x 1024 x 28672 27.3 | 12.8.
+static bool few_rows(int64_t M, int64_t K) { return M <= 8 || (M <= 16 && K <= 8192); }
+size_t matmul_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return few_rows(M, K) ? 0 : mx4_tile_workspace_bytes(M, N, K);
+}
 
 template <int PPW>
 static void run_vec(const Mx4Args& a, bool f32_out, dim3 grid, int units, int nw, hipStream_t st) {
@@ -221,7 +226,7 @@ static void run_vec(const Mx4Args& a, bool f32_out, dim3 grid, int units, int nw
 
 hipError_t launch_matmul_mxfp4(const void* x, const uint8_t* w, const uint8_t* w_scale, int64_t M, int64_t N, int64_t K,
                                bool f32_out, void* out, void* ws, hipStream_t st) {
-  if (!few_rows(M)) return launch_mx4_tiles(x, w, w_scale, M, N, K, f32_out, out, ws, st);
+  if (!few_rows(M, K)) return launch_mx4_tiles(x, w, w_scale, M, N, K, f32_out, out, ws, st);
   const Mx4Args a{(const bf16_t*)x, w, w_scale, M, (int)N, (int)K, out};
   const int units = (int)((N + 15) / 16), P = (int)((K + 255) / 256), nw = std::min(8, P);
   const int ppw = std::min(4, (P + nw - 1) / nw);
