@@ -613,7 +613,11 @@ size_t decode_mxfp4_workspace_bytes(int T, int E, int k, int f, int fs) {
 
 template <int PPW, int TS>
 static hipError_t run_up(const D4Args& a, int grid, int nw, hipStream_t st) {
-  constexpr int D = PPW <= 2 ? 4 : TS == 1 ? 3 : 2;
+  // Units in flight.  Two are the fewest that keep the stream going, and more delay the first unit's codes (its requests queue
+  // behind theirs) or spill (16 tokens, d 7168).  With 1 | 2 | 3 | 4, the whole call, us: 8 tokens, d 2048, f 1408, 64 experts
+  // 77.5 | 70.2 | 70.8 | 71.8; 1 token, d 4096, f 1024, 512 experts 37.0 | 37.9 | 38.5 | 40.4, 16 tokens 224 | 202 | 207 | 210;
+  // 1 token, d 7168, f 2048, 256 experts 60.1 | 61.4 | 62.6 | 65.1, 16 tokens 449 | 454 | 971 | 1267.
+  constexpr int D = 2;
   if (a.E > 512) d4_up_kernel<PPW, TS, D, 16><<<grid, 64 * nw, 0, st>>>(a);
   else if (a.E > 256) d4_up_kernel<PPW, TS, D, 8><<<grid, 64 * nw, 0, st>>>(a);
   else d4_up_kernel<PPW, TS, D, 4><<<grid, 64 * nw, 0, st>>>(a);
