@@ -6,13 +6,15 @@
 //
 // Every used expert's weights are read once, whatever the number of tokens that chose it (mx4.h: up to eight tokens are
 // columns of one product).  h is formed in fp32 and kept as two bf16 parts, hi = bf16(h) and lo = bf16(h - hi)
-// (2^-17 of h is left out; y's own rounding is 2^-9).
+// (at most 2^-16 of h is left out; y's own rounding is 2^-8).
 //
 // Three launches: the logits (d in eight splits), gate and up, down.  Every workgroup of gate and up joins the logits and makes the
 // choice for itself, 2 to 5 us in which it would wait for one that makes it (moe_route_scored's kernels, three launches, took
 // 20 to 26 in this place); the first one leaves the down product's entries for the next launch while its weights come.
-// What bounds it is the weight stream.  One token of 8 + 1 of 256 experts, 7168 x 2048: logits 4.2 us, gate and up 35 (140 MB:
-// the first codes are asked for after 6 us, then 5.2 TB/s), down 19 (70 MB).  Eight tokens: 7, 167 (5.5 TB/s), 79 (5.7 TB/s).
+// What bounds it is the weight stream, each line of which is read once (fetched bytes: 1.03 times gate and up's, 1.07
+// to 1.10 times down's).  One token of 8 + 1 of 256 experts, 7168 x 2048, medians of a kernel trace: logits 4.9 us, gate and up 34.8 (140 MB:
+// the first codes are asked for after 6 us, then 5.2 TB/s), down 18.6 (70 MB).  Eight tokens, the least and the median of 31 calls:
+// 7.5 and 9.6, 164 and 182 (5.6 and 5.1 TB/s), 79 and 96 (5.8 and 4.8 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -406,7 +408,7 @@ __global__ __launch_bounds__(512) void d4_up_kernel(D4Args p) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[D4_UP_LDS<PPW, TS>];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), NW = blockDim.x >> 6;
   float* row = (float*)lds + wave * 64 * VPL;      // the choice's, before anything else
-  constexpr int Z = VPL == 4 ? D4_KS : 4;          // planes in flight: eight of a wide row spill
+  constexpr int Z = VPL == 4 ? D4_KS : 4;          // planes in flight: of 8 experts a lane eight spill (the choice among 16 spills 86 registers with any number)
   float v[Z][VPL], bias[VPL], bal[VPL];
   d4_planes<VPL, Z>(p, min(wave, p.T - 1), 0, v, bias, bal);
   d4_clear(L);

@@ -27,6 +27,10 @@ namespace moe {
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
+// Compute units of an MI355X.  The product's plan is made for these and not for the current device's: its workspace is a function of
+// the sizes alone.
+constexpr int CUS = 256;
+
 constexpr uint32_t RSRC_WORD3 = 0x00027000;   // raw buffer, 32-bit data
 constexpr uint32_t OUTSIDE = 0x80000000u;      // an offset past every buffer (they are below 2 GiB): the load returns zeros
 constexpr int NT_LOAD = 2;                     // cache policy of a buffer load: non-temporal

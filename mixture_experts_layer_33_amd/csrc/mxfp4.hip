@@ -11,6 +11,8 @@ namespace moe {
 // Four lanes hold one block of 32 (8 bf16 each).  X = floor(log2 amax) - 2 (2 = exponent of the largest E2M1 value 6 =
 // 1.5 2^2), clamped to -127 below; code = RNE_E2M1(v / 2^X), values above 6 saturating.  gfx950's
 // v_cvt_scalef32_pk_fp4_bf16 divides, rounds and saturates two values at once.  A block with an infinity or a NaN: byte 255.
+// What bounds it is HBM (2 bytes read and 17/32 written a value): 524,288 x 7168 1.95 ms (4.9 TB/s; a copy moves 4.8), 16,384 x 8192
+// 76 us (4.5), 4,168 x 7168 20.5 us (3.7); one row 3.3 us, a launch.
 __device__ __forceinline__ bf16x2_t pair_of(uint32_t v) { return __builtin_bit_cast(bf16x2_t, v); }
 
 __global__ __launch_bounds__(256) void quantize_mxfp4_kernel(const bf16_t* __restrict__ src, int64_t nvec, int64_t rows,
@@ -64,9 +66,9 @@ hipError_t launch_quantize_mxfp4(const void* src, int64_t rows, int64_t cols, ui
 // keep their part of x in registers over all units of the workgroup (rows longer than NW PPW pairs, of up to eight tokens: read
 // again for every chunk of them), and join their sums through LDS in a fixed order.  D chunks of codes are in flight, without a branch
 // between their requests: what lies past the end has addresses outside its buffer.
-// What bounds it is latency, of the launch, the first codes and x.  1 x 7168 x 2048 4.6 us (1.7 TB/s), 8 x 4096 x 7168 7.2 (2.2
-// TB/s; 9.9 with x read straight into the operand's layout), 12 x 16384 x 8192 21.5 (3.3 TB/s).  Tiles (mxfp4_tile.hip) take 7.0, 10.6
-// and 23.9 us there, and 16 x 4096 x 7168 10.7 against 9.9.
+// What bounds it is latency, of the launch, the first codes and x.  (Times here and in mxfp4_tile.hip: a call's, the median of replays
+// of a graph of calls on different weights.)  1 x 7168 x 2048 5.4 us (1.5 TB/s), 8 x 4096 x 7168 8.0 (2.0 TB/s; with x read straight into
+// the operand's layout the kernel took 9.9 where it takes 7.2), 12 x 16384 x 8192 20 (3.6 TB/s).
 struct Mx4Args {
   const bf16_t* x;
   const uint8_t* w;
@@ -214,7 +216,10 @@ size_t matmul_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 
 template <int PPW>
 static void run_vec(const Mx4Args& a, bool f32_out, dim3 grid, int units, int nw, hipStream_t st) {
-  constexpr int D = 1;      // most workgroups have one unit: two in flight cost 0.3 to 2 us more (requests past the end), 1 x 7168 x 2048: 5.3 and 5.6
+  // One unit in flight: a workgroup has one to four at these sizes, and a second one's requests (or those past the end) delay the
+  // first one's codes.  One | two, us: 1 x 7168 x 2048 (448 units on 256 workgroups) 5.3 | 5.4, 1 x 4096 x 7168 7.8 | 9.7, 8 x 4096 x
+  // 7168 7.8 | 9.9, 12 x 16384 x 8192 20 | 25.6; two would win where many units are short: 1 x 16384 x 2048 7.8 | 7.1.
+  constexpr int D = 1;
   if (a.M > 8) {
     if (f32_out) mx4_vec_kernel<PPW, 2, D, true><<<grid, 64 * nw, 0, st>>>(a, units);
     else mx4_vec_kernel<PPW, 2, D, false><<<grid, 64 * nw, 0, st>>>(a, units);
@@ -230,7 +235,7 @@ hipError_t launch_matmul_mxfp4(const void* x, const uint8_t* w, const uint8_t* w
   const Mx4Args a{(const bf16_t*)x, w, w_scale, M, (int)N, (int)K, out};
   const int units = (int)((N + 15) / 16), P = (int)((K + 255) / 256), nw = std::min(8, P);
   const int ppw = std::min(4, (P + nw - 1) / nw);
-  const dim3 grid((unsigned)std::min(units, 256));
+  const dim3 grid((unsigned)std::min(units, CUS));
   switch (ppw) {
     case 1: run_vec<1>(a, f32_out, grid, units, nw, st); break;
     case 2: run_vec<2>(a, f32_out, grid, units, nw, st); break;

@@ -10,9 +10,10 @@
 // a lane's codes of a step are one 16-byte read, under one scale.  W's rows are the first operand, so that a lane
 // holds four neighbouring outputs of one row of x.
 //
-// 2045 x 7168 x 4096 takes 94 us, 1.28 PFLOP/s, in 224 tiles of 256 x 256 (bound by the MFMAs at the clock they run at and by
-// 32 tiles too few for the chip); the library's product of bf16 weights, four times the bytes, takes 97.  61 x 4168 x 7168: 13 us, of
-// which the sums of three splits are 2: a tile's copies land 1 us after they are asked for, two steps ahead.
+// 2045 x 7168 x 4096 takes 102 us, 1.18 PFLOP/s, in 224 tiles of 256 x 256 (bound by the MFMAs, busy 52 % of all clocks, and by 32 tiles
+// too few for the chip; a call after a pause, at a higher clock, 95); the library's product of bf16 weights, four times the bytes,
+// takes 95.  61 x 4168 x 7168: 15 us (library 28), of which the sums of three splits are 2: a tile's copies land 1 us after they are
+// asked for, two steps ahead, and bring quarter lines of the codes.
 #include <algorithm>
 
 #include "kernels.h"
@@ -247,11 +248,12 @@ __global__ __launch_bounds__(256) void mx4_join_kernel(const float* planes, int6
     }
 }
 
-// The tile shape and the splits of K.  A round of 256 workgroups takes K / splits times its shape's nanoseconds a column
+// The tile shape and the splits of K.  A round of CUS workgroups takes K / splits times its shape's nanoseconds a column
 // (measured with about 256 tiles), and splits add a launch and the traffic of their sums; the least is taken.  Measured, us:
-// 61 x 4168 x 7168 64 x 64 in 3 splits 14.6, in one 23.5, 32 x 64 in 3 15.7; 32 x 4096 x 7168 32 x 64 in 4 splits 11.5, 64 x 64 in 4
-// 13.0; 512 x 4096 x 4096 64 x 128 23.5, 64 x 64 32.9, 128 x 128 29.3; 1024 x 4096 x 4096 128 x 128 34.7, 128 x 256 50.9;
-// 1024 x 7168 x 2048 128 x 256 31.6, 128 x 128 36.5, 256 x 256 45.3; 2045 x 7168 x 4096 256 x 256 100.6, 128 x 256 105.8.
+// 61 x 4168 x 7168 64 x 64 in 3 splits 14.9, in one 23.7, in 4 21.5, 32 x 64 in 3 16.6; 32 x 4096 x 7168 32 x 64 in 4 splits 11.5,
+// 64 x 64 in 4 13.2; 128 x 4096 x 4096 32 x 64 10.9, 64 x 64 14.5; 256 x 4096 x 4096 64 x 64 15.8, 64 x 128 20.9; 512 x 4096 x 4096
+// 64 x 128 23.4, 64 x 64 30.1, 128 x 128 29.6; 1024 x 4096 x 4096 128 x 128 36.3, 64 x 128 42.0, 128 x 256 51;
+// 1024 x 7168 x 2048 128 x 256 32.9, 128 x 128 36.5, 256 x 256 45.5; 2045 x 7168 x 4096 256 x 256 102, 128 x 256 108.
 struct TilePlan {
   int kind, splits;
   int64_t tiles;
@@ -265,7 +267,7 @@ static TilePlan tile_plan(int64_t M, int64_t N, int64_t K) {
     const int64_t tiles = (M + shapes[k].bm - 1) / shapes[k].bm * ((N + shapes[k].bn - 1) / shapes[k].bn);
     for (int s = 1; s <= 16 && (s == 1 || K >= 128 * (int64_t)s * shapes[k].groups); ++s) {
       const double join = s == 1 ? 0 : 2600 + (double)M * N * s * 8 / 2400;      // ns
-      const double t = (double)((tiles * s + 255) / 256) * K / s * shapes[k].ns + join;
+      const double t = (double)((tiles * s + CUS - 1) / CUS) * K / s * shapes[k].ns + join;
       if (best.tiles == 0 || t < least) {
         best = {k, s, tiles};
         least = t;
